@@ -44,11 +44,13 @@ extern "C" {
 /* Element types of idx_logits_fp8's output (the pages' output_dtype). */
 #define IDX_DTYPE_F32 0 /* float32 (the default on the pages) */
 #define IDX_DTYPE_F16 1 /* IEEE binary16 */
-#define IDX_DTYPE_BF16 2 /* bfloat16 (idx_logits_mxfp4 with head_dim 128 only; its pages' default) */
+#define IDX_DTYPE_BF16 2 /* bfloat16 (of the logits, idx_logits_mxfp4 with head_dim 128 only; its
+                            pages' default) */
 
 /* Device-side status bits (idx_device_status). */
 #define IDX_DEV_WAIT_TIMEOUT 1 /* a pipeline wait gave up after its time limit */
 #define IDX_DEV_BAD_PAGE 2     /* a needed block-table entry was outside [0, num_blocks) */
+#define IDX_DEV_BAD_POSITION 8 /* a position outside the rotary table: its row is not rotated */
 #define IDX_DEV_INEXACT_SCALE 4 /* (MXFP4) a row's block scales span more than 8 binades, or a
                                    scale byte is the NaN code 0xFF: its staging rounded */
 
@@ -344,6 +346,157 @@ int idx_debug_withhold_first_tile(int32_t cta);
  * Synchronous (it copies from the device); a debugging aid, not for the hot path.
  */
 int idx_device_status(int32_t *status_out, int32_t clear);
+
+/* =================================================================================================
+ * The operators around the indexer: rotary positions, the writers of the two 8-bit pools and the
+ * attention over the K/V pool.  The pages have no counterpart to these entry points.
+ *
+ * New tokens.  idx_index_prepare and idx_kv_append take `tokens` rows, request by request.
+ * token_starts: device int32 [batch + 1], non-decreasing: request b's are rows
+ * [token_starts[b], token_starts[b+1]) (possibly none; rows at or past token_starts[batch] belong
+ * to no request and are passed over).  NULL: every request has next_n rows (tokens = batch *
+ * next_n; next_n is not read otherwise).  seq_lens[b] is the request's length WITH its new tokens,
+ * the last of which stands at position seq_lens[b] - 1; where a request is shorter than its rows
+ * (an idle slot of a fixed batch has length 0), the rows before position 0 reach no pool.
+ *
+ * Pages.  Position p of request b is token p % block_size of block
+ * block_tables[b*bt_row_stride + p / block_size].  A position past the table's bt_width columns
+ * or a block id outside [0, num_blocks) is skipped and flagged (IDX_DEV_BAD_PAGE).  Two requests
+ * of one call must not write to the same block.
+ *
+ * Rotation.  table (NULL: none): device float32 [max_positions][rot_dim/2][2], the cosine and
+ * sine of each pair's angle at each position (idx_rotary_table).  The pairs of a head's row x are
+ * a = rot_offset + i, b = a + rot_dim/2 (halves) or a = rot_offset + 2i, b = a + 1 (interleaved),
+ *     x'[a] = x[a] cos - x[b] sin,    x'[b] = x[b] cos + x[a] sin     (float32),
+ * the other elements stay.  A position past the table leaves its row as it is and is flagged
+ * (IDX_DEV_BAD_POSITION).
+ *
+ * Row strides are in elements.  Loads are 16 bytes wide where every base, stride, rot_offset and
+ * rot_dim/2 allows it, single elements otherwise.  IDX_VALIDATE does not look at these calls.
+ */
+#define IDX_ROTARY_NONE 0   /* base^(-2i/rot_dim) */
+#define IDX_ROTARY_LINEAR 1 /* divided by factor */
+#define IDX_ROTARY_NTK 2    /* the base times factor^(rot_dim/(rot_dim-2)) */
+#define IDX_ROTARY_YARN 3   /* by parts: fast pairs as they are, slow ones divided by factor */
+#define IDX_ROTARY_MAX_DIM 1024
+
+/*
+ * The pairs' frequencies in 64 bits (host arithmetic): inv_freq[rot_dim/2], and the factor on the
+ * cosine and sine (1, with IDX_ROTARY_YARN 0.1 ln(factor) + 1).  base > 1, factor >= 1.
+ * IDX_ROTARY_YARN: pairs that turn at least beta_fast times over original_positions keep their
+ * frequency, pairs that turn at most beta_slow times have it divided, with a linear ramp over the
+ * pairs between (their bounds rounded outward to whole pairs).
+ */
+int idx_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                           double original_positions, double beta_fast, double beta_slow,
+                           double *inv_freq, double *magnitude);
+
+/*
+ * table[p][i] = magnitude * (cos, sin)(p * inv_freq[i]), computed in 64 bits and rounded once;
+ * inv_freq is host memory, read before the call returns; table is device float32
+ * [max_positions][rot_dim/2][2].
+ */
+int idx_rotary_table(const double *inv_freq, double magnitude, int32_t max_positions,
+                     int32_t rot_dim, float *table, void *stream);
+
+/*
+ * The rotation of x (device [tokens][num_heads][head_dim] of dtype, any token and head strides,
+ * unit element stride) at positions[tokens] (device int32) into out (the same shape and type):
+ * computed in float32 and rounded once.  out = x with the same strides rotates in place;
+ * otherwise the two must not overlap, and the other elements are copied.  inverse != 0 turns by
+ * the negative angle: the gradient of the output taken back to x.
+ */
+int idx_rotary(const void *x, int64_t x_token_stride, int64_t x_head_stride,
+               const int32_t *positions, int64_t tokens, int32_t num_heads, int32_t head_dim,
+               int32_t dtype, const float *table, int32_t max_positions, int32_t rot_dim,
+               int32_t rot_offset, int32_t interleaved, int32_t inverse, void *out,
+               int64_t out_token_stride, int64_t out_head_stride, void *stream);
+
+/*
+ * The inputs of idx_logits_fp8 from a layer's index keys and queries: rows rotated, divided by
+ * their scale max|x| / 448 (max|x| at least 2^-100, over what is finite) and rounded to e4m3
+ * (infinities to +-448, NaN to NaN).
+ *
+ *   k            [tokens][head_dim]: into kv_fused (see idx_logits_fp8), value and float32 scale
+ *   q            NULL, or [tokens][num_heads][head_dim]: into q_out, device uint8 [tokens]
+ *                [num_heads][head_dim] e4m3, contiguous; weights_out[t][h] = weights[t][h] * the
+ *                row's scale (float32, contiguous; weights has unit head stride)
+ *   dtype        of k and q
+ *   head_dim     64, 128 or 192
+ */
+int idx_index_prepare(const void *k, int64_t k_token_stride, const void *q, int64_t q_token_stride,
+                      int64_t q_head_stride, const float *weights, int64_t weights_token_stride,
+                      int32_t dtype, int64_t tokens, int32_t num_heads, int32_t head_dim,
+                      const float *table, int32_t max_positions, int32_t rot_dim,
+                      int32_t rot_offset, int32_t interleaved, const int32_t *token_starts,
+                      const int32_t *seq_lens, int64_t seq_lens_stride, int32_t batch,
+                      int32_t next_n, const int32_t *block_tables, int64_t bt_row_stride,
+                      int32_t bt_width, int32_t block_size, int64_t num_blocks, uint8_t *kv_fused,
+                      uint8_t *q_out, float *weights_out, void *stream);
+
+/*
+ * New keys (rotated) and values into the 8-bit K/V cache:
+ *
+ *   k_pool, v_pool      device e4m3 [num_blocks][kv_heads][block_size][head_dim], 16-byte aligned
+ *   k_scales, v_scales  device float32 [num_blocks][kv_heads]: a value is its e4m3 times the scale
+ *                       of its block and head
+ *   k, v                [tokens][kv_heads][head_dim] of dtype
+ *   head_dim            64 or 128
+ *
+ * A block's scale is the least power of two, 2^-100 or more, that brings the largest finite
+ * magnitude of its tokens to at most 448.  A block whose first token is new takes the scale of the
+ * new ones, whatever it held.  One that already holds tokens keeps its scale while that is large
+ * enough; else it grows, and the values held are multiplied by old / new and rounded to e4m3
+ * again (which changes them only where they become subnormal).
+ */
+int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                  int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t tokens,
+                  int32_t kv_heads, int32_t head_dim, const float *table, int32_t max_positions,
+                  int32_t rot_dim, int32_t rot_offset, int32_t interleaved,
+                  const int32_t *token_starts, const int32_t *seq_lens, int64_t seq_lens_stride,
+                  int32_t batch, int32_t next_n, const int32_t *block_tables,
+                  int64_t bt_row_stride, int32_t bt_width, int32_t block_size, int64_t num_blocks,
+                  uint8_t *k_pool, uint8_t *v_pool, float *k_scales, float *v_scales,
+                  void *stream);
+
+/*
+ * Attention over the 8-bit K/V cache (layout as for idx_kv_append; the scales may be any finite
+ * numbers).  For row r = b*next_n + t and query head h, with K/V head g = h / (num_heads/kv_heads):
+ *
+ *   z_p = softmax_scale * k_scale[page(p)][g] * (q[b,t,h,:] . k[p,g,:])
+ *   out[b,t,h,:] = sum_p softmax(z)_p * v_scale[page(p)][g] * v[p,g,:]
+ *
+ * over the positions p <= seq_lens[b] - next_n + t (the extents of idx_logits_fp8's rows), or,
+ * with candidates, over the positions stored in slots [ranges[0][r], ranges[1][r]) of row r: what
+ * idx_threshold_select and idx_indexer_threshold_select leave there (all that the slots hold, of
+ * which the exact top_k is a part; a position outside the extent is passed over, one stored twice
+ * counts twice).  A row without positions gives zeros and lse = -inf.  What stands in the cache
+ * at a position that a row does not see never reaches it, NaN included.
+ *
+ *   q             device [batch][next_n][num_heads][head_dim] of dtype (IDX_DTYPE_F16 or _BF16),
+ *                 16-byte aligned, strides in elements, multiples of 8
+ *   num_heads     a multiple of kv_heads, at most 4096
+ *   head_dim      64 or 128; block_size 32, 64 or 128; next_n 1..4; batch 0..4096
+ *   num_blocks    (num_blocks + 1) * kv_heads * block_size must stay below 2^31
+ *   candidates    NULL, or device int32 [batch*next_n][slots][2] (position, anything), 8-byte
+ *                 aligned, with ranges, device int32 [2][batch*next_n]
+ *   num_sms       CTAs a SM-wide wave of the grid (0 = this device's SM count)
+ *   out           device, dtype [batch][next_n][num_heads][head_dim], contiguous, 16-byte aligned
+ *   lse           NULL, or device float32 [batch][next_n][num_heads]: ln sum_p exp(z_p)
+ *   workspace     device, 256-byte aligned, idx_attention_workspace_bytes(...) bytes
+ */
+int64_t idx_attention_workspace_bytes(int32_t batch, int32_t next_n, int32_t num_heads,
+                                      int32_t kv_heads, int32_t head_dim, int32_t num_sms);
+int idx_attention_fp8(const void *q, int64_t q_batch_stride, int64_t q_token_stride,
+                      int64_t q_head_stride, int32_t dtype, const uint8_t *k_pool,
+                      const uint8_t *v_pool, const float *k_scales, const float *v_scales,
+                      int64_t num_blocks, int32_t block_size, const int32_t *block_tables,
+                      int64_t bt_row_stride, int32_t bt_width, const int32_t *seq_lens,
+                      int64_t seq_lens_stride, int32_t batch, int32_t next_n, int32_t num_heads,
+                      int32_t kv_heads, int32_t head_dim, float softmax_scale,
+                      const int32_t *candidates, int32_t slots, const int32_t *ranges,
+                      int32_t num_sms, void *out, float *lse, void *workspace,
+                      int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

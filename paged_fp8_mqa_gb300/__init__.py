@@ -9,6 +9,9 @@ Low-level names mirror the C ABI (``idx_logits_fp8``, ``idx_threshold_select``,
 ``idx_min_block_table_width``, ...); they take raw pointers and sizes.  The torch-facing helpers
 (``logits_fp8``, ``threshold_select``, ``indexer_threshold_select``, ``schedule``) take tensors,
 check dtypes/devices, and pass pointers, strides and the current CUDA stream through.
+
+The operators around the indexer (rotary positions, the writers of the two 8-bit pools, attention
+over the K/V pool) are bound in ``layer`` and reached from here by the same names.
 """
 from __future__ import annotations
 
@@ -29,6 +32,7 @@ IDX_DTYPE_BF16 = 2
 IDX_DEV_WAIT_TIMEOUT = 1
 IDX_DEV_BAD_PAGE = 2
 IDX_DEV_INEXACT_SCALE = 4
+IDX_DEV_BAD_POSITION = 8
 
 TILE_TOKENS = 128  # KV positions per work unit of the persistent logits kernel
 
@@ -406,3 +410,10 @@ def indexer_threshold_select(q, kv_fused, weights, block_tables, seq_lens, max_s
 def device_status(clear: bool = False) -> int:
     """OR of the IDX_DEV_* bits raised by the kernels since the last clear (synchronous)."""
     return idx_device_status(clear)
+
+
+from .layer import (IDX_ROTARY_LINEAR, IDX_ROTARY_MAX_DIM, IDX_ROTARY_NONE,  # noqa: E402
+                    IDX_ROTARY_NTK, IDX_ROTARY_YARN, attention_fp8, idx_attention_fp8,
+                    idx_attention_workspace_bytes, idx_index_prepare, idx_kv_append, idx_rotary,
+                    idx_rotary_frequencies, idx_rotary_table, index_prepare, kv_append, rotary,
+                    rotary_table)

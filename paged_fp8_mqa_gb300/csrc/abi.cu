@@ -13,23 +13,64 @@
 
 #include "../../include/idx.h"
 #include "internal.h"
+#include "layer.h"
 #include "mxfp4.h"
 
 #define IDX_EXPORT extern "C" __attribute__((visibility("default")))
 
 namespace {
-
 thread_local std::string g_error;
+}  // namespace
+
+namespace idx {
 
 int fail(int code, const std::string &msg) {
   g_error = msg;
   return code;
 }
 
+int fail(int code, const char *msg) {
+  try {
+    g_error = msg;
+  } catch (...) {  // out of host memory: the code alone is the answer
+    g_error.clear();
+  }
+  return code;
+}
+
 int cuda_fail(cudaError_t e, const char *what) {
-  g_error = std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
+  try {
+    g_error = std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
+  } catch (...) {
+    g_error.clear();
+  }
   return IDX_CUDA;
 }
+
+void clear_error() { g_error.clear(); }
+
+int resolve_sms(int32_t requested, int32_t *out) {
+  if (requested < 0 || requested > 1024) return fail(IDX_INVALID_ARG, "num_sms must be 0..1024");
+  if (requested > 0) {
+    *out = requested;
+    return IDX_OK;
+  }
+  int dev = 0, n = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  *out = n;
+  return IDX_OK;
+}
+
+}  // namespace idx
+
+namespace {
+
+using idx::cuda_fail;
+using idx::fail;
+using idx::resolve_sms;
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -106,21 +147,6 @@ int encode_kblocks_q(CUtensorMap *map, const void *base, uint64_t rows, uint32_t
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(IDX_CUDA, "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(r));
-  return IDX_OK;
-}
-
-int resolve_sms(int32_t requested, int32_t *out) {
-  if (requested < 0 || requested > 1024) return fail(IDX_INVALID_ARG, "num_sms must be 0..1024");
-  if (requested > 0) {
-    *out = requested;
-    return IDX_OK;
-  }
-  int dev = 0, n = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-  *out = n;
   return IDX_OK;
 }
 
@@ -667,7 +693,14 @@ IDX_EXPORT int idx_device_status(int32_t *status_out, int32_t clear) {
   cudaError_t e = idx::logits_status(&a, clear != 0);
   if (e == cudaSuccess) e = idx::select_status(&b, clear != 0);
   if (e == cudaSuccess) e = idx::mxfp4_status(&c, clear != 0);
+  int32_t all = a | b | c;
+  for (const auto unit : {idx::rotary_status, idx::index_status, idx::append_status,
+                          idx::attention_status}) {
+    int32_t bits = 0;
+    if (e == cudaSuccess) e = unit(&bits, clear != 0);
+    all |= bits;
+  }
   if (e != cudaSuccess) return cuda_fail(e, "status copy");
-  *status_out = a | b | c;
+  *status_out = all;
   return IDX_OK;
 }

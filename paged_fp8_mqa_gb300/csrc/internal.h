@@ -5,10 +5,21 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <string>
 
 #include "../../include/idx.h"
 
 namespace idx {
+
+// The calling thread's error message (idx_last_error): each returns the status code it is given
+// (IDX_CUDA for cuda_fail).
+int fail(int code, const std::string &msg);
+int fail(int code, const char *msg);
+int cuda_fail(cudaError_t e, const char *what);
+void clear_error();
+
+// The persistent grid: `requested` (1 .. 1024), or the current device's SM count for 0.
+int resolve_sms(int32_t requested, int32_t *out);
 
 // Launches `kernel` as a programmatic dependent of the previous kernel in `stream`: the launch may
 // be processed while that kernel still runs, so its latency hides behind it.  Every kernel of

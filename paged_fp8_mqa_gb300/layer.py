@@ -1,0 +1,404 @@
+"""The operators around the indexer: rotary positions, the writers of the two 8-bit pools and the
+attention over the K/V pool.
+
+Like the rest of the binding it only marshals: the C-ABI mirrors (``idx_...``) take raw pointers
+and sizes in the order of ``include/idx.h``, the torch-facing functions take tensors.  Tensors that
+a call allocates (outputs, workspace) belong to PyTorch's caching allocator; they are recorded on
+``stream`` when it is not the current one.
+"""
+from __future__ import annotations
+
+import ctypes
+
+IDX_ROTARY_NONE = 0
+IDX_ROTARY_LINEAR = 1
+IDX_ROTARY_NTK = 2
+IDX_ROTARY_YARN = 3
+IDX_ROTARY_MAX_DIM = 1024
+
+_SCALINGS = {"none": IDX_ROTARY_NONE, "linear": IDX_ROTARY_LINEAR, "ntk": IDX_ROTARY_NTK,
+             "yarn": IDX_ROTARY_YARN}
+
+_P, _I, _L, _F, _D = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
+                      ctypes.c_double)
+_SIGNATURES = {
+    "idx_rotary_frequencies": (ctypes.c_int, [_I, _D, _I, _D, _D, _D, _D, _P, _P]),
+    "idx_rotary_table": (ctypes.c_int, [_P, _D, _I, _I, _P, _P]),
+    "idx_rotary": (ctypes.c_int, [_P, _L, _L, _P, _L, _I, _I, _I, _P, _I, _I, _I, _I, _I, _P, _L,
+                                  _L, _P]),
+    "idx_index_prepare": (ctypes.c_int, [_P, _L, _P, _L, _L, _P, _L, _I, _L, _I, _I, _P, _I, _I,
+                                         _I, _I, _P, _P, _L, _I, _I, _P, _L, _I, _I, _L, _P, _P,
+                                         _P, _P]),
+    "idx_kv_append": (ctypes.c_int, [_P, _L, _L, _P, _L, _L, _I, _L, _I, _I, _P, _I, _I, _I, _I,
+                                     _P, _P, _L, _I, _I, _P, _L, _I, _I, _L, _P, _P, _P, _P, _P]),
+    "idx_attention_workspace_bytes": (ctypes.c_int64, [_I, _I, _I, _I, _I, _I]),
+    "idx_attention_fp8": (ctypes.c_int, [_P, _L, _L, _L, _I, _P, _P, _P, _P, _L, _I, _P, _L, _I,
+                                         _P, _L, _I, _I, _I, _I, _I, _F, _P, _I, _P, _I, _P, _P,
+                                         _P, _L, _P]),
+}
+_functions: dict = {}
+
+
+def _c(name):
+    f = _functions.get(name)
+    if f is None:
+        from . import lib
+        f = getattr(lib(), name)
+        f.restype, f.argtypes = _SIGNATURES[name]
+        _functions[name] = f
+    return f
+
+
+# ---- C-ABI mirrors (raw pointers / ints) -------------------------------------------------------
+
+def idx_rotary_frequencies(*args) -> int:
+    return _c("idx_rotary_frequencies")(*args)
+
+
+def idx_rotary_table(*args) -> int:
+    return _c("idx_rotary_table")(*args)
+
+
+def idx_rotary(*args) -> int:
+    return _c("idx_rotary")(*args)
+
+
+def idx_index_prepare(*args) -> int:
+    return _c("idx_index_prepare")(*args)
+
+
+def idx_kv_append(*args) -> int:
+    return _c("idx_kv_append")(*args)
+
+
+def idx_attention_workspace_bytes(*args) -> int:
+    return int(_c("idx_attention_workspace_bytes")(*args))
+
+
+def idx_attention_fp8(*args) -> int:
+    return _c("idx_attention_fp8")(*args)
+
+
+# ---- torch-facing marshalling ------------------------------------------------------------------
+
+_codes: dict = {}
+
+
+def _code(dtype):
+    """The IDX_DTYPE_* code of float32, float16 or bfloat16, or None."""
+    if not _codes:
+        import torch
+        from . import IDX_DTYPE_BF16, IDX_DTYPE_F16, IDX_DTYPE_F32
+        _codes.update({torch.float32: IDX_DTYPE_F32, torch.float16: IDX_DTYPE_F16,
+                       torch.bfloat16: IDX_DTYPE_BF16})
+    return _codes.get(dtype)
+
+
+def _check(status: int) -> None:
+    if status:
+        from . import IdxError, idx_last_error
+        raise IdxError(status, idx_last_error())
+
+
+def _tensor(t, name, dims, dtype=None, device=None):
+    """A CUDA tensor (of the first argument's device) with `dims` dimensions."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dims, got {t.dim()}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _rows(t, name, dims, device=None):
+    """Rows of float32, float16 or bfloat16 elements with unit element stride: their dtype code."""
+    _tensor(t, name, dims, None, device)
+    code = _code(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    return code
+
+
+def _pool8(t, name, dims, device):
+    """e4m3 values (or their uint8 view), contiguous."""
+    import torch
+    _tensor(t, name, dims, None, device)
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{name} must be float8_e4m3fn (or its uint8 view), got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on(stream, device, *allocated):
+    """The raw stream to launch on; tensors allocated for another stream's work are recorded."""
+    import torch
+    current = torch.cuda.current_stream(device)
+    if stream is None:
+        return current.cuda_stream
+    if stream != current:
+        for t in allocated:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _table(table, device):
+    """(pointer, max_positions, rot_dim) of a rotary table, or of none."""
+    import torch
+    if table is None:
+        return None, 0, 0
+    _tensor(table, "table", 3, torch.float32, device)
+    if table.shape[2] != 2 or not table.is_contiguous():
+        raise ValueError("table must be contiguous [max_positions, rot_dim / 2, 2]")
+    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+
+
+def _tokens(block_tables, seq_lens, token_starts, rows, device):
+    """The arguments that place new tokens: (starts, seq_lens, stride, batch, next_n, tables, row
+    stride, width)."""
+    import torch
+    _tensor(block_tables, "block_tables", 2, torch.int32, device)
+    _tensor(seq_lens, "seq_lens", 1, torch.int32, device)
+    batch, width = block_tables.shape
+    if seq_lens.shape[0] != batch:
+        raise ValueError("block_tables and seq_lens must have a row for each request")
+    if width > 1 and block_tables.stride(1) != 1:
+        raise ValueError("block_tables rows must be contiguous (stride(1) == 1)")
+    starts, next_n = None, 0
+    if token_starts is not None:
+        _tensor(token_starts, "token_starts", 1, torch.int32, device)
+        if token_starts.shape[0] != batch + 1 or not token_starts.is_contiguous():
+            raise ValueError("token_starts must be contiguous, one more than the requests")
+        starts = token_starts.data_ptr()
+    elif batch:
+        next_n = rows // batch
+        if next_n * batch != rows:
+            raise ValueError("without token_starts every request has the same number of tokens")
+    return (starts, seq_lens.data_ptr(), max(seq_lens.stride(0), 1), batch, next_n,
+            block_tables.data_ptr(), max(block_tables.stride(0), width), width)
+
+
+def rotary_table(max_positions: int, rot_dim: int, *, base: float = 10000.0, scaling: str = "none",
+                 factor: float = 1.0, original_positions: float = 0.0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, device=None, stream=None):
+    """The cosine and sine of every position's angles, float32 [max_positions, rot_dim / 2, 2],
+    computed in 64 bits.  scaling: "none", "linear" (angles divided by factor), "ntk" (the base
+    grows) or "yarn" (by parts: pairs that turn at least beta_fast times over original_positions
+    are left alone, those that turn at most beta_slow times are divided by factor, and the cosines
+    and sines are multiplied by 0.1 ln(factor) + 1).  Built once and kept by the caller."""
+    import torch
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+    freq = (ctypes.c_double * max(1, rot_dim // 2))()
+    magnitude = ctypes.c_double()
+    _check(idx_rotary_frequencies(rot_dim, base, _SCALINGS[scaling], factor, original_positions,
+                                  beta_fast, beta_slow, freq, ctypes.byref(magnitude)))
+    device = torch.device("cuda" if device is None else device)
+    with torch.cuda.device(device):
+        table = torch.empty(max_positions, rot_dim // 2, 2, dtype=torch.float32, device=device)
+        _check(idx_rotary_table(freq, magnitude.value, max_positions, rot_dim, table.data_ptr(),
+                                _on(stream, table.device, table)))
+    return table
+
+
+def rotary(x, positions, table, *, interleaved: bool = False, rot_offset: int = 0,
+           inverse: bool = False, out=None, stream=None):
+    """Rotary positions: x [T, H, D] (float32, float16 or bfloat16; any token and head strides) at
+    positions (int32 [T]), elements [rot_offset, rot_offset + rot_dim) of each head turned by the
+    angles of ``table`` (see ``rotary_table``), in halves or in interleaved pairs.  ``out=x``
+    rotates in place; ``inverse`` turns back (the gradient with respect to x)."""
+    import torch
+    code = _rows(x, "x", 3)
+    dev = x.device
+    _tensor(positions, "positions", 1, torch.int32, dev)
+    T, H, D = x.shape
+    if positions.shape[0] != T or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous, one for each token of x")
+    tab, most, rot = _table(table, dev)
+    if tab is None:
+        raise TypeError("table must be a CUDA tensor")
+    made = ()
+    if out is None:
+        out = torch.empty(T, H, D, dtype=x.dtype, device=dev)
+        made = (out,)
+    else:
+        _tensor(out, "out", 3, x.dtype, dev)
+        if out.shape != x.shape or (D > 1 and out.stride(2) != 1):
+            raise ValueError("out must have the shape of x and contiguous rows")
+    if out.numel() == 0:
+        return out
+    _check(idx_rotary(x.data_ptr(), x.stride(0), x.stride(1), positions.data_ptr(), T, H, D, code,
+                      tab, most, rot, rot_offset, interleaved, inverse, out.data_ptr(),
+                      out.stride(0), out.stride(1), _on(stream, dev, *made)))
+    return out
+
+
+def index_prepare(k, kv_fused, block_tables, seq_lens, *, token_starts=None, q=None, weights=None,
+                  table=None, interleaved: bool = False, rot_offset: int = 0, q_out=None,
+                  weights_out=None, stream=None):
+    """The inputs of ``logits_fp8`` from a layer's index keys and queries.
+
+    k [T, D] (D = 64, 128 or 192) is rotated, quantised to e4m3 with a float32 scale for each row
+    and written to the requests' pages of ``kv_fused``; the T rows are the requests' newest tokens,
+    the same number for each, or rows [token_starts[b], token_starts[b+1]) (int32 [B + 1]);
+    seq_lens counts them already.  q [T, H, D] with weights [T, H] float32, if given, is rotated
+    and quantised likewise, its scales folded into the weights: returns (q e4m3 [T, H, D],
+    weights float32 [T, H]), which ``logits_fp8`` takes (q viewed as [B, next_n, H, D])."""
+    import torch
+    code = _rows(k, "k", 2)
+    dev = k.device
+    T, D = k.shape
+    _tensor(kv_fused, "kv_fused", kv_fused.dim() if isinstance(kv_fused, torch.Tensor) else 2,
+            torch.uint8, dev)
+    blocks = kv_fused.shape[0] if kv_fused.dim() else 0
+    if not kv_fused.is_contiguous() or blocks == 0:
+        raise ValueError("kv_fused must be contiguous with a leading dim of blocks")
+    block_size, rest = divmod(kv_fused.numel() // blocks, D + 4)
+    if rest:
+        raise ValueError(f"kv_fused blocks must be block_size * (D + 4) bytes, D = {D}")
+    H, made = 0, []
+    qa = (None, 0, 0, None, 0)
+    if q is not None:
+        if _rows(q, "q", 3, dev) != code:
+            raise TypeError("q and k must have the same dtype")
+        _tensor(weights, "weights", 2, torch.float32, dev)
+        H = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D or weights.shape[0] != T or weights.shape[1] != H:
+            raise ValueError("q must be [T, H, D] and weights [T, H] for k [T, D]")
+        if H > 1 and weights.stride(1) != 1:
+            raise ValueError("weights rows must be contiguous")
+        if q_out is None:
+            q_out = torch.empty(T, H, D, dtype=torch.float8_e4m3fn, device=dev)
+            made.append(q_out)
+        if weights_out is None:
+            weights_out = torch.empty(T, H, dtype=torch.float32, device=dev)
+            made.append(weights_out)
+        _pool8(q_out, "q_out", 3, dev)
+        _tensor(weights_out, "weights_out", 2, torch.float32, dev)
+        if q_out.shape != q.shape or weights_out.shape != weights.shape \
+                or not weights_out.is_contiguous():
+            raise ValueError("q_out and weights_out must be contiguous with the shapes of q and "
+                             "weights")
+        qa = (q.data_ptr(), q.stride(0), q.stride(1), weights.data_ptr(), weights.stride(0))
+    place = _tokens(block_tables, seq_lens, token_starts, T, dev)
+    if T and (q is None or H):
+        _check(idx_index_prepare(
+            k.data_ptr(), k.stride(0), *qa, code, T, H, D, *_table(table, dev), rot_offset,
+            interleaved, *place, block_size, blocks, kv_fused.data_ptr(),
+            None if q is None else q_out.data_ptr(),
+            None if q is None else weights_out.data_ptr(), _on(stream, dev, *made)))
+    return None if q is None else (q_out, weights_out)
+
+
+def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,
+              token_starts=None, table=None, interleaved: bool = False, rot_offset: int = 0,
+              stream=None):
+    """New keys (rotated) and values, [T, Hkv, D] with D = 64 or 128, into the 8-bit cache: pools
+    e4m3 [blocks, Hkv, block_size, D], scales float32 [blocks, Hkv] (powers of two).  The T rows
+    are placed as in ``index_prepare``.  A block that already holds tokens keeps its scale while
+    the new ones fit it; otherwise the scale grows and what it holds is rescaled."""
+    import torch
+    code = _rows(k, "k", 3)
+    dev = k.device
+    if _rows(v, "v", 3, dev) != code or v.shape != k.shape:
+        raise TypeError("k and v must have the same dtype and shape")
+    T, H, D = k.shape
+    _pool8(k_pool, "k_pool", 4, dev)
+    _pool8(v_pool, "v_pool", 4, dev)
+    _tensor(k_scales, "k_scales", 2, torch.float32, dev)
+    _tensor(v_scales, "v_scales", 2, torch.float32, dev)
+    blocks, heads, block_size, dim = k_pool.shape
+    if v_pool.shape != k_pool.shape or heads != H or dim != D:
+        raise ValueError("k_pool and v_pool must be [blocks, Hkv, block_size, D] for k [T, Hkv, D]")
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t.shape != k_pool.shape[:2] or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous [blocks, Hkv]")
+    place = _tokens(block_tables, seq_lens, token_starts, T, dev)
+    if T and H:
+        _check(idx_kv_append(
+            k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), code,
+            T, H, D, *_table(table, dev), rot_offset, interleaved, *place, block_size, blocks,
+            k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            _on(stream, dev)))
+
+
+def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,
+                  softmax_scale: float | None = None, candidates=None, ranges=None, out=None,
+                  lse=None, workspace=None, num_sms: int = 0, stream=None):
+    """Attention over the 8-bit K/V cache: q [B, next_n, H, D] (float16 or bfloat16; strides that
+    are multiples of 8), pools and scales as for ``kv_append``, H a multiple of Hkv; row (b, t)
+    sees positions 0 .. seq_lens[b] - next_n + t.  With ``candidates`` (int32 [B*next_n, slots, 2])
+    and ``ranges`` (int32 [2, B*next_n]) as the select leaves them, each row sees only the
+    positions stored in its slot range.  Rows that see nothing give zeros.  softmax_scale defaults
+    to D ** -0.5; ``lse`` (float32 [B, next_n, H]) receives the log-sums; ``workspace`` (uint8, at
+    least idx_attention_workspace_bytes) is allocated if not given.  Returns out, contiguous
+    [B, next_n, H, D] in q's dtype."""
+    import torch
+    _tensor(q, "q", 4)
+    dev = q.device
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"q must be float16 or bfloat16, got {q.dtype}")
+    B, n, H, D = q.shape
+    if q.stride(3) != 1 and D > 1:
+        raise ValueError("q rows must be contiguous")
+    _pool8(k_pool, "k_pool", 4, dev)
+    _pool8(v_pool, "v_pool", 4, dev)
+    blocks, kv_heads, block_size, dim = k_pool.shape
+    if v_pool.shape != k_pool.shape or dim != D:
+        raise ValueError("k_pool and v_pool must be [blocks, Hkv, block_size, D] for q's D")
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        _tensor(t, name, 2, torch.float32, dev)
+        if t.shape != k_pool.shape[:2] or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous [blocks, Hkv]")
+    _tensor(block_tables, "block_tables", 2, torch.int32, dev)
+    _tensor(seq_lens, "seq_lens", 1, torch.int32, dev)
+    width = block_tables.shape[1]
+    if block_tables.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("block_tables and seq_lens must have a row for each request")
+    if width > 1 and block_tables.stride(1) != 1:
+        raise ValueError("block_tables rows must be contiguous (stride(1) == 1)")
+    sel = (None, 0, None)
+    if candidates is not None:
+        _tensor(candidates, "candidates", 3, torch.int32, dev)
+        if ranges is None:
+            raise ValueError("ranges is required with candidates")
+        _tensor(ranges, "ranges", 2, torch.int32, dev)
+        if candidates.shape[0] != B * n or candidates.shape[2] != 2 \
+                or not candidates.is_contiguous():
+            raise ValueError("candidates must be contiguous [B * next_n, slots, 2]")
+        if ranges.shape[0] != 2 or ranges.shape[1] != B * n or not ranges.is_contiguous():
+            raise ValueError("ranges must be contiguous [2, B * next_n]")
+        sel = (candidates.data_ptr(), candidates.shape[1], ranges.data_ptr())
+    made = []
+    if out is None:
+        out = torch.empty(B, n, H, D, dtype=q.dtype, device=dev)
+        made.append(out)
+    else:
+        _tensor(out, "out", 4, q.dtype, dev)
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous with the shape of q")
+    if lse is not None:
+        _tensor(lse, "lse", 3, torch.float32, dev)
+        if lse.shape != q.shape[:3] or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous [B, next_n, H]")
+    if out.numel() == 0:
+        return out
+    if workspace is None:
+        need = idx_attention_workspace_bytes(B, n, H, kv_heads, D, num_sms)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    else:
+        _tensor(workspace, "workspace", 1, torch.uint8, dev)
+    _check(idx_attention_fp8(
+        q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _code(q.dtype), k_pool.data_ptr(),
+        v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), blocks, block_size,
+        block_tables.data_ptr(), max(block_tables.stride(0), width), width, seq_lens.data_ptr(),
+        max(seq_lens.stride(0), 1), B, n, H, kv_heads, D,
+        D ** -0.5 if softmax_scale is None else softmax_scale, *sel, num_sms, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _on(stream, dev, *made)))
+    return out
