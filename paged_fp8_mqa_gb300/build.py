@@ -18,7 +18,7 @@ LIB = HERE / "libidx.so"
 BUILD = HERE.parent / "_build"
 SOURCES = ["logits.cu", "logits_d64.cu", "logits_d192.cu", "logits_h16.cu", "logits_h8.cu",
            "logits_mxfp4.cu", "select.cu", "schedule.cu", "mxfp4.cu", "abi.cu",
-           "rotary.cu", "index_prepare.cu", "kv_append.cu", "attention.cu", "abi_layer.cu"]
+           "rotary.cu", "index_prepare.cu", "kv_append.cu", "attention_d64.cu", "attention_d128.cu", "abi_layer.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

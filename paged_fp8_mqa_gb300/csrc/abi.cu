@@ -69,6 +69,7 @@ int resolve_sms(int32_t requested, int32_t *out) {
 namespace {
 
 using idx::cuda_fail;
+using idx::encode_rows;
 using idx::fail;
 using idx::resolve_sms;
 
@@ -92,26 +93,6 @@ EncodeTiled encode_tiled() {
       fn = reinterpret_cast<EncodeTiled>(p);
   });
   return fn;
-}
-
-// A 2-D uint8 tensor of `rows` rows of `row_bytes` = 128 or 64 bytes (one e4m3 row of head_dim
-// elements), read in boxes of `box_rows` rows with the 128- or 64-byte swizzle: the layout the
-// tensor core's descriptors expect.
-int encode_rows(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes,
-                uint32_t box_rows) {
-  EncodeTiled fn = encode_tiled();
-  if (fn == nullptr) return fail(IDX_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint64_t dims[2] = {row_bytes, rows};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {row_bytes, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    return fail(IDX_CUDA, "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(r));
-  return IDX_OK;
 }
 
 // head_dim 192: the pool as [num_blocks][block_size tokens][3 K blocks][64 bytes] (page stride
@@ -197,6 +178,30 @@ int validate_logits_contents(const int32_t *block_tables, int64_t bt_row_stride,
 }
 
 }  // namespace
+
+namespace idx {
+
+// A 2-D uint8 tensor of `rows` rows of `row_bytes` = 128 or 64 bytes (one e4m3 row of head_dim
+// elements), read in boxes of `box_rows` rows with the 128- or 64-byte swizzle: the layout the
+// tensor core's descriptors expect.
+int encode_rows(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes,
+                uint32_t box_rows) {
+  EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return fail(IDX_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[2] = {row_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {row_bytes, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(IDX_CUDA, "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(r));
+  return IDX_OK;
+}
+
+}  // namespace idx
 
 IDX_EXPORT const char *idx_last_error(void) { return g_error.c_str(); }
 
@@ -695,7 +700,7 @@ IDX_EXPORT int idx_device_status(int32_t *status_out, int32_t clear) {
   if (e == cudaSuccess) e = idx::mxfp4_status(&c, clear != 0);
   int32_t all = a | b | c;
   for (const auto unit : {idx::rotary_status, idx::index_status, idx::append_status,
-                          idx::attention_status}) {
+                          idx::attention_d64_status, idx::attention_d128_status}) {
     int32_t bits = 0;
     if (e == cudaSuccess) e = unit(&bits, clear != 0);
     all |= bits;

@@ -300,7 +300,9 @@ IDX_EXPORT int64_t idx_attention_workspace_bytes(int32_t batch, int32_t next_n, 
                                                  int32_t num_sms) {
   if (batch < 0 || next_n < 1 || num_heads < 1 || kv_heads < 1 || head_dim < 1 || num_sms < 0)
     return -1;
-  return 0;
+  int32_t sms = 0;
+  if (idx::resolve_sms(num_sms, &sms) != IDX_OK) return -1;
+  return idx::attention_workspace(batch, next_n, num_heads, kv_heads, head_dim, sms);
 }
 
 IDX_EXPORT int idx_attention_fp8(
@@ -346,7 +348,7 @@ IDX_EXPORT int idx_attention_fp8(
     return fail(IDX_INVALID_ARG, "pools and out must be 16-byte aligned, candidates 8-byte, "
                                  "workspace 256-byte, the rest 4-byte");
   int32_t ctas = 0;
-  const int st = idx::resolve_sms(num_sms, &ctas);
+  int st = idx::resolve_sms(num_sms, &ctas);
   if (st != IDX_OK) return st;
   const int64_t need =
       idx_attention_workspace_bytes(batch, next_n, num_heads, kv_heads, head_dim, ctas);
@@ -382,6 +384,14 @@ IDX_EXPORT int idx_attention_fp8(
   a.out = out;
   a.lse = lse;
   a.workspace = static_cast<float *>(workspace);
-  const cudaError_t e = idx::launch_attention(a, dtype, ctas, static_cast<cudaStream_t>(stream));
+  CUtensorMap k_map, v_map;
+  const uint64_t rows = static_cast<uint64_t>(num_blocks) * kv_heads * block_size;
+  const uint32_t box = candidates != nullptr ? 1u : static_cast<uint32_t>(block_size);
+  st = idx::encode_rows(&k_map, k_pool, rows, static_cast<uint32_t>(head_dim), box);
+  if (st != IDX_OK) return st;
+  st = idx::encode_rows(&v_map, v_pool, rows, static_cast<uint32_t>(head_dim), box);
+  if (st != IDX_OK) return st;
+  const auto launch = head_dim == 64 ? idx::launch_attention_d64 : idx::launch_attention_d128;
+  const cudaError_t e = launch(k_map, v_map, a, dtype, ctas, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? IDX_OK : cuda_fail(e, "attention launch");
 }

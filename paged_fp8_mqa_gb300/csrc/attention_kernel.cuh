@@ -1,0 +1,996 @@
+// attention_kernel.cuh -- attention over the 8-bit K/V cache: for row (b, t) and query head h with
+// K/V head g = h / (heads / kv_heads),
+//   z_p = scale * ks[page(p), g] * (q . k_p),  out = sum_p softmax(z)_p * vs[page(p), g] * v_p
+// over the positions p <= seq_lens[b] - next_n + t, or over those of them that the select stored
+// in the row's slots.
+//
+// Both products run on the tensor core in e4m3, straight from the cache's bytes: the cache is
+// never converted.  The other operand keeps its precision by being split into e4m3 parts side by
+// side along the product's N:
+//   * a query row is scaled by a power of two to [128, 256) and written as hi + lo, each the
+//     e4m3 nearest to what is left: 4 + 4 bits hold a bfloat16's 8 exactly (down to 2^-18 of the
+//     row's largest magnitude); a float16's 11 bits take three parts.  Products of e4m3 values
+//     are exact and sums float32, so the scores are those of the unrounded queries.
+//   * a weight exp2(z - max) in [0, 1], times 256 and its block's share of the tile's largest
+//     value scale, is written the same way: within 2^-8 of itself with two parts (what a bfloat16
+//     weight would be), 2^-12 with three.  The sum of the weights is taken from the unrounded ones.
+//
+// A tile is 128 positions of one K/V head.  S^T[128 positions x parts * rows] = K Q^T puts a
+// position in each lane of tensor memory and the rows that share the K/V head (query heads times
+// draft slots) in its columns, so that K and V are read once for all of them and the softmax of a
+// position's rows is one thread's work; O^T[dim x parts * rows] = V^T P^T takes V as it lies
+// (M-major) and a dimension in each lane.  O of a tile is added to float32 registers, scaled by the
+// running maximum's change, so the block scales may differ from tile to tile.
+//
+// The tiles of all (request, K/V head) groups in one line are cut into equal runs, one for each CTA
+// of the grid; a group that a run's end cuts leaves partial sums in the workspace and a second
+// launch joins them in order.  Every wait has a limit; nothing waits on another CTA.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+namespace idx {
+namespace {
+
+__device__ int g_attention_status;
+
+constexpr int kTile = 128;                     // positions of a tile
+constexpr uint64_t kWaitNs = 1000000000ull;    // 1 s: far beyond any legitimate wait
+constexpr int kNone = INT_MAX;                 // the position of a token that no row sees
+constexpr float kPScale = 256.0f;              // weights times this fill e4m3's range
+
+// One kernel's shape: R rows in PARTS parts, head_dim D.
+template <int D_, int R_, int PARTS_, bool SELECT_>
+struct AttnCfg {
+  static constexpr int D = D_, R = R_, PARTS = PARTS_;
+  static constexpr bool SELECT = SELECT_;
+  static constexpr int N = R * PARTS;                 // columns of both products
+  static constexpr int WG = R >= 32 ? 2 : 1;          // softmax warpgroups, R / WG rows each
+  static constexpr int RT = R / WG;
+  static constexpr int SOFT_WARPS = 4 * WG;
+  static constexpr int THREADS = 64 + 128 * WG;
+  static constexpr int S_BUFS = N <= 128 ? 2 : 1;
+  static constexpr int COLS = N * (S_BUFS + 1);
+  static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr int CTAS = N == 16 || (N == 32 && D == 64) ? 3 : TMEM <= 256 ? 2 : 1;  // on an SM
+  static constexpr int KV_BYTES = 2 * kTile * D;
+  static constexpr int Q_BYTES = (N * D + 1023) / 1024 * 1024;
+  static constexpr int P_BYTES = N * kTile;
+  static constexpr int STAGE_AUX = kTile * 12 + 16;   // float2 scales, positions, the value scale
+  static constexpr int MISC = 8 * R * 4 * 2 + R * 16 + 3 * D * 4 + 512;
+  static constexpr int FIXED = 1024 + Q_BYTES + P_BYTES + MISC;
+  static constexpr int ROOM = (CTAS == 3 ? 75 : CTAS == 2 ? 112 : 226) * 1024;
+  static constexpr int FIT = (ROOM - FIXED) / (KV_BYTES + STAGE_AUX);
+  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+  static constexpr int SMEM = FIXED + STAGES * (KV_BYTES + STAGE_AUX);
+  static_assert(STAGES >= 2 && SMEM <= 232448, "fits the 227 KiB per-CTA limit");
+  static_assert(COLS <= 512 && N % 16 == 0 && N <= 256, "tensor memory and N");
+};
+
+// Where the runs' parts of a group are, written by the CTA that has the group's first tile.
+struct GroupParts {
+  int32_t cta;    // that CTA
+  int32_t parts;  // CTAs that share the group (1: written whole; 0: no tiles)
+};
+
+__device__ __forceinline__ void attn_flag(int bits) { atomicOr(&g_attention_status, bits); }
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The largest x of the warp's lanes (a NaN loses against a number).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four rows of the tensor (box one row high) into four consecutive rows of shared memory.
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int32_t y0, int32_t y1, int32_t y2, int32_t y3,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(y0), "r"(y1), "r"(y2),
+      "r"(y3), "l"(policy)
+      : "memory");
+}
+
+// Each thread of the warp reads NC consecutive columns of its TMEM lane.
+template <int NC>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[NC]) {
+  static_assert(NC == 8 || NC == 16 || NC == 32, "columns");
+  if constexpr (NC == 32) {
+    tmem_ld_32x32b_x32(taddr, r);
+  } else if constexpr (NC == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr));
+  }
+}
+
+// Shared-memory descriptor of an M- or N-major operand whose rows (one for each k) are ROW bytes
+// with the matching swizzle: groups of eight k lie 8 * ROW bytes apart (stride offset).
+template <int ROW>
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+  return smem_desc_rows<ROW>(saddr);
+}
+
+// An N-major operand without swizzle: 16-byte rows of 16 n, eight k contiguous (128 bytes); the
+// next eight k follow at 128 bytes (leading offset), the next 16 n at kTile * 16 (stride offset).
+__device__ __forceinline__ uint64_t smem_desc_p(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128u >> 4) << 16;
+  d |= static_cast<uint64_t>((kTile * 16u) >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  return d;
+}
+
+constexpr uint32_t kMajorMN_A = 1u << 15, kMajorMN_B = 1u << 16;
+
+// Byte offset of byte x of row n in K-major rows of D bytes with the matching swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t swizzled(uint32_t n, uint32_t x) {
+  if constexpr (D == 128)
+    return n * 128 + (x ^ ((n & 7) << 4));
+  else
+    return n * 64 + (x ^ (((n >> 1) & 3) << 4));
+}
+
+// Keys of the line of groups: a request (all its draft slots see one list of positions), or with
+// SELECT a row.  Each has kv_heads * chunks groups.
+template <bool SELECT>
+__device__ __forceinline__ int key_length(const AttentionArgs &a, int key) {
+  if constexpr (SELECT) {
+    const int rows = a.batch * a.next_n;
+    const int lo = max(0, __ldg(a.ranges + key));
+    return max(0, min(__ldg(a.ranges + rows + key), a.slots) - lo);
+  } else {
+    return max(0, min(__ldg(a.seq_lens + key * a.sl_stride), INT_MAX - kTile));
+  }
+}
+
+__device__ __forceinline__ int tiles_for(int length) {
+  return length / kTile + (length % kTile != 0);
+}
+
+// A CTA's run over the line: the segments (group, first tile, tiles) in order.  Every role walks
+// its own copy; all lanes of a warp step together.
+template <bool SELECT>
+struct Walk {
+  int64_t left;  // tiles of the run not yet handed out
+  int key, group, tile, length, tiles;
+  int seg_tile, seg_tiles;  // the current segment
+
+  __device__ __forceinline__ bool next(const AttentionArgs &a, int groups, int keys) {
+    if (left <= 0) return false;
+    while (tile >= tiles) {  // the group is finished: the next one of this key, or the next key's
+      tile = 0;
+      if (tiles == 0 || ++group >= groups) {
+        group = 0;
+        if (++key >= keys) return false;  // (lengths that changed under the call)
+        length = key_length<SELECT>(a, key);
+        tiles = tiles_for(length);
+      }
+    }
+    seg_tile = tile;
+    seg_tiles = static_cast<int>(min(static_cast<int64_t>(tiles - tile), left));
+    tile += seg_tiles;
+    left -= seg_tiles;
+    return true;
+  }
+};
+
+// Rows of one segment: query heads of one K/V head, times draft slots unless selected.
+struct RowMap {
+  int b, g;
+  int first, rows;  // rows [first, first + rows) of the group's key
+  int t_select;     // the draft slot (SELECT)
+};
+
+template <class C>
+__device__ __forceinline__ RowMap rows_of(const AttentionArgs &a, int key, int group, int chunks,
+                                          int chunk_rows) {
+  RowMap m;
+  const int per = a.heads / a.kv_heads;
+  const int all = C::SELECT ? per : per * a.next_n;
+  m.g = group / chunks;
+  m.first = (group - m.g * chunks) * chunk_rows;
+  m.rows = min(chunk_rows, all - m.first);
+  m.b = C::SELECT ? key / a.next_n : key;
+  m.t_select = C::SELECT ? key - m.b * a.next_n : 0;
+  return m;
+}
+
+// Draft slot and query head of row i of the group.
+template <class C>
+__device__ __forceinline__ int2 slot_head(const AttentionArgs &a, const RowMap &m, int i) {
+  const int per = a.heads / a.kv_heads;
+  i += m.first;
+  if constexpr (C::SELECT) return make_int2(m.t_select, m.g * per + i);
+  const int t = i / per;
+  return make_int2(t, m.g * per + i - t * per);
+}
+
+struct AttnSplit {
+  int32_t chunks, chunk_rows;  // of a K/V head's rows
+};
+
+// Offsets in the workspace: partial sums of slots 2 * cta (a group continued from the CTA before)
+// and 2 * cta + 1 (a group that the CTA begins and does not finish): R rows of D floats, then the
+// rows' maxima, then their sums; after all slots the groups' GroupParts.
+template <class C>
+__device__ __forceinline__ float *partial(const AttentionArgs &a, int slot) {
+  return a.workspace + static_cast<int64_t>(slot) * C::R * (C::D + 2);
+}
+
+template <class C, typename T>
+__global__ void __launch_bounds__(C::THREADS, C::CTAS)
+    k_attention(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                const AttentionArgs a, const AttnSplit split, GroupParts *parts) {
+  constexpr int D = C::D, R = C::R, RT = C::RT, N = C::N, PARTS = C::PARTS;
+  extern __shared__ uint8_t s_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *s_kv = base;                              // [stage][K tile, V tile]
+  uint8_t *s_q = s_kv + C::STAGES * C::KV_BYTES;     // [N][D], K-major, swizzled
+  uint8_t *s_p = s_q + C::Q_BYTES;                   // [N / 16][kTile][16]
+  uint8_t *at = s_p + C::P_BYTES;
+  float2 *s_sc = reinterpret_cast<float2 *>(at);     // [stage][kTile]: key factor, value share
+  at += C::STAGES * kTile * 8;
+  int *s_pos = reinterpret_cast<int *>(at);          // [stage][kTile]
+  at += C::STAGES * kTile * 4;
+  float *s_max = reinterpret_cast<float *>(at);      // [2][R][4 warps]
+  at += 2 * R * 16;
+  float *s_sum = reinterpret_cast<float *>(at);      // [R][4 warps]
+  at += R * 16;
+  float *s_rs = reinterpret_cast<float *>(at);       // [R]: a query row's power of two, undone
+  at += R * 4;
+  int *s_ext = reinterpret_cast<int *>(at);          // [R]: positions a row sees
+  at += R * 4;
+  int *s_nan = reinterpret_cast<int *>(at);          // [3][D]: see below
+  at += 3 * D * 4;
+  float *s_vref = reinterpret_cast<float *>(at);     // [stage]
+  at += 32;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(at);
+  uint64_t *kv_full = bars, *kv_empty = bars + C::STAGES, *s_full = bars + 2 * C::STAGES,
+           *p_full = s_full + 2, *o_full = p_full + 1, *q_full = o_full + 1, *wg_bar = q_full + 1,
+           *drain = wg_bar + 2;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(drain + 1);
+  __shared__ int64_t s_scan[C::THREADS / 32];
+  __shared__ int64_t s_begin[2];  // the run's first tile within its key; tiles in the run
+  __shared__ int s_key;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int groups = a.kv_heads * split.chunks;
+  const int keys = C::SELECT ? a.batch * a.next_n : a.batch;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensor_map(&k_map);
+    prefetch_tensor_map(&v_map);
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&kv_full[i], 32);
+      mbar_init(&kv_empty[i], 1);
+    }
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(p_full, C::SOFT_WARPS);
+    mbar_init(o_full, 1);
+    mbar_init(q_full, C::SOFT_WARPS);
+    mbar_init(&wg_bar[0], 4);
+    mbar_init(&wg_bar[1], 4);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, C::TMEM);
+    tmem_relinquish();
+  }
+  for (int i = tid; i < 3 * D; i += C::THREADS) s_nan[i] = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- the run ---------------------------------------------------------------------------------
+  const int per = (keys + C::THREADS - 1) / C::THREADS;
+  const int k_lo = min(tid * per, keys), k_hi = min(k_lo + per, keys);
+  int64_t mine = 0;
+  for (int k = k_lo; k < k_hi; ++k) mine += tiles_for(key_length<C::SELECT>(a, k));
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < C::THREADS / 32; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  total *= groups;
+  // (No more runs than tiles: a group's parts lie in consecutive CTAs.)
+  const int64_t runs = max(static_cast<int64_t>(1), min(total, static_cast<int64_t>(gridDim.x)));
+  const int64_t f0 = blockIdx.x < runs ? total * blockIdx.x / runs : total;
+  const int64_t f1 = blockIdx.x < runs ? total * (blockIdx.x + 1) / runs : total;
+  if (f0 < f1 && f0 >= before * groups && f0 < (before + mine) * groups) {
+    for (int k = k_lo; k < k_hi; ++k) {
+      const int n = tiles_for(key_length<C::SELECT>(a, k));
+      if (f0 < (before + n) * groups) {
+        s_key = k;
+        s_begin[0] = f0 - before * groups;
+        break;
+      }
+      before += n;
+    }
+  }
+  // Keys without positions: their rows are zeros, their groups have no parts.
+  for (int k = blockIdx.x; k < keys; k += gridDim.x) {
+    if (key_length<C::SELECT>(a, k) > 0) continue;
+    for (int g = tid; g < groups; g += C::THREADS)
+      parts[static_cast<int64_t>(k) * groups + g] = GroupParts{0, 0};
+    const int slots = C::SELECT ? 1 : a.next_n;
+    const int64_t row0 = static_cast<int64_t>(k) * slots * a.heads;
+    T *out = static_cast<T *>(a.out) + row0 * D;
+    for (int i = tid; i < slots * a.heads * D / 8; i += C::THREADS)
+      reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse != nullptr)
+      for (int i = tid; i < slots * a.heads; i += C::THREADS) a.lse[row0 + i] = -INFINITY;
+  }
+  __syncthreads();
+
+  const uint32_t tmem = *s_tmem;
+  Walk<C::SELECT> w;
+  w.left = f1 - f0;
+  w.seg_tile = w.seg_tiles = 0;
+  if (w.left > 0) {
+    w.key = s_key;
+    w.length = key_length<C::SELECT>(a, w.key);
+    w.tiles = tiles_for(w.length);
+    w.group = static_cast<int>(s_begin[0] / w.tiles);
+    w.tile = static_cast<int>(s_begin[0] - static_cast<int64_t>(w.group) * w.tiles);
+  }
+  bool ok = true;
+  uint32_t issued = 0;  // producer: tiles whose copies were started; MMA: nothing
+  int stage = 0;
+  uint32_t phase = 0;
+
+  if (warp == 0) {
+    // ============================== producer ====================================================
+    const uint64_t policy = l2_policy_evict_first();
+    const int shift = a.block_size == 32 ? 5 : a.block_size == 64 ? 6 : 7;
+    const float z_unit = a.scale * 1.4426950408889634f;  // scores in units of ln 2
+    while (ok && w.next(a, groups, keys)) {
+      const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
+      const int32_t *table = a.block_tables + m.b * a.bt_stride;
+      const int2 *cand = nullptr;
+      int extent = w.length;
+      if constexpr (C::SELECT) {
+        cand = a.candidates + w.key * a.cand_stride + max(0, __ldg(a.ranges + w.key));
+        extent = __ldg(a.seq_lens + m.b * a.sl_stride) - a.next_n + m.t_select + 1;
+      }
+      for (int i = w.seg_tile; i < w.seg_tile + w.seg_tiles; ++i) {
+        // Four consecutive tokens a lane: their positions, rows of the pool and scales.  (Read
+        // before the wait for the stage, so that their latency runs beside the tiles in flight.)
+        int pos[4], row[4];
+        float ks[4], vs[4];
+        bool bad = false;
+        if constexpr (C::SELECT) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int s = i * kTile + lane * 4 + j;
+            pos[j] = s < w.length ? __ldg(&cand[s].x) : kNone;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            int id = -1;
+            if (pos[j] >= 0 && pos[j] < extent) {
+              const int blk = pos[j] >> shift;
+              id = blk < a.bt_width ? __ldg(table + blk) : -1;
+              if (id < 0 || id >= a.num_blocks) {
+                bad = true;
+                id = -1;
+              }
+            }
+            row[j] = id;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            ks[j] = vs[j] = 0.0f;
+            if (row[j] >= 0) {
+              const int page = row[j] * a.kv_heads + m.g;
+              ks[j] = __ldg(a.k_scales + page);
+              vs[j] = __ldg(a.v_scales + page);
+              row[j] = (page << shift) + (pos[j] & (a.block_size - 1));
+              pos[j] = 0;
+            } else {
+              row[j] = 0;  // some row of the pool, whose values are not used
+              pos[j] = kNone;
+            }
+          }
+        } else {
+          const int p = i * kTile + lane * 4, blk = p >> shift;
+          int id = -1;
+          if (p < w.length) {
+            id = blk < a.bt_width ? __ldg(table + blk) : -1;
+            if (id < 0 || id >= a.num_blocks) {
+              bad = true;
+              id = -1;
+            }
+          }
+          const int page = id * a.kv_heads + m.g;
+          ks[0] = id >= 0 ? __ldg(a.k_scales + page) : 0.0f;
+          vs[0] = id >= 0 ? __ldg(a.v_scales + page) : 0.0f;
+          row[0] = id >= 0 ? page << shift : -1;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            pos[j] = id >= 0 && p + j < w.length ? p + j : kNone;
+            ks[j] = ks[0];
+            vs[j] = vs[0];
+          }
+        }
+        if (bad) attn_flag(IDX_DEV_BAD_PAGE);
+        float most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(vs[j]));
+        most = warp_max(most);
+        const float share = most > 1e-37f ? 1.0f / most : 0.0f;
+        ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], phase ^ 1, kWaitNs));
+        if (!ok) break;
+        uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
+        float4 *sc = reinterpret_cast<float4 *>(s_sc + stage * kTile + lane * 4);
+        sc[0] = make_float4(ks[0] * z_unit, vs[0] * share, ks[1] * z_unit, vs[1] * share);
+        sc[1] = make_float4(ks[2] * z_unit, vs[2] * share, ks[3] * z_unit, vs[3] * share);
+        *reinterpret_cast<int4 *>(s_pos + stage * kTile + lane * 4) =
+            make_int4(pos[0], pos[1], pos[2], pos[3]);
+        if (lane == 0) s_vref[stage] = most * (1.0f / kPScale);
+        if constexpr (C::SELECT) {
+          mbar_arrive_expect_tx(&kv_full[stage], 8 * D);
+          tma_gather4(kt + lane * 4 * D, &k_map, &kv_full[stage], row[0], row[1], row[2], row[3],
+                      policy);
+          tma_gather4(vt + lane * 4 * D, &v_map, &kv_full[stage], row[0], row[1], row[2], row[3],
+                      policy);
+        } else {
+          const int in_page = (lane * 4) & (a.block_size - 1);
+          if (in_page == 0 && row[0] >= 0) {
+            mbar_arrive_expect_tx(&kv_full[stage], 2 * D * a.block_size);
+            tma_load_2d(kt + lane * 4 * D, &k_map, &kv_full[stage], 0, row[0], policy);
+            tma_load_2d(vt + lane * 4 * D, &v_map, &kv_full[stage], 0, row[0], policy);
+          } else {
+            mbar_arrive(&kv_full[stage]);
+          }
+        }
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ============================== MMA issuer ==================================================
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, N);
+      constexpr uint32_t idesc_o = idesc_e4m3_f32(D, N) | kMajorMN_A | kMajorMN_B;
+      const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
+      const uint64_t p_desc = smem_desc_p(smem_addr(s_p));
+      const uint32_t o_tmem = tmem + C::S_BUFS * N;
+      uint32_t tile = 0, seg = 0;
+      const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
+        const uint64_t k_desc = smem_desc_rows<D>(smem_addr(s_kv + st * C::KV_BYTES));
+        const uint32_t buf = C::S_BUFS == 2 ? n & 1 : 0;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          mma_f8f6f4(tmem + buf * N, k_desc + 2 * k, q_desc + 2 * k, idesc_s, k > 0);
+        mma_commit(&s_full[buf]);
+      };
+      while (ok && w.next(a, groups, keys)) {
+        ok = mbar_wait(q_full, seg & 1, kWaitNs);
+        ++seg;
+        if (!ok) break;
+        tc_fence_after_sync();
+        bool ahead = false;  // S of the tile has been issued already
+        for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
+          if (!ahead) {
+            ok = mbar_wait(&kv_full[stage], phase, kWaitNs);
+            if (!ok) break;
+            tc_fence_after_sync();
+            scores(tile, stage);
+          }
+          // The next tile's scores, if its keys are here, before this tile's weights are.
+          const int next = stage + 1 == C::STAGES ? 0 : stage + 1;
+          const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
+          ahead = false;
+          if (C::S_BUFS == 2 && i + 1 < w.seg_tiles && mbar_try_wait(&kv_full[next], next_phase)) {
+            tc_fence_after_sync();
+            scores(tile + 1, next);
+            ahead = true;
+          }
+          ok = mbar_wait(p_full, tile & 1, kWaitNs);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint64_t v_desc =
+              smem_desc_mn<D>(smem_addr(s_kv + stage * C::KV_BYTES + kTile * D));
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k)
+            mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o, k > 0);
+          mma_commit(o_full);
+          mma_commit(&kv_empty[stage]);
+          stage = next;
+          phase = next_phase;
+        }
+      }
+      mma_commit(drain);
+    }
+    __syncwarp();
+  } else {
+    // ============================== softmax =====================================================
+    const int wg = (warp - 2) >> 2, quarter = warp & 3;
+    const int r0 = wg * RT;                      // the thread's rows
+    const int token = quarter * 32 + lane;       // the thread's position in the tile
+    // The thread's dimension of the output, or -1 (M = 64: 16 lanes of each quarter).
+    const int dim = D == 128 ? token : lane < 16 ? quarter * 16 + lane : -1;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint32_t tile = 0, syncs = 0;
+    int seg = 0;
+    const auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs)) != 0;
+    };
+    const auto wg_sync = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&wg_bar[wg]);
+      return wait(&wg_bar[wg], syncs++ & 1);
+    };
+    while (ok && w.next(a, groups, keys)) {
+      const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
+      const int len = C::SELECT ? 0 : w.length;
+      ++seg;
+      // ---- the rows' queries, in parts -----------------------------------------------------------
+      {
+        constexpr int LANES = D / 8;  // eight elements a lane
+        const int x = (tid & (LANES - 1)) * 8;
+        for (int r = r0 + ((tid - 64 - wg * 128) / LANES); r < r0 + RT; r += 128 / LANES) {
+          Piece<T, 8> v;
+          const int2 th = slot_head<C>(a, m, r);
+          if (r < m.rows) {
+            v = load_piece<T, 8>(static_cast<const T *>(a.q) + m.b * a.q_batch + th.x * a.q_token +
+                                 th.y * a.q_head + x);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v.e[j] = from_f32<T>(0.0f);
+          }
+          float f[8], amax = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            f[j] = to_f32(v.e[j]);
+            amax = fmaxf(amax, fabsf(f[j]));
+          }
+#pragma unroll
+          for (int o = 1; o < LANES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // 2^e <= amax < 2^(e+1); rows below 2^-100 keep their scores to 2^-118 only.
+          const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+          const float up = e > 127 ? __int_as_float(0x7FC00000)  // an infinity: the row is NaN
+                                   : __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - 7 + min(e, 127)) << 23);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] *= up;
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            const uint2 b = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+            *reinterpret_cast<uint2 *>(s_q + swizzled<D>(part * R + r, x)) = b;
+            if (part + 1 < PARTS) {
+              const float2 b0 = e4m3x2_to_f32(b.x), b1 = e4m3x2_to_f32(b.x >> 16);
+              const float2 b2 = e4m3x2_to_f32(b.y), b3 = e4m3x2_to_f32(b.y >> 16);
+              f[0] -= b0.x, f[1] -= b0.y, f[2] -= b1.x, f[3] -= b1.y;
+              f[4] -= b2.x, f[5] -= b2.y, f[6] -= b3.x, f[7] -= b3.y;
+            }
+          }
+          if (x == 0) {
+            s_rs[r] = down;
+            s_ext[r] = r >= m.rows ? 0 : C::SELECT ? 1 : max(0, len - a.next_n + th.x + 1);
+          }
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        ok = wait(q_full, (seg - 1) & 1);
+        if (!ok) break;
+      }
+      float acc[RT], sum[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r] = sum[r] = 0.0f;
+      float m_run = -INFINITY;  // lane r: the running maximum of row r0 + r
+      // Positions below this are seen by every row of the segment.
+      const int all_see = C::SELECT ? kNone : len - a.next_n + 1 + (slot_head<C>(a, m, 0).x);
+      for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
+        const uint32_t buf = C::S_BUFS == 2 ? tile & 1 : 0;
+        const uint32_t sph = C::S_BUFS == 2 ? (tile >> 1) & 1 : tile & 1;
+        ok = wait(&kv_full[stage], phase) && wait(&s_full[buf], sph);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const float2 sc = s_sc[stage * kTile + token];
+        const int pos = s_pos[stage * kTile + token];
+        const float vref = s_vref[stage];
+        float z[RT];
+        {
+          uint32_t part[PARTS][RT];
+#pragma unroll
+          for (int j = 0; j < PARTS; ++j)
+            tmem_ld_cols<RT>(lane_base + buf * N + j * R + r0, part[j]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < PARTS; ++j) reg_fence(part[j]);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            float s = __uint_as_float(part[0][r]);
+#pragma unroll
+            for (int j = 1; j < PARTS; ++j) s += __uint_as_float(part[j][r]);
+            z[r] = s * s_rs[r0 + r] * sc.x;
+          }
+        }
+        const bool seen = pos < all_see;
+        if (!__all_sync(0xffffffffu, seen)) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            if (!seen && pos >= s_ext[r0 + r]) z[r] = -INFINITY;
+        }
+        // ---- the rows' maxima over the tile --------------------------------------------------------
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const float x = warp_max(z[r]);
+          if (lane == r) top = x;
+        }
+        float *mx = s_max + (tile & 1) * R * 4;
+        if (lane < RT) mx[(r0 + lane) * 4 + quarter] = top;
+        ok = wg_sync();
+        if (!ok) break;
+        float m_new = m_run, keep = 1.0f;
+        if (lane < RT) {
+          const float4 t4 = *reinterpret_cast<const float4 *>(mx + (r0 + lane) * 4);
+          m_new = fmaxf(fmaxf(m_run, fmaxf(t4.x, t4.y)), fmaxf(t4.z, t4.w));
+          keep = m_new == m_run ? 1.0f : fast_exp2(m_run - m_new);
+        }
+        const float ref = m_new == -INFINITY ? 0.0f : m_new;
+        m_run = m_new;
+        const bool moved = __any_sync(0xffffffffu, keep != 1.0f);
+        // ---- weights, their parts, the running sums ------------------------------------------------
+        const float vshare = sc.y * kPScale;
+        uint32_t bytes[PARTS][RT / 4];
+#pragma unroll
+        for (int r = 0; r < RT; r += 4) {
+          float p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            p[j] = fast_exp2(z[r + j] - __shfl_sync(0xffffffffu, ref, r + j));
+            if (moved) sum[r + j] *= __shfl_sync(0xffffffffu, keep, r + j);
+            sum[r + j] += p[j];
+            p[j] *= vshare;
+          }
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            const uint32_t b = e4m3x4(p[0], p[1], p[2], p[3]);
+            bytes[part][r / 4] = b;
+            if (part + 1 < PARTS) {
+              const float2 b0 = e4m3x2_to_f32(b), b1 = e4m3x2_to_f32(b >> 16);
+              p[0] -= b0.x, p[1] -= b0.y, p[2] -= b1.x, p[3] -= b1.y;
+            }
+          }
+        }
+        if constexpr (RT == 8) {  // PARTS = 2: both parts of the eight rows are one group of 16 n
+          *reinterpret_cast<uint4 *>(s_p + token * 16) =
+              make_uint4(bytes[0][0], bytes[0][1], bytes[1][0], bytes[1][1]);
+        } else {
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+            for (int q = 0; q < RT / 16; ++q)
+              *reinterpret_cast<uint4 *>(s_p + ((part * R + r0) / 16 + q) * (kTile * 16) + token * 16) =
+                  make_uint4(bytes[part][4 * q], bytes[part][4 * q + 1], bytes[part][4 * q + 2],
+                             bytes[part][4 * q + 3]);
+        }
+        // A value that some row does not see must not meet its weight of 0 as a NaN (a code of the
+        // cache, or bytes that were never written): what no row sees becomes 0; in the newest
+        // tokens, which only the later draft slots see, a NaN becomes 0 and is noted in s_nan (as
+        // this segment's number) for the rows that do see it.
+        if (wg == 0 && !seen) {
+          uint8_t *v = s_kv + stage * C::KV_BYTES + kTile * D;
+          if (pos == kNone) {
+            for (int x = 0; x < D; x += 16)
+              *reinterpret_cast<uint4 *>(v + token * D + x) = make_uint4(0, 0, 0, 0);
+          } else {
+            for (int x = 0; x < D; x += 4) {
+              const uint32_t at4 = swizzled<D>(token, x);
+              const uint32_t four = *reinterpret_cast<const uint32_t *>(v + at4);
+              if ((((four & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) == 0) continue;
+              for (int y = 0; y < 4; ++y)
+                if (((four >> (8 * y)) & 0x7F) == 0x7F) {
+                  v[at4 + y] = 0;
+                  s_nan[(len - 1 - pos) * D + x + y] = seg;
+                }
+            }
+          }
+        }
+        fence_proxy_async_shared();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        ok = wait(o_full, tile & 1);
+        if (!ok) break;
+        tc_fence_after_sync();
+        {
+          uint32_t part[PARTS][RT];
+#pragma unroll
+          for (int j = 0; j < PARTS; ++j)
+            tmem_ld_cols<RT>(lane_base + C::S_BUFS * N + j * R + r0, part[j]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < PARTS; ++j) reg_fence(part[j]);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            float o = __uint_as_float(part[0][r]);
+#pragma unroll
+            for (int j = 1; j < PARTS; ++j) o += __uint_as_float(part[j][r]);
+            if (moved) acc[r] *= __shfl_sync(0xffffffffu, keep, r);
+            acc[r] += vref * o;
+          }
+        }
+        tc_fence_before_sync();
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      // ---- the segment's result ----------------------------------------------------------------------
+      // (s_rs and s_ext are not read past the wg_sync below: the next segment's are written then.)
+      if (!C::SELECT && a.next_n > 1 && dim >= 0) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          for (int u = 0; u < a.next_n - 1; ++u)
+            if (s_nan[u * D + dim] == seg && len - 1 - u < s_ext[r0 + r])
+              acc[r] = __int_as_float(0x7FC00000);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float x = sum[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) s_sum[(r0 + r) * 4 + quarter] = x;
+      }
+      ok = wg_sync();
+      if (!ok) break;
+      float l = 0.0f;  // lane r: the sum of row r0 + r
+      if (lane < RT) {
+        const float4 t4 = *reinterpret_cast<const float4 *>(s_sum + (r0 + lane) * 4);
+        l = (t4.x + t4.y) + (t4.z + t4.w);
+      }
+      const bool from_start = w.seg_tile == 0, to_end = w.seg_tile + w.seg_tiles == w.tiles;
+      const int64_t gid = static_cast<int64_t>(w.key) * groups + w.group;
+      if (from_start && wg == 0 && quarter == 2 && lane == 0) {
+        // The last tile of the group is tile x of the line; its owner is the last part.
+        int n = 1;
+        if (!to_end) {
+          const int64_t x = f1 - 1 + (w.tiles - (w.seg_tile + w.seg_tiles));
+          n = static_cast<int>(((x + 1) * runs - 1) / total) - static_cast<int>(blockIdx.x) + 1;
+        }
+        parts[gid] = GroupParts{static_cast<int>(blockIdx.x), n};
+      }
+      if (from_start && to_end) {
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const float f = __shfl_sync(0xffffffffu, inv, r);
+          if (r0 + r < m.rows && dim >= 0) {
+            const int2 th = slot_head<C>(a, m, r0 + r);
+            const int64_t row =
+                (static_cast<int64_t>(m.b) * a.next_n + th.x) * a.heads + th.y;
+            static_cast<T *>(a.out)[row * D + dim] = from_f32<T>(f == 0.0f ? 0.0f : acc[r] * f);
+          }
+        }
+        if (a.lse != nullptr && quarter == 0 && lane < RT && r0 + lane < m.rows) {
+          const int2 th = slot_head<C>(a, m, r0 + lane);
+          a.lse[(static_cast<int64_t>(m.b) * a.next_n + th.x) * a.heads + th.y] =
+              l == 0.0f ? -INFINITY : (m_run + log2f(l)) * 0.6931471805599453f;
+        }
+      } else {
+        float *ws = partial<C>(a, 2 * blockIdx.x + (from_start ? 1 : 0));
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          if (r0 + r < m.rows && dim >= 0) ws[(r0 + r) * D + dim] = acc[r];
+        if (quarter == 0 && lane < RT) {
+          ws[R * D + r0 + lane] = m_run;
+          ws[R * D + R + r0 + lane] = l;
+        }
+      }
+    }
+  }
+
+  // ---- teardown ----------------------------------------------------------------------------------
+  if (__syncthreads_or(!ok)) {
+    // A wait gave up: let the copies and products in flight end before the memory is given back.
+    if (!ok) attn_flag(IDX_DEV_WAIT_TIMEOUT);
+    if (warp == 0 && lane == 0) {
+      const uint32_t tail = issued < C::STAGES ? issued : C::STAGES;
+      for (uint32_t d = 1; d <= tail; ++d) {
+        const uint32_t n = issued - d;
+        if (!mbar_wait(&kv_full[n % C::STAGES], (n / C::STAGES) & 1, kWaitNs))
+          attn_flag(IDX_DEV_WAIT_TIMEOUT);
+      }
+    }
+  }
+  if (warp == 1 && lane == 0 && !mbar_wait(drain, 0, kWaitNs)) attn_flag(IDX_DEV_WAIT_TIMEOUT);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, C::TMEM);
+}
+
+constexpr int kJoinThreads = 256;
+
+// Joins the parts of one group's rows: block (group, y) takes rows y, y + gridDim.y, ...; its
+// warps share a row's parts, and the warps' sums are added in order.
+template <class C, typename T>
+__global__ void __launch_bounds__(kJoinThreads)
+    k_attention_join(const AttentionArgs a, const AttnSplit split, const GroupParts *parts) {
+  constexpr int D = C::D, R = C::R, W = kJoinThreads / 32, E = D / 32;
+  __shared__ float s_o[W][D], s_m[W], s_l[W];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t gid = blockIdx.x;
+  const GroupParts p = parts[gid];
+  if (p.parts <= 1) return;
+  const int groups = a.kv_heads * split.chunks;
+  const int key = static_cast<int>(gid / groups);
+  const RowMap m = rows_of<C>(a, key, static_cast<int>(gid - static_cast<int64_t>(key) * groups),
+                              split.chunks, split.chunk_rows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = blockIdx.y; r < m.rows; r += gridDim.y) {
+    float top = -INFINITY;
+    for (int i = threadIdx.x; i < p.parts; i += kJoinThreads) {
+      const float *ws = partial<C>(a, 2 * (p.cta + i) + (i == 0));
+      top = fmaxf(top, ws[R * D + r]);
+    }
+    top = warp_max(top);
+    if (lane == 0) s_m[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < W; ++x) top = fmaxf(top, s_m[x]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float o[E], l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 4
+    for (int i = warp; i < p.parts; i += W) {
+      const float *ws = partial<C>(a, 2 * (p.cta + i) + (i == 0));
+      const float f = fast_exp2(ws[R * D + r] - ref);
+      l += f * ws[R * D + R + r];
+      const Piece<float, E> v = load_piece<float, E>(ws + r * D + lane * E);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += f * v.e[e];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    const int2 th = slot_head<C>(a, m, r);
+    const int64_t row = (static_cast<int64_t>(m.b) * a.next_n + th.x) * a.heads + th.y;
+    if (threadIdx.x < D) {
+      float x = 0.0f, all = 0.0f;
+#pragma unroll
+      for (int y = 0; y < W; ++y) {
+        x += s_o[y][threadIdx.x];
+        all += s_l[y];
+      }
+      static_cast<T *>(a.out)[row * D + threadIdx.x] = from_f32<T>(all == 0.0f ? 0.0f : x / all);
+      if (a.lse != nullptr && threadIdx.x == 0)
+        a.lse[row] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+  }
+}
+
+// Rows that share a K/V head, cut into chunks of at most 64, and the kernel's R for a chunk.
+struct AttnShape {
+  int chunks, chunk_rows, r;
+};
+inline AttnShape attn_shape(int rows, bool f16) {
+  AttnShape s;
+  s.chunks = (rows + 63) / 64;
+  s.chunk_rows = (rows + s.chunks - 1) / s.chunks;
+  s.r = s.chunk_rows <= 8 && !f16 ? 8 : s.chunk_rows <= 16 ? 16 : s.chunk_rows <= 32 ? 32 : 64;
+  return s;
+}
+
+inline int64_t attn_slots_bytes(int64_t ctas, int r, int dim) {
+  return (2 * ctas * r * (dim + 2) * 4 + 255) / 256 * 256;
+}
+
+template <class C, typename T>
+cudaError_t launch_cfg(const CUtensorMap &k_map, const CUtensorMap &v_map, const AttentionArgs &a,
+                       const AttnShape &s, int sms, cudaStream_t stream) {
+  static PerDeviceOnce configured;
+  cudaError_t e = configured.run([] {
+    return cudaFuncSetAttribute(k_attention<C, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  const int ctas = sms * C::CTAS;
+  const AttnSplit split{s.chunks, s.chunk_rows};
+  auto *parts = reinterpret_cast<GroupParts *>(reinterpret_cast<uint8_t *>(a.workspace) +
+                                               attn_slots_bytes(ctas, C::R, C::D));
+  e = launch_dependent(k_attention<C, T>, dim3(ctas), dim3(C::THREADS), C::SMEM, stream, k_map,
+                       v_map, a, split, parts);
+  if (e != cudaSuccess) return e;
+  const int64_t groups = static_cast<int64_t>(C::SELECT ? a.batch * a.next_n : a.batch) *
+                         a.kv_heads * s.chunks;
+  const int64_t spread = (2 * sms + groups - 1) / groups;
+  const int y = static_cast<int>(spread < s.chunk_rows ? spread : s.chunk_rows);
+  return launch_dependent(k_attention_join<C, T>, dim3(static_cast<unsigned>(groups), y),
+                          dim3(kJoinThreads), 0, stream, a, split, parts);
+}
+
+template <int D, bool SELECT>
+cudaError_t launch_rows(const CUtensorMap &k_map, const CUtensorMap &v_map, const AttentionArgs &a,
+                        int dtype, int sms, cudaStream_t stream) {
+  const bool f16 = dtype == IDX_DTYPE_F16;
+  const AttnShape s = attn_shape(a.heads / a.kv_heads * (SELECT ? 1 : a.next_n), f16);
+  if (f16) {
+    switch (s.r) {
+      case 16: return launch_cfg<AttnCfg<D, 16, 3, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
+      case 32: return launch_cfg<AttnCfg<D, 32, 3, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
+      default: return launch_cfg<AttnCfg<D, 64, 3, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
+    }
+  }
+  using B = __nv_bfloat16;
+  switch (s.r) {
+    case 8: return launch_cfg<AttnCfg<D, 8, 2, SELECT>, B>(k_map, v_map, a, s, sms, stream);
+    case 16: return launch_cfg<AttnCfg<D, 16, 2, SELECT>, B>(k_map, v_map, a, s, sms, stream);
+    case 32: return launch_cfg<AttnCfg<D, 32, 2, SELECT>, B>(k_map, v_map, a, s, sms, stream);
+    default: return launch_cfg<AttnCfg<D, 64, 2, SELECT>, B>(k_map, v_map, a, s, sms, stream);
+  }
+}
+
+// The CTAs on an SM of the kernel that a shape takes.
+template <int D, bool SELECT>
+int ctas_for(int r, bool f16) {
+  if (f16)
+    return r == 16 ? AttnCfg<D, 16, 3, SELECT>::CTAS
+                   : r == 32 ? AttnCfg<D, 32, 3, SELECT>::CTAS : AttnCfg<D, 64, 3, SELECT>::CTAS;
+  return r == 8 ? AttnCfg<D, 8, 2, SELECT>::CTAS
+                : r == 16 ? AttnCfg<D, 16, 2, SELECT>::CTAS
+                          : r == 32 ? AttnCfg<D, 32, 2, SELECT>::CTAS
+                                    : AttnCfg<D, 64, 2, SELECT>::CTAS;
+}
+
+inline cudaError_t read_attention_status(int32_t *value, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_attention_status, sizeof(int32_t));
+  if (e != cudaSuccess || !clear) return e;
+  const int32_t zero = 0;
+  return cudaMemcpyToSymbol(g_attention_status, &zero, sizeof(int32_t));
+}
+
+}  // namespace
+}  // namespace idx

@@ -21,6 +21,11 @@ void clear_error();
 // The persistent grid: `requested` (1 .. 1024), or the current device's SM count for 0.
 int resolve_sms(int32_t requested, int32_t *out);
 
+// A tensor map of `rows` rows of `row_bytes` = 128 or 64 bytes, read `box_rows` at a time with the
+// 128- or 64-byte swizzle (abi.cu).
+int encode_rows(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes,
+                uint32_t box_rows);
+
 // Launches `kernel` as a programmatic dependent of the previous kernel in `stream`: the launch may
 // be processed while that kernel still runs, so its latency hides behind it.  Every kernel of
 // this library calls griddep_wait() before it touches global memory, which keeps stream order.

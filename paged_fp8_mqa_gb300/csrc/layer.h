@@ -105,12 +105,20 @@ struct AttentionArgs {
   float *lse;   // nullable: [batch, next_n, heads]
   float *workspace;
 };
-cudaError_t launch_attention(const AttentionArgs &a, int dtype, int ctas, cudaStream_t stream);
+// sms * (CTAs on an SM) runs; the workspace is attention_workspace(...) bytes.  k_map, v_map: the
+// pools as rows of dim bytes, in boxes of block_size rows (of one row with candidates).
+cudaError_t launch_attention_d64(const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                 const AttentionArgs &a, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_attention_d128(const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                  const AttentionArgs &a, int dtype, int sms, cudaStream_t stream);
+// The most that any call of these sizes needs (either dtype, with candidates or without).
+int64_t attention_workspace(int batch, int next_n, int heads, int kv_heads, int dim, int sms);
 
 // Device-side status words (IDX_DEV_* bits) of the translation units above.
 cudaError_t rotary_status(int32_t *value, bool clear);
 cudaError_t index_status(int32_t *value, bool clear);
 cudaError_t append_status(int32_t *value, bool clear);
-cudaError_t attention_status(int32_t *value, bool clear);
+cudaError_t attention_d64_status(int32_t *value, bool clear);
+cudaError_t attention_d128_status(int32_t *value, bool clear);
 
 }  // namespace idx
