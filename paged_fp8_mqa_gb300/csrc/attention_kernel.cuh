@@ -5,22 +5,28 @@
 // in the row's slots.
 //
 // Both products run on the tensor core in e4m3, straight from the cache's bytes: the cache is
-// never converted.  The other operand keeps its precision by being split into e4m3 parts side by
-// side along the product's N:
+// never converted.  The other operand keeps its precision by being split into e4m3 parts whose
+// products are summed in the accumulator:
 //   * a query row is scaled by a power of two to [128, 256) and written as hi + lo, each the
 //     e4m3 nearest to what is left: 4 + 4 bits hold a bfloat16's 8 exactly (down to 2^-18 of the
 //     row's largest magnitude); a float16's 11 bits take three parts.  Products of e4m3 values
 //     are exact and sums float32, so the scores are those of the unrounded queries.
-//   * a weight exp2(z - max) in [0, 1], times 256 and its block's share of the tile's largest
-//     value scale, is written the same way: within 2^-8 of itself with two parts (what a bfloat16
-//     weight would be), 2^-12 with three.  The sum of the weights is taken from the unrounded ones.
+//   * a weight is written the same way: within 2^-8 of itself with two parts (what a bfloat16
+//     weight would be), 2^-12 with three, or 2^-18 of the row's largest.
+// The weights that meet V carry the block scales: with z' = log2(e) z + log2|vs| they are
+// u = 2^(z' - ref), sign(vs) applied, so that O = sum u v needs no scale of its own and may be
+// accumulated in tensor memory over tiles of any scales, and the softmax's denominator is
+// l = sum u / |vs| in float32; out = O / l.  ref follows the running maximum of z' from below: it
+// moves (to the maximum) only when some u would pass e4m3's range, 2^0.8 times what it was, and
+// then O and l are rescaled.  With scores of ordinary spread that is a few tiles of a thousand;
+// the exact running maximum, read back, rescaled and exchanged among the warps in every tile, took
+// three times the instructions (draft verification 304 us).
 //
-// A tile is 128 positions of one K/V head.  S^T[128 positions x parts * rows] = K Q^T puts a
-// position in each lane of tensor memory and the rows that share the K/V head (query heads times
-// draft slots) in its columns, so that K and V are read once for all of them and the softmax of a
-// position's rows is one thread's work; O^T[dim x parts * rows] = V^T P^T takes V as it lies
-// (M-major) and a dimension in each lane.  O of a tile is added to float32 registers, scaled by the
-// running maximum's change, so the block scales may differ from tile to tile.
+// A tile is 128 positions of one K/V head.  S^T[128 positions x rows] = K Q^T puts a position in
+// each lane of tensor memory and the rows that share the K/V head (query heads times draft slots)
+// in its columns, so that K and V are read once for all of them and the softmax of a position's
+// rows is one thread's work; O^T[dim x rows] = V^T P^T takes V as it lies (M-major) and a
+// dimension in each lane.
 //
 // The tiles of all (request, K/V head) groups in one line are cut into equal runs, one for each CTA
 // of the grid; a group that a run's end cuts leaves partial sums in the workspace and a second
@@ -41,34 +47,48 @@ __device__ int g_attention_status;
 constexpr int kTile = 128;                     // positions of a tile
 constexpr uint64_t kWaitNs = 1000000000ull;    // 1 s: far beyond any legitimate wait
 constexpr int kNone = INT_MAX;                 // the position of a token that no row sees
-constexpr float kPScale = 256.0f;              // weights times this fill e4m3's range
+constexpr float kRefNone = -1e30f;             // the reference of a row that has seen nothing
+// Weights are 2^(z' - ref + 8), at most 256 when ref is set; ref moves when one would pass 2^8.8 =
+// 446, just inside e4m3's 448.
+constexpr float kTop = 8.0f, kMost = 8.8f;
+constexpr float kLeastScale = 7.8886090522101180541e-31f;  // 2^-100: a value scale below it is 0
 
-// One kernel's shape: R rows in PARTS parts, head_dim D.
+// One kernel's shape: R rows, PARTS parts a row, head_dim D.
 template <int D_, int R_, int PARTS_, bool SELECT_>
 struct AttnCfg {
   static constexpr int D = D_, R = R_, PARTS = PARTS_;
   static constexpr bool SELECT = SELECT_;
-  static constexpr int N = R * PARTS;                 // columns of both products
-  static constexpr int WG = R >= 32 ? 2 : 1;          // softmax warpgroups, R / WG rows each
+  // With R = 8 the two parts stand side by side in the least N (16) and are added when read; else
+  // each part is a product of its own into the same columns.
+  static constexpr bool CAT = R == 8;
+  static constexpr int N = CAT ? 16 : R;              // columns of both products
+  static constexpr int PASSES = CAT ? 1 : PARTS;
+  static constexpr int WG = R == 64 ? 2 : 1;          // softmax warpgroups, R / WG rows each
   static constexpr int RT = R / WG;
   static constexpr int SOFT_WARPS = 4 * WG;
   static constexpr int THREADS = 64 + 128 * WG;
-  static constexpr int S_BUFS = N <= 128 ? 2 : 1;
-  static constexpr int COLS = N * (S_BUFS + 1);
-  static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  static constexpr int CTAS = N == 16 || (N == 32 && D == 64) ? 3 : TMEM <= 256 ? 2 : 1;  // on an SM
+  static constexpr int TMEM = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 256;  // two of S, one of O
+  static constexpr int CTAS = R == 64 ? 1 : 2;        // on an SM
   static constexpr int KV_BYTES = 2 * kTile * D;
-  static constexpr int Q_BYTES = (N * D + 1023) / 1024 * 1024;
-  static constexpr int P_BYTES = N * kTile;
-  static constexpr int STAGE_AUX = kTile * 12 + 16;   // float2 scales, positions, the value scale
-  static constexpr int MISC = 8 * R * 4 * 2 + R * 16 + 3 * D * 4 + 512;
-  static constexpr int FIXED = 1024 + Q_BYTES + P_BYTES + MISC;
-  static constexpr int ROOM = (CTAS == 3 ? 75 : CTAS == 2 ? 112 : 226) * 1024;
-  static constexpr int FIT = (ROOM - FIXED) / (KV_BYTES + STAGE_AUX);
+  static constexpr int Q_BYTES = (R * PARTS * D + 1023) / 1024 * 1024;
+  static constexpr int P_BYTES = R * PARTS * kTile;   // one of two
+  static constexpr int AUX = kTile * 16;              // a stage's Token records
+  static constexpr int MISC = 72 * R + 3 * D * 4 + 512;
+  static constexpr int FIXED = 1024 + Q_BYTES + 2 * P_BYTES + MISC;
+  static constexpr int ROOM = CTAS == 2 ? 115456 : 231424;
+  static constexpr int FIT = (ROOM - FIXED) / (KV_BYTES + AUX);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
-  static constexpr int SMEM = FIXED + STAGES * (KV_BYTES + STAGE_AUX);
+  static constexpr int SMEM = FIXED + STAGES * (KV_BYTES + AUX);
   static_assert(STAGES >= 2 && SMEM <= 232448, "fits the 227 KiB per-CTA limit");
-  static_assert(COLS <= 512 && N % 16 == 0 && N <= 256, "tensor memory and N");
+  static_assert(!CAT || PARTS == 2, "side by side: two parts of eight rows");
+};
+
+// What a tile's position brings to its scores and weights.
+struct alignas(16) Token {
+  float k;       // softmax_scale * log2(e) * k_scale
+  float log_v;   // log2|v_scale|
+  float inv_v;   // 1 / |v_scale|, with v_scale's sign
+  int32_t pos;   // its position (0 with SELECT), or kNone
 };
 
 // Where the runs' parts of a group are, written by the CTA that has the group's first tile.
@@ -125,6 +145,23 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[NC]) 
           "=r"(r[7])
         : "r"(taddr));
   }
+}
+
+// Each thread of the warp writes NC consecutive columns of its TMEM lane.
+template <int NC>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[NC]) {
+  static_assert(NC == 8 || NC == 16 || NC == 32, "columns");
+#pragma unroll
+  for (int i = 0; i < NC; i += 8)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+            taddr + i),
+        "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]),
+        "r"(r[i + 6]), "r"(r[i + 7])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // Shared-memory descriptor of an M- or N-major operand whose rows (one for each k) are ROW bytes
@@ -252,15 +289,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *s_kv = base;                              // [stage][K tile, V tile]
-  uint8_t *s_q = s_kv + C::STAGES * C::KV_BYTES;     // [N][D], K-major, swizzled
-  uint8_t *s_p = s_q + C::Q_BYTES;                   // [N / 16][kTile][16]
-  uint8_t *at = s_p + C::P_BYTES;
-  float2 *s_sc = reinterpret_cast<float2 *>(at);     // [stage][kTile]: key factor, value share
-  at += C::STAGES * kTile * 8;
-  int *s_pos = reinterpret_cast<int *>(at);          // [stage][kTile]
-  at += C::STAGES * kTile * 4;
-  float *s_max = reinterpret_cast<float *>(at);      // [2][R][4 warps]
-  at += 2 * R * 16;
+  uint8_t *s_q = s_kv + C::STAGES * C::KV_BYTES;     // [PARTS * R][D], K-major, swizzled
+  uint8_t *s_p = s_q + C::Q_BYTES;                   // [2][PARTS * R / 16][kTile][16]
+  uint8_t *at = s_p + 2 * C::P_BYTES;
+  Token *s_tok = reinterpret_cast<Token *>(at);      // [stage][kTile]
+  at += C::STAGES * C::AUX;
+  float *s_max = reinterpret_cast<float *>(at);      // [R][4 warps]
+  at += R * 16;
   float *s_sum = reinterpret_cast<float *>(at);      // [R][4 warps]
   at += R * 16;
   float *s_rs = reinterpret_cast<float *>(at);       // [R]: a query row's power of two, undone
@@ -269,12 +304,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   at += R * 4;
   int *s_nan = reinterpret_cast<int *>(at);          // [3][D]: see below
   at += 3 * D * 4;
-  float *s_vref = reinterpret_cast<float *>(at);     // [stage]
-  at += 32;
   uint64_t *bars = reinterpret_cast<uint64_t *>(at);
   uint64_t *kv_full = bars, *kv_empty = bars + C::STAGES, *s_full = bars + 2 * C::STAGES,
-           *p_full = s_full + 2, *o_full = p_full + 1, *q_full = o_full + 1, *wg_bar = q_full + 1,
-           *drain = wg_bar + 2;
+           *p_full = s_full + 2, *pv_done = p_full + 1, *q_full = pv_done + 2, *drain = q_full + 1;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(drain + 1);
   __shared__ int64_t s_scan[C::THREADS / 32];
   __shared__ int64_t s_begin[2];  // the run's first tile within its key; tiles in the run
@@ -294,10 +326,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(p_full, C::SOFT_WARPS);
-    mbar_init(o_full, 1);
+    mbar_init(&pv_done[0], 1);
+    mbar_init(&pv_done[1], 1);
     mbar_init(q_full, C::SOFT_WARPS);
-    mbar_init(&wg_bar[0], 4);
-    mbar_init(&wg_bar[1], 4);
     mbar_init(drain, 1);
     fence_barrier_init();
   }
@@ -452,20 +483,21 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
         }
         if (bad) attn_flag(IDX_DEV_BAD_PAGE);
-        float most = 0.0f;
+        Token tok[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(vs[j]));
-        most = warp_max(most);
-        const float share = most > 1e-37f ? 1.0f / most : 0.0f;
+        for (int j = 0; j < 4; ++j) {
+          const float v = fabsf(vs[j]);
+          const float held = fmaxf(v, kLeastScale);
+          tok[j].k = ks[j] * z_unit;
+          tok[j].log_v = __log2f(held);
+          tok[j].inv_v = copysignf(1.0f / held, vs[j]);
+          tok[j].pos = pos[j];
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], phase ^ 1, kWaitNs));
         if (!ok) break;
         uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
-        float4 *sc = reinterpret_cast<float4 *>(s_sc + stage * kTile + lane * 4);
-        sc[0] = make_float4(ks[0] * z_unit, vs[0] * share, ks[1] * z_unit, vs[1] * share);
-        sc[1] = make_float4(ks[2] * z_unit, vs[2] * share, ks[3] * z_unit, vs[3] * share);
-        *reinterpret_cast<int4 *>(s_pos + stage * kTile + lane * 4) =
-            make_int4(pos[0], pos[1], pos[2], pos[3]);
-        if (lane == 0) s_vref[stage] = most * (1.0f / kPScale);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s_tok[stage * kTile + lane * 4 + j] = tok[j];
         if constexpr (C::SELECT) {
           mbar_arrive_expect_tx(&kv_full[stage], 8 * D);
           tma_gather4(kt + lane * 4 * D, &k_map, &kv_full[stage], row[0], row[1], row[2], row[3],
@@ -495,16 +527,17 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, N);
       constexpr uint32_t idesc_o = idesc_e4m3_f32(D, N) | kMajorMN_A | kMajorMN_B;
       const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
-      const uint64_t p_desc = smem_desc_p(smem_addr(s_p));
-      const uint32_t o_tmem = tmem + C::S_BUFS * N;
+      const uint32_t o_tmem = tmem + 2 * N;
       uint32_t tile = 0, seg = 0;
       const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
         const uint64_t k_desc = smem_desc_rows<D>(smem_addr(s_kv + st * C::KV_BYTES));
-        const uint32_t buf = C::S_BUFS == 2 ? n & 1 : 0;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          mma_f8f6f4(tmem + buf * N, k_desc + 2 * k, q_desc + 2 * k, idesc_s, k > 0);
-        mma_commit(&s_full[buf]);
+        for (int part = 0; part < C::PASSES; ++part)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            mma_f8f6f4(tmem + (n & 1) * N, k_desc + 2 * k, q_desc + part * (R * D >> 4) + 2 * k,
+                       idesc_s, part + k > 0);
+        mma_commit(&s_full[n & 1]);
       };
       while (ok && w.next(a, groups, keys)) {
         ok = mbar_wait(q_full, seg & 1, kWaitNs);
@@ -523,7 +556,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           const int next = stage + 1 == C::STAGES ? 0 : stage + 1;
           const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
           ahead = false;
-          if (C::S_BUFS == 2 && i + 1 < w.seg_tiles && mbar_try_wait(&kv_full[next], next_phase)) {
+          if (i + 1 < w.seg_tiles && mbar_try_wait(&kv_full[next], next_phase)) {
             tc_fence_after_sync();
             scores(tile + 1, next);
             ahead = true;
@@ -533,10 +566,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           tc_fence_after_sync();
           const uint64_t v_desc =
               smem_desc_mn<D>(smem_addr(s_kv + stage * C::KV_BYTES + kTile * D));
+          const uint64_t p_desc = smem_desc_p(smem_addr(s_p + (tile & 1) * C::P_BYTES));
 #pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
-            mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o, k > 0);
-          mma_commit(o_full);
+          for (int part = 0; part < C::PASSES; ++part)
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+              mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4),
+                         p_desc + part * (R * kTile >> 4) + k * (512 >> 4), idesc_o,
+                         i + part + k > 0);
+          mma_commit(&pv_done[tile & 1]);
           mma_commit(&kv_empty[stage]);
           stage = next;
           phase = next_phase;
@@ -553,17 +591,27 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     // The thread's dimension of the output, or -1 (M = 64: 16 lanes of each quarter).
     const int dim = D == 128 ? token : lane < 16 ? quarter * 16 + lane : -1;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint32_t tile = 0, syncs = 0;
+    uint32_t tile = 0;
     int seg = 0;
+    // Once a wait has given up the warp goes on without waiting, so that the barriers below (which
+    // have no limit of their own) find every warp of the warpgroup.
     const auto wait = [&](uint64_t *bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs)) != 0;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs));
     };
-    const auto wg_sync = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&wg_bar[wg]);
-      return wait(&wg_bar[wg], syncs++ & 1);
+    const auto any_of_group = [&](bool x) {
+      uint32_t y;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+          "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+          : "=r"(y)
+          : "r"(static_cast<uint32_t>(x)), "r"(1 + wg)
+          : "memory");
+      return y != 0;
     };
-    while (ok && w.next(a, groups, keys)) {
+    const auto sync_group = [&]() {
+      asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + wg) : "memory");
+    };
+    while (w.next(a, groups, keys)) {
       const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
       const int len = C::SELECT ? 0 : w.length;
       ++seg;
@@ -615,101 +663,152 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
-        ok = wait(q_full, (seg - 1) & 1);
-        if (!ok) break;
+        wait(q_full, (seg - 1) & 1);
       }
-      float acc[RT], sum[RT];
+      float sum[RT], ref[RT];  // ref: minus kTop, so that a weight is 2^(z' - ref)
+      constexpr bool kHoldRs = RT <= 16;  // (32 rows more would spill: read from shared memory then)
+      float rs[kHoldRs ? RT : 1];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] = sum[r] = 0.0f;
-      float m_run = -INFINITY;  // lane r: the running maximum of row r0 + r
+      for (int r = 0; r < RT; ++r) {
+        sum[r] = 0.0f;
+        ref[r] = 0.0f;
+        if constexpr (kHoldRs) rs[r] = s_rs[r0 + r];
+      }
+      uint32_t unset = 0xFFFFFFFFu;  // bit r: row r0 + r has seen nothing yet, and ref[r] means nothing
       // Positions below this are seen by every row of the segment.
       const int all_see = C::SELECT ? kNone : len - a.next_n + 1 + (slot_head<C>(a, m, 0).x);
       for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
-        const uint32_t buf = C::S_BUFS == 2 ? tile & 1 : 0;
-        const uint32_t sph = C::S_BUFS == 2 ? (tile >> 1) & 1 : tile & 1;
-        ok = wait(&kv_full[stage], phase) && wait(&s_full[buf], sph);
-        if (!ok) break;
+        wait(&kv_full[stage], phase);
+        wait(&s_full[tile & 1], (tile >> 1) & 1);
         tc_fence_after_sync();
-        const float2 sc = s_sc[stage * kTile + token];
-        const int pos = s_pos[stage * kTile + token];
-        const float vref = s_vref[stage];
-        float z[RT];
+        const Token tok = s_tok[stage * kTile + token];
+        float y[RT];  // the weights' logarithms
         {
-          uint32_t part[PARTS][RT];
+          uint32_t v[RT];
+          tmem_ld_cols<RT>(lane_base + (tile & 1) * N + (C::CAT ? 0 : r0), v);
+          if constexpr (C::CAT) {
+            uint32_t u[RT];
+            tmem_ld_cols<RT>(lane_base + (tile & 1) * N + R, u);
+            tmem_ld_wait();
+            reg_fence(v);
+            reg_fence(u);
 #pragma unroll
-          for (int j = 0; j < PARTS; ++j)
-            tmem_ld_cols<RT>(lane_base + buf * N + j * R + r0, part[j]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < PARTS; ++j) reg_fence(part[j]);
+            for (int r = 0; r < RT; ++r)
+              v[r] = __float_as_uint(__uint_as_float(v[r]) + __uint_as_float(u[r]));
+          } else {
+            tmem_ld_wait();
+            reg_fence(v);
+          }
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            float s = __uint_as_float(part[0][r]);
-#pragma unroll
-            for (int j = 1; j < PARTS; ++j) s += __uint_as_float(part[j][r]);
-            z[r] = s * s_rs[r0 + r] * sc.x;
+            float f;
+            if constexpr (kHoldRs)
+              f = rs[r];
+            else
+              f = s_rs[r0 + r];
+            y[r] = fmaf(__uint_as_float(v[r]), f * tok.k, tok.log_v - ref[r]);
           }
         }
-        const bool seen = pos < all_see;
+        const bool seen = tok.pos < all_see;
         if (!__all_sync(0xffffffffu, seen)) {
 #pragma unroll
           for (int r = 0; r < RT; ++r)
-            if (!seen && pos >= s_ext[r0 + r]) z[r] = -INFINITY;
+            if (!seen && tok.pos >= s_ext[r0 + r]) y[r] = -INFINITY;
         }
-        // ---- the rows' maxima over the tile --------------------------------------------------------
-        float top = -INFINITY;
+        float most = y[0];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const float x = warp_max(z[r]);
-          if (lane == r) top = x;
+        for (int r = 1; r < RT; ++r) most = fmaxf(most, y[r]);
+        bool move = most > kMost;
+        if (unset != 0) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) move |= ((unset >> r) & 1u) != 0 && y[r] != -INFINITY;
         }
-        float *mx = s_max + (tile & 1) * R * 4;
-        if (lane < RT) mx[(r0 + lane) * 4 + quarter] = top;
-        ok = wg_sync();
-        if (!ok) break;
-        float m_new = m_run, keep = 1.0f;
-        if (lane < RT) {
-          const float4 t4 = *reinterpret_cast<const float4 *>(mx + (r0 + lane) * 4);
-          m_new = fmaxf(fmaxf(m_run, fmaxf(t4.x, t4.y)), fmaxf(t4.z, t4.w));
-          keep = m_new == m_run ? 1.0f : fast_exp2(m_run - m_new);
+        if (any_of_group(move)) {
+          // Some weight would leave e4m3's range, or a row sees its first position: the references
+          // move to the maxima so far.
+          float mine = -INFINITY;  // lane r: row r0 + r
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const float x = warp_max(y[r]);
+            if (lane == r) mine = x;
+          }
+          if (lane < RT) s_max[(r0 + lane) * 4 + quarter] = mine;
+          sync_group();
+          float up = 0.0f, keep = 1.0f;
+          bool set = false;
+          if (lane < RT) {
+            const float4 t4 = *reinterpret_cast<const float4 *>(s_max + (r0 + lane) * 4);
+            const float t = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
+            set = t > -INFINITY;
+            if ((unset >> lane) & 1u) {
+              up = set ? t - kTop : 0.0f;  // (its sums are 0: nothing to rescale)
+            } else {
+              up = fmaxf(t - kTop, 0.0f);
+              keep = fast_exp2(-up);
+            }
+          }
+          unset &= ~__ballot_sync(0xffffffffu, set);
+          sync_group();  // (s_max may be written again)
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const float d = __shfl_sync(0xffffffffu, up, r);
+            y[r] -= d;
+            ref[r] += d;
+            sum[r] *= __shfl_sync(0xffffffffu, keep, r);
+          }
+          if (i > 0) {
+            wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
+            tc_fence_after_sync();
+            uint32_t v[RT];
+#pragma unroll
+            for (int half = 0; half < (C::CAT ? 2 : 1); ++half) {
+              const uint32_t o_at = lane_base + 2 * N + (C::CAT ? half * R : r0);
+              tmem_ld_cols<RT>(o_at, v);
+              tmem_ld_wait();
+              reg_fence(v);
+#pragma unroll
+              for (int r = 0; r < RT; ++r)
+                v[r] = __float_as_uint(__uint_as_float(v[r]) * __shfl_sync(0xffffffffu, keep, r));
+              tmem_st_cols<RT>(o_at, v);
+            }
+            tmem_st_wait();
+          }
         }
-        const float ref = m_new == -INFINITY ? 0.0f : m_new;
-        m_run = m_new;
-        const bool moved = __any_sync(0xffffffffu, keep != 1.0f);
         // ---- weights, their parts, the running sums ------------------------------------------------
-        const float vshare = sc.y * kPScale;
-        uint32_t bytes[PARTS][RT / 4];
+        // The weights' buffer was last read by the product two tiles ago.
+        if (tile >= 2) wait(&pv_done[tile & 1], ((tile >> 1) - 1) & 1);
+        uint8_t *sp = s_p + (tile & 1) * C::P_BYTES + token * 16;
+        const uint32_t flip = tok.inv_v < 0.0f ? 0x80808080u : 0u;
+        const uint32_t live = fabsf(tok.inv_v) < 1.0f / kLeastScale ? 0xFFFFFFFFu : 0u;
+        const float inv_v = fabsf(tok.inv_v);
+        uint32_t bytes[PARTS][4];
 #pragma unroll
         for (int r = 0; r < RT; r += 4) {
           float p[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            p[j] = fast_exp2(z[r + j] - __shfl_sync(0xffffffffu, ref, r + j));
-            if (moved) sum[r + j] *= __shfl_sync(0xffffffffu, keep, r + j);
-            sum[r + j] += p[j];
-            p[j] *= vshare;
+            p[j] = fast_exp2(y[r + j]);
+            sum[r + j] = fmaf(p[j], inv_v, sum[r + j]);
           }
 #pragma unroll
           for (int part = 0; part < PARTS; ++part) {
             const uint32_t b = e4m3x4(p[0], p[1], p[2], p[3]);
-            bytes[part][r / 4] = b;
+            bytes[part][(r / 4) % 4] = (b & live) ^ flip;
             if (part + 1 < PARTS) {
               const float2 b0 = e4m3x2_to_f32(b), b1 = e4m3x2_to_f32(b >> 16);
               p[0] -= b0.x, p[1] -= b0.y, p[2] -= b1.x, p[3] -= b1.y;
             }
           }
-        }
-        if constexpr (RT == 8) {  // PARTS = 2: both parts of the eight rows are one group of 16 n
-          *reinterpret_cast<uint4 *>(s_p + token * 16) =
-              make_uint4(bytes[0][0], bytes[0][1], bytes[1][0], bytes[1][1]);
-        } else {
+          if constexpr (C::CAT) {  // both parts of the eight rows are one group of 16 n
+            if (r == 4)
+              *reinterpret_cast<uint4 *>(sp) =
+                  make_uint4(bytes[0][0], bytes[0][1], bytes[1][0], bytes[1][1]);
+          } else if (r % 16 == 12) {
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-            for (int q = 0; q < RT / 16; ++q)
-              *reinterpret_cast<uint4 *>(s_p + ((part * R + r0) / 16 + q) * (kTile * 16) + token * 16) =
-                  make_uint4(bytes[part][4 * q], bytes[part][4 * q + 1], bytes[part][4 * q + 2],
-                             bytes[part][4 * q + 3]);
+            for (int part = 0; part < PARTS; ++part)
+              *reinterpret_cast<uint4 *>(sp + (part * R + r0 + r - 12) / 16 * (kTile * 16)) =
+                  make_uint4(bytes[part][0], bytes[part][1], bytes[part][2], bytes[part][3]);
+          }
         }
         // A value that some row does not see must not meet its weight of 0 as a NaN (a code of the
         // cache, or bytes that were never written): what no row sees becomes 0; in the newest
@@ -717,7 +816,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // this segment's number) for the rows that do see it.
         if (wg == 0 && !seen) {
           uint8_t *v = s_kv + stage * C::KV_BYTES + kTile * D;
-          if (pos == kNone) {
+          if (tok.pos == kNone) {
             for (int x = 0; x < D; x += 16)
               *reinterpret_cast<uint4 *>(v + token * D + x) = make_uint4(0, 0, 0, 0);
           } else {
@@ -725,10 +824,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               const uint32_t at4 = swizzled<D>(token, x);
               const uint32_t four = *reinterpret_cast<const uint32_t *>(v + at4);
               if ((((four & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) == 0) continue;
-              for (int y = 0; y < 4; ++y)
-                if (((four >> (8 * y)) & 0x7F) == 0x7F) {
-                  v[at4 + y] = 0;
-                  s_nan[(len - 1 - pos) * D + x + y] = seg;
+              for (int e = 0; e < 4; ++e)
+                if (((four >> (8 * e)) & 0x7F) == 0x7F) {
+                  v[at4 + e] = 0;
+                  s_nan[(len - 1 - tok.pos) * D + x + e] = seg;
                 }
             }
           }
@@ -737,35 +836,37 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
-        ok = wait(o_full, tile & 1);
-        if (!ok) break;
-        tc_fence_after_sync();
-        {
-          uint32_t part[PARTS][RT];
-#pragma unroll
-          for (int j = 0; j < PARTS; ++j)
-            tmem_ld_cols<RT>(lane_base + C::S_BUFS * N + j * R + r0, part[j]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < PARTS; ++j) reg_fence(part[j]);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            float o = __uint_as_float(part[0][r]);
-#pragma unroll
-            for (int j = 1; j < PARTS; ++j) o += __uint_as_float(part[j][r]);
-            if (moved) acc[r] *= __shfl_sync(0xffffffffu, keep, r);
-            acc[r] += vref * o;
-          }
-        }
-        tc_fence_before_sync();
         if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
-      if (!ok) break;
+      // ---- the segment's sums ------------------------------------------------------------------------
+      wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
+      tc_fence_after_sync();
+      float acc[RT];
+      {
+        uint32_t v[RT];
+        tmem_ld_cols<RT>(lane_base + 2 * N + (C::CAT ? 0 : r0), v);
+        tmem_ld_wait();
+        reg_fence(v);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r] = __uint_as_float(v[r]);
+        if constexpr (C::CAT) {
+          tmem_ld_cols<RT>(lane_base + 2 * N + R, v);
+          tmem_ld_wait();
+          reg_fence(v);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[r] += __uint_as_float(v[r]);
+        }
+      }
+      tc_fence_before_sync();
+      float m_run = kRefNone;  // lane r: the reference of row r0 + r
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        if (lane == r && ((unset >> r) & 1u) == 0) m_run = ref[r];
       // ---- the segment's result ----------------------------------------------------------------------
-      // (s_rs and s_ext are not read past the wg_sync below: the next segment's are written then.)
+      // (s_rs and s_ext are not read past the barrier below: the next segment's are written then.)
       if (!C::SELECT && a.next_n > 1 && dim >= 0) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -780,8 +881,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == 0) s_sum[(r0 + r) * 4 + quarter] = x;
       }
-      ok = wg_sync();
-      if (!ok) break;
+      sync_group();
       float l = 0.0f;  // lane r: the sum of row r0 + r
       if (lane < RT) {
         const float4 t4 = *reinterpret_cast<const float4 *>(s_sum + (r0 + lane) * 4);
