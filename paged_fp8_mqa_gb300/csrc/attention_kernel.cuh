@@ -5,22 +5,20 @@
 // in the row's slots.
 //
 // Both products run on the tensor core in e4m3, straight from the cache's bytes: the cache is
-// never converted.  The other operand keeps its precision by being split into e4m3 parts whose
-// products are summed in the accumulator:
+// never converted.  The other operand keeps its precision by being split into e4m3 parts:
 //   * a query row is scaled by a power of two to [128, 256) and written as hi + lo, each the
 //     e4m3 nearest to what is left: 4 + 4 bits hold a bfloat16's 8 exactly (down to 2^-18 of the
 //     row's largest magnitude); a float16's 11 bits take three parts.  Products of e4m3 values
-//     are exact and sums float32, so the scores are those of the unrounded queries.
+//     are exact and sums float32, so the scores are those of the unrounded queries.  The parts'
+//     products go into the same accumulator.
 //   * a weight is written the same way: within 2^-8 of itself with two parts (what a bfloat16
-//     weight would be), 2^-12 with three, or 2^-18 of the row's largest.
+//     weight would be), 2^-12 with three, or 2^-18 of the row's largest.  Its parts stand at
+//     different powers of two, in columns of their own, and are added when O is read.
 // The weights that meet V carry the block scales: with z' = log2(e) z + log2|vs| they are
 // u = 2^(z' - ref), sign(vs) applied, so that O = sum u v needs no scale of its own and may be
 // accumulated in tensor memory over tiles of any scales, and the softmax's denominator is
 // l = sum u / |vs| in float32; out = O / l.  ref follows the running maximum of z' from below: it
-// moves (to the maximum) only when some u would pass e4m3's range, 2^0.8 times what it was, and
-// then O and l are rescaled.  With scores of ordinary spread that is a few tiles of a thousand;
-// the exact running maximum, read back, rescaled and exchanged among the warps in every tile, took
-// three times the instructions (draft verification 304 us).
+// moves (to the maximum) only when some u would leave e4m3's range, and then O and l are rescaled.
 //
 // A tile is 128 positions of one K/V head.  S^T[128 positions x rows] = K Q^T puts a position in
 // each lane of tensor memory and the rows that share the K/V head (query heads times draft slots)
@@ -48,9 +46,11 @@ constexpr int kTile = 128;                     // positions of a tile
 constexpr uint64_t kWaitNs = 1000000000ull;    // 1 s: far beyond any legitimate wait
 constexpr int kNone = INT_MAX;                 // the position of a token that no row sees
 constexpr float kRefNone = -1e30f;             // the reference of a row that has seen nothing
-// Weights are 2^(z' - ref + 8), at most 256 when ref is set; ref moves when one would pass 2^8.8 =
-// 446, just inside e4m3's 448.
-constexpr float kTop = 8.0f, kMost = 8.8f;
+// Weights are 2^(z' - ref), at most 2^4 when ref is set; ref moves when one would pass 2^8.8 = 446,
+// just inside e4m3's 448, that is when a row's maximum has grown 28-fold.  Each part after the
+// first is held times 2^4 more, which keeps what two parts cannot hold at 2^-18 of the largest
+// weight as if it stood at the top of e4m3's range, where a growth of 1.7 would move ref.
+constexpr float kTop = 4.0f, kMost = 8.8f, kPartUp = 16.0f;
 constexpr float kLeastScale = 7.8886090522101180541e-31f;  // 2^-100: a value scale below it is 0
 
 // One kernel's shape: R rows, PARTS parts a row, head_dim D.
@@ -58,16 +58,18 @@ template <int D_, int R_, int PARTS_, bool SELECT_>
 struct AttnCfg {
   static constexpr int D = D_, R = R_, PARTS = PARTS_;
   static constexpr bool SELECT = SELECT_;
-  // With R = 8 the two parts stand side by side in the least N (16) and are added when read; else
-  // each part is a product of its own into the same columns.
+  // With R = 8 a query's two parts stand side by side in the least N (16) and are added when read;
+  // else each part is a product of its own into the same columns.
   static constexpr bool CAT = R == 8;
-  static constexpr int N = CAT ? 16 : R;              // columns of both products
-  static constexpr int PASSES = CAT ? 1 : PARTS;
+  static constexpr int NS = CAT ? 16 : R;             // columns of S
+  static constexpr int NO = R * PARTS;                // columns of O
+  static constexpr int PASSES = CAT ? 1 : PARTS;      // products that make S
   static constexpr int WG = R == 64 ? 2 : 1;          // softmax warpgroups, R / WG rows each
   static constexpr int RT = R / WG;
   static constexpr int SOFT_WARPS = 4 * WG;
   static constexpr int THREADS = 64 + 128 * WG;
-  static constexpr int TMEM = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 256;  // two of S, one of O
+  static constexpr int COLS = 2 * NS + NO;            // two of S, one of O
+  static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static constexpr int CTAS = R == 64 ? 1 : 2;        // on an SM
   static constexpr int KV_BYTES = 2 * kTile * D;
   static constexpr int Q_BYTES = (R * PARTS * D + 1023) / 1024 * 1024;
@@ -284,7 +286,7 @@ template <class C, typename T>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     k_attention(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const AttentionArgs a, const AttnSplit split, GroupParts *parts) {
-  constexpr int D = C::D, R = C::R, RT = C::RT, N = C::N, PARTS = C::PARTS;
+  constexpr int D = C::D, R = C::R, RT = C::RT, NS = C::NS, PARTS = C::PARTS;
   extern __shared__ uint8_t s_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   at += 3 * D * 4;
   uint64_t *bars = reinterpret_cast<uint64_t *>(at);
   uint64_t *kv_full = bars, *kv_empty = bars + C::STAGES, *s_full = bars + 2 * C::STAGES,
-           *p_full = s_full + 2, *pv_done = p_full + 1, *q_full = pv_done + 2, *drain = q_full + 1;
+           *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *drain = q_full + 1;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(drain + 1);
   __shared__ int64_t s_scan[C::THREADS / 32];
   __shared__ int64_t s_begin[2];  // the run's first tile within its key; tiles in the run
@@ -325,7 +327,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     }
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
-    mbar_init(p_full, C::SOFT_WARPS);
+    // (Two, as the softmax may finish a tile before the issuer has seen the one before.)
+    mbar_init(&p_full[0], C::SOFT_WARPS);
+    mbar_init(&p_full[1], C::SOFT_WARPS);
     mbar_init(&pv_done[0], 1);
     mbar_init(&pv_done[1], 1);
     mbar_init(q_full, C::SOFT_WARPS);
@@ -524,10 +528,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   } else if (warp == 1) {
     // ============================== MMA issuer ==================================================
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, N);
-      constexpr uint32_t idesc_o = idesc_e4m3_f32(D, N) | kMajorMN_A | kMajorMN_B;
+      constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, NS);
+      constexpr uint32_t idesc_o = idesc_e4m3_f32(D, C::NO) | kMajorMN_A | kMajorMN_B;
       const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
-      const uint32_t o_tmem = tmem + 2 * N;
+      const uint32_t o_tmem = tmem + 2 * NS;
       uint32_t tile = 0, seg = 0;
       const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
         const uint64_t k_desc = smem_desc_rows<D>(smem_addr(s_kv + st * C::KV_BYTES));
@@ -535,7 +539,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         for (int part = 0; part < C::PASSES; ++part)
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            mma_f8f6f4(tmem + (n & 1) * N, k_desc + 2 * k, q_desc + part * (R * D >> 4) + 2 * k,
+            mma_f8f6f4(tmem + (n & 1) * NS, k_desc + 2 * k, q_desc + part * (R * D >> 4) + 2 * k,
                        idesc_s, part + k > 0);
         mma_commit(&s_full[n & 1]);
       };
@@ -561,19 +565,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             scores(tile + 1, next);
             ahead = true;
           }
-          ok = mbar_wait(p_full, tile & 1, kWaitNs);
+          ok = mbar_wait(&p_full[tile & 1], (tile >> 1) & 1, kWaitNs);
           if (!ok) break;
           tc_fence_after_sync();
           const uint64_t v_desc =
               smem_desc_mn<D>(smem_addr(s_kv + stage * C::KV_BYTES + kTile * D));
           const uint64_t p_desc = smem_desc_p(smem_addr(s_p + (tile & 1) * C::P_BYTES));
 #pragma unroll
-          for (int part = 0; part < C::PASSES; ++part)
-#pragma unroll
-            for (int k = 0; k < kTile / 32; ++k)
-              mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4),
-                         p_desc + part * (R * kTile >> 4) + k * (512 >> 4), idesc_o,
-                         i + part + k > 0);
+          for (int k = 0; k < kTile / 32; ++k)
+            mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o,
+                       i + k > 0);
           mma_commit(&pv_done[tile & 1]);
           mma_commit(&kv_empty[stage]);
           stage = next;
@@ -665,14 +666,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if (lane == 0) mbar_arrive(q_full);
         wait(q_full, (seg - 1) & 1);
       }
-      float sum[RT], ref[RT];  // ref: minus kTop, so that a weight is 2^(z' - ref)
-      constexpr bool kHoldRs = RT <= 16;  // (32 rows more would spill: read from shared memory then)
-      float rs[kHoldRs ? RT : 1];
+      // Pairs of rows, for the packed float32 operations: the sums and minus the references.
+      float2 sum[RT / 2], nref[RT / 2];
+      constexpr bool kHoldRs = RT <= 8;  // (more rows would spill: read from shared memory then)
+      float2 rs[kHoldRs ? RT / 2 : 1];
+      const float2 *rs_at = reinterpret_cast<const float2 *>(s_rs + r0);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        sum[r] = 0.0f;
-        ref[r] = 0.0f;
-        if constexpr (kHoldRs) rs[r] = s_rs[r0 + r];
+      for (int r = 0; r < RT / 2; ++r) {
+        sum[r] = nref[r] = make_float2(0.0f, 0.0f);
+        if constexpr (kHoldRs) rs[r] = rs_at[r];
       }
       uint32_t unset = 0xFFFFFFFFu;  // bit r: row r0 + r has seen nothing yet, and ref[r] means nothing
       // Positions below this are seen by every row of the segment.
@@ -682,13 +684,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         wait(&s_full[tile & 1], (tile >> 1) & 1);
         tc_fence_after_sync();
         const Token tok = s_tok[stage * kTile + token];
-        float y[RT];  // the weights' logarithms
+        float2 y[RT / 2];  // the weights' logarithms
         {
           uint32_t v[RT];
-          tmem_ld_cols<RT>(lane_base + (tile & 1) * N + (C::CAT ? 0 : r0), v);
+          tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + (C::CAT ? 0 : r0), v);
           if constexpr (C::CAT) {
             uint32_t u[RT];
-            tmem_ld_cols<RT>(lane_base + (tile & 1) * N + R, u);
+            tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + R, u);
             tmem_ld_wait();
             reg_fence(v);
             reg_fence(u);
@@ -699,29 +701,38 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             tmem_ld_wait();
             reg_fence(v);
           }
+          const float2 k2 = make_float2(tok.k, tok.k), lv2 = make_float2(tok.log_v, tok.log_v);
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            float f;
+          for (int r = 0; r < RT / 2; ++r) {
+            float2 f;
             if constexpr (kHoldRs)
               f = rs[r];
             else
-              f = s_rs[r0 + r];
-            y[r] = fmaf(__uint_as_float(v[r]), f * tok.k, tok.log_v - ref[r]);
+              f = rs_at[r];
+            const float2 s2 = make_float2(__uint_as_float(v[2 * r]), __uint_as_float(v[2 * r + 1]));
+            y[r] = __ffma2_rn(s2, __fmul2_rn(f, k2), __fadd2_rn(lv2, nref[r]));
           }
         }
         const bool seen = tok.pos < all_see;
         if (!__all_sync(0xffffffffu, seen)) {
+          if (!seen) {
 #pragma unroll
-          for (int r = 0; r < RT; ++r)
-            if (!seen && tok.pos >= s_ext[r0 + r]) y[r] = -INFINITY;
+            for (int r = 0; r < RT / 2; ++r) {
+              if (tok.pos >= s_ext[r0 + 2 * r]) y[r].x = -INFINITY;
+              if (tok.pos >= s_ext[r0 + 2 * r + 1]) y[r].y = -INFINITY;
+            }
+          }
         }
-        float most = y[0];
+        float most = fmaxf(y[0].x, y[0].y);
 #pragma unroll
-        for (int r = 1; r < RT; ++r) most = fmaxf(most, y[r]);
+        for (int r = 1; r < RT / 2; ++r) most = fmaxf(most, fmaxf(y[r].x, y[r].y));
         bool move = most > kMost;
         if (unset != 0) {
 #pragma unroll
-          for (int r = 0; r < RT; ++r) move |= ((unset >> r) & 1u) != 0 && y[r] != -INFINITY;
+          for (int r = 0; r < RT / 2; ++r) {
+            move |= ((unset >> (2 * r)) & 1u) != 0 && y[r].x != -INFINITY;
+            move |= ((unset >> (2 * r + 1)) & 1u) != 0 && y[r].y != -INFINITY;
+          }
         }
         if (any_of_group(move)) {
           // Some weight would leave e4m3's range, or a row sees its first position: the references
@@ -729,7 +740,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           float mine = -INFINITY;  // lane r: row r0 + r
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            const float x = warp_max(y[r]);
+            const float x = warp_max(r & 1 ? y[r / 2].y : y[r / 2].x);
             if (lane == r) mine = x;
           }
           if (lane < RT) s_max[(r0 + lane) * 4 + quarter] = mine;
@@ -750,19 +761,21 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           unset &= ~__ballot_sync(0xffffffffu, set);
           sync_group();  // (s_max may be written again)
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const float d = __shfl_sync(0xffffffffu, up, r);
-            y[r] -= d;
-            ref[r] += d;
-            sum[r] *= __shfl_sync(0xffffffffu, keep, r);
+          for (int r = 0; r < RT / 2; ++r) {
+            const float2 d = make_float2(-__shfl_sync(0xffffffffu, up, 2 * r),
+                                         -__shfl_sync(0xffffffffu, up, 2 * r + 1));
+            y[r] = __fadd2_rn(y[r], d);
+            nref[r] = __fadd2_rn(nref[r], d);
+            sum[r].x *= __shfl_sync(0xffffffffu, keep, 2 * r);
+            sum[r].y *= __shfl_sync(0xffffffffu, keep, 2 * r + 1);
           }
           if (i > 0) {
             wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
             tc_fence_after_sync();
-            uint32_t v[RT];
-#pragma unroll
-            for (int half = 0; half < (C::CAT ? 2 : 1); ++half) {
-              const uint32_t o_at = lane_base + 2 * N + (C::CAT ? half * R : r0);
+#pragma unroll 1
+            for (int part = 0; part < PARTS; ++part) {
+              const uint32_t o_at = lane_base + 2 * NS + part * R + r0;
+              uint32_t v[RT];
               tmem_ld_cols<RT>(o_at, v);
               tmem_ld_wait();
               reg_fence(v);
@@ -782,21 +795,24 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const uint32_t live = fabsf(tok.inv_v) < 1.0f / kLeastScale ? 0xFFFFFFFFu : 0u;
         const float inv_v = fabsf(tok.inv_v);
         uint32_t bytes[PARTS][4];
+        const float2 inv2 = make_float2(inv_v, inv_v), up2 = make_float2(kPartUp, kPartUp);
 #pragma unroll
         for (int r = 0; r < RT; r += 4) {
-          float p[4];
+          float2 p[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            p[j] = fast_exp2(y[r + j]);
-            sum[r + j] = fmaf(p[j], inv_v, sum[r + j]);
+          for (int j = 0; j < 2; ++j) {
+            p[j] = make_float2(fast_exp2(y[r / 2 + j].x), fast_exp2(y[r / 2 + j].y));
+            sum[r / 2 + j] = __ffma2_rn(p[j], inv2, sum[r / 2 + j]);
           }
 #pragma unroll
           for (int part = 0; part < PARTS; ++part) {
-            const uint32_t b = e4m3x4(p[0], p[1], p[2], p[3]);
+            const uint32_t b = e4m3x4(p[0].x, p[0].y, p[1].x, p[1].y);
             bytes[part][(r / 4) % 4] = (b & live) ^ flip;
             if (part + 1 < PARTS) {
+              // 16 (p - b), both products exact.
               const float2 b0 = e4m3x2_to_f32(b), b1 = e4m3x2_to_f32(b >> 16);
-              p[0] -= b0.x, p[1] -= b0.y, p[2] -= b1.x, p[3] -= b1.y;
+              p[0] = __fmul2_rn(make_float2(p[0].x - b0.x, p[0].y - b0.y), up2);
+              p[1] = __fmul2_rn(make_float2(p[1].x - b1.x, p[1].y - b1.y), up2);
             }
           }
           if constexpr (C::CAT) {  // both parts of the eight rows are one group of 16 n
@@ -835,7 +851,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         fence_proxy_async_shared();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(&p_full[tile & 1]);
         if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1;
@@ -845,26 +861,22 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
       tc_fence_after_sync();
       float acc[RT];
-      {
+#pragma unroll
+      for (int part = PARTS - 1; part >= 0; --part) {
         uint32_t v[RT];
-        tmem_ld_cols<RT>(lane_base + 2 * N + (C::CAT ? 0 : r0), v);
+        tmem_ld_cols<RT>(lane_base + 2 * NS + part * R + r0, v);
         tmem_ld_wait();
         reg_fence(v);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r] = __uint_as_float(v[r]);
-        if constexpr (C::CAT) {
-          tmem_ld_cols<RT>(lane_base + 2 * N + R, v);
-          tmem_ld_wait();
-          reg_fence(v);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) acc[r] += __uint_as_float(v[r]);
-        }
+        for (int r = 0; r < RT; ++r)
+          acc[r] = part == PARTS - 1 ? __uint_as_float(v[r])
+                                     : fmaf(acc[r], 1.0f / kPartUp, __uint_as_float(v[r]));
       }
       tc_fence_before_sync();
       float m_run = kRefNone;  // lane r: the reference of row r0 + r
 #pragma unroll
       for (int r = 0; r < RT; ++r)
-        if (lane == r && ((unset >> r) & 1u) == 0) m_run = ref[r];
+        if (lane == r && ((unset >> r) & 1u) == 0) m_run = -(r & 1 ? nref[r / 2].y : nref[r / 2].x);
       // ---- the segment's result ----------------------------------------------------------------------
       // (s_rs and s_ext are not read past the barrier below: the next segment's are written then.)
       if (!C::SELECT && a.next_n > 1 && dim >= 0) {
@@ -876,7 +888,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        float x = sum[r];
+        float x = r & 1 ? sum[r / 2].y : sum[r / 2].x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == 0) s_sum[(r0 + r) * 4 + quarter] = x;
