@@ -384,13 +384,16 @@ IDX_EXPORT int idx_attention_fp8(
   a.out = out;
   a.lse = lse;
   a.workspace = static_cast<float *>(workspace);
-  CUtensorMap k_map, v_map;
-  const uint64_t rows = static_cast<uint64_t>(num_blocks) * kv_heads * block_size;
-  const uint32_t box = candidates != nullptr ? 1u : static_cast<uint32_t>(block_size);
-  st = idx::encode_rows(&k_map, k_pool, rows, static_cast<uint32_t>(head_dim), box);
-  if (st != IDX_OK) return st;
-  st = idx::encode_rows(&v_map, v_pool, rows, static_cast<uint32_t>(head_dim), box);
-  if (st != IDX_OK) return st;
+  CUtensorMap k_map{}, v_map{};  // (with candidates the rows are gathered without them)
+  if (candidates == nullptr) {
+    const uint64_t rows = static_cast<uint64_t>(num_blocks) * kv_heads * block_size;
+    st = idx::encode_rows(&k_map, k_pool, rows, static_cast<uint32_t>(head_dim),
+                          static_cast<uint32_t>(block_size));
+    if (st != IDX_OK) return st;
+    st = idx::encode_rows(&v_map, v_pool, rows, static_cast<uint32_t>(head_dim),
+                          static_cast<uint32_t>(block_size));
+    if (st != IDX_OK) return st;
+  }
   const auto launch = head_dim == 64 ? idx::launch_attention_d64 : idx::launch_attention_d128;
   const cudaError_t e = launch(k_map, v_map, a, dtype, ctas, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? IDX_OK : cuda_fail(e, "attention launch");

@@ -75,7 +75,7 @@ struct AttnCfg {
   static constexpr int Q_BYTES = (R * PARTS * D + 1023) / 1024 * 1024;
   static constexpr int P_BYTES = R * PARTS * kTile;   // one of two
   static constexpr int AUX = kTile * 16;              // a stage's Token records
-  static constexpr int MISC = 72 * R + 3 * D * 4 + 512;
+  static constexpr int MISC = 48 * R + 3 * D * 4 + 256;
   static constexpr int FIXED = 1024 + Q_BYTES + 2 * P_BYTES + MISC;
   static constexpr int ROOM = CTAS == 2 ? 115456 : 231424;
   static constexpr int FIT = (ROOM - FIXED) / (KV_BYTES + AUX);
@@ -92,6 +92,16 @@ struct alignas(16) Token {
   float inv_v;   // 1 / |v_scale|, with v_scale's sign
   int32_t pos;   // its position (0 with SELECT), or kNone
 };
+
+__device__ __forceinline__ Token token_of(float k, float v_scale, int pos) {
+  Token t;
+  const float held = fmaxf(fabsf(v_scale), kLeastScale);
+  t.k = k;
+  t.log_v = __log2f(held);
+  t.inv_v = copysignf(1.0f / held, v_scale);
+  t.pos = pos;
+  return t;
+}
 
 // Where the runs' parts of a group are, written by the CTA that has the group's first tile.
 struct GroupParts {
@@ -112,18 +122,6 @@ __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Four rows of the tensor (box one row high) into four consecutive rows of shared memory.
-__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, uint64_t *bar,
-                                            int32_t y0, int32_t y1, int32_t y2, int32_t y3,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(y0), "r"(y1), "r"(y2),
-      "r"(y3), "l"(policy)
-      : "memory");
 }
 
 // Each thread of the warp reads NC consecutive columns of its TMEM lane.
@@ -304,6 +302,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   at += R * 4;
   int *s_ext = reinterpret_cast<int *>(at);          // [R]: positions a row sees
   at += R * 4;
+  int *s_row = reinterpret_cast<int *>(at);          // [2][R]: a row's (b, t, h) in line, by segment
+  at += 2 * R * 4;
   int *s_nan = reinterpret_cast<int *>(at);          // [3][D]: see below
   at += 3 * D * 4;
   uint64_t *bars = reinterpret_cast<uint64_t *>(at);
@@ -319,10 +319,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   const int keys = C::SELECT ? a.batch * a.next_n : a.batch;
 
   if (warp == 0 && lane == 0) {
-    prefetch_tensor_map(&k_map);
-    prefetch_tensor_map(&v_map);
+    if constexpr (!C::SELECT) {
+      prefetch_tensor_map(&k_map);
+      prefetch_tensor_map(&v_map);
+    }
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&kv_full[i], 32);
+      // A lane's arrival; with SELECT also one when its copies have landed.
+      mbar_init(&kv_full[i], C::SELECT ? 64 : 32);
       mbar_init(&kv_empty[i], 1);
     }
     mbar_init(&s_full[0], 1);
@@ -417,111 +420,161 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const uint64_t policy = l2_policy_evict_first();
     const int shift = a.block_size == 32 ? 5 : a.block_size == 64 ? 6 : 7;
     const float z_unit = a.scale * 1.4426950408889634f;  // scores in units of ln 2
+    const auto stage_free = [&]() {
+      ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], phase ^ 1, kWaitNs));
+      return ok;
+    };
+    const auto next_stage = [&]() {
+      ++issued;
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    };
     while (ok && w.next(a, groups, keys)) {
       const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
       const int32_t *table = a.block_tables + m.b * a.bt_stride;
-      const int2 *cand = nullptr;
-      int extent = w.length;
       if constexpr (C::SELECT) {
-        cand = a.candidates + w.key * a.cand_stride + max(0, __ldg(a.ranges + w.key));
-        extent = __ldg(a.seq_lens + m.b * a.sl_stride) - a.next_n + m.t_select + 1;
-      }
-      for (int i = w.seg_tile; i < w.seg_tile + w.seg_tiles; ++i) {
-        // Four consecutive tokens a lane: their positions, rows of the pool and scales.  (Read
-        // before the wait for the stage, so that their latency runs beside the tiles in flight.)
-        int pos[4], row[4];
-        float ks[4], vs[4];
-        bool bad = false;
-        if constexpr (C::SELECT) {
+        // A lane looks after tokens lane, lane + 32, ... of a tile: position, then page, then the
+        // page's scales, each read one tile further ahead than the next, so that a tile pays for
+        // one memory round trip and not for three.
+        const int2 *cand =
+            a.candidates + w.key * a.cand_stride + max(0, __ldg(a.ranges + w.key)) + lane;
+        const int extent = __ldg(a.seq_lens + m.b * a.sl_stride) - a.next_n + m.t_select + 1;
+        const int end = min((w.seg_tile + w.seg_tiles) * kTile, w.length) - lane;
+        const auto positions = [&](int tile, int (&pos)[4]) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int s = i * kTile + lane * 4 + j;
-            pos[j] = s < w.length ? __ldg(&cand[s].x) : kNone;
+            const int s = tile * kTile + 32 * j;
+            pos[j] = s < end ? __ldg(&cand[s].x) : -1;
           }
+        };
+        // Each token's row of the pool, or -1.
+        const auto pool_rows = [&](const int (&pos)[4], int (&row)[4]) {
+          bool bad = false;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            int id = -1;
+            row[j] = -1;
             if (pos[j] >= 0 && pos[j] < extent) {
               const int blk = pos[j] >> shift;
-              id = blk < a.bt_width ? __ldg(table + blk) : -1;
-              if (id < 0 || id >= a.num_blocks) {
+              const int id = blk < a.bt_width ? __ldg(table + blk) : -1;
+              if (id >= 0 && id < a.num_blocks)
+                row[j] = ((id * a.kv_heads + m.g) << shift) + (pos[j] & (a.block_size - 1));
+              else
                 bad = true;
-                id = -1;
-              }
             }
-            row[j] = id;
+          }
+          if (bad) attn_flag(IDX_DEV_BAD_PAGE);
+        };
+        const auto scales = [&](const int (&row)[4], float (&ks)[4], float (&vs)[4]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            ks[j] = row[j] >= 0 ? __ldg(a.k_scales + (row[j] >> shift)) : 0.0f;
+            vs[j] = row[j] >= 0 ? __ldg(a.v_scales + (row[j] >> shift)) : 0.0f;
+          }
+        };
+        int pos1[4], pos2[4], row0[4], row1[4];
+        float ks0[4], vs0[4], ks1[4], vs1[4];
+        positions(w.seg_tile, pos1);
+        positions(w.seg_tile + 1, pos2);
+        pool_rows(pos1, row0);
+        pool_rows(pos2, row1);
+        scales(row0, ks0, vs0);
+        // 16 bytes a lane and copy: a warp's copy is 512 / D rows of K or of V, stored with the
+        // swizzle that the products expect.  (As gathers of four rows by the TMA unit, 64 a tile, a
+        // tile took 2.1 us to issue, and the serving mix's 343 MB of selected rows 176 us.)
+        constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+        const int x = (lane % kLanes) * 16, sub = lane / kLanes;
+        for (int i = w.seg_tile; i < w.seg_tile + w.seg_tiles; ++i) {
+          positions(i + 2, pos2);
+          scales(row1, ks1, vs1);
+          if (!stage_free()) break;
+          uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 32 / kRows; ++j) {
+              const int n = j * kRows + sub;  // the token 32 q + n is lane n's q-th
+              const int row = __shfl_sync(0xffffffffu, row0[q], n);
+              if (row < 0) continue;  // (the softmax clears the value row of a token that is not)
+              const int64_t src = static_cast<int64_t>(row) * D + x;
+              const uint32_t dst = swizzled<D>(32 * q + n, x);
+              cp_async_16(kt + dst, a.k_pool + src, policy);
+              cp_async_16(vt + dst, a.v_pool + src, policy);
+            }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s_tok[stage * kTile + lane + 32 * j] =
+                token_of(ks0[j] * z_unit, vs0[j], row0[j] >= 0 ? 0 : kNone);
+          cp_async_arrive_noinc(&kv_full[stage]);
+          mbar_arrive(&kv_full[stage]);
+          next_stage();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            row0[j] = row1[j];
+            ks0[j] = ks1[j];
+            vs0[j] = vs1[j];
+          }
+          pool_rows(pos2, row1);
+        }
+      } else {
+        // A lane reads one page's id and scales, 32 pages ahead of the ones in hand: the ids while
+        // the first tile of a batch is issued, their scales after it.
+        const int n_pages = (w.length + a.block_size - 1) >> shift;
+        const int per_tile = kTile >> shift;
+        int first = w.seg_tile * per_tile;  // the page of lane 0
+        const auto ids = [&](int page) {
+          if (page >= n_pages || page >= (w.seg_tile + w.seg_tiles) * per_tile) return -1;
+          const int id = page < a.bt_width ? __ldg(table + page) : -1;
+          if (id >= 0 && id < a.num_blocks) return id;
+          attn_flag(IDX_DEV_BAD_PAGE);
+          return -1;
+        };
+        int id = ids(first + lane), id_next = -1;
+        float ks = 0.0f, vs = 0.0f, ks_next = 0.0f, vs_next = 0.0f;
+        const auto scales = [&](int block, float &k, float &v) {
+          const int page = block * a.kv_heads + m.g;
+          k = block >= 0 ? __ldg(a.k_scales + page) : 0.0f;
+          v = block >= 0 ? __ldg(a.v_scales + page) : 0.0f;
+        };
+        scales(id, ks, vs);
+        id_next = ids(first + 32 + lane);
+        Token mine = token_of(ks * z_unit, vs, 0);
+        bool fetch = true;  // the next batch's scales are still to be read
+        for (int i = w.seg_tile; i < w.seg_tile + w.seg_tiles; ++i) {
+          if (i * per_tile >= first + 32) {
+            first += 32;
+            id = id_next;
+            mine = token_of(ks_next * z_unit, vs_next, 0);
+            id_next = ids(first + 32 + lane);
+            fetch = true;
+          }
+          const int p = i * kTile + lane * 4;
+          const int from = (p >> shift) - first;  // the lane that holds this lane's page
+          const int block = __shfl_sync(0xffffffffu, id, from);
+          Token tok;
+          tok.k = __shfl_sync(0xffffffffu, mine.k, from);
+          tok.log_v = __shfl_sync(0xffffffffu, mine.log_v, from);
+          tok.inv_v = __shfl_sync(0xffffffffu, mine.inv_v, from);
+          if (!stage_free()) break;
+          uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
+          if (block >= 0 && (p & (a.block_size - 1)) == 0) {
+            const int row = (block * a.kv_heads + m.g) << shift;
+            mbar_expect_tx(&kv_full[stage], 2 * D * a.block_size);
+            tma_load_2d(kt + lane * 4 * D, &k_map, &kv_full[stage], 0, row, policy);
+            tma_load_2d(vt + lane * 4 * D, &v_map, &kv_full[stage], 0, row, policy);
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            ks[j] = vs[j] = 0.0f;
-            if (row[j] >= 0) {
-              const int page = row[j] * a.kv_heads + m.g;
-              ks[j] = __ldg(a.k_scales + page);
-              vs[j] = __ldg(a.v_scales + page);
-              row[j] = (page << shift) + (pos[j] & (a.block_size - 1));
-              pos[j] = 0;
-            } else {
-              row[j] = 0;  // some row of the pool, whose values are not used
-              pos[j] = kNone;
-            }
+            tok.pos = block >= 0 && p + j < w.length ? p + j : kNone;
+            s_tok[stage * kTile + lane * 4 + j] = tok;
           }
-        } else {
-          const int p = i * kTile + lane * 4, blk = p >> shift;
-          int id = -1;
-          if (p < w.length) {
-            id = blk < a.bt_width ? __ldg(table + blk) : -1;
-            if (id < 0 || id >= a.num_blocks) {
-              bad = true;
-              id = -1;
-            }
+          mbar_arrive(&kv_full[stage]);
+          next_stage();
+          if (fetch) {
+            scales(id_next, ks_next, vs_next);
+            fetch = false;
           }
-          const int page = id * a.kv_heads + m.g;
-          ks[0] = id >= 0 ? __ldg(a.k_scales + page) : 0.0f;
-          vs[0] = id >= 0 ? __ldg(a.v_scales + page) : 0.0f;
-          row[0] = id >= 0 ? page << shift : -1;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            pos[j] = id >= 0 && p + j < w.length ? p + j : kNone;
-            ks[j] = ks[0];
-            vs[j] = vs[0];
-          }
-        }
-        if (bad) attn_flag(IDX_DEV_BAD_PAGE);
-        Token tok[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float v = fabsf(vs[j]);
-          const float held = fmaxf(v, kLeastScale);
-          tok[j].k = ks[j] * z_unit;
-          tok[j].log_v = __log2f(held);
-          tok[j].inv_v = copysignf(1.0f / held, vs[j]);
-          tok[j].pos = pos[j];
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], phase ^ 1, kWaitNs));
-        if (!ok) break;
-        uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s_tok[stage * kTile + lane * 4 + j] = tok[j];
-        if constexpr (C::SELECT) {
-          mbar_arrive_expect_tx(&kv_full[stage], 8 * D);
-          tma_gather4(kt + lane * 4 * D, &k_map, &kv_full[stage], row[0], row[1], row[2], row[3],
-                      policy);
-          tma_gather4(vt + lane * 4 * D, &v_map, &kv_full[stage], row[0], row[1], row[2], row[3],
-                      policy);
-        } else {
-          const int in_page = (lane * 4) & (a.block_size - 1);
-          if (in_page == 0 && row[0] >= 0) {
-            mbar_arrive_expect_tx(&kv_full[stage], 2 * D * a.block_size);
-            tma_load_2d(kt + lane * 4 * D, &k_map, &kv_full[stage], 0, row[0], policy);
-            tma_load_2d(vt + lane * 4 * D, &v_map, &kv_full[stage], 0, row[0], policy);
-          } else {
-            mbar_arrive(&kv_full[stage]);
-          }
-        }
-        ++issued;
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1;
         }
       }
     }
@@ -553,6 +606,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           if (!ahead) {
             ok = mbar_wait(&kv_full[stage], phase, kWaitNs);
             if (!ok) break;
+            // (The selected rows were written by ordinary asynchronous copies.)
+            if constexpr (C::SELECT) fence_proxy_async_shared();
             tc_fence_after_sync();
             scores(tile, stage);
           }
@@ -561,6 +616,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
           ahead = false;
           if (i + 1 < w.seg_tiles && mbar_try_wait(&kv_full[next], next_phase)) {
+            if constexpr (C::SELECT) fence_proxy_async_shared();
             tc_fence_after_sync();
             scores(tile + 1, next);
             ahead = true;
@@ -619,21 +675,31 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       // ---- the rows' queries, in parts -----------------------------------------------------------
       {
         constexpr int LANES = D / 8;  // eight elements a lane
+        constexpr int PER = 128 / LANES;                       // rows at a time
+        constexpr int ROUNDS = RT > PER ? RT / PER : 1;
         const int x = (tid & (LANES - 1)) * 8;
-        for (int r = r0 + ((tid - 64 - wg * 128) / LANES); r < r0 + RT; r += 128 / LANES) {
-          Piece<T, 8> v;
-          const int2 th = slot_head<C>(a, m, r);
-          if (r < m.rows) {
-            v = load_piece<T, 8>(static_cast<const T *>(a.q) + m.b * a.q_batch + th.x * a.q_token +
-                                 th.y * a.q_head + x);
-          } else {
+        const int mine = (tid - 64 - wg * 128) / LANES;
+        Piece<T, 8> v[ROUNDS];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v.e[j] = from_f32<T>(0.0f);
+        for (int i = 0; i < ROUNDS; ++i) {
+          const int r = r0 + mine + i * PER;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i].e[j] = from_f32<T>(0.0f);
+          if (r < r0 + RT && r < m.rows) {
+            const int2 th = slot_head<C>(a, m, r);
+            v[i] = load_piece<T, 8>(static_cast<const T *>(a.q) + m.b * a.q_batch +
+                                    th.x * a.q_token + th.y * a.q_head + x);
           }
+        }
+#pragma unroll
+        for (int i = 0; i < ROUNDS; ++i) {
+          const int r = r0 + mine + i * PER;
+          if (r >= r0 + RT) break;  // (whole warps)
+          const int2 th = slot_head<C>(a, m, r);
           float f[8], amax = 0.0f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            f[j] = to_f32(v.e[j]);
+            f[j] = to_f32(v[i].e[j]);
             amax = fmaxf(amax, fabsf(f[j]));
           }
 #pragma unroll
@@ -658,6 +724,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
           if (x == 0) {
             s_rs[r] = down;
+            s_row[(seg & 1) * R + r] = (m.b * a.next_n + th.x) * a.heads + th.y;
             s_ext[r] = r >= m.rows ? 0 : C::SELECT ? 1 : max(0, len - a.next_n + th.x + 1);
           }
         }
@@ -886,12 +953,22 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             if (s_nan[u * D + dim] == seg && len - 1 - u < s_ext[r0 + r])
               acc[r] = __int_as_float(0x7FC00000);
       }
+      // The lanes' sums, a row to a lane: halves of the rows change places at each step.
+      {
+        float v[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float x = r & 1 ? sum[r / 2].y : sum[r / 2].x;
+        for (int r = 0; r < RT; ++r) v[r] = r & 1 ? sum[r / 2].y : sum[r / 2].x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) s_sum[(r0 + r) * 4 + quarter] = x;
+        for (int o = RT / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int r = 0; r < o; ++r) {
+            const float send = (lane & o) ? v[r] : v[r + o];
+            const float hold = (lane & o) ? v[r + o] : v[r];
+            v[r] = hold + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+#pragma unroll
+        for (int o = RT; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        if (lane < RT) s_sum[(r0 + lane) * 4 + quarter] = v[0];
       }
       sync_group();
       float l = 0.0f;  // lane r: the sum of row r0 + r
@@ -912,21 +989,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       }
       if (from_start && to_end) {
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        const int *rows = s_row + (seg & 1) * R + r0;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           const float f = __shfl_sync(0xffffffffu, inv, r);
-          if (r0 + r < m.rows && dim >= 0) {
-            const int2 th = slot_head<C>(a, m, r0 + r);
-            const int64_t row =
-                (static_cast<int64_t>(m.b) * a.next_n + th.x) * a.heads + th.y;
-            static_cast<T *>(a.out)[row * D + dim] = from_f32<T>(f == 0.0f ? 0.0f : acc[r] * f);
-          }
+          if (r0 + r < m.rows && dim >= 0)
+            static_cast<T *>(a.out)[static_cast<int64_t>(rows[r]) * D + dim] =
+                from_f32<T>(f == 0.0f ? 0.0f : acc[r] * f);
         }
-        if (a.lse != nullptr && quarter == 0 && lane < RT && r0 + lane < m.rows) {
-          const int2 th = slot_head<C>(a, m, r0 + lane);
-          a.lse[(static_cast<int64_t>(m.b) * a.next_n + th.x) * a.heads + th.y] =
-              l == 0.0f ? -INFINITY : (m_run + log2f(l)) * 0.6931471805599453f;
-        }
+        if (a.lse != nullptr && quarter == 0 && lane < RT && r0 + lane < m.rows)
+          a.lse[rows[lane]] = l == 0.0f ? -INFINITY : (m_run + log2f(l)) * 0.6931471805599453f;
       } else {
         float *ws = partial<C>(a, 2 * blockIdx.x + (from_start ? 1 : 0));
 #pragma unroll

@@ -106,7 +106,7 @@ struct AttentionArgs {
   float *workspace;
 };
 // sms * (CTAs on an SM) runs; the workspace is attention_workspace(...) bytes.  k_map, v_map: the
-// pools as rows of dim bytes, in boxes of block_size rows (of one row with candidates).
+// pools as rows of dim bytes, in boxes of block_size rows (not read with candidates).
 cudaError_t launch_attention_d64(const CUtensorMap &k_map, const CUtensorMap &v_map,
                                  const AttentionArgs &a, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_attention_d128(const CUtensorMap &k_map, const CUtensorMap &v_map,
