@@ -67,7 +67,10 @@ struct AttnCfg {
   static constexpr int WG = R == 64 ? 2 : 1;          // softmax warpgroups, R / WG rows each
   static constexpr int RT = R / WG;
   static constexpr int SOFT_WARPS = 4 * WG;
-  static constexpr int THREADS = 64 + 128 * WG;
+  // Warps that load: one for whole pages; up to four share the rows of a selection, as many as the
+  // softmax's registers leave room for.
+  static constexpr int LOADERS = !SELECT || R == 32 ? 1 : R == 8 ? 4 : 2;
+  static constexpr int THREADS = 32 * (LOADERS + 1 + SOFT_WARPS);
   static constexpr int COLS = 2 * NS + NO;            // two of S, one of O
   static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static constexpr int CTAS = R == 64 ? 1 : 2;        // on an SM
@@ -324,8 +327,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       prefetch_tensor_map(&v_map);
     }
     for (int i = 0; i < C::STAGES; ++i) {
-      // A lane's arrival; with SELECT also one when its copies have landed.
-      mbar_init(&kv_full[i], C::SELECT ? 64 : 32);
+      // A loading lane's arrival; with SELECT also one when its copies have landed.
+      mbar_init(&kv_full[i], C::SELECT ? 64 * C::LOADERS : 32);
       mbar_init(&kv_empty[i], 1);
     }
     mbar_init(&s_full[0], 1);
@@ -415,8 +418,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   int stage = 0;
   uint32_t phase = 0;
 
-  if (warp == 0) {
-    // ============================== producer ====================================================
+  if (warp == 0 || warp >= 2 + C::SOFT_WARPS) {
+    // ============================== loaders =====================================================
     const uint64_t policy = l2_policy_evict_first();
     const int shift = a.block_size == 32 ? 5 : a.block_size == 64 ? 6 : 7;
     const float z_unit = a.scale * 1.4426950408889634f;  // scores in units of ln 2
@@ -431,93 +434,118 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         phase ^= 1;
       }
     };
-    while (ok && w.next(a, groups, keys)) {
-      const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
-      const int32_t *table = a.block_tables + m.b * a.bt_stride;
-      if constexpr (C::SELECT) {
-        // A lane looks after tokens lane, lane + 32, ... of a tile: position, then page, then the
-        // page's scales, each read one tile further ahead than the next, so that a tile pays for
-        // one memory round trip and not for three.
-        const int2 *cand =
-            a.candidates + w.key * a.cand_stride + max(0, __ldg(a.ranges + w.key)) + lane;
-        const int extent = __ldg(a.seq_lens + m.b * a.sl_stride) - a.next_n + m.t_select + 1;
-        const int end = min((w.seg_tile + w.seg_tiles) * kTile, w.length) - lane;
-        const auto positions = [&](int tile, int (&pos)[4]) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int s = tile * kTile + 32 * j;
-            pos[j] = s < end ? __ldg(&cand[s].x) : -1;
-          }
-        };
-        // Each token's row of the pool, or -1.
-        const auto pool_rows = [&](const int (&pos)[4], int (&row)[4]) {
-          bool bad = false;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            row[j] = -1;
-            if (pos[j] >= 0 && pos[j] < extent) {
-              const int blk = pos[j] >> shift;
-              const int id = blk < a.bt_width ? __ldg(table + blk) : -1;
-              if (id >= 0 && id < a.num_blocks)
-                row[j] = ((id * a.kv_heads + m.g) << shift) + (pos[j] & (a.block_size - 1));
-              else
-                bad = true;
-            }
-          }
-          if (bad) attn_flag(IDX_DEV_BAD_PAGE);
-        };
-        const auto scales = [&](const int (&row)[4], float (&ks)[4], float (&vs)[4]) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ks[j] = row[j] >= 0 ? __ldg(a.k_scales + (row[j] >> shift)) : 0.0f;
-            vs[j] = row[j] >= 0 ? __ldg(a.v_scales + (row[j] >> shift)) : 0.0f;
-          }
-        };
-        int pos1[4], pos2[4], row0[4], row1[4];
-        float ks0[4], vs0[4], ks1[4], vs1[4];
-        positions(w.seg_tile, pos1);
-        positions(w.seg_tile + 1, pos2);
-        pool_rows(pos1, row0);
-        pool_rows(pos2, row1);
-        scales(row0, ks0, vs0);
-        // 16 bytes a lane and copy: a warp's copy is 512 / D rows of K or of V, stored with the
-        // swizzle that the products expect.  (As gathers of four rows by the TMA unit, 64 a tile, a
-        // tile took 2.1 us to issue, and the serving mix's 343 MB of selected rows 176 us.)
-        constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-        const int x = (lane % kLanes) * 16, sub = lane / kLanes;
-        for (int i = w.seg_tile; i < w.seg_tile + w.seg_tiles; ++i) {
-          positions(i + 2, pos2);
-          scales(row1, ks1, vs1);
-          if (!stage_free()) break;
-          uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 32 / kRows; ++j) {
-              const int n = j * kRows + sub;  // the token 32 q + n is lane n's q-th
-              const int row = __shfl_sync(0xffffffffu, row0[q], n);
-              if (row < 0) continue;  // (the softmax clears the value row of a token that is not)
-              const int64_t src = static_cast<int64_t>(row) * D + x;
-              const uint32_t dst = swizzled<D>(32 * q + n, x);
-              cp_async_16(kt + dst, a.k_pool + src, policy);
-              cp_async_16(vt + dst, a.v_pool + src, policy);
-            }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            s_tok[stage * kTile + lane + 32 * j] =
-                token_of(ks0[j] * z_unit, vs0[j], row0[j] >= 0 ? 0 : kNone);
-          cp_async_arrive_noinc(&kv_full[stage]);
-          mbar_arrive(&kv_full[stage]);
-          next_stage();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            row0[j] = row1[j];
-            ks0[j] = ks1[j];
-            vs0[j] = vs1[j];
-          }
-          pool_rows(pos2, row1);
+    if constexpr (C::SELECT) {
+      // A lane looks after EACH tokens of a tile, 32 apart: position, then page, then the page's
+      // scales, each read one tile further ahead than the next (segments and all), so that a tile
+      // pays for one memory round trip and not for three.
+      constexpr int EACH = 4 / C::LOADERS;
+      const int loader = warp == 0 ? 0 : warp - 1 - C::SOFT_WARPS;
+      const int token0 = loader * 32 * EACH + lane;
+      struct Ahead {
+        int pos[EACH];
+        const int32_t *table;
+        int extent, g;
+        bool live;
+      };
+      const int2 *cand = nullptr;
+      Ahead far{};
+      int slot = 0, end = 0;  // of the walk: the tile's first slot, and the segment's end
+      const auto positions = [&]() {
+        if (slot >= end) {
+          far.live = w.next(a, groups, keys);
+          if (!far.live) return;
+          const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
+          far.table = a.block_tables + m.b * a.bt_stride;
+          far.extent = __ldg(a.seq_lens + m.b * a.sl_stride) - a.next_n + m.t_select + 1;
+          far.g = m.g;
+          cand = a.candidates + w.key * a.cand_stride + max(0, __ldg(a.ranges + w.key));
+          slot = w.seg_tile * kTile;
+          end = min((w.seg_tile + w.seg_tiles) * kTile, w.length);
         }
-      } else {
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+          const int s = slot + token0 + 32 * j;
+          far.pos[j] = s < end ? __ldg(&cand[s].x) : -1;
+        }
+        slot += kTile;
+      };
+      // Each token's row of the pool, or -1.
+      const auto pool_rows = [&](int (&row)[EACH]) {
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+          row[j] = -1;
+          if (far.live && far.pos[j] >= 0 && far.pos[j] < far.extent) {
+            const int blk = far.pos[j] >> shift;
+            const int id = blk < a.bt_width ? __ldg(far.table + blk) : -1;
+            if (id >= 0 && id < a.num_blocks)
+              row[j] = ((id * a.kv_heads + far.g) << shift) + (far.pos[j] & (a.block_size - 1));
+            else
+              bad = true;
+          }
+        }
+        if (bad) attn_flag(IDX_DEV_BAD_PAGE);
+      };
+      const auto scales = [&](const int (&row)[EACH], float (&ks)[EACH], float (&vs)[EACH]) {
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+          ks[j] = row[j] >= 0 ? __ldg(a.k_scales + (row[j] >> shift)) : 0.0f;
+          vs[j] = row[j] >= 0 ? __ldg(a.v_scales + (row[j] >> shift)) : 0.0f;
+        }
+      };
+      int row0[EACH], row1[EACH];
+      float ks0[EACH], vs0[EACH], ks1[EACH], vs1[EACH];
+      positions();
+      bool live0 = far.live;
+      pool_rows(row0);
+      positions();
+      bool live1 = far.live;
+      scales(row0, ks0, vs0);
+      pool_rows(row1);
+      positions();
+      // 16 bytes a lane and copy: a warp's copy is 512 / D rows of K or of V, stored with the swizzle
+      // that the products expect.  (As gathers of four rows by the TMA unit, 64 a tile, a tile took
+      // 2.1 us to issue, and the serving mix's 343 MB of selected rows 176 us.)
+      constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+      const int x = (lane % kLanes) * 16, sub = lane / kLanes;
+      while (live0) {
+        scales(row1, ks1, vs1);
+        if (!stage_free()) break;
+        uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
+#pragma unroll
+        for (int q = 0; q < EACH; ++q)
+#pragma unroll
+          for (int j = 0; j < 32 / kRows; ++j) {
+            const int n = j * kRows + sub;  // lane n's q-th token
+            const int row = __shfl_sync(0xffffffffu, row0[q], n);
+            if (row < 0) continue;  // (the softmax clears the value row of a token that is not)
+            const int64_t src = static_cast<int64_t>(row) * D + x;
+            const uint32_t dst = swizzled<D>(token0 - lane + 32 * q + n, x);
+            cp_async_16(kt + dst, a.k_pool + src, policy);
+            cp_async_16(vt + dst, a.v_pool + src, policy);
+          }
+#pragma unroll
+        for (int j = 0; j < EACH; ++j)
+          s_tok[stage * kTile + token0 + 32 * j] =
+              token_of(ks0[j] * z_unit, vs0[j], row0[j] >= 0 ? 0 : kNone);
+        cp_async_arrive_noinc(&kv_full[stage]);
+        mbar_arrive(&kv_full[stage]);
+        next_stage();
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+          row0[j] = row1[j];
+          ks0[j] = ks1[j];
+          vs0[j] = vs1[j];
+        }
+        live0 = live1;
+        pool_rows(row1);
+        live1 = far.live;
+        if (live1) positions();
+      }
+    } else {
+      while (ok && w.next(a, groups, keys)) {
+        const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
+        const int32_t *table = a.block_tables + m.b * a.bt_stride;
         // A lane reads one page's id and scales, 32 pages ahead of the ones in hand: the ids while
         // the first tile of a batch is issued, their scales after it.
         const int n_pages = (w.length + a.block_size - 1) >> shift;
@@ -946,12 +974,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if (lane == r && ((unset >> r) & 1u) == 0) m_run = -(r & 1 ? nref[r / 2].y : nref[r / 2].x);
       // ---- the segment's result ----------------------------------------------------------------------
       // (s_rs and s_ext are not read past the barrier below: the next segment's are written then.)
-      if (!C::SELECT && a.next_n > 1 && dim >= 0) {
+      if (!C::SELECT && a.next_n > 1) {
+        for (int u = 0; u < a.next_n - 1; ++u) {
+          const bool noted = dim >= 0 && s_nan[u * D + max(dim, 0)] == seg;
+          if (!__any_sync(0xffffffffu, noted)) continue;
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-          for (int u = 0; u < a.next_n - 1; ++u)
-            if (s_nan[u * D + dim] == seg && len - 1 - u < s_ext[r0 + r])
-              acc[r] = __int_as_float(0x7FC00000);
+          for (int r = 0; r < RT; ++r)
+            if (noted && len - 1 - u < s_ext[r0 + r]) acc[r] = __int_as_float(0x7FC00000);
+        }
       }
       // The lanes' sums, a row to a lane: halves of the rows change places at each step.
       {
