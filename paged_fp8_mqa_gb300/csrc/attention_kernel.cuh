@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
            *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *drain = q_full + 1;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(drain + 1);
   __shared__ int64_t s_scan[C::THREADS / 32];
-  __shared__ int64_t s_begin[2];  // the run's first tile within its key; tiles in the run
+  __shared__ int64_t s_begin;  // the run's first tile within its key
   __shared__ int s_key;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -374,31 +374,27 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   total *= groups;
   // (No more runs than tiles: a group's parts lie in consecutive CTAs.)
   const int64_t runs = max(static_cast<int64_t>(1), min(total, static_cast<int64_t>(gridDim.x)));
-  const int64_t f0 = blockIdx.x < runs ? total * blockIdx.x / runs : total;
-  const int64_t f1 = blockIdx.x < runs ? total * (blockIdx.x + 1) / runs : total;
+  int64_t f0 = total, f1 = total;
+  if (blockIdx.x < runs) {
+    if (total < (1 << 21)) {  // (32-bit divisions are a tenth of the 64-bit ones)
+      const uint32_t n = static_cast<uint32_t>(total), c = static_cast<uint32_t>(runs);
+      f0 = n * blockIdx.x / c;
+      f1 = n * (blockIdx.x + 1) / c;
+    } else {
+      f0 = total * blockIdx.x / runs;
+      f1 = total * (blockIdx.x + 1) / runs;
+    }
+  }
   if (f0 < f1 && f0 >= before * groups && f0 < (before + mine) * groups) {
     for (int k = k_lo; k < k_hi; ++k) {
       const int n = tiles_for(key_length<C::SELECT>(a, k));
       if (f0 < (before + n) * groups) {
         s_key = k;
-        s_begin[0] = f0 - before * groups;
+        s_begin = f0 - before * groups;
         break;
       }
       before += n;
     }
-  }
-  // Keys without positions: their rows are zeros, their groups have no parts.
-  for (int k = blockIdx.x; k < keys; k += gridDim.x) {
-    if (key_length<C::SELECT>(a, k) > 0) continue;
-    for (int g = tid; g < groups; g += C::THREADS)
-      parts[static_cast<int64_t>(k) * groups + g] = GroupParts{0, 0};
-    const int slots = C::SELECT ? 1 : a.next_n;
-    const int64_t row0 = static_cast<int64_t>(k) * slots * a.heads;
-    T *out = static_cast<T *>(a.out) + row0 * D;
-    for (int i = tid; i < slots * a.heads * D / 8; i += C::THREADS)
-      reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse != nullptr)
-      for (int i = tid; i < slots * a.heads; i += C::THREADS) a.lse[row0 + i] = -INFINITY;
   }
   __syncthreads();
 
@@ -410,8 +406,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     w.key = s_key;
     w.length = key_length<C::SELECT>(a, w.key);
     w.tiles = tiles_for(w.length);
-    w.group = static_cast<int>(s_begin[0] / w.tiles);
-    w.tile = static_cast<int>(s_begin[0] - static_cast<int64_t>(w.group) * w.tiles);
+    const int64_t at0 = s_begin;
+    w.group = at0 < INT_MAX ? static_cast<int>(at0) / w.tiles : static_cast<int>(at0 / w.tiles);
+    w.tile = static_cast<int>(at0 - static_cast<int64_t>(w.group) * w.tiles);
   }
   bool ok = true;
   uint32_t issued = 0;  // producer: tiles whose copies were started; MMA: nothing
@@ -496,20 +493,17 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       int row0[EACH], row1[EACH];
       float ks0[EACH], vs0[EACH], ks1[EACH], vs1[EACH];
       positions();
-      bool live0 = far.live;
+      bool live0 = far.live, live1 = false, primed = false;
       pool_rows(row0);
-      positions();
-      bool live1 = far.live;
       scales(row0, ks0, vs0);
-      pool_rows(row1);
-      positions();
+      if (live0) positions();
       // 16 bytes a lane and copy: a warp's copy is 512 / D rows of K or of V, stored with the swizzle
       // that the products expect.  (As gathers of four rows by the TMA unit, 64 a tile, a tile took
       // 2.1 us to issue, and the serving mix's 343 MB of selected rows 176 us.)
       constexpr int kLanes = D / 16, kRows = 32 / kLanes;
       const int x = (lane % kLanes) * 16, sub = lane / kLanes;
       while (live0) {
-        scales(row1, ks1, vs1);
+        if (primed) scales(row1, ks1, vs1);
         if (!stage_free()) break;
         uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
 #pragma unroll
@@ -524,6 +518,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             cp_async_16(kt + dst, a.k_pool + src, policy);
             cp_async_16(vt + dst, a.v_pool + src, policy);
           }
+        if (!primed) {  // (the first tile's copies go out before anything waits for the second's ids)
+          primed = true;
+          pool_rows(row1);
+          live1 = far.live;
+          if (live1) positions();
+          scales(row1, ks1, vs1);
+        }
 #pragma unroll
         for (int j = 0; j < EACH; ++j)
           s_tok[stage * kTile + token0 + 32 * j] =
@@ -1013,7 +1014,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         int n = 1;
         if (!to_end) {
           const int64_t x = f1 - 1 + (w.tiles - (w.seg_tile + w.seg_tiles));
-          n = static_cast<int>(((x + 1) * runs - 1) / total) - static_cast<int>(blockIdx.x) + 1;
+          const int64_t y = (x + 1) * runs - 1;
+          n = (y < INT_MAX ? static_cast<int>(y) / static_cast<int>(total)
+                           : static_cast<int>(y / total)) -
+              static_cast<int>(blockIdx.x) + 1;
         }
         parts[gid] = GroupParts{static_cast<int>(blockIdx.x), n};
       }
@@ -1042,6 +1046,20 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     }
   }
 
+  // Keys without positions: their rows are zeros, their groups have no parts.
+  for (int k = blockIdx.x; k < keys; k += gridDim.x) {
+    if (key_length<C::SELECT>(a, k) > 0) continue;
+    for (int g = tid; g < groups; g += C::THREADS)
+      parts[static_cast<int64_t>(k) * groups + g] = GroupParts{0, 0};
+    const int slots = C::SELECT ? 1 : a.next_n;
+    const int64_t row0 = static_cast<int64_t>(k) * slots * a.heads;
+    T *out = static_cast<T *>(a.out) + row0 * D;
+    for (int i = tid; i < slots * a.heads * D / 8; i += C::THREADS)
+      reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse != nullptr)
+      for (int i = tid; i < slots * a.heads; i += C::THREADS) a.lse[row0 + i] = -INFINITY;
+  }
+
   // ---- teardown ----------------------------------------------------------------------------------
   if (__syncthreads_or(!ok)) {
     // A wait gave up: let the copies and products in flight end before the memory is given back.
@@ -1065,11 +1083,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 constexpr int kJoinThreads = 256;
 
 // Joins the parts of one group's rows: block (group, y) takes rows y, y + gridDim.y, ...; its
-// warps share a row's parts, and the warps' sums are added in order.
+// warps share a row's parts, eight at a time (their maxima, sums and vectors read at once, none
+// waiting for another), and the warps' results are joined in order.
 template <class C, typename T>
 __global__ void __launch_bounds__(kJoinThreads)
     k_attention_join(const AttentionArgs a, const AttnSplit split, const GroupParts *parts) {
-  constexpr int D = C::D, R = C::R, W = kJoinThreads / 32, E = D / 32;
+  constexpr int D = C::D, R = C::R, W = kJoinThreads / 32, E = D / 32, AT_ONCE = 8;
   __shared__ float s_o[W][D], s_m[W], s_l[W];
   griddep_wait();
   griddep_launch_dependents();
@@ -1082,42 +1101,61 @@ __global__ void __launch_bounds__(kJoinThreads)
                               split.chunks, split.chunk_rows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int r = blockIdx.y; r < m.rows; r += gridDim.y) {
-    float top = -INFINITY;
-    for (int i = threadIdx.x; i < p.parts; i += kJoinThreads) {
-      const float *ws = partial<C>(a, 2 * (p.cta + i) + (i == 0));
-      top = fmaxf(top, ws[R * D + r]);
-    }
-    top = warp_max(top);
-    if (lane == 0) s_m[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < W; ++x) top = fmaxf(top, s_m[x]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float o[E], l = 0.0f;
+    float top = kRefNone, l = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-#pragma unroll 4
-    for (int i = warp; i < p.parts; i += W) {
-      const float *ws = partial<C>(a, 2 * (p.cta + i) + (i == 0));
-      const float f = fast_exp2(ws[R * D + r] - ref);
-      l += f * ws[R * D + R + r];
-      const Piece<float, E> v = load_piece<float, E>(ws + r * D + lane * E);
+    for (int i0 = warp; i0 < p.parts; i0 += W * AT_ONCE) {
+      float pm[AT_ONCE], pl[AT_ONCE];
+      Piece<float, E> v[AT_ONCE];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * v.e[e];
+      for (int j = 0; j < AT_ONCE; ++j) {
+        const int i = i0 + j * W;
+        pm[j] = kRefNone;
+        pl[j] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[j].e[e] = 0.0f;
+        if (i < p.parts) {
+          const float *ws = partial<C>(a, 2 * (p.cta + i) + (i == 0));
+          pm[j] = ws[R * D + r];
+          pl[j] = ws[R * D + R + r];
+          v[j] = load_piece<float, E>(ws + r * D + lane * E);
+        }
+      }
+      float now = top;
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j) now = fmaxf(now, pm[j]);
+      const float keep = fast_exp2(top - now);
+      top = now;
+      l *= keep;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= keep;
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j) {
+        const float f = fast_exp2(pm[j] - now);
+        l += f * pl[j];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += f * v[j].e[e];
+      }
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-    if (lane == 0) s_l[warp] = l;
+    if (lane == 0) {
+      s_m[warp] = top;
+      s_l[warp] = l;
+    }
     __syncthreads();
-    const int2 th = slot_head<C>(a, m, r);
-    const int64_t row = (static_cast<int64_t>(m.b) * a.next_n + th.x) * a.heads + th.y;
     if (threadIdx.x < D) {
+#pragma unroll
+      for (int y = 0; y < W; ++y) top = fmaxf(top, s_m[y]);
       float x = 0.0f, all = 0.0f;
 #pragma unroll
       for (int y = 0; y < W; ++y) {
-        x += s_o[y][threadIdx.x];
-        all += s_l[y];
+        const float f = fast_exp2(s_m[y] - top);
+        x += f * s_o[y][threadIdx.x];
+        all += f * s_l[y];
       }
+      const int2 th = slot_head<C>(a, m, r);
+      const int64_t row = (static_cast<int64_t>(m.b) * a.next_n + th.x) * a.heads + th.y;
       static_cast<T *>(a.out)[row * D + threadIdx.x] = from_f32<T>(all == 0.0f ? 0.0f : x / all);
       if (a.lse != nullptr && threadIdx.x == 0)
         a.lse[row] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
@@ -1160,7 +1198,8 @@ cudaError_t launch_cfg(const CUtensorMap &k_map, const CUtensorMap &v_map, const
   if (e != cudaSuccess) return e;
   const int64_t groups = static_cast<int64_t>(C::SELECT ? a.batch * a.next_n : a.batch) *
                          a.kv_heads * s.chunks;
-  const int64_t spread = (2 * sms + groups - 1) / groups;
+  // A row a block while that is at most eight blocks an SM (groups that were not cut leave at once).
+  const int64_t spread = (8 * sms + groups - 1) / groups;
   const int y = static_cast<int>(spread < s.chunk_rows ? spread : s.chunk_rows);
   return launch_dependent(k_attention_join<C, T>, dim3(static_cast<unsigned>(groups), y),
                           dim3(kJoinThreads), 0, stream, a, split, parts);
