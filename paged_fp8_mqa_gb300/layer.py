@@ -82,6 +82,7 @@ def idx_attention_fp8(*args) -> int:
 # ---- torch-facing marshalling ------------------------------------------------------------------
 
 _codes: dict = {}
+_sizes: dict = {}
 
 
 def _code(dtype):
@@ -100,77 +101,114 @@ def _check(status: int) -> None:
         raise IdxError(status, idx_last_error())
 
 
-def _tensor(t, name, dims, dtype=None, device=None):
-    """A CUDA tensor (of the first argument's device) with `dims` dimensions."""
+def _index(t, name):
+    """The device index of a CUDA tensor."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    return t.get_device()
+
+
+def _tensor(t, name, dims, dtype, index):
+    """A CUDA tensor of dtype on device `index` with `dims` dimensions.  (One test for the usual
+    case: a call's checks are a good part of its time on the host.)"""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.dim() == dims:
+            return
+    except AttributeError:
+        pass
+    if _index(t, name) != index:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{index}")
+    if t.dtype != dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dims, got {t.dim()}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
-def _rows(t, name, dims, device=None):
-    """Rows of float32, float16 or bfloat16 elements with unit element stride: their dtype code."""
-    _tensor(t, name, dims, None, device)
+def _rows(t, name, dims, index):
+    """Rows of float32, float16 or bfloat16 elements with unit element stride: their dtype code and
+    strides."""
+    if _index(t, name) != index:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{index}")
     code = _code(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if len(strides) != dims:
+        raise ValueError(f"{name} must have {dims} dims, got {len(strides)}")
+    if strides[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} rows must be contiguous")
-    return code
+    return code, strides
 
 
-def _pool8(t, name, dims, device):
-    """e4m3 values (or their uint8 view), contiguous."""
+def _pool8(t, name, dims, index):
+    """e4m3 values (or their uint8 view), contiguous: their address."""
     import torch
-    _tensor(t, name, dims, None, device)
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-        raise TypeError(f"{name} must be float8_e4m3fn (or its uint8 view), got {t.dtype}")
+    raw = getattr(t, "dtype", None) is torch.uint8
+    _tensor(t, name, dims, torch.uint8 if raw else torch.float8_e4m3fn, index)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _on(stream, device, *allocated):
+def _scales(t, name, shape, index):
+    """A pool's float32 scales [blocks, Hkv]: their address."""
+    import torch
+    _tensor(t, name, 2, torch.float32, index)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [blocks, Hkv]")
+    return t.data_ptr()
+
+
+def _on(stream, index, *allocated):
     """The raw stream to launch on; tensors allocated for another stream's work are recorded."""
     import torch
-    current = torch.cuda.current_stream(device)
     if stream is None:
-        return current.cuda_stream
-    if stream != current:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream != torch.cuda.current_stream(index):
         for t in allocated:
             t.record_stream(stream)
     return stream.cuda_stream
 
 
-def _table(table, device):
+def _table(table, index):
     """(pointer, max_positions, rot_dim) of a rotary table, or of none."""
     import torch
     if table is None:
         return None, 0, 0
-    _tensor(table, "table", 3, torch.float32, device)
-    if table.shape[2] != 2 or not table.is_contiguous():
+    _tensor(table, "table", 3, torch.float32, index)
+    most, half, two = table.shape
+    if two != 2 or not table.is_contiguous():
         raise ValueError("table must be contiguous [max_positions, rot_dim / 2, 2]")
-    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+    return table.data_ptr(), most, 2 * half
 
 
-def _tokens(block_tables, seq_lens, token_starts, rows, device):
+def _requests(block_tables, seq_lens, batch, index):
+    """The arguments of a batch's pages: (block_tables, row stride, width, seq_lens, stride)."""
+    import torch
+    _tensor(block_tables, "block_tables", 2, torch.int32, index)
+    _tensor(seq_lens, "seq_lens", 1, torch.int32, index)
+    rows, width = block_tables.shape
+    if batch is None:
+        batch = rows
+    if rows != batch or seq_lens.shape[0] != batch:
+        raise ValueError("block_tables and seq_lens must have a row for each request")
+    row_stride, unit = block_tables.stride()
+    if width > 1 and unit != 1:
+        raise ValueError("block_tables rows must be contiguous (stride(1) == 1)")
+    return (block_tables.data_ptr(), max(row_stride, width), width, seq_lens.data_ptr(),
+            max(seq_lens.stride(0), 1))
+
+
+def _tokens(block_tables, seq_lens, token_starts, rows, index):
     """The arguments that place new tokens: (starts, seq_lens, stride, batch, next_n, tables, row
     stride, width)."""
     import torch
-    _tensor(block_tables, "block_tables", 2, torch.int32, device)
-    _tensor(seq_lens, "seq_lens", 1, torch.int32, device)
-    batch, width = block_tables.shape
-    if seq_lens.shape[0] != batch:
-        raise ValueError("block_tables and seq_lens must have a row for each request")
-    if width > 1 and block_tables.stride(1) != 1:
-        raise ValueError("block_tables rows must be contiguous (stride(1) == 1)")
+    tables, row_stride, width, lens, stride = _requests(block_tables, seq_lens, None, index)
+    batch = seq_lens.shape[0]
     starts, next_n = None, 0
     if token_starts is not None:
-        _tensor(token_starts, "token_starts", 1, torch.int32, device)
+        _tensor(token_starts, "token_starts", 1, torch.int32, index)
         if token_starts.shape[0] != batch + 1 or not token_starts.is_contiguous():
             raise ValueError("token_starts must be contiguous, one more than the requests")
         starts = token_starts.data_ptr()
@@ -178,8 +216,7 @@ def _tokens(block_tables, seq_lens, token_starts, rows, device):
         next_n = rows // batch
         if next_n * batch != rows:
             raise ValueError("without token_starts every request has the same number of tokens")
-    return (starts, seq_lens.data_ptr(), max(seq_lens.stride(0), 1), batch, next_n,
-            block_tables.data_ptr(), max(block_tables.stride(0), width), width)
+    return starts, lens, stride, batch, next_n, tables, row_stride, width
 
 
 def rotary_table(max_positions: int, rot_dim: int, *, base: float = 10000.0, scaling: str = "none",
@@ -201,7 +238,7 @@ def rotary_table(max_positions: int, rot_dim: int, *, base: float = 10000.0, sca
     with torch.cuda.device(device):
         table = torch.empty(max_positions, rot_dim // 2, 2, dtype=torch.float32, device=device)
         _check(idx_rotary_table(freq, magnitude.value, max_positions, rot_dim, table.data_ptr(),
-                                _on(stream, table.device, table)))
+                                _on(stream, table.get_device(), table)))
     return table
 
 
@@ -212,28 +249,30 @@ def rotary(x, positions, table, *, interleaved: bool = False, rot_offset: int = 
     angles of ``table`` (see ``rotary_table``), in halves or in interleaved pairs.  ``out=x``
     rotates in place; ``inverse`` turns back (the gradient with respect to x)."""
     import torch
-    code = _rows(x, "x", 3)
-    dev = x.device
-    _tensor(positions, "positions", 1, torch.int32, dev)
+    index = _index(x, "x")
+    code, (x_token, x_head, _) = _rows(x, "x", 3, index)
+    _tensor(positions, "positions", 1, torch.int32, index)
     T, H, D = x.shape
     if positions.shape[0] != T or not positions.is_contiguous():
         raise ValueError("positions must be contiguous, one for each token of x")
-    tab, most, rot = _table(table, dev)
+    tab, most, rot = _table(table, index)
     if tab is None:
         raise TypeError("table must be a CUDA tensor")
     made = ()
     if out is None:
-        out = torch.empty(T, H, D, dtype=x.dtype, device=dev)
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
         made = (out,)
+        o_token, o_head = H * D, D
     else:
-        _tensor(out, "out", 3, x.dtype, dev)
+        _tensor(out, "out", 3, x.dtype, index)
         if out.shape != x.shape or (D > 1 and out.stride(2) != 1):
             raise ValueError("out must have the shape of x and contiguous rows")
-    if out.numel() == 0:
+        o_token, o_head, _ = out.stride()
+    if not (T and H and D):
         return out
-    _check(idx_rotary(x.data_ptr(), x.stride(0), x.stride(1), positions.data_ptr(), T, H, D, code,
-                      tab, most, rot, rot_offset, interleaved, inverse, out.data_ptr(),
-                      out.stride(0), out.stride(1), _on(stream, dev, *made)))
+    _check(idx_rotary(x.data_ptr(), x_token, x_head, positions.data_ptr(), T, H, D, code, tab, most,
+                      rot, rot_offset, interleaved, inverse, out.data_ptr(), o_token, o_head,
+                      _on(stream, index, *made)))
     return out
 
 
@@ -249,48 +288,50 @@ def index_prepare(k, kv_fused, block_tables, seq_lens, *, token_starts=None, q=N
     and quantised likewise, its scales folded into the weights: returns (q e4m3 [T, H, D],
     weights float32 [T, H]), which ``logits_fp8`` takes (q viewed as [B, next_n, H, D])."""
     import torch
-    code = _rows(k, "k", 2)
-    dev = k.device
+    index = _index(k, "k")
+    code, (k_token, _) = _rows(k, "k", 2, index)
     T, D = k.shape
-    _tensor(kv_fused, "kv_fused", kv_fused.dim() if isinstance(kv_fused, torch.Tensor) else 2,
-            torch.uint8, dev)
+    if _index(kv_fused, "kv_fused") != index or kv_fused.dtype is not torch.uint8:
+        raise TypeError("kv_fused must be a uint8 tensor on the device of k")
     blocks = kv_fused.shape[0] if kv_fused.dim() else 0
-    if not kv_fused.is_contiguous() or blocks == 0:
+    if blocks == 0 or not kv_fused.is_contiguous():
         raise ValueError("kv_fused must be contiguous with a leading dim of blocks")
     block_size, rest = divmod(kv_fused.numel() // blocks, D + 4)
     if rest:
         raise ValueError(f"kv_fused blocks must be block_size * (D + 4) bytes, D = {D}")
     H, made = 0, []
-    qa = (None, 0, 0, None, 0)
+    q_args, q_to, w_to = (None, 0, 0, None, 0), None, None
     if q is not None:
-        if _rows(q, "q", 3, dev) != code:
+        q_code, (q_token, q_head, _) = _rows(q, "q", 3, index)
+        if q_code != code:
             raise TypeError("q and k must have the same dtype")
-        _tensor(weights, "weights", 2, torch.float32, dev)
+        _tensor(weights, "weights", 2, torch.float32, index)
         H = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != D or weights.shape[0] != T or weights.shape[1] != H:
+        w_token, w_head = weights.stride()
+        if q.shape != (T, H, D) or weights.shape != (T, H):
             raise ValueError("q must be [T, H, D] and weights [T, H] for k [T, D]")
-        if H > 1 and weights.stride(1) != 1:
+        if H > 1 and w_head != 1:
             raise ValueError("weights rows must be contiguous")
         if q_out is None:
-            q_out = torch.empty(T, H, D, dtype=torch.float8_e4m3fn, device=dev)
+            q_out = torch.empty((T, H, D), dtype=torch.float8_e4m3fn, device=k.device)
             made.append(q_out)
         if weights_out is None:
-            weights_out = torch.empty(T, H, dtype=torch.float32, device=dev)
+            weights_out = torch.empty((T, H), dtype=torch.float32, device=k.device)
             made.append(weights_out)
-        _pool8(q_out, "q_out", 3, dev)
-        _tensor(weights_out, "weights_out", 2, torch.float32, dev)
+        q_to = _pool8(q_out, "q_out", 3, index)
+        _tensor(weights_out, "weights_out", 2, torch.float32, index)
         if q_out.shape != q.shape or weights_out.shape != weights.shape \
                 or not weights_out.is_contiguous():
             raise ValueError("q_out and weights_out must be contiguous with the shapes of q and "
                              "weights")
-        qa = (q.data_ptr(), q.stride(0), q.stride(1), weights.data_ptr(), weights.stride(0))
-    place = _tokens(block_tables, seq_lens, token_starts, T, dev)
+        w_to = weights_out.data_ptr()
+        q_args = (q.data_ptr(), q_token, q_head, weights.data_ptr(), w_token)
+    place = _tokens(block_tables, seq_lens, token_starts, T, index)
     if T and (q is None or H):
         _check(idx_index_prepare(
-            k.data_ptr(), k.stride(0), *qa, code, T, H, D, *_table(table, dev), rot_offset,
-            interleaved, *place, block_size, blocks, kv_fused.data_ptr(),
-            None if q is None else q_out.data_ptr(),
-            None if q is None else weights_out.data_ptr(), _on(stream, dev, *made)))
+            k.data_ptr(), k_token, *q_args, code, T, H, D, *_table(table, index), rot_offset,
+            interleaved, *place, block_size, blocks, kv_fused.data_ptr(), q_to, w_to,
+            _on(stream, index, *made)))
     return None if q is None else (q_out, weights_out)
 
 
@@ -301,29 +342,24 @@ def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, 
     e4m3 [blocks, Hkv, block_size, D], scales float32 [blocks, Hkv] (powers of two).  The T rows
     are placed as in ``index_prepare``.  A block that already holds tokens keeps its scale while
     the new ones fit it; otherwise the scale grows and what it holds is rescaled."""
-    import torch
-    code = _rows(k, "k", 3)
-    dev = k.device
-    if _rows(v, "v", 3, dev) != code or v.shape != k.shape:
+    index = _index(k, "k")
+    code, (k_token, k_head, _) = _rows(k, "k", 3, index)
+    v_code, (v_token, v_head, _) = _rows(v, "v", 3, index)
+    shape = T, H, D = k.shape
+    if v_code != code or v.shape != shape:
         raise TypeError("k and v must have the same dtype and shape")
-    T, H, D = k.shape
-    _pool8(k_pool, "k_pool", 4, dev)
-    _pool8(v_pool, "v_pool", 4, dev)
-    _tensor(k_scales, "k_scales", 2, torch.float32, dev)
-    _tensor(v_scales, "v_scales", 2, torch.float32, dev)
+    pools = _pool8(k_pool, "k_pool", 4, index), _pool8(v_pool, "v_pool", 4, index)
     blocks, heads, block_size, dim = k_pool.shape
-    if v_pool.shape != k_pool.shape or heads != H or dim != D:
+    if heads != H or dim != D or v_pool.shape != k_pool.shape:
         raise ValueError("k_pool and v_pool must be [blocks, Hkv, block_size, D] for k [T, Hkv, D]")
-    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        if t.shape != k_pool.shape[:2] or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous [blocks, Hkv]")
-    place = _tokens(block_tables, seq_lens, token_starts, T, dev)
+    scales = (_scales(k_scales, "k_scales", (blocks, H), index),
+              _scales(v_scales, "v_scales", (blocks, H), index))
+    place = _tokens(block_tables, seq_lens, token_starts, T, index)
     if T and H:
         _check(idx_kv_append(
-            k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), code,
-            T, H, D, *_table(table, dev), rot_offset, interleaved, *place, block_size, blocks,
-            k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-            _on(stream, dev)))
+            k.data_ptr(), k_token, k_head, v.data_ptr(), v_token, v_head, code, T, H, D,
+            *_table(table, index), rot_offset, interleaved, *place, block_size, blocks, *pools,
+            *scales, _on(stream, index)))
 
 
 def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,
@@ -338,67 +374,68 @@ def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
     least idx_attention_workspace_bytes) is allocated if not given.  Returns out, contiguous
     [B, next_n, H, D] in q's dtype."""
     import torch
-    _tensor(q, "q", 4)
-    dev = q.device
-    if q.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"q must be float16 or bfloat16, got {q.dtype}")
-    B, n, H, D = q.shape
-    if q.stride(3) != 1 and D > 1:
+    index = _index(q, "q")
+    dtype = q.dtype
+    code = _code(dtype)
+    if code is None or dtype is torch.float32:
+        raise TypeError(f"q must be float16 or bfloat16, got {dtype}")
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q must have 4 dims, got {len(shape)}")
+    B, n, H, D = shape
+    q_batch, q_token, q_head, q_unit = q.stride()
+    if q_unit != 1 and D > 1:
         raise ValueError("q rows must be contiguous")
-    _pool8(k_pool, "k_pool", 4, dev)
-    _pool8(v_pool, "v_pool", 4, dev)
+    pools = _pool8(k_pool, "k_pool", 4, index), _pool8(v_pool, "v_pool", 4, index)
     blocks, kv_heads, block_size, dim = k_pool.shape
-    if v_pool.shape != k_pool.shape or dim != D:
+    if dim != D or v_pool.shape != k_pool.shape:
         raise ValueError("k_pool and v_pool must be [blocks, Hkv, block_size, D] for q's D")
-    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        _tensor(t, name, 2, torch.float32, dev)
-        if t.shape != k_pool.shape[:2] or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous [blocks, Hkv]")
-    _tensor(block_tables, "block_tables", 2, torch.int32, dev)
-    _tensor(seq_lens, "seq_lens", 1, torch.int32, dev)
-    width = block_tables.shape[1]
-    if block_tables.shape[0] != B or seq_lens.shape[0] != B:
-        raise ValueError("block_tables and seq_lens must have a row for each request")
-    if width > 1 and block_tables.stride(1) != 1:
-        raise ValueError("block_tables rows must be contiguous (stride(1) == 1)")
-    sel = (None, 0, None)
+    scales = (_scales(k_scales, "k_scales", (blocks, kv_heads), index),
+              _scales(v_scales, "v_scales", (blocks, kv_heads), index))
+    pages = _requests(block_tables, seq_lens, B, index)
+    cand, slots, cand_ranges = None, 0, None
     if candidates is not None:
-        _tensor(candidates, "candidates", 3, torch.int32, dev)
+        _tensor(candidates, "candidates", 3, torch.int32, index)
         if ranges is None:
             raise ValueError("ranges is required with candidates")
-        _tensor(ranges, "ranges", 2, torch.int32, dev)
-        if candidates.shape[0] != B * n or candidates.shape[2] != 2 \
-                or not candidates.is_contiguous():
+        _tensor(ranges, "ranges", 2, torch.int32, index)
+        rows, slots, pair = candidates.shape
+        if rows != B * n or pair != 2 or not candidates.is_contiguous():
             raise ValueError("candidates must be contiguous [B * next_n, slots, 2]")
-        if ranges.shape[0] != 2 or ranges.shape[1] != B * n or not ranges.is_contiguous():
+        if ranges.shape != (2, rows) or not ranges.is_contiguous():
             raise ValueError("ranges must be contiguous [2, B * next_n]")
-        sel = (candidates.data_ptr(), candidates.shape[1], ranges.data_ptr())
+        cand, cand_ranges = candidates.data_ptr(), ranges.data_ptr()
     made = []
     if out is None:
-        out = torch.empty(B, n, H, D, dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
         made.append(out)
     else:
-        _tensor(out, "out", 4, q.dtype, dev)
-        if out.shape != q.shape or not out.is_contiguous():
+        _tensor(out, "out", 4, dtype, index)
+        if out.shape != shape or not out.is_contiguous():
             raise ValueError("out must be contiguous with the shape of q")
+    lse_to = None
     if lse is not None:
-        _tensor(lse, "lse", 3, torch.float32, dev)
-        if lse.shape != q.shape[:3] or not lse.is_contiguous():
+        _tensor(lse, "lse", 3, torch.float32, index)
+        if lse.shape != shape[:3] or not lse.is_contiguous():
             raise ValueError("lse must be contiguous [B, next_n, H]")
-    if out.numel() == 0:
+        lse_to = lse.data_ptr()
+    if not (B and n and H and D):
         return out
     if workspace is None:
-        need = idx_attention_workspace_bytes(B, n, H, kv_heads, D, num_sms)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        sizes = (index, B, n, H, kv_heads, D, num_sms)
+        need = _sizes.get(sizes)
+        if need is None:
+            need = idx_attention_workspace_bytes(*sizes[1:])
+            if len(_sizes) < 4096:
+                _sizes[sizes] = need
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
         made.append(workspace)
     else:
-        _tensor(workspace, "workspace", 1, torch.uint8, dev)
+        _tensor(workspace, "workspace", 1, torch.uint8, index)
+        need = workspace.shape[0]
     _check(idx_attention_fp8(
-        q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), _code(q.dtype), k_pool.data_ptr(),
-        v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), blocks, block_size,
-        block_tables.data_ptr(), max(block_tables.stride(0), width), width, seq_lens.data_ptr(),
-        max(seq_lens.stride(0), 1), B, n, H, kv_heads, D,
-        D ** -0.5 if softmax_scale is None else softmax_scale, *sel, num_sms, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        _on(stream, dev, *made)))
+        q.data_ptr(), q_batch, q_token, q_head, code, *pools, *scales, blocks, block_size, *pages,
+        B, n, H, kv_heads, D, D ** -0.5 if softmax_scale is None else softmax_scale, cand, slots,
+        cand_ranges, num_sms, out.data_ptr(), lse_to, workspace.data_ptr(), need,
+        _on(stream, index, *made)))
     return out
