@@ -104,18 +104,6 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t four, float f) {
   return e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
 }
 
-template <int V>
-__device__ __forceinline__ void store_e4m3(uint8_t *dst, const float (&v)[V], float inv) {
-  if constexpr (V == 1) {
-    *dst = static_cast<uint8_t>(e4m3x4(v[0] * inv, 0.0f, 0.0f, 0.0f));
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<uint32_t *>(dst + i) =
-          e4m3x4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
-  }
-}
-
 // One item: a block of one head of K or of V.  GROUP = 32: a warp of its own (a few new tokens);
 // GROUP = kThreads: the whole CTA (long runs of tokens).  The new tokens are read once for the
 // largest magnitude and, from L1, once more to be written.
@@ -145,9 +133,8 @@ __device__ __forceinline__ void append_item(const AppendArgs &a, const Unit &u, 
   for (int i = tid; i < n; i += GROUP) {
     float v[V];
     const int tk = i / kPer, d = (i % kPer) * V;
-    load_turned<T, V>(x + tk * token, d, a.r, row(tk), v);
-#pragma unroll
-    for (int e = 0; e < V; ++e) amax = fmaxf(amax, finite_abs(v[e]));
+    turned<T, V>(load_piece<T, V>(x + tk * token + d), x + tk * token, d, a.r, row(tk), v);
+    amax = largest_finite(v, amax);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -172,7 +159,7 @@ __device__ __forceinline__ void append_item(const AppendArgs &a, const Unit &u, 
   for (int i = tid; i < n; i += GROUP) {
     float v[V];
     const int tk = i / kPer, d = (i % kPer) * V;
-    load_turned<T, V>(x + tk * token, d, a.r, row(tk), v);
+    turned<T, V>(load_piece<T, V>(x + tk * token + d), x + tk * token, d, a.r, row(tk), v);
     store_e4m3<V>(block + (off0 + tk) * D + d, v, inv);
   }
 }
@@ -180,7 +167,7 @@ __device__ __forceinline__ void append_item(const AppendArgs &a, const Unit &u, 
 template <typename T, int V, int D, int GROUP>
 __global__ void __launch_bounds__(kThreads) k_kv_append(const AppendArgs a) {
   __shared__ int s_warp[kWarps];
-  __shared__ float s_max[kWarps];
+  __shared__ float s_max[2][kWarps];
   __shared__ Unit s_unit;
   griddep_wait();
   griddep_launch_dependents();
@@ -202,9 +189,11 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const AppendArgs a) {
     if (threadIdx.x == 0) atomicOr(&g_append_status, IDX_DEV_BAD_PAGE);
     return;
   }
-  const int item = GROUP == 32 ? blockIdx.y * kWarps + (threadIdx.x >> 5) : blockIdx.y;
-  if (item >= 2 * a.heads) return;
-  append_item<T, V, D, GROUP>(a, u, id, item >> 1, (item & 1) == 0, s_max);
+  const int warps = GROUP == 32 ? kWarps : 1;
+  int set = 0;  // (two sets of maxima: a fast warp may be an item ahead)
+  for (int item = blockIdx.y * warps + (GROUP == 32 ? threadIdx.x >> 5 : 0); item < 2 * a.heads;
+       item += gridDim.y * warps, set ^= 1)
+    append_item<T, V, D, GROUP>(a, u, id, item >> 1, (item & 1) == 0, s_max[set]);
 }
 
 template <typename T, int V, int D>
@@ -224,9 +213,12 @@ cudaError_t launch_dim(const AppendArgs &a, cudaStream_t stream) {
   // Every request touches at most (its tokens) / bs + 2 blocks, and no more than its tokens.
   const int64_t most = a.m.tokens / bs + 2 * static_cast<int64_t>(a.m.batch);
   const int64_t units = most < a.m.tokens ? most : a.m.tokens;
-  return launch_dependent(k_kv_append<T, V, D, kThreads>,
-                          dim3(static_cast<unsigned>(units), 2 * a.heads), dim3(kThreads), 0,
-                          stream, a);
+  // An item a CTA, until there are some thousands of CTAs; then several, one after the other, which
+  // share the search for their block.
+  int y = 2 * a.heads;
+  while (y % 2 == 0 && units * y > 4096) y /= 2;
+  return launch_dependent(k_kv_append<T, V, D, kThreads>, dim3(static_cast<unsigned>(units), y),
+                          dim3(kThreads), 0, stream, a);
 }
 
 template <typename T, int V>

@@ -65,11 +65,18 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotaryArgs a, uint32_
   float2 cs[V];
   if (static_cast<uint32_t>(pos) < static_cast<uint32_t>(a.r.max_positions)) {
     const float2 *row = a.r.table + static_cast<int64_t>(pos) * half + item * V;
+    if constexpr (V == 1) {
+      cs[0] = __ldg(row);
+    } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      cs[j] = __ldg(row + j);
-      cs[j].y *= a.sin_sign;
+      for (int j = 0; j < V / 2; ++j) {
+        const float4 two = __ldg(reinterpret_cast<const float4 *>(row) + j);
+        cs[2 * j] = make_float2(two.x, two.y);
+        cs[2 * j + 1] = make_float2(two.z, two.w);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < V; ++j) cs[j].y *= a.sin_sign;
   } else {
     if (item == 0 && h0 == 0) atomicOr(&g_rotary_status, IDX_DEV_BAD_POSITION);
 #pragma unroll
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) k_rotary_table(const __grid_constant
 
 template <typename T, int V>
 cudaError_t launch(const RotaryArgs &a, cudaStream_t stream) {
-  constexpr int kHeads = 4;
+  constexpr int kHeads = 2;
   const int64_t per_token =
       static_cast<int64_t>(a.r.rot / 2 / V + (a.copy ? (a.dim - a.r.rot) / V : 0)) *
       ((a.heads + kHeads - 1) / kHeads);

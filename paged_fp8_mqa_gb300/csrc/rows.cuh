@@ -55,13 +55,12 @@ __device__ __forceinline__ float turn_b(float a, float b, float2 cs) {
   return __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
 }
 
-// Elements [d, d + V) of the row at `x`, rotated by the angles at `cs` (one per pair; nullptr: as
-// they are), in float32.  With V > 1 the caller has checked that offset, rot / 2 and d are
-// multiples of V.
+// Elements [d, d + V) of the row at `x`, read as `own`, rotated by the angles at `cs` (one per
+// pair; nullptr: as they are), in float32.  With V > 1 the caller has checked that offset, rot / 2
+// and d are multiples of V.
 template <typename T, int V>
-__device__ __forceinline__ void load_turned(const T *x, int d, const Rotation &r, const float2 *cs,
-                                            float (&out)[V]) {
-  const Piece<T, V> own = load_piece<T, V>(x + d);
+__device__ __forceinline__ void turned(const Piece<T, V> &own, const T *x, int d, const Rotation &r,
+                                       const float2 *cs, float (&out)[V]) {
   const int i = d - r.offset;
   if (cs == nullptr || i < 0 || i >= r.rot) {
 #pragma unroll
@@ -94,25 +93,60 @@ __device__ __forceinline__ void load_turned(const T *x, int d, const Rotation &r
                    : turn_b(to_f32(other.e[j]), to_f32(own.e[j]), c[j]);
 }
 
-// |x| for the largest magnitude of a row: 0 for what is not finite, which has no say in a scale.
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a < __int_as_float(0x7F800000) ? a : 0.0f;
+// The largest magnitude of N values; NaN has no say in it (fmaxf passes it over), infinities have.
+template <int N>
+__device__ __forceinline__ float largest(const float (&v)[N], float so_far) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) so_far = fmaxf(so_far, fabsf(v[j]));
+  return so_far;
 }
+// The same without the infinities, for the rare case that there are some.
+template <int N>
+__device__ __forceinline__ float largest_finite(const float (&v)[N], float so_far) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float a = fabsf(v[j]);
+    so_far = a < __int_as_float(0x7F800000) ? fmaxf(so_far, a) : so_far;
+  }
+  return so_far;
+}
+__device__ __forceinline__ bool is_inf(float x) { return x == __int_as_float(0x7F800000); }
 
 // Four floats as e4m3 bytes: to nearest even, values past +-448 (infinities too) to +-448, NaN to
 // the NaN code.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+  uint32_t out;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}\n"
+      : "=r"(out)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return out;
 }
 
-// Two e4m3 bytes as floats (exact: every e4m3 value is a float16).
+// V values times inv as e4m3 bytes.
+template <int V>
+__device__ __forceinline__ void store_e4m3(uint8_t *dst, const float (&v)[V], float inv) {
+  if constexpr (V == 1) {
+    *dst = static_cast<uint8_t>(e4m3x4(v[0] * inv, 0.0f, 0.0f, 0.0f));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<uint32_t *>(dst + i) =
+          e4m3x4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+  }
+}
+
+// The low two e4m3 bytes as floats (exact: every e4m3 value is a float16).
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
-  return __half22float2(__half2(h));
+  uint32_t h;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}\n"
+      : "=r"(h)
+      : "r"(two));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
 // The request that token t belongs to, found by the whole warp together (every lane passes the
@@ -132,22 +166,24 @@ __device__ __forceinline__ int find_request(const int32_t *starts, int batch, in
 }
 
 struct Place {
-  int b;    // request; -1: the token is past the last request's (padding)
+  int b;    // request; -1: the token is no request's (padding)
   int pos;  // position in it; negative: the request is shorter than its new tokens
 };
 
 __device__ __forceinline__ Place place_of(const TokenMap &m, int t, int lane) {
   Place p;
-  int end;  // the token one past the request's
+  int begin, end;  // the request's rows
   if (m.starts == nullptr) {
     p.b = t / m.next_n;
-    end = (p.b + 1) * m.next_n;
+    begin = p.b * m.next_n;
+    end = begin + m.next_n;
   } else {
     p.b = find_request(m.starts, m.batch, t, lane);
+    begin = __ldg(m.starts + p.b);
     end = __ldg(m.starts + p.b + 1);
   }
   p.pos = __ldg(m.seq_lens + p.b * m.sl_stride) - (end - t);
-  if (t >= end) p.b = p.pos = -1;
+  if (t < begin || t >= end) p.b = p.pos = -1;
   return p;
 }
 
