@@ -22,13 +22,13 @@ constexpr float kTiny = 7.8886090522101180541e-31f;  // 2^-100: a row of zeros h
 // A warp takes four rows of one token (its query heads, then its key), eight lanes a row; lane j
 // of the eight holds pieces j, j + 8, ... of V elements.
 //
-// What bounds the kernel is its instructions (some 260 a warp, 68% of the issue slots) and the
-// latency of finding a token's place, behind which only other warps help: 40 registers, 48 warps
-// an SM.  465 MB of prompts take 131 us (floor 69).  Several rows a warp, rows read ahead into
-// registers, and a token's place found once for a CTA each took more registers than they saved time
-// (165 to 335 us).
+// What bounds the kernel is its instructions (some 260 a warp, two thirds of the issue slots) and
+// the latency of finding a token's place, behind which only other warps help: 32 registers, 64
+// warps an SM.  465 MB of prompts take 114 us (floor 69; at 40 registers 132).  Several rows a warp,
+// rows read ahead into registers, and a token's place found once for a CTA each took more registers
+// than they saved time (165 to 335 us).
 template <typename T, int V, int D>
-__global__ void __launch_bounds__(kThreads) k_index_prepare(const IndexArgs a, uint32_t units) {
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 8 : 5) k_index_prepare(const IndexArgs a, uint32_t units) {
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t unit = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;

@@ -8,6 +8,7 @@
 #include <cuda_fp8.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "layer.h"
 
@@ -41,6 +42,28 @@ __device__ __forceinline__ Piece<T, V> load_piece(const T *p) {
   return *reinterpret_cast<const Piece<T, V> *>(p);
 }
 
+// A piece's values in float32.
+template <typename T, int V>
+__device__ __forceinline__ void piece_f32(const Piece<T, V> &p, float (&out)[V]) {
+  if constexpr (V > 1 && sizeof(T) == 2) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&p);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        out[2 * j] = __uint_as_float(w[j] << 16);
+        out[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(w + j));
+        out[2 * j] = f.x;
+        out[2 * j + 1] = f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) out[j] = to_f32(p.e[j]);
+  }
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void store_piece(T *p, const Piece<T, V> &v) {
   *reinterpret_cast<Piece<T, V> *>(p) = v;
@@ -61,22 +84,19 @@ __device__ __forceinline__ float turn_b(float a, float b, float2 cs) {
 template <typename T, int V>
 __device__ __forceinline__ void turned(const Piece<T, V> &own, const T *x, int d, const Rotation &r,
                                        const float2 *cs, float (&out)[V]) {
+  piece_f32<T, V>(own, out);
   const int i = d - r.offset;
-  if (cs == nullptr || i < 0 || i >= r.rot) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) out[j] = to_f32(own.e[j]);
-    return;
-  }
+  if (cs == nullptr || i < 0 || i >= r.rot) return;
   if (r.interleaved) {
     if constexpr (V == 1) {
       const float2 c = cs[i >> 1];
       const float other = to_f32(x[(i & 1) ? d - 1 : d + 1]);
-      out[0] = (i & 1) ? turn_b(other, to_f32(own.e[0]), c) : turn_a(to_f32(own.e[0]), other, c);
+      out[0] = (i & 1) ? turn_b(other, out[0], c) : turn_a(out[0], other, c);
     } else {
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
         const float2 c = cs[(i >> 1) + j];
-        const float a = to_f32(own.e[2 * j]), b = to_f32(own.e[2 * j + 1]);
+        const float a = out[2 * j], b = out[2 * j + 1];
         out[2 * j] = turn_a(a, b, c);
         out[2 * j + 1] = turn_b(a, b, c);
       }
@@ -85,12 +105,12 @@ __device__ __forceinline__ void turned(const Piece<T, V> &own, const T *x, int d
   }
   const int half = r.rot >> 1;
   const bool first = i < half;
-  const Piece<T, V> other = load_piece<T, V>(x + (first ? d + half : d - half));
+  float other[V];
+  piece_f32<T, V>(load_piece<T, V>(x + (first ? d + half : d - half)), other);
   const float2 *c = cs + (first ? i : i - half);
+  // own cos - other sin for the pair's first element, own cos + other sin for its second.
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    out[j] = first ? turn_a(to_f32(own.e[j]), to_f32(other.e[j]), c[j])
-                   : turn_b(to_f32(other.e[j]), to_f32(own.e[j]), c[j]);
+  for (int j = 0; j < V; ++j) out[j] = turn_b(first ? -other[j] : other[j], out[j], c[j]);
 }
 
 // The largest magnitude of N values; NaN has no say in it (fmaxf passes it over), infinities have.

@@ -680,3 +680,32 @@ def test_append_then_attend():
             # and on each value; ten times that, over the weights' spread.
             lim = 10 * 0.09 * np.sqrt((w ** 2) @ f64(v)[a:e, h // 4] ** 2) + 0.01
             assert (np.abs(out[b, 0, h] - ref) <= lim).all()
+
+
+def test_kv_append_long_runs_equal_their_parts():
+    """A prompt long enough that a CTA takes several heads, in one call and in calls of a few blocks
+    each: the same bytes and scales."""
+    T, H, D, bs = 21000, 8, 64, 64
+    g = gen(12)
+    blocks = -(-T // bs)
+    x = (torch.randn(T, H, D, generator=g) * torch.exp2(torch.randint(-4, 5, (T, 1, 1), generator=g).float())).bfloat16().to(dev())
+    y = torch.randn(T, H, D, generator=g).bfloat16().to(dev())
+    table = idx.rotary_table(T, 32)
+    bt = torch.randperm(blocks, generator=g).int()[None].to(dev())
+    ends = []
+    for step in (T, 40 * bs):
+        kp, vp = (torch.zeros(blocks, H, bs, D, dtype=torch.uint8, device=dev()) for _ in range(2))
+        ks, vs = (torch.zeros(blocks, H, device=dev()) for _ in range(2))
+        for a in range(0, T, step):
+            e = min(a + step, T)
+            idx.kv_append(x[a:e], y[a:e], kp, vp, ks, vs, bt, torch.tensor([e], dtype=torch.int32, device=dev()),
+                          token_starts=torch.tensor([0, e - a], dtype=torch.int32, device=dev()), table=table)
+        ends.append((kp, vp, ks, vs))
+    clean()
+    for a, b in zip(*ends):
+        assert torch.equal(a, b)
+    v = values8(ends[0][1]) * f64(ends[0][3])[:, :, None, None]
+    order = bt[0].cpu().numpy()
+    whole = v[order].transpose(0, 2, 1, 3).reshape(-1, H, D)[:T]
+    s = f64(ends[0][3])[order].repeat(bs, 0)[:T, :, None]
+    assert (np.abs(whole - f64(y)) <= np.maximum(2.0 ** -4 * np.abs(f64(y)), 2.0 ** -10 * s)).all()
