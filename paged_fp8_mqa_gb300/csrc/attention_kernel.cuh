@@ -213,8 +213,8 @@ __device__ __forceinline__ int tiles_for(int length) {
   return length / kTile + (length % kTile != 0);
 }
 
-// A CTA's run over the line: the segments (group, first tile, tiles) in order.  Every role walks
-// its own copy; all lanes of a warp step together.
+// A CTA's run over the line: the segments (group, first tile, tiles) in order.  Every warp walks
+// its own copy, all its lanes together: keys without positions are passed over 32 at a time.
 template <bool SELECT>
 struct Walk {
   int64_t left;  // tiles of the run not yet handed out
@@ -223,12 +223,23 @@ struct Walk {
 
   __device__ __forceinline__ bool next(const AttentionArgs &a, int groups, int keys) {
     if (left <= 0) return false;
-    while (tile >= tiles) {  // the group is finished: the next one of this key, or the next key's
+    if (tile >= tiles) {  // the group is finished: the next one of this key, or the next key's
       tile = 0;
-      if (tiles == 0 || ++group >= groups) {
+      if (++group >= groups) {
         group = 0;
-        if (++key >= keys) return false;  // (lengths that changed under the call)
-        length = key_length<SELECT>(a, key);
+        const int lane = threadIdx.x & 31;
+        for (;;) {
+          const int n = key + 1 + lane < keys ? key_length<SELECT>(a, key + 1 + lane) : 0;
+          const unsigned some = __ballot_sync(0xffffffffu, n > 0);
+          if (some != 0) {
+            const int at = __ffs(some) - 1;
+            key += 1 + at;
+            length = __shfl_sync(0xffffffffu, n, at);
+            break;
+          }
+          key += 32;
+          if (key >= keys) return false;  // (lengths that changed under the call)
+        }
         tiles = tiles_for(length);
       }
     }
@@ -609,65 +620,65 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     }
   } else if (warp == 1) {
     // ============================== MMA issuer ==================================================
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, NS);
-      constexpr uint32_t idesc_o = idesc_e4m3_f32(D, C::NO) | kMajorMN_A | kMajorMN_B;
-      const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
-      const uint32_t o_tmem = tmem + 2 * NS;
-      uint32_t tile = 0, seg = 0;
-      const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
-        const uint64_t k_desc = smem_desc_rows<D>(smem_addr(s_kv + st * C::KV_BYTES));
+    constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, NS);
+    constexpr uint32_t idesc_o = idesc_e4m3_f32(D, C::NO) | kMajorMN_A | kMajorMN_B;
+    const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
+    const uint32_t o_tmem = tmem + 2 * NS;
+    uint32_t tile = 0, seg = 0;
+    const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
+      const uint64_t k_desc = smem_desc_rows<D>(smem_addr(s_kv + st * C::KV_BYTES));
 #pragma unroll
-        for (int part = 0; part < C::PASSES; ++part)
+      for (int part = 0; part < C::PASSES; ++part)
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            mma_f8f6f4(tmem + (n & 1) * NS, k_desc + 2 * k, q_desc + part * (R * D >> 4) + 2 * k,
-                       idesc_s, part + k > 0);
-        mma_commit(&s_full[n & 1]);
-      };
-      while (ok && w.next(a, groups, keys)) {
-        ok = mbar_wait(q_full, seg & 1, kWaitNs);
-        ++seg;
-        if (!ok) break;
-        tc_fence_after_sync();
-        bool ahead = false;  // S of the tile has been issued already
-        for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
-          if (!ahead) {
-            ok = mbar_wait(&kv_full[stage], phase, kWaitNs);
-            if (!ok) break;
-            // (The selected rows were written by ordinary asynchronous copies.)
-            if constexpr (C::SELECT) fence_proxy_async_shared();
-            tc_fence_after_sync();
-            scores(tile, stage);
-          }
-          // The next tile's scores, if its keys are here, before this tile's weights are.
-          const int next = stage + 1 == C::STAGES ? 0 : stage + 1;
-          const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
-          ahead = false;
-          if (i + 1 < w.seg_tiles && mbar_try_wait(&kv_full[next], next_phase)) {
-            if constexpr (C::SELECT) fence_proxy_async_shared();
-            tc_fence_after_sync();
-            scores(tile + 1, next);
-            ahead = true;
-          }
-          ok = mbar_wait(&p_full[tile & 1], (tile >> 1) & 1, kWaitNs);
-          if (!ok) break;
-          tc_fence_after_sync();
-          const uint64_t v_desc =
-              smem_desc_mn<D>(smem_addr(s_kv + stage * C::KV_BYTES + kTile * D));
-          const uint64_t p_desc = smem_desc_p(smem_addr(s_p + (tile & 1) * C::P_BYTES));
-#pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
-            mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o,
-                       i + k > 0);
-          mma_commit(&pv_done[tile & 1]);
-          mma_commit(&kv_empty[stage]);
-          stage = next;
-          phase = next_phase;
+        for (int k = 0; k < D / 32; ++k)
+          mma_f8f6f4(tmem + (n & 1) * NS, k_desc + 2 * k, q_desc + part * (R * D >> 4) + 2 * k,
+                     idesc_s, part + k > 0);
+      mma_commit(&s_full[n & 1]);
+    };
+    const auto keys_here = [&]() {
+      // (The selected rows were written by ordinary asynchronous copies.)
+      if constexpr (C::SELECT) fence_proxy_async_shared();
+      tc_fence_after_sync();
+    };
+    // One thread's work: the segment's products; false if a wait gave up.
+    const auto segment = [&]() {
+      if (!mbar_wait(q_full, seg & 1, kWaitNs)) return false;
+      tc_fence_after_sync();
+      bool ahead = false;  // S of the tile has been issued already
+      for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
+        if (!ahead) {
+          if (!mbar_wait(&kv_full[stage], phase, kWaitNs)) return false;
+          keys_here();
+          scores(tile, stage);
         }
+        // The next tile's scores, if its keys are here, before this tile's weights are.
+        const int next = stage + 1 == C::STAGES ? 0 : stage + 1;
+        const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
+        ahead = i + 1 < w.seg_tiles && mbar_try_wait(&kv_full[next], next_phase);
+        if (ahead) {
+          keys_here();
+          scores(tile + 1, next);
+        }
+        if (!mbar_wait(&p_full[tile & 1], (tile >> 1) & 1, kWaitNs)) return false;
+        tc_fence_after_sync();
+        const uint64_t v_desc = smem_desc_mn<D>(smem_addr(s_kv + stage * C::KV_BYTES + kTile * D));
+        const uint64_t p_desc = smem_desc_p(smem_addr(s_p + (tile & 1) * C::P_BYTES));
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+          mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o, i + k > 0);
+        mma_commit(&pv_done[tile & 1]);
+        mma_commit(&kv_empty[stage]);
+        stage = next;
+        phase = next_phase;
       }
-      mma_commit(drain);
+      return true;
+    };
+    while (ok && w.next(a, groups, keys)) {
+      if (lane == 0) ok = segment();
+      ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
+      ++seg;
     }
+    if (lane == 0) mma_commit(drain);
     __syncwarp();
   } else {
     // ============================== softmax =====================================================

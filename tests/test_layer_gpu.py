@@ -487,6 +487,19 @@ def test_attention_split_any_way(num_sms):
     clean()
 
 
+def test_attention_among_idle_slots():
+    """A fixed batch most of whose slots are idle, in stretches longer than a warp."""
+    lens = [0] * 70 + [40] + [0] * 33 + [300, 0, 5] + [0] * 100 + [129] + [0] * 40
+    c = attention_case(lens, 1, 8, 2, 64, 32, "bf16", 47)
+    for num_sms in (1, 0):
+        out, lse = run_attention(c, num_sms=num_sms)
+        check_attention(c, out, lse)
+    cand, ranges, picked = selections(c, 30, gen(3))
+    out, lse = run_attention(c, candidates=cand, ranges=ranges)
+    check_attention(c, out, lse, picked)
+    clean()
+
+
 def selections(c, top_k, g, extra=3):
     """Slots as the select leaves them, with positions no row can see among them."""
     B, n = c["q"].shape[:2]
