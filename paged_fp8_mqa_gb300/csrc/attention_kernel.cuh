@@ -810,14 +810,19 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
           const float2 k2 = make_float2(tok.k, tok.k), lv2 = make_float2(tok.log_v, tok.log_v);
 #pragma unroll
-          for (int r = 0; r < RT / 2; ++r) {
-            float2 f;
+          for (int r = 0; r < RT / 2; r += 2) {
+            float4 f;
             if constexpr (kHoldRs)
-              f = rs[r];
+              f = make_float4(rs[r].x, rs[r].y, rs[r + 1].x, rs[r + 1].y);
             else
-              f = rs_at[r];
-            const float2 s2 = make_float2(__uint_as_float(v[2 * r]), __uint_as_float(v[2 * r + 1]));
-            y[r] = __ffma2_rn(s2, __fmul2_rn(f, k2), __fadd2_rn(lv2, nref[r]));
+              f = *reinterpret_cast<const float4 *>(rs_at + r);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float2 s2 = make_float2(__uint_as_float(v[2 * (r + h)]),
+                                            __uint_as_float(v[2 * (r + h) + 1]));
+              y[r + h] = __ffma2_rn(s2, __fmul2_rn(h ? make_float2(f.z, f.w) : make_float2(f.x, f.y), k2),
+                                    __fadd2_rn(lv2, nref[r + h]));
+            }
           }
         }
         const bool seen = tok.pos < all_see;
@@ -898,11 +903,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // The weights' buffer was last read by the product two tiles ago.
         if (tile >= 2) wait(&pv_done[tile & 1], ((tile >> 1) - 1) & 1);
         uint8_t *sp = s_p + (tile & 1) * C::P_BYTES + token * 16;
-        const uint32_t flip = tok.inv_v < 0.0f ? 0x80808080u : 0u;
-        const uint32_t live = fabsf(tok.inv_v) < 1.0f / kLeastScale ? 0xFFFFFFFFu : 0u;
         const float inv_v = fabsf(tok.inv_v);
+        // The weights of a position whose value scale is negative or 0 (as good as): rare, so asked
+        // of the whole warp.
+        const bool odd = __any_sync(0xffffffffu, tok.inv_v < 0.0f || inv_v >= 1.0f / kLeastScale);
+        const uint32_t flip = tok.inv_v < 0.0f ? 0x80808080u : 0u;
+        const uint32_t live = inv_v < 1.0f / kLeastScale ? 0xFFFFFFFFu : 0u;
         uint32_t bytes[PARTS][4];
-        const float2 inv2 = make_float2(inv_v, inv_v), up2 = make_float2(kPartUp, kPartUp);
+        const float2 inv2 = make_float2(inv_v, inv_v), up2 = make_float2(kPartUp, kPartUp),
+                     down2 = make_float2(-kPartUp, -kPartUp);
 #pragma unroll
         for (int r = 0; r < RT; r += 4) {
           float2 p[2];
@@ -914,13 +923,17 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
           for (int part = 0; part < PARTS; ++part) {
             const uint32_t b = e4m3x4(p[0].x, p[0].y, p[1].x, p[1].y);
-            bytes[part][(r / 4) % 4] = (b & live) ^ flip;
-            if (part + 1 < PARTS) {
-              // 16 (p - b), both products exact.
-              const float2 b0 = e4m3x2_to_f32(b), b1 = e4m3x2_to_f32(b >> 16);
-              p[0] = __fmul2_rn(make_float2(p[0].x - b0.x, p[0].y - b0.y), up2);
-              p[1] = __fmul2_rn(make_float2(p[1].x - b1.x, p[1].y - b1.y), up2);
+            bytes[part][(r / 4) % 4] = b;
+            if (part + 1 < PARTS) {  // 16 (p - b), exact
+              p[0] = __ffma2_rn(e4m3x2_to_f32(b), down2, __fmul2_rn(p[0], up2));
+              p[1] = __ffma2_rn(e4m3x2_to_f32(b >> 16), down2, __fmul2_rn(p[1], up2));
             }
+          }
+          if (odd && (r % 16 == 12 || r + 4 == RT)) {
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) bytes[part][q] = (bytes[part][q] & live) ^ flip;
           }
           if constexpr (C::CAT) {  // both parts of the eight rows are one group of 16 n
             if (r == 4)

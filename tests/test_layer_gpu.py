@@ -570,6 +570,24 @@ def test_attention_with_block_scales_far_apart():
     clean()
 
 
+@pytest.mark.parametrize("H,Hkv,D,bs,name", [(8, 1, 128, 64, "bf16"), (64, 2, 64, 32, "f16")])
+def test_attention_with_negative_and_zero_scales(H, Hkv, D, bs, name):
+    """Scales of either sign; a block whose values all count as 0; all of them 0."""
+    c = attention_case([300, 64, 129], 1, H, Hkv, D, bs, name, 53)
+    flip = (torch.arange(c["vs"].numel(), device=dev()) % 3 == 0).view_as(c["vs"])
+    c["vs"] = torch.where(flip, -c["vs"], c["vs"])
+    c["ks"] = torch.where(flip.roll(1, 0), -c["ks"], c["ks"])
+    c["vs"][c["rows"][0][1]] = 0.0
+    out, lse = run_attention(c)
+    check_attention(c, out, lse)
+    for page in c["rows"][2][:-(-129 // bs)]:
+        c["vs"][page] = 0.0
+    out, lse = run_attention(c)
+    check_attention(c, out, lse)
+    assert (out[2] == 0).all()
+    clean()
+
+
 def test_attention_never_sees_what_a_draft_slot_does_not():
     """NaN in the values and keys of the newest tokens reaches the slots that see them, and only
     those."""
