@@ -44,9 +44,10 @@ int check_rotation(const float *table, int32_t max_positions, int32_t rot_dim, i
   return IDX_OK;
 }
 
-// Whether the rotated part can be read in pieces of v elements.
+// Whether the rotated part can be read in pieces of v elements (and its angles two at a time).
 bool rotation_in_pieces(const idx::Rotation &r, int v) {
-  return r.table == nullptr || (r.offset % v == 0 && (r.rot / 2) % v == 0);
+  return r.table == nullptr ||
+         (r.offset % v == 0 && (r.rot / 2) % v == 0 && aligned(r.table, 16));
 }
 
 // The new tokens' map to requests, positions and pages.
@@ -78,8 +79,9 @@ int check_tokens(const int32_t *token_starts, int64_t tokens, const int32_t *seq
   return IDX_OK;
 }
 
-bool pieces(const void *p, int64_t s0, int64_t s1, int v) {
-  return aligned(p, 16) && s0 % v == 0 && s1 % v == 0;
+// Whether rows can be read in pieces of v elements of `size` bytes.
+bool pieces(const void *p, int64_t s0, int64_t s1, int v, int size) {
+  return aligned(p, v * size) && s0 % v == 0 && s1 % v == 0;
 }
 
 }  // namespace
@@ -184,8 +186,8 @@ IDX_EXPORT int idx_rotary(const void *x, int64_t x_token_stride, int64_t x_head_
   a.sin_sign = inverse ? -1.0f : 1.0f;
   a.copy = !(x == out && x_token_stride == out_token_stride && x_head_stride == out_head_stride);
   const int v = 16 / size;
-  const bool vectors = pieces(x, x_token_stride, x_head_stride, v) &&
-                       pieces(out, out_token_stride, out_head_stride, v) && head_dim % v == 0 &&
+  const bool vectors = pieces(x, x_token_stride, x_head_stride, v, size) &&
+                       pieces(out, out_token_stride, out_head_stride, v, size) && head_dim % v == 0 &&
                        rotation_in_pieces(a.r, v);
   const cudaError_t e = idx::launch_rotary(a, dtype, vectors, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? IDX_OK : cuda_fail(e, "rotary launch");
@@ -234,12 +236,11 @@ IDX_EXPORT int idx_index_prepare(
   a.block_size = block_size;
   a.heads = q != nullptr ? num_heads : 0;
   a.dim = head_dim;
-  const int v = 16 / size;
-  const bool vectors = pieces(k, k_token_stride, 0, v) &&
-                       (q == nullptr || pieces(q, q_token_stride, q_head_stride, v)) &&
-                       rotation_in_pieces(a.r, v);
+  const bool pairs = pieces(k, k_token_stride, 0, 2, size) &&
+                     (q == nullptr || pieces(q, q_token_stride, q_head_stride, 2, size)) &&
+                     rotation_in_pieces(a.r, 2);
   const cudaError_t e =
-      idx::launch_index_prepare(a, dtype, vectors, static_cast<cudaStream_t>(stream));
+      idx::launch_index_prepare(a, dtype, pairs, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? IDX_OK : cuda_fail(e, "index_prepare launch");
 }
 
@@ -289,8 +290,9 @@ IDX_EXPORT int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_he
   a.heads = kv_heads;
   a.dim = head_dim;
   const int n = 16 / size;
-  const bool vectors = pieces(k, k_token_stride, k_head_stride, n) &&
-                       pieces(v, v_token_stride, v_head_stride, n) && rotation_in_pieces(a.r, n);
+  const bool vectors = pieces(k, k_token_stride, k_head_stride, n, size) &&
+                       pieces(v, v_token_stride, v_head_stride, n, size) &&
+                       rotation_in_pieces(a.r, n);
   const cudaError_t e = idx::launch_kv_append(a, dtype, vectors, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? IDX_OK : cuda_fail(e, "kv_append launch");
 }

@@ -120,13 +120,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// The largest x of the warp's lanes (a NaN loses against a number).
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Each thread of the warp reads NC consecutive columns of its TMEM lane.
 template <int NC>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[NC]) {

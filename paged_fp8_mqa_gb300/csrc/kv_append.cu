@@ -104,6 +104,41 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t four, float f) {
   return e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
 }
 
+// Elements [d, d + V) of the row at `x`, read as `own`, rotated by the angles at `cs` (one per
+// pair; nullptr: as they are), in float32.  With V > 1 the caller has checked that offset, rot / 2
+// and d are multiples of V.
+template <typename T, int V>
+__device__ __forceinline__ void turned_piece(const Piece<T, V> &own, const T *x, int d, const Rotation &r,
+                                       const float2 *cs, float (&out)[V]) {
+  piece_f32<T, V>(own, out);
+  const int i = d - r.offset;
+  if (cs == nullptr || i < 0 || i >= r.rot) return;
+  if (r.interleaved) {
+    if constexpr (V == 1) {
+      const float2 c = cs[i >> 1];
+      const float other = to_f32(x[(i & 1) ? d - 1 : d + 1]);
+      out[0] = (i & 1) ? turn_b(other, out[0], c) : turn_a(out[0], other, c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 c = cs[(i >> 1) + j];
+        const float a = out[2 * j], b = out[2 * j + 1];
+        out[2 * j] = turn_a(a, b, c);
+        out[2 * j + 1] = turn_b(a, b, c);
+      }
+    }
+    return;
+  }
+  const int half = r.rot >> 1;
+  const bool first = i < half;
+  float other[V];
+  piece_f32<T, V>(load_piece<T, V>(x + (first ? d + half : d - half)), other);
+  const float2 *c = cs + (first ? i : i - half);
+  // own cos - other sin for the pair's first element, own cos + other sin for its second.
+#pragma unroll
+  for (int j = 0; j < V; ++j) out[j] = turn_b(first ? -other[j] : other[j], out[j], c[j]);
+}
+
 // One item: a block of one head of K or of V.  GROUP = 32: a warp of its own (a few new tokens);
 // GROUP = kThreads: the whole CTA (long runs of tokens).  The new tokens are read once for the
 // largest magnitude and, from L1, once more to be written.
@@ -133,7 +168,7 @@ __device__ __forceinline__ void append_item(const AppendArgs &a, const Unit &u, 
   for (int i = tid; i < n; i += GROUP) {
     float v[V];
     const int tk = i / kPer, d = (i % kPer) * V;
-    turned<T, V>(load_piece<T, V>(x + tk * token + d), x + tk * token, d, a.r, row(tk), v);
+    turned_piece<T, V>(load_piece<T, V>(x + tk * token + d), x + tk * token, d, a.r, row(tk), v);
     amax = largest_finite(v, amax);
   }
 #pragma unroll
@@ -159,7 +194,7 @@ __device__ __forceinline__ void append_item(const AppendArgs &a, const Unit &u, 
   for (int i = tid; i < n; i += GROUP) {
     float v[V];
     const int tk = i / kPer, d = (i % kPer) * V;
-    turned<T, V>(load_piece<T, V>(x + tk * token + d), x + tk * token, d, a.r, row(tk), v);
+    turned_piece<T, V>(load_piece<T, V>(x + tk * token + d), x + tk * token, d, a.r, row(tk), v);
     store_e4m3<V>(block + (off0 + tk) * D + d, v, inv);
   }
 }

@@ -68,7 +68,8 @@ struct IndexArgs {
   Rotation r;
   TokenMap m;
 };
-cudaError_t launch_index_prepare(const IndexArgs &a, int dtype, bool vectors, cudaStream_t stream);
+// pairs: rows and angles may be read two elements at a time.
+cudaError_t launch_index_prepare(const IndexArgs &a, int dtype, bool pairs, cudaStream_t stream);
 
 struct AppendArgs {
   const void *k, *v;  // [tokens, heads, dim]

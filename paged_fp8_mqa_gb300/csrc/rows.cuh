@@ -69,8 +69,8 @@ __device__ __forceinline__ void store_piece(T *p, const Piece<T, V> &v) {
   *reinterpret_cast<Piece<T, V> *>(p) = v;
 }
 
-// The two products are rounded before the sum, so that a value does not depend on which of them
-// the compiler would have fused.
+// A pair turned: x cos - y sin and y cos + x sin.  The two products are rounded before the sum, so
+// that a value does not depend on which of them the compiler would have fused.
 __device__ __forceinline__ float turn_a(float a, float b, float2 cs) {
   return __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
 }
@@ -78,39 +78,79 @@ __device__ __forceinline__ float turn_b(float a, float b, float2 cs) {
   return __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
 }
 
-// Elements [d, d + V) of the row at `x`, read as `own`, rotated by the angles at `cs` (one per
-// pair; nullptr: as they are), in float32.  With V > 1 the caller has checked that offset, rot / 2
-// and d are multiples of V.
-template <typename T, int V>
-__device__ __forceinline__ void turned(const Piece<T, V> &own, const T *x, int d, const Rotation &r,
-                                       const float2 *cs, float (&out)[V]) {
-  piece_f32<T, V>(own, out);
-  const int i = d - r.offset;
-  if (cs == nullptr || i < 0 || i >= r.rot) return;
-  if (r.interleaved) {
-    if constexpr (V == 1) {
-      const float2 c = cs[i >> 1];
-      const float other = to_f32(x[(i & 1) ? d - 1 : d + 1]);
-      out[0] = (i & 1) ? turn_b(other, out[0], c) : turn_a(out[0], other, c);
-    } else {
+// Rows of D elements in the hands of a warp: lane l holds pieces l, l + 32, ... of V elements (V = 2,
+// or 1 where bases, strides or the rotated part are odd).  Two elements a lane, because a warp's
+// loads of angles, which are as many floats as there are elements, are then whole lines.
+template <int V, int D>
+constexpr int kPieces = D / (32 * V);
+
+// How a piece is turned: element j becomes own c[j] + other s[j], the pair's first element with the
+// negated sine.  The others stand `apart` elements further in the row, or, with apart = 0, in the
+// piece itself, swapped (interleaved, V = 2).
+template <int V>
+struct Turn {
+  float c[V], s[V];
+  int apart;
+  bool on;  // false: the elements stay as they are
+};
+
+// The turn of elements [d, d + V) of a row whose angles are at `row` (nullptr: none).  With V = 2
+// offset and rot / 2 are even and the angles 16-byte aligned (the caller has checked).
+template <int V>
+__device__ __forceinline__ Turn<V> turn_of(const Rotation &r, const float2 *row, int d) {
+  Turn<V> t;
+  const int i = d - r.offset, half = r.rot >> 1;
+  t.on = row != nullptr && i >= 0 && i < r.rot;
+  t.apart = 0;
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const float2 c = cs[(i >> 1) + j];
-        const float a = out[2 * j], b = out[2 * j + 1];
-        out[2 * j] = turn_a(a, b, c);
-        out[2 * j + 1] = turn_b(a, b, c);
-      }
-    }
-    return;
+  for (int j = 0; j < V; ++j) t.c[j] = t.s[j] = 0.0f;
+  if (!t.on) return t;
+  const bool first = r.interleaved ? (i & 1) == 0 : i < half;
+  if constexpr (V == 1) {
+    const float2 cs = __ldg(row + (r.interleaved ? i >> 1 : first ? i : i - half));
+    t.c[0] = cs.x;
+    t.s[0] = first ? -cs.y : cs.y;
+    t.apart = r.interleaved ? (first ? 1 : -1) : first ? half : -half;
+  } else if (r.interleaved) {
+    const float2 cs = __ldg(row + (i >> 1));
+    t.c[0] = t.c[1] = cs.x;
+    t.s[0] = -cs.y;
+    t.s[1] = cs.y;
+  } else {
+    const float4 cs = __ldg(reinterpret_cast<const float4 *>(row + (first ? i : i - half)));
+    t.c[0] = cs.x;
+    t.c[1] = cs.z;
+    t.s[0] = first ? -cs.y : cs.y;
+    t.s[1] = first ? -cs.w : cs.w;
+    t.apart = first ? half : -half;
   }
-  const int half = r.rot >> 1;
-  const bool first = i < half;
+  return t;
+}
+
+// The piece `own` of V elements at x in float32, turned (the others are read from memory, where
+// their lines are in L1 by then).
+template <typename T, int V>
+__device__ __forceinline__ void turned(const Piece<T, V> &own, const T *x, const Turn<V> &t,
+                                       float (&out)[V]) {
+  piece_f32<T, V>(own, out);
+  if (!t.on) return;
   float other[V];
-  piece_f32<T, V>(load_piece<T, V>(x + (first ? d + half : d - half)), other);
-  const float2 *c = cs + (first ? i : i - half);
-  // own cos - other sin for the pair's first element, own cos + other sin for its second.
+  if (V == 2 && t.apart == 0) {
+    other[0] = out[V - 1];
+    other[V - 1] = out[0];
+  } else {
+    piece_f32<T, V>(load_piece<T, V>(x + t.apart), other);
+  }
 #pragma unroll
-  for (int j = 0; j < V; ++j) out[j] = turn_b(first ? -other[j] : other[j], out[j], c[j]);
+  for (int j = 0; j < V; ++j)
+    out[j] = __fadd_rn(__fmul_rn(out[j], t.c[j]), __fmul_rn(other[j], t.s[j]));
+}
+
+// The largest x of the warp's lanes (a NaN loses against a number).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // The largest magnitude of N values; NaN has no say in it (fmaxf passes it over), infinities have.
@@ -150,6 +190,9 @@ template <int V>
 __device__ __forceinline__ void store_e4m3(uint8_t *dst, const float (&v)[V], float inv) {
   if constexpr (V == 1) {
     *dst = static_cast<uint8_t>(e4m3x4(v[0] * inv, 0.0f, 0.0f, 0.0f));
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<uint16_t *>(dst) =
+        static_cast<uint16_t>(e4m3x4(v[0] * inv, v[1] * inv, 0.0f, 0.0f));
   } else {
 #pragma unroll
     for (int i = 0; i < V; i += 4)
