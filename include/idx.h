@@ -479,7 +479,7 @@ int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, 
  *   num_blocks    (num_blocks + 1) * kv_heads * block_size must stay below 2^31
  *   candidates    NULL, or device int32 [batch*next_n][slots][2] (position, anything), 8-byte
  *                 aligned, with ranges, device int32 [2][batch*next_n]
- *   num_sms       CTAs a SM-wide wave of the grid (0 = this device's SM count)
+ *   num_sms       SMs the grid is sized for, one or two CTAs each (0 = this device's SM count)
  *   out           device, dtype [batch][next_n][num_heads][head_dim], contiguous, 16-byte aligned
  *   lse           NULL, or device float32 [batch][next_n][num_heads]: ln sum_p exp(z_p)
  *   workspace     device, 256-byte aligned, idx_attention_workspace_bytes(...) bytes

@@ -73,7 +73,11 @@ struct AttnCfg {
   static constexpr int THREADS = 32 * (LOADERS + 1 + SOFT_WARPS);
   static constexpr int COLS = 2 * NS + NO;            // two of S, one of O
   static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  static constexpr int CTAS = R == 64 ? 1 : 2;        // on an SM
+  // CTAs on an SM, each with a pipeline of its own, so that one's loads and products run beside the
+  // other's softmax.  Three of two stages instead of two of three: decode 466 us for 338, as what
+  // the next launch needs no longer fits beside them.  64 rows in chunks of 32, two CTAs an SM:
+  // one long request 29 us for 27, a batch of 64 requests with 64 heads on one 128 for 96.
+  static constexpr int CTAS = R == 64 ? 1 : 2;
   static constexpr int KV_BYTES = 2 * kTile * D;
   static constexpr int Q_BYTES = (R * PARTS * D + 1023) / 1024 * 1024;
   static constexpr int P_BYTES = R * PARTS * kTile;   // one of two
