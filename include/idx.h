@@ -371,7 +371,9 @@ int idx_device_status(int32_t *status_out, int32_t clear);
  * the other elements stay.  A position past the table leaves its row as it is and is flagged
  * (IDX_DEV_BAD_POSITION).
  *
- * Row strides are in elements.  Loads are wide (16 bytes; two elements in idx_index_prepare) where every base, stride, rot_offset and rot_dim/2 allows it, single elements otherwise.  IDX_VALIDATE does not look at these calls.
+ * Row strides are in elements.  Loads are wide (16 bytes in idx_rotary, two elements in the
+ * writers) where every base, stride, rot_offset and rot_dim/2 allows it, single elements
+ * otherwise.  IDX_VALIDATE does not look at these calls.
  */
 #define IDX_ROTARY_NONE 0   /* base^(-2i/rot_dim) */
 #define IDX_ROTARY_LINEAR 1 /* divided by factor */

@@ -289,11 +289,9 @@ IDX_EXPORT int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_he
   a.block_size = block_size;
   a.heads = kv_heads;
   a.dim = head_dim;
-  const int n = 16 / size;
-  const bool vectors = pieces(k, k_token_stride, k_head_stride, n, size) &&
-                       pieces(v, v_token_stride, v_head_stride, n, size) &&
-                       rotation_in_pieces(a.r, n);
-  const cudaError_t e = idx::launch_kv_append(a, dtype, vectors, static_cast<cudaStream_t>(stream));
+  const bool pairs = pieces(k, k_token_stride, k_head_stride, 2, size) &&
+                     pieces(v, v_token_stride, v_head_stride, 2, size) && rotation_in_pieces(a.r, 2);
+  const cudaError_t e = idx::launch_kv_append(a, dtype, pairs, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? IDX_OK : cuda_fail(e, "kv_append launch");
 }
 

@@ -104,83 +104,62 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t four, float f) {
   return e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
 }
 
-// Elements [d, d + V) of the row at `x`, read as `own`, rotated by the angles at `cs` (one per
-// pair; nullptr: as they are), in float32.  With V > 1 the caller has checked that offset, rot / 2
-// and d are multiples of V.
-template <typename T, int V>
-__device__ __forceinline__ void turned_piece(const Piece<T, V> &own, const T *x, int d, const Rotation &r,
-                                       const float2 *cs, float (&out)[V]) {
-  piece_f32<T, V>(own, out);
-  const int i = d - r.offset;
-  if (cs == nullptr || i < 0 || i >= r.rot) return;
-  if (r.interleaved) {
-    if constexpr (V == 1) {
-      const float2 c = cs[i >> 1];
-      const float other = to_f32(x[(i & 1) ? d - 1 : d + 1]);
-      out[0] = (i & 1) ? turn_b(other, out[0], c) : turn_a(out[0], other, c);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const float2 c = cs[(i >> 1) + j];
-        const float a = out[2 * j], b = out[2 * j + 1];
-        out[2 * j] = turn_a(a, b, c);
-        out[2 * j + 1] = turn_b(a, b, c);
-      }
-    }
-    return;
-  }
-  const int half = r.rot >> 1;
-  const bool first = i < half;
-  float other[V];
-  piece_f32<T, V>(load_piece<T, V>(x + (first ? d + half : d - half)), other);
-  const float2 *c = cs + (first ? i : i - half);
-  // own cos - other sin for the pair's first element, own cos + other sin for its second.
-#pragma unroll
-  for (int j = 0; j < V; ++j) out[j] = turn_b(first ? -other[j] : other[j], out[j], c[j]);
+// One item: a block of one head of K or of V.
+template <typename T>
+struct Item {
+  const T *x;  // the first new token's row
+  int64_t token;
+  uint8_t *block;
+  float *scale;
+  bool turn;
+};
+
+template <typename T>
+__device__ __forceinline__ Item<T> item_of(const AppendArgs &a, const Unit &u, int64_t page,
+                                           int item, int dim) {
+  Item<T> r;
+  const int h = item >> 1;
+  const bool is_k = (item & 1) == 0;
+  r.token = is_k ? a.k_token : a.v_token;
+  r.x = static_cast<const T *>(is_k ? a.k : a.v) + u.tok * r.token + h * (is_k ? a.k_head : a.v_head);
+  const int64_t at = page * a.heads + h;
+  r.block = (is_k ? a.k_pool : a.v_pool) + at * a.block_size * dim;
+  r.scale = (is_k ? a.k_scales : a.v_scales) + at;
+  r.turn = is_k && a.r.table != nullptr;
+  return r;
 }
 
-// One item: a block of one head of K or of V.  GROUP = 32: a warp of its own (a few new tokens);
-// GROUP = kThreads: the whole CTA (long runs of tokens).  The new tokens are read once for the
-// largest magnitude and, from L1, once more to be written.
-template <typename T, int V, int D, int GROUP>
-__device__ __forceinline__ void append_item(const AppendArgs &a, const Unit &u, int64_t page, int h,
-                                            bool is_k, float *s_max) {
-  const int tid = GROUP == 32 ? threadIdx.x & 31 : threadIdx.x;
-  constexpr int kPer = D / V;  // pieces of a row
-  const int64_t token = is_k ? a.k_token : a.v_token, head = is_k ? a.k_head : a.v_head;
-  const T *x = static_cast<const T *>(is_k ? a.k : a.v) + u.tok * token + h * head;
-  const int64_t at = page * a.heads + h;
-  uint8_t *block = (is_k ? a.k_pool : a.v_pool) + at * a.block_size * D;
-  float *scale_at = (is_k ? a.k_scales : a.v_scales) + at;
-  const int off0 = u.first - u.j * a.block_size;
-  const float was = off0 > 0 ? *scale_at : 0.0f;
-  const bool turn = is_k && a.r.table != nullptr;
-  const auto row = [&](int i) -> const float2 * {
-    const int pos = u.first + i;
-    if (!turn || pos >= a.r.max_positions) return nullptr;
-    return a.r.table + static_cast<int64_t>(pos) * (a.r.rot >> 1);
-  };
-  if (turn && h == 0 && tid == 0 && u.first + u.count > a.r.max_positions)
-    atomicOr(&g_append_status, IDX_DEV_BAD_POSITION);
-  float amax = 0.0f;
-  const int n = u.count * kPer;
-#pragma unroll 4
-  for (int i = tid; i < n; i += GROUP) {
-    float v[V];
-    const int tk = i / kPer, d = (i % kPer) * V;
-    turned_piece<T, V>(load_piece<T, V>(x + tk * token + d), x + tk * token, d, a.r, row(tk), v);
-    amax = largest_finite(v, amax);
-  }
+// A token's row of an item in a warp (see kPieces).
+template <typename T, int V, int D>
+struct Row {
+  static constexpr int N = kPieces<V, D>;
+  Piece<T, V> own[N];
+
+  __device__ __forceinline__ void load(const Item<T> &it, int tk, int lane) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if constexpr (GROUP != 32) {
-    if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-    __syncthreads();  // (also: every thread has read the old scale)
-#pragma unroll
-    for (int w = 0; w < GROUP / 32; ++w) amax = fmaxf(amax, s_max[w]);
-  } else {
-    __syncwarp();
+    for (int i = 0; i < N; ++i)
+      own[i] = load_piece<T, V>(it.x + tk * it.token + (lane + 32 * i) * V);
   }
+  // In float32, turned.
+  __device__ __forceinline__ void values(const AppendArgs &a, const Unit &u, const Item<T> &it, int tk,
+                                         int lane, float (&v)[N][V]) const {
+    const int pos = u.first + tk;
+    const float2 *angles = it.turn && pos < a.r.max_positions
+                               ? a.r.table + static_cast<int64_t>(pos) * (a.r.rot >> 1)
+                               : nullptr;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int d = (lane + 32 * i) * V;
+      turned<T, V>(own[i], it.x + tk * it.token + d, turn_of<V>(a.r, angles, d), v[i]);
+    }
+  }
+};
+
+// The block's scale for new values of magnitude amax at most; where it grows, the tokens before
+// off0 are rescaled by the GROUP threads.
+template <int D, int GROUP>
+__device__ __forceinline__ float settle_scale(uint8_t *block, float was, float amax, int off0,
+                                              int tid) {
   float scale = block_scale(amax);
   if (off0 > 0 && !(scale > was)) scale = was;
   if (off0 > 0 && scale != was) {
@@ -188,72 +167,160 @@ __device__ __forceinline__ void append_item(const AppendArgs &a, const Unit &u, 
     uint32_t *p = reinterpret_cast<uint32_t *>(block);
     for (int i = tid; i < off0 * D / 4; i += GROUP) p[i] = rescale4(p[i], f);
   }
-  if (tid == 0) *scale_at = scale;
-  const float inv = 1.0f / scale;  // exact: scale is a power of two (or what another writer left)
-#pragma unroll 4
-  for (int i = tid; i < n; i += GROUP) {
-    float v[V];
-    const int tk = i / kPer, d = (i % kPer) * V;
-    turned_piece<T, V>(load_piece<T, V>(x + tk * token + d), x + tk * token, d, a.r, row(tk), v);
-    store_e4m3<V>(block + (off0 + tk) * D + d, v, inv);
+  return scale;
+}
+
+// The page of the request's block, or -1: nothing to do, or flagged.
+__device__ __forceinline__ int page_of(const AppendArgs &a, const Unit &u) {
+  if (u.count <= 0) return -1;
+  int id = -1;
+  if (u.j < a.m.bt_width) id = __ldg(a.m.block_tables + u.b * a.m.bt_stride + u.j);
+  const bool good = id >= 0 && id < a.num_blocks && u.tok >= 0 && u.tok + u.count <= a.m.tokens;
+  if (threadIdx.x == 0 && blockIdx.y == 0) {
+    if (!good)
+      atomicOr(&g_append_status, IDX_DEV_BAD_PAGE);
+    else if (a.r.table != nullptr && u.first + u.count > a.r.max_positions)
+      atomicOr(&g_append_status, IDX_DEV_BAD_POSITION);
+  }
+  return good ? id : -1;
+}
+
+// Unit x of equal requests: each touches so many blocks at most.
+__device__ __forceinline__ Unit equal_unit(const AppendArgs &a, int x) {
+  const int per = (a.m.next_n - 1 + a.block_size - 1) / a.block_size + 1;
+  const int b = x / per;
+  const int len = __ldg(a.m.seq_lens + b * a.m.sl_stride);
+  return unit_of(b, x - b * per, len - a.m.next_n, len, static_cast<int64_t>(b) * a.m.next_n,
+                 a.block_size);
+}
+
+// A few new tokens a block (kFew at most): a warp an item, whose rows stay in registers between the
+// largest magnitude and the writing.
+constexpr int kFew = 4;
+
+template <typename T, int V, int D>
+__global__ void __launch_bounds__(kThreads) k_append_few(const AppendArgs a) {
+  constexpr int N = kPieces<V, D>;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int n = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  const Unit u = equal_unit(a, blockIdx.x);
+  const int id = page_of(a, u);
+  if (id < 0 || n >= 2 * a.heads) return;
+  const Item<T> it = item_of<T>(a, u, id, n, D);
+  const int off0 = u.first - u.j * a.block_size;
+  const float was = off0 > 0 ? *it.scale : 0.0f;
+  float v[kFew][N][V], amax = 0.0f;
+#pragma unroll
+  for (int tk = 0; tk < kFew; ++tk) {
+    if (tk >= u.count) break;
+    Row<T, V, D> row;
+    row.load(it, tk, lane);
+    row.values(a, u, it, tk, lane, v[tk]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) amax = largest_finite(v[tk][i], amax);
+  }
+  amax = warp_max(amax);
+  const float scale = settle_scale<D, 32>(it.block, was, amax, off0, lane);
+  if (lane == 0) *it.scale = scale;
+  const float inv = 1.0f / scale;  // exact: a power of two (or what another writer left)
+#pragma unroll
+  for (int tk = 0; tk < kFew; ++tk) {
+    if (tk >= u.count) break;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      store_e4m3<V>(it.block + (off0 + tk) * D + (lane + 32 * i) * V, v[tk][i], inv);
   }
 }
 
-template <typename T, int V, int D, int GROUP>
-__global__ void __launch_bounds__(kThreads) k_kv_append(const AppendArgs a) {
+// Runs of tokens: a CTA takes one request's block (of 8 * HELD tokens) and, of its 2 * heads items,
+// every gridDim.y-th; a warp every eighth token, HELD at most.  All its rows are asked for at once
+// (a token past the block's last new one is read as that one: a branch would keep the loads apart),
+// and stay in registers between the largest magnitude and the writing.
+//
+// 217 MB of prompts take 89 us (floor 32): an item is a chain of a search, loads, a barrier and
+// stores, of which four CTAs an SM overlap.  With the rows behind branches it was 114 us, with
+// 16-byte pieces read twice 98, with one, two or eight items a CTA 112, 93 and 93 (four: 89).
+template <typename T, int V, int D, int HELD>
+__global__ void __launch_bounds__(kThreads, HELD <= 8 ? 4 : 2) k_append_run(const AppendArgs a) {
+  constexpr int N = kPieces<V, D>;
   __shared__ int s_warp[kWarps];
   __shared__ float s_max[2][kWarps];
   __shared__ Unit s_unit;
   griddep_wait();
   griddep_launch_dependents();
-  Unit u;
-  if (a.m.starts == nullptr) {
-    // Two units at most of a request whose next_n tokens are no more than a block.
-    const int per = (a.m.next_n - 1 + a.block_size - 1) / a.block_size + 1;
-    const int b = blockIdx.x / per;
-    const int len = __ldg(a.m.seq_lens + b * a.m.sl_stride);
-    u = unit_of(b, blockIdx.x - b * per, len - a.m.next_n, len,
-                static_cast<int64_t>(b) * a.m.next_n, a.block_size);
-  } else {
-    u = find_unit(a.m, blockIdx.x, a.block_size, s_warp, &s_unit);
-  }
-  if (u.count <= 0) return;
-  int id = -1;
-  if (u.j < a.m.bt_width) id = __ldg(a.m.block_tables + u.b * a.m.bt_stride + u.j);
-  if (id < 0 || id >= a.num_blocks || u.tok < 0 || u.tok + u.count > a.m.tokens) {
-    if (threadIdx.x == 0) atomicOr(&g_append_status, IDX_DEV_BAD_PAGE);
-    return;
-  }
-  const int warps = GROUP == 32 ? kWarps : 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, items = 2 * a.heads;
+  const Unit u = a.m.starts == nullptr ? equal_unit(a, blockIdx.x)
+                                       : find_unit(a.m, blockIdx.x, a.block_size, s_warp, &s_unit);
+  const int id = page_of(a, u);
+  if (id < 0) return;
+  const int off0 = u.first - u.j * a.block_size;
   int set = 0;  // (two sets of maxima: a fast warp may be an item ahead)
-  for (int item = blockIdx.y * warps + (GROUP == 32 ? threadIdx.x >> 5 : 0); item < 2 * a.heads;
-       item += gridDim.y * warps, set ^= 1)
-    append_item<T, V, D, GROUP>(a, u, id, item >> 1, (item & 1) == 0, s_max[set]);
+  for (int n = blockIdx.y; n < items; n += gridDim.y, set ^= 1) {
+    const Item<T> it = item_of<T>(a, u, id, n, D);
+    const float was = off0 > 0 ? *it.scale : 0.0f;
+    Row<T, V, D> row[HELD];
+#pragma unroll
+    for (int p = 0; p < HELD; ++p) row[p].load(it, min(warp + p * kWarps, u.count - 1), lane);
+    float v[HELD][N][V], amax = 0.0f;
+#pragma unroll
+    for (int p = 0; p < HELD; ++p) {
+      row[p].values(a, u, it, min(warp + p * kWarps, u.count - 1), lane, v[p]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) amax = largest(v[p][i], amax);
+    }
+    if (is_inf(amax)) {
+      amax = 0.0f;
+#pragma unroll
+      for (int p = 0; p < HELD; ++p)
+#pragma unroll
+        for (int i = 0; i < N; ++i) amax = largest_finite(v[p][i], amax);
+    }
+    amax = warp_max(amax);
+    if (lane == 0) s_max[set][warp] = amax;
+    __syncthreads();  // (also: every thread has read the old scale)
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_max[set][w]);
+    const float scale = settle_scale<D, kThreads>(it.block, was, amax, off0, tid);
+    if (tid == 0) *it.scale = scale;
+    const float inv = 1.0f / scale;  // exact: a power of two (or what another writer left)
+#pragma unroll
+    for (int p = 0; p < HELD; ++p) {
+      const int tk = warp + p * kWarps;
+      if (tk < u.count) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          store_e4m3<V>(it.block + (off0 + tk) * D + (lane + 32 * i) * V, v[p][i], inv);
+      }
+    }
+  }
 }
 
 template <typename T, int V, int D>
 cudaError_t launch_dim(const AppendArgs &a, cudaStream_t stream) {
   const int64_t bs = a.block_size;
-  if (a.m.starts == nullptr) {
-    const int64_t units = a.m.batch * ((a.m.next_n - 1 + bs - 1) / bs + 1);
-    // A draft's few tokens occupy a warp an item; runs of 16 tokens and more the CTA.
-    if (a.m.next_n < 16)
-      return launch_dependent(k_kv_append<T, V, D, 32>,
-                              dim3(static_cast<unsigned>(units), (2 * a.heads + kWarps - 1) / kWarps),
-                              dim3(kThreads), 0, stream, a);
-    return launch_dependent(k_kv_append<T, V, D, kThreads>,
-                            dim3(static_cast<unsigned>(units), 2 * a.heads), dim3(kThreads), 0,
-                            stream, a);
+  const int items = 2 * a.heads;
+  int64_t units = a.m.batch * ((a.m.next_n - 1 + bs - 1) / bs + 1);
+  if (a.m.starts == nullptr && a.m.next_n <= kFew)
+    return launch_dependent(k_append_few<T, V, D>,
+                            dim3(static_cast<unsigned>(units), (items + kWarps - 1) / kWarps),
+                            dim3(kThreads), 0, stream, a);
+  if (a.m.starts != nullptr) {
+    // Every request touches at most (its tokens) / bs + 2 blocks, and no more than its tokens.
+    units = a.m.tokens / bs + 2 * static_cast<int64_t>(a.m.batch);
+    if (units > a.m.tokens) units = a.m.tokens;
   }
-  // Every request touches at most (its tokens) / bs + 2 blocks, and no more than its tokens.
-  const int64_t most = a.m.tokens / bs + 2 * static_cast<int64_t>(a.m.batch);
-  const int64_t units = most < a.m.tokens ? most : a.m.tokens;
   // An item a CTA, until there are some thousands of CTAs; then several, one after the other, which
   // share the search for their block.
-  int y = 2 * a.heads;
+  int y = items;
   while (y % 2 == 0 && units * y > 4096) y /= 2;
-  return launch_dependent(k_kv_append<T, V, D, kThreads>, dim3(static_cast<unsigned>(units), y),
-                          dim3(kThreads), 0, stream, a);
+  const dim3 grid(static_cast<unsigned>(units), y);
+  switch (a.block_size) {
+    case 32: return launch_dependent(k_append_run<T, V, D, 4>, grid, dim3(kThreads), 0, stream, a);
+    case 64: return launch_dependent(k_append_run<T, V, D, 8>, grid, dim3(kThreads), 0, stream, a);
+    default: return launch_dependent(k_append_run<T, V, D, 16>, grid, dim3(kThreads), 0, stream, a);
+  }
 }
 
 template <typename T, int V>
@@ -267,14 +334,14 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_kv_append(const AppendArgs &a, int dtype, bool vectors, cudaStream_t stream) {
+cudaError_t launch_kv_append(const AppendArgs &a, int dtype, bool pairs, cudaStream_t stream) {
   switch (dtype) {
     case IDX_DTYPE_F32:
-      return vectors ? launch<float, 4>(a, stream) : launch<float, 1>(a, stream);
+      return pairs ? launch<float, 2>(a, stream) : launch<float, 1>(a, stream);
     case IDX_DTYPE_F16:
-      return vectors ? launch<__half, 8>(a, stream) : launch<__half, 1>(a, stream);
+      return pairs ? launch<__half, 2>(a, stream) : launch<__half, 1>(a, stream);
     default:
-      return vectors ? launch<__nv_bfloat16, 8>(a, stream) : launch<__nv_bfloat16, 1>(a, stream);
+      return pairs ? launch<__nv_bfloat16, 2>(a, stream) : launch<__nv_bfloat16, 1>(a, stream);
   }
 }
 

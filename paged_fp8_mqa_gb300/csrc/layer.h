@@ -83,7 +83,7 @@ struct AppendArgs {
   Rotation r;
   TokenMap m;
 };
-cudaError_t launch_kv_append(const AppendArgs &a, int dtype, bool vectors, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendArgs &a, int dtype, bool pairs, cudaStream_t stream);
 
 struct AttentionArgs {
   const void *q;  // [batch, next_n, heads, dim]

@@ -190,14 +190,10 @@ template <int V>
 __device__ __forceinline__ void store_e4m3(uint8_t *dst, const float (&v)[V], float inv) {
   if constexpr (V == 1) {
     *dst = static_cast<uint8_t>(e4m3x4(v[0] * inv, 0.0f, 0.0f, 0.0f));
-  } else if constexpr (V == 2) {
+  } else {
+    static_assert(V == 2, "one or two");
     *reinterpret_cast<uint16_t *>(dst) =
         static_cast<uint16_t>(e4m3x4(v[0] * inv, v[1] * inv, 0.0f, 0.0f));
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<uint32_t *>(dst + i) =
-          e4m3x4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
   }
 }
 

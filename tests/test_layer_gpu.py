@@ -157,6 +157,8 @@ CASES = [  # (seq_lens after the write, new tokens of each)
     ([130, 4, 67, 0, 3], [4, 4, 4, 4, 4]),             # one idle, one shorter than its tokens
     ([100, 33, 300, 64, 129], [37, 0, 170, 64, 1]),    # ragged, one without new tokens
     ([257, 31], [257, 30]),
+    ([70, 20, 12, 7], [12, 12, 12, 12]),               # equal runs over a block's end; one too short
+    ([200, 90], [80, 80]),
 ]
 
 
