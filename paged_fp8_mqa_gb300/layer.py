@@ -196,8 +196,12 @@ def _requests(block_tables, seq_lens, batch, index):
     row_stride, unit = block_tables.stride()
     if width > 1 and unit != 1:
         raise ValueError("block_tables rows must be contiguous (stride(1) == 1)")
-    return (block_tables.data_ptr(), max(row_stride, width), width, seq_lens.data_ptr(),
-            max(seq_lens.stride(0), 1))
+    len_stride, = seq_lens.stride()
+    if batch < 2:  # (the stride of a single row means nothing)
+        row_stride, len_stride = width, 1
+    elif row_stride < width or len_stride < 1:
+        raise ValueError("block_tables and seq_lens must not repeat rows (expanded tensors)")
+    return block_tables.data_ptr(), row_stride, width, seq_lens.data_ptr(), len_stride
 
 
 def _tokens(block_tables, seq_lens, token_starts, rows, index):

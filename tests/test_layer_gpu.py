@@ -742,3 +742,25 @@ def test_kv_append_long_runs_equal_their_parts():
     whole = v[order].transpose(0, 2, 1, 3).reshape(-1, H, D)[:T]
     s = f64(ends[0][3])[order].repeat(bs, 0)[:T, :, None]
     assert (np.abs(whole - f64(y)) <= np.maximum(2.0 ** -4 * np.abs(f64(y)), 2.0 ** -10 * s)).all()
+
+
+@pytest.mark.parametrize("which", ["tables", "lens"])
+def test_expanded_tables_and_lengths_are_refused(which):
+    B, H, D, bs = 3, 2, 64, 32
+    pool = torch.zeros(8, H, bs, D, dtype=torch.uint8, device="cuda")
+    sc = torch.ones(8, H, device="cuda")
+    bt = torch.zeros(B, 2, dtype=torch.int32, device="cuda")
+    sl = torch.ones(B, dtype=torch.int32, device="cuda")
+    if which == "tables":
+        bt = bt[:1].expand(B, 2)
+    else:
+        sl = sl[:1].expand(B)
+    x = torch.zeros(B, H, D, dtype=torch.bfloat16, device="cuda")
+    fused = torch.zeros(8, bs * (D + 4), dtype=torch.uint8, device="cuda")
+    for call in (lambda: idx.attention_fp8(x[:, None], pool, pool, sc, sc, bt, sl),
+                 lambda: idx.kv_append(x, x, pool, pool, sc, sc, bt, sl),
+                 lambda: idx.index_prepare(x[:, 0], fused, bt, sl)):
+        with pytest.raises(ValueError, match="expanded"):
+            call()
+    # One request: the strides of its only row mean nothing.
+    idx.attention_fp8(x[:1, None], pool, pool, sc, sc, bt[:1], sl[:1].expand(1))
