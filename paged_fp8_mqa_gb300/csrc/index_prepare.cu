@@ -19,6 +19,21 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kTiny = 7.8886090522101180541e-31f;  // 2^-100: a row of zeros has a scale too
 
+// x / scale, rounded, for a piece (inv: 1 / scale within a unit or two).
+template <int V>
+__device__ __forceinline__ void quotients(float (&x)[V], float scale, float inv) {
+  if constexpr (V == 2) {
+    const float2 a = make_float2(x[0], x[1]), i2 = make_float2(inv, inv);
+    const float2 q = __fmul2_rn(a, i2);
+    const float2 r = __ffma2_rn(__ffma2_rn(q, make_float2(-scale, -scale), a), i2, q);
+    x[0] = r.x;
+    x[1] = r.y;
+  } else {
+    const float q = x[0] * inv;
+    x[0] = fmaf(fmaf(q, -scale, x[0]), inv, q);
+  }
+}
+
 // A row of D elements in a warp (see kPieces).
 template <typename T, int V, int D>
 struct Row {
@@ -44,16 +59,26 @@ struct Row {
       amax = 0.0f;
 #pragma unroll
       for (int i = 0; i < N; ++i) amax = largest_finite(v[i], amax);
-      amax = warp_max(amax);
+      amax = fmaxf(warp_max(amax), kTiny);
+#pragma unroll
+      for (int i = 0; i < N; ++i)  // (an infinity is held at the largest code, as this is)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (is_inf(fabsf(v[i][j]))) v[i][j] = copysignf(amax, v[i][j]);
     }
-    // No division (46 instructions each): the scale is within a unit of the 24th bit of
-    // max|x| / 448, and the quotients, by its reciprocal, within three, before they are rounded to
-    // four bits.
+    // The scale is within a unit of the 24th bit of max|x| / 448 (a product).  The codes are those of
+    // the quotients by it as a division rounds them.  A division an element would be 46
+    // instructions; the product with a reciprocal alone, three units off, put one code in 10^5 on
+    // its neighbour.  One step of Markstein's mends it: the remainder x - q scale comes out of one
+    // fused operation, and q + remainder * inv is within 2^-21 of a unit before it is rounded.
     const float scale = fmaxf(amax, kTiny) * (1.0f / 448.0f);
     const float inv = __fdividef(1.0f, scale);
     if (dst != nullptr) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) store_e4m3<V>(dst + (lane + 32 * i) * V, v[i], inv);
+      for (int i = 0; i < N; ++i) {
+        quotients(v[i], scale, inv);
+        store_e4m3<V>(dst + (lane + 32 * i) * V, v[i]);
+      }
     }
     return scale;
   }
@@ -63,10 +88,10 @@ struct Row {
 // are found once for them; their loads are on their way before that, four rows at a time.  Units
 // after that: a key each.
 //
-// 465 MB of prompts take 103 us (floor 69): a warp a row and two elements a lane, so that a warp's
-// loads of angles are whole lines and its lanes hold four registers of them for sixteen rows.  With
-// eight lanes a row and 16-byte pieces, whose angles lie 64 bytes apart, it was 114 to 141 us, at
-// best with 32 registers and no row ahead.
+// 465 MB of prompts take 117 us (floor 69; 103 with a product in place of the rounded quotient): a
+// warp a row and two elements a lane, so that a warp's loads of angles are whole lines and its lanes
+// hold four registers of them for sixteen rows.  With eight lanes a row and 16-byte pieces, whose
+// angles lie 64 bytes apart, it was 11 to 38 us more, at best with 32 registers and no row ahead.
 template <typename T, int V, int D, int HEADS>
 __global__ void __launch_bounds__(kThreads, 6) k_index_prepare(const IndexArgs a, uint32_t units,
                                                             uint32_t share) {

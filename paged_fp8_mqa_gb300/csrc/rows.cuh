@@ -185,16 +185,23 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return out;
 }
 
-// V values times inv as e4m3 bytes.
+// V values as e4m3 bytes.
 template <int V>
-__device__ __forceinline__ void store_e4m3(uint8_t *dst, const float (&v)[V], float inv) {
+__device__ __forceinline__ void store_e4m3(uint8_t *dst, const float (&v)[V]) {
   if constexpr (V == 1) {
-    *dst = static_cast<uint8_t>(e4m3x4(v[0] * inv, 0.0f, 0.0f, 0.0f));
+    *dst = static_cast<uint8_t>(e4m3x4(v[0], 0.0f, 0.0f, 0.0f));
   } else {
     static_assert(V == 2, "one or two");
-    *reinterpret_cast<uint16_t *>(dst) =
-        static_cast<uint16_t>(e4m3x4(v[0] * inv, v[1] * inv, 0.0f, 0.0f));
+    *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(e4m3x4(v[0], v[1], 0.0f, 0.0f));
   }
+}
+// V values times inv.
+template <int V>
+__device__ __forceinline__ void store_e4m3(uint8_t *dst, const float (&v)[V], float inv) {
+  float scaled[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) scaled[j] = v[j] * inv;
+  store_e4m3<V>(dst, scaled);
 }
 
 // The low two e4m3 bytes as floats (exact: every e4m3 value is a float16).
