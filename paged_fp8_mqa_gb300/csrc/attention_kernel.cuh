@@ -4,21 +4,26 @@
 // over the positions p <= seq_lens[b] - next_n + t, or over those of them that the select stored
 // in the row's slots.
 //
-// Both products run on the tensor core in e4m3, straight from the cache's bytes: the cache is
-// never converted.  The other operand keeps its precision by being split into e4m3 parts:
+// Both products run on the tensor core in 8 bits, straight from the cache's bytes: the cache is
+// never converted.  The other operand keeps its precision by being split into 8-bit parts:
 //   * a query row is scaled by a power of two to [128, 256) and written as hi + lo, each the
 //     e4m3 nearest to what is left: 4 + 4 bits hold a bfloat16's 8 exactly (down to 2^-18 of the
 //     row's largest magnitude); a float16's 11 bits take three parts.  Products of e4m3 values
 //     are exact and sums float32, so the scores are those of the unrounded queries.  The parts'
 //     products go into the same accumulator.
-//   * a weight is written the same way: within 2^-8 of itself with two parts (what a bfloat16
-//     weight would be), 2^-12 with three, or 2^-18 of the row's largest.  Its parts stand at
-//     different powers of two, in columns of their own, and are added when O is read.
+//   * a weight is written as e5m2 parts, three for bfloat16 and four for float16, held 2^3, 2^7 and
+//     2^11 up after the first: within 2^-10 of itself (2^-14 with four), or 2^-34 (2^-38) of the
+//     row's largest.  The parts stand in columns of their own and are added when O is read.  e5m2 for
+//     its reach: a first token of no value that takes most of a row's weight, or a block with a
+//     large value scale, leaves an output that is all small weights, and the denominator counts
+//     them all.  (Two e4m3 parts ended 2^-18 below the largest: with 131,072 positions behind
+//     such a token the output was 0.8 of itself off.  e4m3 and e5m2 reach as far, but hold what is
+//     2^-14 below the largest to one part in eight.)
 // The weights that meet V carry the block scales: with z' = log2(e) z + log2|vs| they are
 // u = 2^(z' - ref), sign(vs) applied, so that O = sum u v needs no scale of its own and may be
 // accumulated in tensor memory over tiles of any scales, and the softmax's denominator is
 // l = sum u / |vs| in float32; out = O / l.  ref follows the running maximum of z' from below: it
-// moves (to the maximum) only when some u would leave e4m3's range, and then O and l are rescaled.
+// moves (to the maximum) only when some u would leave e5m2's range, and then O and l are rescaled.
 //
 // A tile is 128 positions of one K/V head.  S^T[128 positions x rows] = K Q^T puts a position in
 // each lane of tensor memory and the rows that share the K/V head (query heads times draft slots)
@@ -46,14 +51,14 @@ constexpr int kTile = 128;                     // positions of a tile
 constexpr uint64_t kWaitNs = 1000000000ull;    // 1 s: far beyond any legitimate wait
 constexpr int kNone = INT_MAX;                 // the position of a token that no row sees
 constexpr float kRefNone = -1e30f;             // the reference of a row that has seen nothing
-// Weights are 2^(z' - ref), at most 2^4 when ref is set; ref moves when one would pass 2^8.8 = 446,
-// just inside e4m3's 448, that is when a row's maximum has grown 28-fold.  Each part after the
-// first is held times 2^4 more, which keeps what two parts cannot hold at 2^-18 of the largest
-// weight as if it stood at the top of e4m3's range, where a growth of 1.7 would move ref.
-constexpr float kTop = 4.0f, kMost = 8.8f, kPartUp = 16.0f;
+// Weights are 2^(z' - ref), at most 2^11 when ref is set; ref moves when one would pass 2^15.8 = 57,052,
+// just inside e5m2's 57,344, that is when a row's maximum has grown 28-fold.  Each part's rounding
+// leaves at most 2^-3 of the binade to the second and 2^-4 to those after it, so that no part leaves
+// the range either, and the last of three ends at 2^-24, the last of four at 2^-28.
+constexpr float kTop = 11.0f, kMost = 15.8f, kUp2 = 8.0f, kUp = 16.0f;
 constexpr float kLeastScale = 7.8886090522101180541e-31f;  // 2^-100: a value scale below it is 0
 
-// One kernel's shape: R rows, PARTS parts a row, head_dim D.
+// One kernel's shape: R rows, PARTS parts a query row, one more a weight, head_dim D.
 template <int D_, int R_, int PARTS_, bool SELECT_>
 struct AttnCfg {
   static constexpr int D = D_, R = R_, PARTS = PARTS_;
@@ -62,7 +67,8 @@ struct AttnCfg {
   // else each part is a product of its own into the same columns.
   static constexpr bool CAT = R == 8;
   static constexpr int NS = CAT ? 16 : R;             // columns of S
-  static constexpr int NO = R * PARTS;                // columns of O
+  static constexpr int WPARTS = PARTS + 1;
+  static constexpr int NO = (R * WPARTS + 15) / 16 * 16;  // columns of O (N in steps of 16)
   static constexpr int PASSES = CAT ? 1 : PARTS;      // products that make S
   static constexpr int WG = R == 64 ? 2 : 1;          // softmax warpgroups, R / WG rows each
   static constexpr int RT = R / WG;
@@ -74,16 +80,19 @@ struct AttnCfg {
   static constexpr int COLS = 2 * NS + NO;            // two of S, one of O
   static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   // CTAs on an SM, each with a pipeline of its own, so that one's loads and products run beside the
-  // other's softmax.  Three of two stages instead of two of three: decode 466 us for 338, as what
-  // the next launch needs no longer fits beside them.  64 rows in chunks of 32, two CTAs an SM:
+  // other's softmax.  Three of two stages instead of two of three: decode took 1.4 times as long, as
+  // what the next launch needs no longer fits beside them.  64 rows in chunks of 32, two CTAs an SM:
   // one long request 29 us for 27, a batch of 64 requests with 64 heads on one 128 for 96.
   static constexpr int CTAS = R == 64 ? 1 : 2;
   static constexpr int KV_BYTES = 2 * kTile * D;
   static constexpr int Q_BYTES = (R * PARTS * D + 1023) / 1024 * 1024;
-  static constexpr int P_BYTES = R * PARTS * kTile;   // one of two
+  static constexpr int P_BYTES = NO * kTile;          // a tile's weights
+  // They take the place of the tile's keys, which have been read by then, where they fit it; else
+  // two buffers of their own.
+  static constexpr bool OVER_K = P_BYTES <= kTile * D;
   static constexpr int AUX = kTile * 16;              // a stage's Token records
   static constexpr int MISC = 48 * R + 3 * D * 4 + 256;
-  static constexpr int FIXED = 1024 + Q_BYTES + 2 * P_BYTES + MISC;
+  static constexpr int FIXED = 1024 + Q_BYTES + (OVER_K ? 0 : 2 * P_BYTES) + MISC;
   static constexpr int ROOM = CTAS == 2 ? 115456 : 231424;
   static constexpr int FIT = (ROOM - FIXED) / (KV_BYTES + AUX);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
@@ -122,6 +131,54 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Float16 pairs rounded to e5m2, which is their upper bytes: half a unit added, in sign and
+// magnitude (halves go up; what is left over is exact, whichever way).  The value stands in bytes 1
+// and 3; the low bytes mean nothing.  (A NaN becomes -0: its row's sum is NaN.)
+__device__ __forceinline__ uint32_t round_e5m2(uint32_t h2) { return h2 + 0x00800080u; }
+// The four e5m2 bytes of two rounded pairs.
+__device__ __forceinline__ uint32_t e5m2_bytes(uint32_t lo, uint32_t hi) {
+  return __byte_perm(lo, hi, 0x7531);
+}
+// up times what rounding left of a pair, exact.
+__device__ __forceinline__ uint32_t rest_e5m2(uint32_t h2, uint32_t rounded, float up) {
+  const uint32_t d = rounded & 0xFF00FF00u;
+  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&h2),
+                                    *reinterpret_cast<const __half2 *>(&d)),
+                            __float2half2_rn(up));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Four weights (0 .. 2^kMost) as W e5m2 parts each, a word a part.
+template <int W>
+__device__ __forceinline__ void weight_parts(float2 p0, float2 p1, uint32_t (&out)[W]) {
+  uint32_t h0, h1;
+  constexpr int FIRST = W == 4 ? 1 : 0;
+  if constexpr (W == 4) {
+    // A float16 holds 2^-11 of the whole weight; of what a first part leaves, 2^-15.
+    uint32_t lo = round_e5m2(half2_bits(p0.x, p0.y)), hi = round_e5m2(half2_bits(p1.x, p1.y));
+    out[0] = e5m2_bytes(lo, hi);
+    lo &= 0xFF00FF00u, hi &= 0xFF00FF00u;
+    const float2 up = make_float2(kUp2, kUp2), down = make_float2(-kUp2, -kUp2);
+    p0 = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&lo)), down, __fmul2_rn(p0, up));
+    p1 = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&hi)), down, __fmul2_rn(p1, up));
+  }
+  h0 = half2_bits(p0.x, p0.y);
+  h1 = half2_bits(p1.x, p1.y);
+#pragma unroll
+  for (int part = FIRST; part < W; ++part) {
+    const uint32_t lo = round_e5m2(h0), hi = round_e5m2(h1);
+    out[part] = e5m2_bytes(lo, hi);
+    if (part + 1 < W) {
+      h0 = rest_e5m2(h0, lo, part == 0 ? kUp2 : kUp);
+      h1 = rest_e5m2(h1, hi, part == 0 ? kUp2 : kUp);
+    }
+  }
 }
 
 // Each thread of the warp reads NC consecutive columns of its TMEM lane.
@@ -183,6 +240,7 @@ __device__ __forceinline__ uint64_t smem_desc_p(uint32_t saddr) {
 }
 
 constexpr uint32_t kMajorMN_A = 1u << 15, kMajorMN_B = 1u << 16;
+constexpr uint32_t kE5m2_B = 1u << 10;  // (the operands' types are set one by one)
 
 // Byte offset of byte x of row n in K-major rows of D bytes with the matching swizzle.
 template <int D>
@@ -295,14 +353,19 @@ template <class C, typename T>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     k_attention(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const AttentionArgs a, const AttnSplit split, GroupParts *parts) {
-  constexpr int D = C::D, R = C::R, RT = C::RT, NS = C::NS, PARTS = C::PARTS;
+  constexpr int D = C::D, R = C::R, RT = C::RT, NS = C::NS, PARTS = C::PARTS, WPARTS = C::WPARTS;
   extern __shared__ uint8_t s_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *s_kv = base;                              // [stage][K tile, V tile]
   uint8_t *s_q = s_kv + C::STAGES * C::KV_BYTES;     // [PARTS * R][D], K-major, swizzled
-  uint8_t *s_p = s_q + C::Q_BYTES;                   // [2][PARTS * R / 16][kTile][16]
-  uint8_t *at = s_p + 2 * C::P_BYTES;
+  uint8_t *at = s_q + C::Q_BYTES;
+  // A tile's weights, [NO / 16][kTile][16].
+  uint8_t *s_p = at;
+  if constexpr (!C::OVER_K) at += 2 * C::P_BYTES;
+  const auto weights_of = [&](uint32_t tile, int stage) {
+    return C::OVER_K ? s_kv + stage * C::KV_BYTES : s_p + (tile & 1) * C::P_BYTES;
+  };
   Token *s_tok = reinterpret_cast<Token *>(at);      // [stage][kTile]
   at += C::STAGES * C::AUX;
   float *s_max = reinterpret_cast<float *>(at);      // [R][4 warps]
@@ -618,7 +681,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   } else if (warp == 1) {
     // ============================== MMA issuer ==================================================
     constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, NS);
-    constexpr uint32_t idesc_o = idesc_e4m3_f32(D, C::NO) | kMajorMN_A | kMajorMN_B;
+    constexpr uint32_t idesc_o = idesc_e4m3_f32(D, C::NO) | kE5m2_B | kMajorMN_A | kMajorMN_B;
     const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
     const uint32_t o_tmem = tmem + 2 * NS;
     uint32_t tile = 0, seg = 0;
@@ -659,7 +722,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if (!mbar_wait(&p_full[tile & 1], (tile >> 1) & 1, kWaitNs)) return false;
         tc_fence_after_sync();
         const uint64_t v_desc = smem_desc_mn<D>(smem_addr(s_kv + stage * C::KV_BYTES + kTile * D));
-        const uint64_t p_desc = smem_desc_p(smem_addr(s_p + (tile & 1) * C::P_BYTES));
+        const uint64_t p_desc = smem_desc_p(smem_addr(weights_of(tile, stage)));
 #pragma unroll
         for (int k = 0; k < kTile / 32; ++k)
           mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o, i + k > 0);
@@ -844,7 +907,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
         }
         if (any_of_group(move)) {
-          // Some weight would leave e4m3's range, or a row sees its first position: the references
+          // Some weight would leave e5m2's range, or a row sees its first position: the references
           // move to the maxima so far.
           float mine = -INFINITY;  // lane r: row r0 + r
 #pragma unroll
@@ -882,7 +945,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
             tc_fence_after_sync();
 #pragma unroll 1
-            for (int part = 0; part < PARTS; ++part) {
+            for (int part = 0; part < WPARTS; ++part) {
               const uint32_t o_at = lane_base + 2 * NS + part * R + r0;
               uint32_t v[RT];
               tmem_ld_cols<RT>(o_at, v);
@@ -897,18 +960,18 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
         }
         // ---- weights, their parts, the running sums ------------------------------------------------
-        // The weights' buffer was last read by the product two tiles ago.
+        // The weights' buffer was last read by the product two tiles ago.  (In the place of the keys
+        // they need not wait; but whoever waits for a barrier has to see all its phases.)
         if (tile >= 2) wait(&pv_done[tile & 1], ((tile >> 1) - 1) & 1);
-        uint8_t *sp = s_p + (tile & 1) * C::P_BYTES + token * 16;
+        uint8_t *sp = weights_of(tile, stage) + token * 16;
         const float inv_v = fabsf(tok.inv_v);
         // The weights of a position whose value scale is negative or 0 (as good as): rare, so asked
         // of the whole warp.
         const bool odd = __any_sync(0xffffffffu, tok.inv_v < 0.0f || inv_v >= 1.0f / kLeastScale);
         const uint32_t flip = tok.inv_v < 0.0f ? 0x80808080u : 0u;
         const uint32_t live = inv_v < 1.0f / kLeastScale ? 0xFFFFFFFFu : 0u;
-        uint32_t bytes[PARTS][4];
-        const float2 inv2 = make_float2(inv_v, inv_v), up2 = make_float2(kPartUp, kPartUp),
-                     down2 = make_float2(-kPartUp, -kPartUp);
+        uint32_t bytes[WPARTS][4];
+        const float2 inv2 = make_float2(inv_v, inv_v);
 #pragma unroll
         for (int r = 0; r < RT; r += 4) {
           float2 p[2];
@@ -917,28 +980,26 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             p[j] = make_float2(fast_exp2(y[r / 2 + j].x), fast_exp2(y[r / 2 + j].y));
             sum[r / 2 + j] = __ffma2_rn(p[j], inv2, sum[r / 2 + j]);
           }
+          uint32_t four[WPARTS];
+          weight_parts<WPARTS>(p[0], p[1], four);
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part) {
-            const uint32_t b = e4m3x4(p[0].x, p[0].y, p[1].x, p[1].y);
-            bytes[part][(r / 4) % 4] = b;
-            if (part + 1 < PARTS) {  // 16 (p - b), exact
-              p[0] = __ffma2_rn(e4m3x2_to_f32(b), down2, __fmul2_rn(p[0], up2));
-              p[1] = __ffma2_rn(e4m3x2_to_f32(b >> 16), down2, __fmul2_rn(p[1], up2));
-            }
-          }
+          for (int part = 0; part < WPARTS; ++part) bytes[part][(r / 4) % 4] = four[part];
           if (odd && (r % 16 == 12 || r + 4 == RT)) {
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
+            for (int part = 0; part < WPARTS; ++part)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) bytes[part][q] = (bytes[part][q] & live) ^ flip;
+              for (int q = 0; q < (RT < 16 ? RT / 4 : 4); ++q)
+                bytes[part][q] = (bytes[part][q] & live) ^ flip;
           }
-          if constexpr (C::CAT) {  // both parts of the eight rows are one group of 16 n
-            if (r == 4)
+          if constexpr (C::CAT) {  // a group of 16 n: the first two parts of the eight rows; then the third
+            if (r == 4) {
               *reinterpret_cast<uint4 *>(sp) =
                   make_uint4(bytes[0][0], bytes[0][1], bytes[1][0], bytes[1][1]);
+              *reinterpret_cast<uint2 *>(sp + kTile * 16) = make_uint2(bytes[2][0], bytes[2][1]);
+            }
           } else if (r % 16 == 12) {
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
+            for (int part = 0; part < WPARTS; ++part)
               *reinterpret_cast<uint4 *>(sp + (part * R + r0 + r - 12) / 16 * (kTile * 16)) =
                   make_uint4(bytes[part][0], bytes[part][1], bytes[part][2], bytes[part][3]);
           }
@@ -979,15 +1040,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       tc_fence_after_sync();
       float acc[RT];
 #pragma unroll
-      for (int part = PARTS - 1; part >= 0; --part) {
+      for (int part = WPARTS - 1; part >= 0; --part) {
         uint32_t v[RT];
         tmem_ld_cols<RT>(lane_base + 2 * NS + part * R + r0, v);
         tmem_ld_wait();
         reg_fence(v);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-          acc[r] = part == PARTS - 1 ? __uint_as_float(v[r])
-                                     : fmaf(acc[r], 1.0f / kPartUp, __uint_as_float(v[r]));
+          acc[r] = part == WPARTS - 1
+                       ? __uint_as_float(v[r])
+                       : fmaf(acc[r], 1.0f / (part == 0 ? kUp2 : kUp), __uint_as_float(v[r]));
       }
       tc_fence_before_sync();
       float m_run = kRefNone;  // lane r: the reference of row r0 + r

@@ -90,3 +90,106 @@ def test_index_rows_with_an_infinity_hold_the_quotients():
     scale = pool[:, bs * D:bs * D + 4].copy().view(np.float32)
     want = plain.e4m3(x.cpu().numpy() / scale)
     np.testing.assert_array_equal(plain.E4M3[pool[:, :D]], want)
+
+
+# ---- weights far below a row's largest -------------------------------------------------------------
+
+def tail_case(N, H, Hkv, D, bs, name, *, share=None, gap=None, spread, ratio=1.0, n=1, seed=0):
+    """Requests of N and of a few positions fewer, whose first position takes `share` of each row's
+    weight (or stands `gap` above the mean score of the others) and has the value 0; the
+    other values have a mean of 1.  ratio: the first block's value scale over the others' (its values
+    are all 0 then)."""
+    g = gen(seed)
+    lens = [N, N - min(7, N - n - 1)]
+    pages = -(-N // bs)
+    rows = [torch.randperm(2 * pages, generator=g)]
+    rows = torch.stack((rows[0][:pages], rows[0][pages:]))
+    k = torch.randn(2 * pages, Hkv, bs, D, generator=g).mul(60).to(torch.float8_e4m3fn)
+    v = (torch.randn(2 * pages, Hkv, bs, D, generator=g) + 1).mul(60).to(torch.float8_e4m3fn)
+    ks, vs = (torch.full((2 * pages, Hkv), 1.0 / 60) for _ in range(2))
+    # Four channels are the first position's alone: its key there and the queries' give it its score.
+    k.view(torch.uint8)[..., :4] = 0
+    q = torch.randn(2, n, H, D, generator=g) * spread
+    q[..., :4] = 16.0
+    q = q.to(DTYPES[name])
+    aim = gap if gap is not None else math.log(share / (1 - share)) + math.log(N) + spread ** 2 / 2
+    code = torch.tensor(aim * D ** 0.5 / 64.0 * 60).to(torch.float8_e4m3fn)
+    assert float(code) < 448
+    for b in range(2):
+        first = rows[b, 0]
+        k[first, :, 0] = torch.zeros(Hkv, D).to(torch.float8_e4m3fn)
+        k[first, :, 0, :4] = code
+        v.view(torch.uint8)[first, :, :bs if ratio != 1 else 1] = 0
+        vs[first] *= ratio
+    on = lambda t: t.to(dev())  # noqa: E731
+    return dict(q=on(q), k=on(k), v=on(v), ks=on(ks), vs=on(vs), bt=on(rows.int()),
+                seq=on(torch.tensor(lens, dtype=torch.int32)), rows=rows.numpy(), lens=lens, bs=bs, name=name)
+
+
+def check_tail(c, picked=False, num_sms=0):
+    """The limit is relative to sum w |v|, with no term that grows with the length: a weight is within
+    2^-10 of itself (bfloat16; float16 2^-14) or 2^-35 of the row's largest, which 2^-14 covers here; the
+    scores are off by dz (a query element to 2^-18 of its row's largest, float32 sums); the output is
+    rounded once (a float16 below its normals to 2^-25)."""
+    q = c["q"]
+    B, n, H, D = q.shape
+    more = {}
+    if picked:  # everything, in an order of its own
+        most = max(c["lens"])
+        cand = torch.zeros(B * n, most + 3, 2, dtype=torch.int32)
+        ranges = torch.tensor([[1] * (B * n), [1 + c["lens"][r // n] for r in range(B * n)]], dtype=torch.int32)
+        for r in range(B * n):
+            m = c["lens"][r // n]
+            cand[r, 1:1 + m, 0] = torch.randperm(m, generator=gen(r)).int()
+        more = dict(candidates=cand.to(dev()), ranges=ranges.to(dev()))
+    lse = torch.empty(B, n, H, device=dev())
+    out = idx.attention_fp8(q, c["k"], c["v"], c["ks"], c["vs"], c["bt"], c["seq"], lse=lse, num_sms=num_sms, **more)
+    clean()
+    qq, kk, vv, ks, vs = f64(q), values8(c["k"]), values8(c["v"]), f64(c["ks"]), f64(c["vs"])
+    ref, ref_lse, mag, _ = plain.attention(qq, kk, vv, ks, vs, c["rows"], c["lens"], c["bs"], D ** -0.5)
+    # |k| is at most 5 sigma of the products' sums here: of N(0, 1) elements, D of them.
+    dz = D ** -0.5 * (2.0 ** -18 * np.abs(qq).max(-1) * 1.2 * D + 2.0 ** -17 * np.abs(qq).sum(-1) * 3)
+    w_rel, half, floor = (2.0 ** -10, 2.0 ** -8, 0.0) if c["name"] == "bf16" else (2.0 ** -14, 2.0 ** -11, 2.0 ** -25)
+    lim = (2 * dz[..., None] + w_rel + 2.0 ** -14) * mag
+    lim = lim + half * (np.abs(ref) + lim) + floor
+    err = np.abs(f64(out) - ref)
+    assert (err <= lim).all(), float((err / np.maximum(mag, 1e-30)).max())
+    assert (np.abs(f64(lse) - ref_lse) <= dz + 2.0 ** -17 * (1 + np.abs(ref_lse))).all()
+
+
+TAIL_SHAPES = [  # H, Hkv, D, block, dtype: every width of rows
+    (8, 1, 128, 64, "bf16"), (16, 1, 64, 32, "bf16"), (24, 1, 128, 64, "bf16"), (32, 1, 64, 32, "bf16"),
+    (40, 1, 64, 128, "bf16"), (64, 1, 128, 64, "bf16"),
+    (8, 1, 64, 32, "f16"), (32, 1, 128, 64, "f16"), (30, 1, 64, 64, "f16"), (64, 1, 128, 64, "f16"),
+]
+
+
+@pytest.mark.parametrize("H,Hkv,D,bs,name", TAIL_SHAPES)
+@pytest.mark.parametrize("N,how", [
+    (8192, dict(share=0.8, spread=2.0)), (32768, dict(share=0.5, spread=1.0)), (32768, dict(gap=10.0, spread=0.3, ratio=64.0)),
+    (32768, dict(gap=8.0, spread=0.3, ratio=256.0)), (4096, dict(gap=13.0, spread=0.5, ratio=256.0)),
+    (20, dict(gap=10.0, spread=0.5)), (20, dict(gap=16.0, spread=0.5)), (5, dict(gap=12.0, spread=0.5))])
+def test_attention_keeps_small_weights(H, Hkv, D, bs, name, N, how):
+    check_tail(tail_case(N, H, Hkv, D, bs, name, **how))
+
+
+@pytest.mark.parametrize("H,Hkv,D,bs,name", [(8, 1, 128, 64, "bf16"), (32, 1, 64, 32, "bf16"), (16, 1, 128, 64, "f16")])
+@pytest.mark.parametrize("share,spread", [(0.5, 0.5), (0.8, 0.5), (0.8, 0.01)])
+@pytest.mark.parametrize("num_sms", [1, 0])
+def test_attention_keeps_small_weights_over_131072_positions(H, Hkv, D, bs, name, share, spread, num_sms):
+    """Two runs for two requests, each uncut, and runs of a few tiles."""
+    check_tail(tail_case(131072, H, Hkv, D, bs, name, share=share, spread=spread), num_sms=num_sms)
+
+
+@pytest.mark.parametrize("H,Hkv,D,bs,name", [(8, 1, 128, 64, "bf16"), (32, 1, 64, 32, "bf16"), (64, 1, 128, 64, "f16")])
+@pytest.mark.parametrize("num_sms", [1, 0])
+def test_attention_keeps_small_weights_of_a_selection(H, Hkv, D, bs, name, num_sms):
+    for N, how in ((8192, dict(share=0.8, spread=1.0)), (2048, dict(gap=10.0, spread=0.3, ratio=64.0)),
+                   (2048, dict(gap=14.0, spread=0.3))):
+        check_tail(tail_case(N, H, Hkv, D, bs, name, **how), picked=True, num_sms=num_sms)
+
+
+@pytest.mark.parametrize("n", [2, 4])
+def test_attention_keeps_small_weights_of_draft_slots(n):
+    check_tail(tail_case(16384, 8, 1, 64, 32, "bf16", share=0.8, spread=0.5, n=n))
+    check_tail(tail_case(2048, 16, 2, 128, 64, "bf16", gap=13.0, spread=0.5, n=n))
