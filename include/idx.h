@@ -488,7 +488,8 @@ int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, 
  *   num_sms       SMs the grid is sized for, one or two CTAs each (0 = this device's SM count)
  *   out           device, dtype [batch][next_n][num_heads][head_dim], contiguous, 16-byte aligned
  *   lse           NULL, or device float32 [batch][next_n][num_heads]: ln sum_p exp(z_p)
- *   workspace     device, 256-byte aligned, idx_attention_workspace_bytes(...) bytes
+ *   workspace     device, 256-byte aligned, idx_attention_workspace_bytes(...) bytes (-1: sizes that
+ *                 idx_attention_fp8 refuses)
  */
 int64_t idx_attention_workspace_bytes(int32_t batch, int32_t next_n, int32_t num_heads,
                                       int32_t kv_heads, int32_t head_dim, int32_t num_sms);

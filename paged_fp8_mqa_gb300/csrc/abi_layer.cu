@@ -298,7 +298,10 @@ IDX_EXPORT int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_he
 IDX_EXPORT int64_t idx_attention_workspace_bytes(int32_t batch, int32_t next_n, int32_t num_heads,
                                                  int32_t kv_heads, int32_t head_dim,
                                                  int32_t num_sms) {
-  if (batch < 0 || next_n < 1 || num_heads < 1 || kv_heads < 1 || head_dim < 1 || num_sms < 0)
+  // (What idx_attention_fp8 refuses has no size; a K/V head without query heads would divide by 0.)
+  if (batch < 0 || batch > idx::kMaxBatch || next_n < 1 || next_n > 4 || kv_heads < 1 ||
+      num_heads < 1 || num_heads > 4096 || num_heads % kv_heads != 0 ||
+      (head_dim != 64 && head_dim != 128) || num_sms < 0)
     return -1;
   int32_t sms = 0;
   if (idx::resolve_sms(num_sms, &sms) != IDX_OK) return -1;

@@ -430,7 +430,7 @@ def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
         need = _sizes.get(sizes)
         if need is None:
             need = idx_attention_workspace_bytes(*sizes[1:])
-            if len(_sizes) < 4096:
+            if need >= 0 and len(_sizes) < 4096:  # (-1: the call below says what is wrong)
                 _sizes[sizes] = need
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
         made.append(workspace)

@@ -193,3 +193,15 @@ def test_attention_keeps_small_weights_of_a_selection(H, Hkv, D, bs, name, num_s
 def test_attention_keeps_small_weights_of_draft_slots(n):
     check_tail(tail_case(16384, 8, 1, 64, 32, "bf16", share=0.8, spread=0.5, n=n))
     check_tail(tail_case(2048, 16, 2, 128, 64, "bf16", gap=13.0, spread=0.5, n=n))
+
+
+# ---- refusals --------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,Hkv", [(4, 8), (1, 2), (12, 8)])
+def test_attention_refuses_heads_that_are_no_multiple(H, Hkv):
+    D, bs = 64, 32
+    pool = torch.zeros(2, Hkv, bs, D, dtype=torch.uint8, device=dev())
+    sc = torch.ones(2, Hkv, device=dev())
+    bt, sl = torch.zeros(2, 1, dtype=torch.int32, device=dev()), torch.ones(2, dtype=torch.int32, device=dev())
+    with pytest.raises(idx.IdxError, match="multiple"):
+        idx.attention_fp8(torch.zeros(2, 1, H, D, dtype=torch.bfloat16, device=dev()), pool, pool, sc, sc, bt, sl)
