@@ -9,6 +9,7 @@ a call allocates (outputs, workspace) belong to PyTorch's caching allocator; the
 from __future__ import annotations
 
 import ctypes
+import functools
 
 IDX_ROTARY_NONE = 0
 IDX_ROTARY_LINEAR = 1
@@ -107,6 +108,22 @@ def _index(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     return t.get_device()
+
+
+def _on_its_device(f):
+    """f with the device of its first argument current: the launch, the SM count and the workspace's
+    size are that device's, whichever is current where f is called."""
+    name = f.__code__.co_varnames[0]
+
+    @functools.wraps(f)
+    def call(*args, **more):
+        import torch
+        index = _index(args[0] if args else more.get(name), name)
+        if index == torch.cuda.current_device():
+            return f(*args, **more)
+        with torch.cuda.device(index):
+            return f(*args, **more)
+    return call
 
 
 def _tensor(t, name, dims, dtype, index):
@@ -246,6 +263,7 @@ def rotary_table(max_positions: int, rot_dim: int, *, base: float = 10000.0, sca
     return table
 
 
+@_on_its_device
 def rotary(x, positions, table, *, interleaved: bool = False, rot_offset: int = 0,
            inverse: bool = False, out=None, stream=None):
     """Rotary positions: x [T, H, D] (float32, float16 or bfloat16; any token and head strides) at
@@ -280,6 +298,7 @@ def rotary(x, positions, table, *, interleaved: bool = False, rot_offset: int = 
     return out
 
 
+@_on_its_device
 def index_prepare(k, kv_fused, block_tables, seq_lens, *, token_starts=None, q=None, weights=None,
                   table=None, interleaved: bool = False, rot_offset: int = 0, q_out=None,
                   weights_out=None, stream=None):
@@ -339,6 +358,7 @@ def index_prepare(k, kv_fused, block_tables, seq_lens, *, token_starts=None, q=N
     return None if q is None else (q_out, weights_out)
 
 
+@_on_its_device
 def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,
               token_starts=None, table=None, interleaved: bool = False, rot_offset: int = 0,
               stream=None):
@@ -366,6 +386,7 @@ def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, 
             *scales, _on(stream, index)))
 
 
+@_on_its_device
 def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,
                   softmax_scale: float | None = None, candidates=None, ranges=None, out=None,
                   lse=None, workspace=None, num_sms: int = 0, stream=None):

@@ -1,7 +1,9 @@
 """The operators around the indexer without a GPU: sizes and devices that they refuse."""
 import pytest
+import torch
 
 import paged_fp8_mqa_gb300 as idx
+from paged_fp8_mqa_gb300 import layer
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -20,3 +22,45 @@ def lib():
 ])
 def test_attention_workspace_of_refused_sizes(batch, next_n, heads, kv_heads, dim, sms):
     assert idx.idx_attention_workspace_bytes(batch, next_n, heads, kv_heads, dim, sms) == -1
+
+
+@pytest.mark.parametrize("call", ["rotary", "index_prepare", "kv_append", "attention_fp8", "keyword"])
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_run_on_their_tensors_device(call, current, monkeypatch):
+    """Tensors said to be on device 1, with device 0 or 1 current: every C call is made with 1 current."""
+    now, entered, seen = [current], [], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+            entered.append(self.index)
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    def c_call(*_):
+        seen.append(now[0])
+        return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(layer, "_index", lambda t, name: 1)
+    monkeypatch.setattr(layer, "_on", lambda *a: 0)
+    monkeypatch.setattr(layer, "_sizes", {})
+    for name in ("idx_rotary", "idx_index_prepare", "idx_kv_append", "idx_attention_fp8",
+                 "idx_attention_workspace_bytes"):
+        monkeypatch.setattr(layer, name, c_call)
+    i32 = torch.int32
+    x, pos = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=i32)
+    table, bt, sl = torch.zeros(8, 32, 2), torch.zeros(2, 1, dtype=i32), torch.ones(2, dtype=i32)
+    pool, sc = torch.zeros(2, 4, 32, 64, dtype=torch.uint8), torch.ones(2, 4)
+    {"rotary": lambda: idx.rotary(x, pos, table),
+     "keyword": lambda: idx.rotary(x=x, positions=pos, table=table),
+     "index_prepare": lambda: idx.index_prepare(x[:, 0], torch.zeros(2, 32 * 68, dtype=torch.uint8), bt, sl),
+     "kv_append": lambda: idx.kv_append(x, x, pool, pool, sc, sc, bt, sl),
+     "attention_fp8": lambda: idx.attention_fp8(x[:, None], pool, pool, sc, sc, bt, sl)}[call]()
+    assert seen == [1] * (2 if call == "attention_fp8" else 1)
+    assert entered == ([1] if current == 0 else []) and now == [current]
