@@ -462,7 +462,8 @@ int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, 
 
 /*
  * Attention over the 8-bit K/V cache (layout as for idx_kv_append; the scales may be any finite
- * numbers).  For row r = b*next_n + t and query head h, with K/V head g = h / (num_heads/kv_heads):
+ * numbers, value scales below 2^-100 counting as 0; a NaN, or an infinite value scale, makes the rows
+ * that see it NaN, lse too).  For row r = b*next_n + t and query head h, with K/V head g = h / (num_heads/kv_heads):
  *
  *   z_p = softmax_scale * k_scale[page(p)][g] * (q[b,t,h,:] . k[p,g,:])
  *   out[b,t,h,:] = sum_p softmax(z)_p * v_scale[page(p)][g] * v[p,g,:]

@@ -113,7 +113,9 @@ __device__ __forceinline__ Token token_of(float k, float v_scale, int pos) {
   Token t;
   const float held = fmaxf(fabsf(v_scale), kLeastScale);
   t.k = k;
-  t.log_v = __log2f(held);
+  // (A NaN makes the weight one in the rows that see the position, and only in those: a weight of 0
+  // meets inv_v, which stays a number.)
+  t.log_v = v_scale == v_scale ? __log2f(held) : v_scale;
   t.inv_v = copysignf(1.0f / held, v_scale);
   t.pos = pos;
   return t;

@@ -195,6 +195,46 @@ def test_attention_keeps_small_weights_of_draft_slots(n):
     check_tail(tail_case(2048, 16, 2, 128, 64, "bf16", gap=13.0, spread=0.5, n=n))
 
 
+# ---- scales that are not finite --------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,Hkv,D,bs,name,n", [(8, 2, 128, 32, "bf16", 4), (64, 2, 64, 32, "f16", 1),
+                                               (48, 2, 64, 32, "bf16", 3)])
+@pytest.mark.parametrize("which,value", [("ks", math.nan), ("vs", math.nan), ("vs", math.inf), ("vs", -math.inf)])
+@pytest.mark.parametrize("picked", [False, True])
+def test_attention_over_a_scale_that_is_not_finite(H, Hkv, D, bs, name, n, which, value, picked):
+    """The rows that see the block are NaN in every element; the others keep their bits."""
+    lens = [65 + (n - 1) // 2, 200, 31]
+    g = gen(71)
+    bt = torch.randperm(16, generator=g).int()[:12].view(3, 4)
+    bt = torch.cat((bt, torch.arange(16, 28).int().view(3, 4)), 1)
+    k, v = (torch.randn(28, Hkv, bs, D, generator=g).mul(60).to(torch.float8_e4m3fn).to(dev()) for _ in range(2))
+    s = {x: (torch.rand(28, Hkv, generator=g) * 0.02 + 0.01).to(dev()) for x in ("ks", "vs")}
+    q = torch.randn(3, n, H, D, generator=g).to(DTYPES[name]).to(dev())
+    more = {}
+    if picked:
+        cand = torch.stack([torch.randperm(200, generator=g) for _ in range(3 * n)]).int()
+        cand = torch.stack((cand, cand), -1).contiguous().to(dev())
+        more = dict(candidates=cand, ranges=torch.tensor([[0] * 3 * n, [200] * 3 * n], dtype=torch.int32, device=dev()))
+    def call():  # noqa: E306
+        return idx.attention_fp8(q, k, v, s["ks"], s["vs"], bt.to(dev()), torch.tensor(lens, dtype=torch.int32, device=dev()),
+                                 **more)
+    base = call()
+    bad = [(0, 2, 0), (1, 5, 1)]  # request, its block, K/V head; request 0's block 2 begins at position 64
+    for b, j, h in bad:
+        s[which][int(bt[b, j]), h] = value
+    out = call()
+    clean()
+    assert not torch.isnan(base).any()
+    per = H // Hkv
+    for b in range(3):
+        for t in range(n):
+            extent = lens[b] - n + t + 1
+            for h in range(Hkv):
+                hit = any(bb == b and hh == h and extent > j * bs for bb, j, hh in bad)
+                got = out[b, t, h * per:(h + 1) * per]
+                assert torch.isnan(got).all() if hit else torch.equal(got, base[b, t, h * per:(h + 1) * per]), (b, t, h)
+
+
 # ---- refusals --------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("H,Hkv", [(4, 8), (1, 2), (12, 8)])
