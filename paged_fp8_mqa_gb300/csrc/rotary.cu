@@ -78,9 +78,15 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotaryArgs a, uint32_
 #pragma unroll
     for (int j = 0; j < V; ++j) cs[j].y *= a.sin_sign;
   } else {
+    // As it is, to the bit: a product with a sine of 0 would make an infinity's partner NaN.
     if (item == 0 && h0 == 0) atomicOr(&g_rotary_status, IDX_DEV_BAD_POSITION);
 #pragma unroll
-    for (int j = 0; j < V; ++j) cs[j] = make_float2(1.0f, 0.0f);
+    for (int h = 0; h < HEADS; ++h)
+      if (h < n) {
+        store_piece<T, V>(out + h * a.out_head + da, va[h]);
+        store_piece<T, V>(out + h * a.out_head + db, vb[h]);
+      }
+    return;
   }
 #pragma unroll
   for (int h = 0; h < HEADS; ++h) {

@@ -92,6 +92,25 @@ def test_index_rows_with_an_infinity_hold_the_quotients():
     np.testing.assert_array_equal(plain.E4M3[pool[:, :D]], want)
 
 
+# ---- rotary positions outside the table --------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot,offset", [(64, 32, 16), (30, 10, 3)])   # wide pieces, single elements
+@pytest.mark.parametrize("layout", ["plain", "in place"])
+def test_rotary_leaves_rows_past_the_table_to_the_bit(name, interleaved, D, rot, offset, layout):
+    clean()
+    x = torch.randn(3, 3, D, generator=gen(5))
+    x[:, :, 1::5], x[:, :, 2::7], x[:, :, 3::11], x[:, :, 4::9] = math.inf, -0.0, math.nan, -math.inf
+    x = x.to(DTYPES[name]).to(dev())
+    bits = torch.int32 if name == "f32" else torch.int16
+    keep = x.clone()
+    y = idx.rotary(x, torch.tensor([-1, 10, 2 ** 31 - 1], dtype=torch.int32, device=dev()), idx.rotary_table(10, rot),
+                   interleaved=interleaved, rot_offset=offset, out=x if layout == "in place" else None)
+    clean(idx.IDX_DEV_BAD_POSITION)
+    assert torch.equal(y.view(bits), keep.view(bits))
+
+
 # ---- weights far below a row's largest -------------------------------------------------------------
 
 def tail_case(N, H, Hkv, D, bs, name, *, share=None, gap=None, spread, ratio=1.0, n=1, seed=0):
