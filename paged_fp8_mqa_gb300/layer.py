@@ -347,10 +347,13 @@ def index_prepare(k, kv_fused, block_tables, seq_lens, *, token_starts=None, q=N
                 or not weights_out.is_contiguous():
             raise ValueError("q_out and weights_out must be contiguous with the shapes of q and "
                              "weights")
-        w_to = weights_out.data_ptr()
-        q_args = (q.data_ptr(), q_token, q_head, weights.data_ptr(), w_token)
+        if H:
+            w_to = weights_out.data_ptr()
+            q_args = (q.data_ptr(), q_token, q_head, weights.data_ptr(), w_token)
+        else:  # the keys alone
+            q_to = None
     place = _tokens(block_tables, seq_lens, token_starts, T, index)
-    if T and (q is None or H):
+    if T:
         _check(idx_index_prepare(
             k.data_ptr(), k_token, *q_args, code, T, H, D, *_table(table, index), rot_offset,
             interleaved, *place, block_size, blocks, kv_fused.data_ptr(), q_to, w_to,

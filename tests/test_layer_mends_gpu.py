@@ -92,6 +92,20 @@ def test_index_rows_with_an_infinity_hold_the_quotients():
     np.testing.assert_array_equal(plain.E4M3[pool[:, :D]], want)
 
 
+def test_index_prepare_writes_the_keys_of_queries_without_heads():
+    B, D, bs = 3, 64, 32
+    k = torch.randn(B, D, generator=gen(7)).bfloat16().to(dev())
+    bt = torch.arange(B, dtype=torch.int32, device=dev())[:, None]
+    seq = torch.tensor([1, 9, 32], dtype=torch.int32, device=dev())
+    want, got = (torch.zeros(B, bs * (D + 4), dtype=torch.uint8, device=dev()) for _ in range(2))
+    idx.index_prepare(k, want, bt, seq)
+    q8, w = idx.index_prepare(k, got, bt, seq, q=torch.zeros(B, 0, D, dtype=torch.bfloat16, device=dev()),
+                              weights=torch.zeros(B, 0, device=dev()))
+    clean()
+    assert q8.shape == (B, 0, D) and w.shape == (B, 0)
+    assert (want != 0).any() and torch.equal(got, want)
+
+
 # ---- rotary positions outside the table --------------------------------------------------------------
 
 @pytest.mark.parametrize("name", ["bf16", "f16", "f32"])
