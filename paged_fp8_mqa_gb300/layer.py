@@ -263,14 +263,41 @@ def rotary_table(max_positions: int, rot_dim: int, *, base: float = 10000.0, sca
     return table
 
 
+@functools.cache
+def _recorded_rotary():
+    """rotary as a step that autograd records: its backward is rotary the other way."""
+    import torch
+
+    class Rotary(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, positions, table, interleaved, rot_offset, inverse, stream):
+            ctx.save_for_backward(positions, table)
+            ctx.how = dict(interleaved=interleaved, rot_offset=rot_offset, inverse=not inverse)
+            return rotary(x, positions, table, interleaved=interleaved, rot_offset=rot_offset,
+                          inverse=inverse, stream=stream)
+
+        @staticmethod
+        def backward(ctx, grad):
+            positions, table = ctx.saved_tensors
+            if grad.shape[-1] > 1 and grad.stride(-1) != 1:  # (of a sum: one element, expanded)
+                grad = grad.contiguous()
+            return (rotary(grad, positions, table, **ctx.how), *[None] * 6)
+
+    return Rotary.apply
+
+
 @_on_its_device
 def rotary(x, positions, table, *, interleaved: bool = False, rot_offset: int = 0,
            inverse: bool = False, out=None, stream=None):
     """Rotary positions: x [T, H, D] (float32, float16 or bfloat16; any token and head strides) at
     positions (int32 [T]), elements [rot_offset, rot_offset + rot_dim) of each head turned by the
     angles of ``table`` (see ``rotary_table``), in halves or in interleaved pairs.  ``out=x``
-    rotates in place; ``inverse`` turns back (the gradient with respect to x)."""
+    rotates in place.  ``inverse`` turns by the negative angles: the gradient with respect to x (and
+    the way back, where the table's magnitude is 1, as it is but for "yarn").  Autograd records the
+    call where x requires a gradient; with ``out`` nothing is recorded."""
     import torch
+    if out is None and torch.is_grad_enabled() and x.requires_grad:
+        return _recorded_rotary()(x, positions, table, interleaved, rot_offset, inverse, stream)
     index = _index(x, "x")
     code, (x_token, x_head, _) = _rows(x, "x", 3, index)
     _tensor(positions, "positions", 1, torch.int32, index)

@@ -125,6 +125,36 @@ def test_rotary_leaves_rows_past_the_table_to_the_bit(name, interleaved, D, rot,
     assert torch.equal(y.view(bits), keep.view(bits))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rotary_is_recorded_by_autograd(interleaved, inverse):
+    """The gradient autograd finds is the formula's; a second backward turns again."""
+    table = idx.rotary_table(50, 16, scaling="yarn", factor=4.0, original_positions=64)
+    pos = torch.tensor([0, 49, 20, 60], dtype=torch.int32, device=dev())   # 60: past the table, left alone
+    w = torch.randn(4, 2, 24, generator=gen(2)).to(dev())
+    wide = torch.randn(4, 3, 32, generator=gen(1)).to(dev()).requires_grad_()
+    x = wide[:, 1:, :24]
+    y = idx.rotary(x, pos, table, interleaved=interleaved, rot_offset=8, inverse=inverse)
+    assert y.requires_grad
+    plain_y = idx.rotary(x.detach(), pos, table, interleaved=interleaved, rot_offset=8, inverse=inverse)
+    assert not plain_y.requires_grad and torch.equal(y, plain_y)
+    with torch.no_grad():
+        assert not idx.rotary(x, pos, table, interleaved=interleaved, rot_offset=8).requires_grad
+    up = w.clone().requires_grad_()
+    (grad,) = torch.autograd.grad(y, wide, up, create_graph=True)
+    turn = f64(table) * ([1, 1] if inverse else [1, -1])
+    want = np.zeros((4, 3, 32))
+    want[:, 1:, :24] = plain.rotate(f64(w), pos.tolist(), turn, interleaved, 8)
+    # Two products and a sum in float32, of a magnitude of at most 1.14 times sqrt(2) max |w|.
+    assert np.abs(f64(grad) - want).max() <= 3 * 2.0 ** -24 * 1.14 * 2 * f64(w.abs().max())
+    (back,) = torch.autograd.grad(grad, up, wide.detach())
+    assert torch.equal(back, plain_y)
+    (ones,) = torch.autograd.grad(idx.rotary(x, pos, table, interleaved=interleaved, rot_offset=8).sum(), wide)
+    flat = idx.rotary(torch.ones_like(w), pos, table, interleaved=interleaved, rot_offset=8, inverse=True)
+    assert torch.equal(ones[:, 1:, :24], flat)
+    idx.device_status(clear=True)
+
+
 # ---- weights far below a row's largest -------------------------------------------------------------
 
 def tail_case(N, H, Hkv, D, bs, name, *, share=None, gap=None, spread, ratio=1.0, n=1, seed=0):
