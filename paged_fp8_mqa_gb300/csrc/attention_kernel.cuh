@@ -41,6 +41,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "rows.cuh"
+#include "runs.h"
 
 namespace idx {
 namespace {
@@ -449,14 +450,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   const int64_t runs = max(static_cast<int64_t>(1), min(total, static_cast<int64_t>(gridDim.x)));
   int64_t f0 = total, f1 = total;
   if (blockIdx.x < runs) {
-    if (total < (1 << 21)) {  // (32-bit divisions are a tenth of the 64-bit ones)
-      const uint32_t n = static_cast<uint32_t>(total), c = static_cast<uint32_t>(runs);
-      f0 = n * blockIdx.x / c;
-      f1 = n * (blockIdx.x + 1) / c;
-    } else {
-      f0 = total * blockIdx.x / runs;
-      f1 = total * (blockIdx.x + 1) / runs;
-    }
+    f0 = run_begin(total, runs, blockIdx.x);
+    f1 = run_begin(total, runs, blockIdx.x + 1);
   }
   if (f0 < f1 && f0 >= before * groups && f0 < (before + mine) * groups) {
     for (int k = k_lo; k < k_hi; ++k) {
@@ -1095,14 +1090,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       const bool from_start = w.seg_tile == 0, to_end = w.seg_tile + w.seg_tiles == w.tiles;
       const int64_t gid = static_cast<int64_t>(w.key) * groups + w.group;
       if (from_start && wg == 0 && quarter == 2 && lane == 0) {
-        // The last tile of the group is tile x of the line; its owner is the last part.
+        // The run that holds the group's last tile has its last part.
         int n = 1;
         if (!to_end) {
-          const int64_t x = f1 - 1 + (w.tiles - (w.seg_tile + w.seg_tiles));
-          const int64_t y = (x + 1) * runs - 1;
-          n = (y < INT_MAX ? static_cast<int>(y) / static_cast<int>(total)
-                           : static_cast<int>(y / total)) -
-              static_cast<int>(blockIdx.x) + 1;
+          const int64_t last = f1 - 1 + (w.tiles - (w.seg_tile + w.seg_tiles));
+          n = run_of(total, runs, last) - static_cast<int>(blockIdx.x) + 1;
         }
         parts[gid] = GroupParts{static_cast<int>(blockIdx.x), n};
       }

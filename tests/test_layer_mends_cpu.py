@@ -1,4 +1,10 @@
-"""The operators around the indexer without a GPU: sizes and devices that they refuse."""
+"""The operators around the indexer without a GPU: sizes that they refuse, the device that they run on,
+the arithmetic of their split."""
+import bisect
+import random
+import shutil
+import subprocess
+
 import pytest
 import torch
 
@@ -64,3 +70,37 @@ def test_calls_run_on_their_tensors_device(call, current, monkeypatch):
      "attention_fp8": lambda: idx.attention_fp8(x[:, None], pool, pool, sc, sc, bt, sl)}[call]()
     assert seen == [1] * (2 if call == "attention_fp8" else 1)
     assert entered == ([1] if current == 0 else []) and now == [current]
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs a host compiler")
+def test_runs_of_a_line(tmp_path):
+    """The split's two formulas against whole numbers without a limit, also for lines of more than 2^31
+    items, the first runs of them among others."""
+    (tmp_path / "runs.cpp").write_text("""
+#include <cstdio>
+#include "runs.h"
+int main() {
+  long long total, runs, c, x;
+  while (scanf("%lld %lld %lld %lld", &total, &runs, &c, &x) == 4)
+    printf("%lld %lld\\n", (long long)idx::run_begin(total, runs, c), (long long)idx::run_of(total, runs, x));
+}
+""")
+    csrc = idx.LIB_PATH.parent / "csrc"
+    subprocess.run(["g++", "-O1", f"-I{csrc}", "-o", str(tmp_path / "runs"), str(tmp_path / "runs.cpp")], check=True)
+    rng, cases = random.Random(5), []
+    for total in (1, 2, 127, 304, 305, 4097, (1 << 21) - 1, 1 << 21, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 1, 3 << 30,
+                  2 ** 32 - 1, 2 ** 32 + 7, 2 ** 40, 2 ** 48):
+        for runs in (1, 2, 151, 304, 2048):
+            if runs > total:
+                continue
+            for _ in range(20):
+                c = rng.choice([0, 1, runs - 1, runs, rng.randint(0, runs)])
+                x = rng.choice([0, total - 1, total * min(c, runs - 1) // runs + rng.randint(-1, 1),
+                                rng.randrange(total), rng.randrange(min(total, 1 << 22))])
+                cases.append((total, runs, c, min(max(x, 0), total - 1)))
+    run = subprocess.run([str(tmp_path / "runs")], input="\n".join("%d %d %d %d" % c for c in cases), text=True,
+                         capture_output=True)
+    assert run.returncode == 0, run.returncode
+    for (total, runs, c, x), line in zip(cases, run.stdout.split("\n")):
+        begins = [total * i // runs for i in range(runs)]
+        assert line == f"{total * c // runs} {bisect.bisect_right(begins, x) - 1}", (total, runs, c, x, line)
