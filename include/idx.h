@@ -475,8 +475,8 @@ int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, 
  * counts twice).  A row without positions gives zeros and lse = -inf.  What stands in the cache
  * at a position that a row does not see never reaches it, NaN included.
  *
- * Products are exact and sums float32; out is rounded once.  A query element is held to 2^-18 of
- * its row's largest magnitude, a weight (softmax times |v_scale|) to 2^-10 of itself with bfloat16
+ * Products are exact and sums float32; out is rounded once.  A query element is held exactly, or to
+ * 2^-31 of its row's largest magnitude, a weight (softmax times |v_scale|) to 2^-10 of itself with bfloat16
  * and 2^-14 with float16, or to 2^-34 of the row's largest.
  *
  *   q             device [batch][next_n][num_heads][head_dim] of dtype (IDX_DTYPE_F16 or _BF16),

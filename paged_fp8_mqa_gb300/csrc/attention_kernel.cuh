@@ -6,13 +6,14 @@
 //
 // Both products run on the tensor core in 8 bits, straight from the cache's bytes: the cache is
 // never converted.  The other operand keeps its precision by being split into 8-bit parts:
-//   * a query row is scaled by a power of two to [128, 256) and written as hi + lo, each the
-//     e4m3 nearest to what is left: 4 + 4 bits hold a bfloat16's 8 exactly (down to 2^-18 of the
-//     row's largest magnitude); a float16's 11 bits take three parts.  Products of e4m3 values
+//   * a query row is scaled by a power of two to [2^14, 2^15) and written as three parts, each the
+//     e5m2 nearest to what is left: 3 + 4 + 4 bits (a rest has a sign) hold a bfloat16's 8 or a
+//     float16's 11 exactly, down to 2^-31 of the row's largest magnitude.  Products of 8-bit values
 //     are exact and sums float32, so the scores are those of the unrounded queries.  The parts'
-//     products go into the same accumulator.
-//   * a weight is written as e5m2 parts, three for bfloat16 and four for float16, held 2^3, 2^7 and
-//     2^11 up after the first: within 2^-10 of itself (2^-14 with four), or 2^-34 (2^-38) of the
+//     products go into the same accumulator.  (e4m3 parts, two would do for bfloat16, end at 2^-18: an
+//     outlier that meets no key's element silenced the rest of its row.)
+//   * a weight is written as such parts too, three for bfloat16 and four for float16, held 2^3, 2^7
+//     and 2^11 up after the first: within 2^-10 of itself (2^-14 with four), or 2^-34 (2^-38) of the
 //     row's largest.  The parts stand in columns of their own and are added when O is read.  e5m2 for
 //     its reach: a first token of no value that takes most of a row's weight, or a block with a
 //     large value scale, leaves an output that is all small weights, and the denominator counts
@@ -59,18 +60,19 @@ constexpr float kRefNone = -1e30f;             // the reference of a row that ha
 constexpr float kTop = 11.0f, kMost = 15.8f, kUp2 = 8.0f, kUp = 16.0f;
 constexpr float kLeastScale = 7.8886090522101180541e-31f;  // 2^-100: a value scale below it is 0
 
-// One kernel's shape: R rows, PARTS parts a query row, one more a weight, head_dim D.
+// One kernel's shape: R rows, PARTS parts a weight, head_dim D.
 template <int D_, int R_, int PARTS_, bool SELECT_>
 struct AttnCfg {
   static constexpr int D = D_, R = R_, PARTS = PARTS_;
   static constexpr bool SELECT = SELECT_;
-  // With R = 8 a query's two parts stand side by side in the least N (16) and are added when read;
-  // else each part is a product of its own into the same columns.
+  static constexpr int QPARTS = 3;                    // parts of a query
+  // With R = 8 a query's parts stand side by side, in columns that are added when read (the last
+  // eight of 32 mean nothing); else each part is a product of its own into the same columns.  (Three
+  // products with R = 8 too: tiny 9.1 us for 8.7, serving 96 for 94.)
   static constexpr bool CAT = R == 8;
-  static constexpr int NS = CAT ? 16 : R;             // columns of S
-  static constexpr int WPARTS = PARTS + 1;
-  static constexpr int NO = (R * WPARTS + 15) / 16 * 16;  // columns of O (N in steps of 16)
-  static constexpr int PASSES = CAT ? 1 : PARTS;      // products that make S
+  static constexpr int NS = CAT ? 32 : R;             // columns of S
+  static constexpr int PASSES = CAT ? 1 : QPARTS;     // products that make S
+  static constexpr int NO = (R * PARTS + 15) / 16 * 16;  // columns of O (N in steps of 16)
   static constexpr int WG = R == 64 ? 2 : 1;          // softmax warpgroups, R / WG rows each
   static constexpr int RT = R / WG;
   static constexpr int SOFT_WARPS = 4 * WG;
@@ -86,7 +88,7 @@ struct AttnCfg {
   // one long request 29 us for 27, a batch of 64 requests with 64 heads on one 128 for 96.
   static constexpr int CTAS = R == 64 ? 1 : 2;
   static constexpr int KV_BYTES = 2 * kTile * D;
-  static constexpr int Q_BYTES = (R * PARTS * D + 1023) / 1024 * 1024;
+  static constexpr int Q_BYTES = NS * (CAT ? 1 : QPARTS) * D;
   static constexpr int P_BYTES = NO * kTile;          // a tile's weights
   // They take the place of the tile's keys, which have been read by then, where they fit it; else
   // two buffers of their own.
@@ -99,7 +101,7 @@ struct AttnCfg {
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int SMEM = FIXED + STAGES * (KV_BYTES + AUX);
   static_assert(STAGES >= 2 && SMEM <= 232448, "fits the 227 KiB per-CTA limit");
-  static_assert(!CAT || PARTS == 2, "side by side: two parts of eight rows");
+  static_assert(Q_BYTES % 1024 == 0 && (!CAT || PARTS == 3), "aligned; eight rows: three parts");
 };
 
 // What a tile's position brings to its scores and weights.
@@ -356,12 +358,12 @@ template <class C, typename T>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     k_attention(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const AttentionArgs a, const AttnSplit split, GroupParts *parts) {
-  constexpr int D = C::D, R = C::R, RT = C::RT, NS = C::NS, PARTS = C::PARTS, WPARTS = C::WPARTS;
+  constexpr int D = C::D, R = C::R, RT = C::RT, NS = C::NS, PARTS = C::PARTS, QPARTS = C::QPARTS;
   extern __shared__ uint8_t s_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *s_kv = base;                              // [stage][K tile, V tile]
-  uint8_t *s_q = s_kv + C::STAGES * C::KV_BYTES;     // [PARTS * R][D], K-major, swizzled
+  uint8_t *s_q = s_kv + C::STAGES * C::KV_BYTES;     // [QPARTS * R][D], K-major, swizzled
   uint8_t *at = s_q + C::Q_BYTES;
   // A tile's weights, [NO / 16][kTile][16].
   uint8_t *s_p = at;
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     }
   } else if (warp == 1) {
     // ============================== MMA issuer ==================================================
-    constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, NS);
+    constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, NS) | kE5m2_B;
     constexpr uint32_t idesc_o = idesc_e4m3_f32(D, C::NO) | kE5m2_B | kMajorMN_A | kMajorMN_B;
     const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
     const uint32_t o_tmem = tmem + 2 * NS;
@@ -801,20 +803,20 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
 #pragma unroll
           for (int o = 1; o < LANES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // 2^e <= amax < 2^(e+1); rows below 2^-100 keep their scores to 2^-118 only.
+          // 2^e <= amax < 2^(e+1); rows below 2^-100 keep their scores to 2^-131 only.
           const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
           const float up = e > 127 ? __int_as_float(0x7FC00000)  // an infinity: the row is NaN
-                                   : __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - 7 + min(e, 127)) << 23);
+                                   : __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + min(e, 127)) << 23);
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] *= up;
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part) {
-            const uint2 b = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+          for (int part = 0; part < QPARTS; ++part) {
+            const uint2 b = make_uint2(e5m2x4(f[0], f[1], f[2], f[3]), e5m2x4(f[4], f[5], f[6], f[7]));
             *reinterpret_cast<uint2 *>(s_q + swizzled<D>(part * R + r, x)) = b;
-            if (part + 1 < PARTS) {
-              const float2 b0 = e4m3x2_to_f32(b.x), b1 = e4m3x2_to_f32(b.x >> 16);
-              const float2 b2 = e4m3x2_to_f32(b.y), b3 = e4m3x2_to_f32(b.y >> 16);
+            if (part + 1 < QPARTS) {
+              const float2 b0 = e5m2x2_to_f32(b.x), b1 = e5m2x2_to_f32(b.x >> 16);
+              const float2 b2 = e5m2x2_to_f32(b.y), b3 = e5m2x2_to_f32(b.y >> 16);
               f[0] -= b0.x, f[1] -= b0.y, f[2] -= b1.x, f[3] -= b1.y;
               f[4] -= b2.x, f[5] -= b2.y, f[6] -= b3.x, f[7] -= b3.y;
             }
@@ -851,16 +853,19 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         float2 y[RT / 2];  // the weights' logarithms
         {
           uint32_t v[RT];
-          tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + (C::CAT ? 0 : r0), v);
+          tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + r0, v);
           if constexpr (C::CAT) {
-            uint32_t u[RT];
+            uint32_t u[RT], t[RT];
             tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + R, u);
+            tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + 2 * R, t);
             tmem_ld_wait();
             reg_fence(v);
             reg_fence(u);
+            reg_fence(t);
 #pragma unroll
             for (int r = 0; r < RT; ++r)
-              v[r] = __float_as_uint(__uint_as_float(v[r]) + __uint_as_float(u[r]));
+              v[r] = __float_as_uint(__uint_as_float(v[r]) +
+                                     (__uint_as_float(u[r]) + __uint_as_float(t[r])));
           } else {
             tmem_ld_wait();
             reg_fence(v);
@@ -942,7 +947,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
             tc_fence_after_sync();
 #pragma unroll 1
-            for (int part = 0; part < WPARTS; ++part) {
+            for (int part = 0; part < PARTS; ++part) {
               const uint32_t o_at = lane_base + 2 * NS + part * R + r0;
               uint32_t v[RT];
               tmem_ld_cols<RT>(o_at, v);
@@ -967,7 +972,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const bool odd = __any_sync(0xffffffffu, tok.inv_v < 0.0f || inv_v >= 1.0f / kLeastScale);
         const uint32_t flip = tok.inv_v < 0.0f ? 0x80808080u : 0u;
         const uint32_t live = inv_v < 1.0f / kLeastScale ? 0xFFFFFFFFu : 0u;
-        uint32_t bytes[WPARTS][4];
+        uint32_t bytes[PARTS][4];
         const float2 inv2 = make_float2(inv_v, inv_v);
 #pragma unroll
         for (int r = 0; r < RT; r += 4) {
@@ -977,13 +982,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             p[j] = make_float2(fast_exp2(y[r / 2 + j].x), fast_exp2(y[r / 2 + j].y));
             sum[r / 2 + j] = __ffma2_rn(p[j], inv2, sum[r / 2 + j]);
           }
-          uint32_t four[WPARTS];
-          weight_parts<WPARTS>(p[0], p[1], four);
+          uint32_t four[PARTS];
+          weight_parts<PARTS>(p[0], p[1], four);
 #pragma unroll
-          for (int part = 0; part < WPARTS; ++part) bytes[part][(r / 4) % 4] = four[part];
+          for (int part = 0; part < PARTS; ++part) bytes[part][(r / 4) % 4] = four[part];
           if (odd && (r % 16 == 12 || r + 4 == RT)) {
 #pragma unroll
-            for (int part = 0; part < WPARTS; ++part)
+            for (int part = 0; part < PARTS; ++part)
 #pragma unroll
               for (int q = 0; q < (RT < 16 ? RT / 4 : 4); ++q)
                 bytes[part][q] = (bytes[part][q] & live) ^ flip;
@@ -996,7 +1001,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             }
           } else if (r % 16 == 12) {
 #pragma unroll
-            for (int part = 0; part < WPARTS; ++part)
+            for (int part = 0; part < PARTS; ++part)
               *reinterpret_cast<uint4 *>(sp + (part * R + r0 + r - 12) / 16 * (kTile * 16)) =
                   make_uint4(bytes[part][0], bytes[part][1], bytes[part][2], bytes[part][3]);
           }
@@ -1037,14 +1042,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       tc_fence_after_sync();
       float acc[RT];
 #pragma unroll
-      for (int part = WPARTS - 1; part >= 0; --part) {
+      for (int part = PARTS - 1; part >= 0; --part) {
         uint32_t v[RT];
         tmem_ld_cols<RT>(lane_base + 2 * NS + part * R + r0, v);
         tmem_ld_wait();
         reg_fence(v);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-          acc[r] = part == WPARTS - 1
+          acc[r] = part == PARTS - 1
                        ? __uint_as_float(v[r])
                        : fmaf(acc[r], 1.0f / (part == 0 ? kUp2 : kUp), __uint_as_float(v[r]));
       }
@@ -1289,17 +1294,17 @@ cudaError_t launch_rows(const CUtensorMap &k_map, const CUtensorMap &v_map, cons
   const AttnShape s = attn_shape(a.heads / a.kv_heads * (SELECT ? 1 : a.next_n), f16);
   if (f16) {
     switch (s.r) {
-      case 16: return launch_cfg<AttnCfg<D, 16, 3, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
-      case 32: return launch_cfg<AttnCfg<D, 32, 3, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
-      default: return launch_cfg<AttnCfg<D, 64, 3, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
+      case 16: return launch_cfg<AttnCfg<D, 16, 4, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
+      case 32: return launch_cfg<AttnCfg<D, 32, 4, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
+      default: return launch_cfg<AttnCfg<D, 64, 4, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
     }
   }
   using B = __nv_bfloat16;
   switch (s.r) {
-    case 8: return launch_cfg<AttnCfg<D, 8, 2, SELECT>, B>(k_map, v_map, a, s, sms, stream);
-    case 16: return launch_cfg<AttnCfg<D, 16, 2, SELECT>, B>(k_map, v_map, a, s, sms, stream);
-    case 32: return launch_cfg<AttnCfg<D, 32, 2, SELECT>, B>(k_map, v_map, a, s, sms, stream);
-    default: return launch_cfg<AttnCfg<D, 64, 2, SELECT>, B>(k_map, v_map, a, s, sms, stream);
+    case 8: return launch_cfg<AttnCfg<D, 8, 3, SELECT>, B>(k_map, v_map, a, s, sms, stream);
+    case 16: return launch_cfg<AttnCfg<D, 16, 3, SELECT>, B>(k_map, v_map, a, s, sms, stream);
+    case 32: return launch_cfg<AttnCfg<D, 32, 3, SELECT>, B>(k_map, v_map, a, s, sms, stream);
+    default: return launch_cfg<AttnCfg<D, 64, 3, SELECT>, B>(k_map, v_map, a, s, sms, stream);
   }
 }
 
@@ -1307,12 +1312,12 @@ cudaError_t launch_rows(const CUtensorMap &k_map, const CUtensorMap &v_map, cons
 template <int D, bool SELECT>
 int ctas_for(int r, bool f16) {
   if (f16)
-    return r == 16 ? AttnCfg<D, 16, 3, SELECT>::CTAS
-                   : r == 32 ? AttnCfg<D, 32, 3, SELECT>::CTAS : AttnCfg<D, 64, 3, SELECT>::CTAS;
-  return r == 8 ? AttnCfg<D, 8, 2, SELECT>::CTAS
-                : r == 16 ? AttnCfg<D, 16, 2, SELECT>::CTAS
-                          : r == 32 ? AttnCfg<D, 32, 2, SELECT>::CTAS
-                                    : AttnCfg<D, 64, 2, SELECT>::CTAS;
+    return r == 16 ? AttnCfg<D, 16, 4, SELECT>::CTAS
+                   : r == 32 ? AttnCfg<D, 32, 4, SELECT>::CTAS : AttnCfg<D, 64, 4, SELECT>::CTAS;
+  return r == 8 ? AttnCfg<D, 8, 3, SELECT>::CTAS
+                : r == 16 ? AttnCfg<D, 16, 3, SELECT>::CTAS
+                          : r == 32 ? AttnCfg<D, 32, 3, SELECT>::CTAS
+                                    : AttnCfg<D, 64, 3, SELECT>::CTAS;
 }
 
 inline cudaError_t read_attention_status(int32_t *value, bool clear) {

@@ -185,6 +185,23 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return out;
 }
 
+// Four floats as e5m2 bytes, to nearest even, and the low two as floats again (an e5m2 value is the
+// float16 whose upper byte it is).
+__device__ __forceinline__ uint32_t e5m2x4(float a, float b, float c, float d) {
+  uint32_t out;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}\n"
+      : "=r"(out)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return out;
+}
+__device__ __forceinline__ float2 e5m2x2_to_f32(uint32_t two) {
+  const uint32_t h = __byte_perm(two, 0, 0x1404);
+  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
 // V values as e4m3 bytes.
 template <int V>
 __device__ __forceinline__ void store_e4m3(uint8_t *dst, const float (&v)[V]) {

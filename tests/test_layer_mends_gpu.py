@@ -258,6 +258,39 @@ def test_attention_keeps_small_weights_of_draft_slots(n):
     check_tail(tail_case(2048, 16, 2, 128, 64, "bf16", gap=13.0, spread=0.5, n=n))
 
 
+@pytest.mark.parametrize("H,Hkv,D,bs,name", TAIL_SHAPES)
+def test_attention_with_an_outlier_in_the_queries(H, Hkv, D, bs, name):
+    """One element of each query 2^19 times the others and no key has its channel: the scores are the
+    others' alone.  Elements are exact, or within 2^-31 of the outlier; sums are float32."""
+    lens = [300, 77]
+    g = gen(H + D)
+    blocks = 16
+    bt = torch.randperm(blocks, generator=g).int()[:2 * -(-300 // bs)].view(2, -1) if bs > 32 else \
+        torch.randperm(20, generator=g).int().view(2, 10)
+    blocks = max(blocks, 20)
+    k, v = (torch.randn(blocks, Hkv, bs, D, generator=g).mul(60).to(torch.float8_e4m3fn) for _ in range(2))
+    k.view(torch.uint8)[..., D // 3] = 0
+    ks, vs = (torch.full((blocks, Hkv), 1.0 / 60) for _ in range(2))
+    q = torch.randn(2, 1, H, D, generator=g) * 2.0 ** -7
+    q[..., D // 3] = 2.0 ** 12
+    q = q.to(DTYPES[name])
+    scale = 2.0 ** 7 * D ** -0.5
+    out = idx.attention_fp8(q.to(dev()), *(t.to(dev()) for t in (k, v, ks, vs, bt)),
+                            torch.tensor(lens, dtype=torch.int32, device=dev()), softmax_scale=scale)
+    clean()
+    kk = values8(k)
+    ref, _, mag, _ = plain.attention(f64(q), kk, values8(v), f64(ks), f64(vs), bt.numpy(), lens, bs, scale)
+    rest = f64(q)
+    rest[..., D // 3] = 0
+    sums = np.abs(kk).sum(-1).max() / 60
+    dz = scale * (2.0 ** -31 * 2.0 ** 12 * sums + 2.0 ** -17 * np.abs(rest).max() * sums)
+    w_rel, half = (2.0 ** -10, 2.0 ** -8) if name == "bf16" else (2.0 ** -14, 2.0 ** -11)
+    lim = (2 * dz + w_rel + 2.0 ** -14) * mag
+    lim = lim + half * (np.abs(ref) + lim)
+    err = np.abs(f64(out) - ref)
+    assert (err <= lim).all(), (dz, float((err / mag).max()))
+
+
 # ---- scales that are not finite --------------------------------------------------------------------
 
 @pytest.mark.parametrize("H,Hkv,D,bs,name,n", [(8, 2, 128, 32, "bf16", 4), (64, 2, 64, 32, "f16", 1),
