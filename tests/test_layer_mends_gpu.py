@@ -331,6 +331,54 @@ def test_attention_over_a_scale_that_is_not_finite(H, Hkv, D, bs, name, n, which
                 assert torch.isnan(got).all() if hit else torch.equal(got, base[b, t, h * per:(h + 1) * per]), (b, t, h)
 
 
+# ---- offsets past 32 bits ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D,bs", [(128, 64), (64, 32)])
+def test_attention_selects_past_32_bits_of_a_pool(D, bs):
+    """Selected rows that lie past 2^31 bytes of the pools: the bits of the same rows in small ones."""
+    B, H, used = 3, 8, 24
+    blocks = (1 << 31) // (bs * D) + used
+    g = gen(81)
+    k, v = (torch.randn(used, 1, bs, D, generator=g).mul(60).to(torch.float8_e4m3fn).to(dev()) for _ in range(2))
+    ks, vs = ((torch.rand(used, 1, generator=g) * 0.02 + 0.01).to(dev()) for _ in range(2))
+    bt = torch.randperm(used, generator=g).int().view(B, -1).to(dev())
+    seq = torch.tensor([8 * bs, 5 * bs + 3, 1], dtype=torch.int32, device=dev())
+    q = torch.randn(B, 1, H, D, generator=g).bfloat16().to(dev())
+    cand = torch.stack([torch.randperm(8 * bs, generator=g)[:150] for _ in range(B)]).int()
+    cand = torch.stack((cand, cand), -1).contiguous().to(dev())
+    ranges = torch.tensor([[0] * B, [150] * B], dtype=torch.int32, device=dev())
+    want = idx.attention_fp8(q, k, v, ks, vs, bt, seq, candidates=cand, ranges=ranges)
+    big, first = [], blocks - used
+    for t in (k, v):
+        pool = torch.empty(blocks, 1, bs, D, dtype=torch.uint8, device=dev())
+        pool[first:] = t.view(torch.uint8)
+        big.append(pool.view(torch.float8_e4m3fn))
+    for t in (ks, vs):
+        big.append(torch.full((blocks, 1), math.nan, device=dev()))
+        big[-1][first:] = t
+    got = idx.attention_fp8(q, *big, bt + first, seq, candidates=cand, ranges=ranges)
+    clean()
+    assert (want[0] != 0).any() and torch.equal(got, want)
+
+
+def test_attention_selects_past_32_bits_of_the_slots():
+    B, H, D, bs, slots = 4096, 2, 64, 32, 70000   # 2.3 GB of slots
+    g = gen(82)
+    k, v = (torch.randn(4, 1, bs, D, generator=g).mul(60).to(torch.float8_e4m3fn).to(dev()) for _ in range(2))
+    sc = torch.full((4, 1), 1.0 / 60, device=dev())
+    bt = torch.randint(4, (B, 3), generator=g, dtype=torch.int32).to(dev())
+    seq = torch.full((B,), 96, dtype=torch.int32, device=dev())
+    q = torch.randn(B, 1, H, D, generator=g).bfloat16().to(dev())
+    few = torch.randint(96, (B, 20, 2), generator=g, dtype=torch.int32).to(dev())
+    few_ranges = torch.tensor([[0] * B, [20] * B], dtype=torch.int32, device=dev())
+    want = idx.attention_fp8(q, k, v, sc, sc, bt, seq, candidates=few, ranges=few_ranges)
+    wide = torch.full((B, slots, 2), -1, dtype=torch.int32, device=dev())
+    wide[:, slots - 20:] = few
+    got = idx.attention_fp8(q, k, v, sc, sc, bt, seq, candidates=wide, ranges=few_ranges + (slots - 20))
+    clean()
+    assert torch.equal(got, want)
+
+
 # ---- refusals --------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("H,Hkv", [(4, 8), (1, 2), (12, 8)])
