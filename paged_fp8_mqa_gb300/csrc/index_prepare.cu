@@ -19,18 +19,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kTiny = 7.8886090522101180541e-31f;  // 2^-100: a row of zeros has a scale too
 
-// x / scale, rounded, for a piece (inv: 1 / scale within a unit or two).
+// x / scale, rounded, for a piece (inv: 1 / scale within a unit or two).  The remainder is taken the
+// other way about, so that a zero keeps its sign.
 template <int V>
 __device__ __forceinline__ void quotients(float (&x)[V], float scale, float inv) {
   if constexpr (V == 2) {
     const float2 a = make_float2(x[0], x[1]), i2 = make_float2(inv, inv);
     const float2 q = __fmul2_rn(a, i2);
-    const float2 r = __ffma2_rn(__ffma2_rn(q, make_float2(-scale, -scale), a), i2, q);
+    const float2 r = __ffma2_rn(__ffma2_rn(q, make_float2(scale, scale), make_float2(-x[0], -x[1])),
+                                make_float2(-inv, -inv), q);
     x[0] = r.x;
     x[1] = r.y;
   } else {
     const float q = x[0] * inv;
-    x[0] = fmaf(fmaf(q, -scale, x[0]), inv, q);
+    x[0] = fmaf(fmaf(q, scale, -x[0]), -inv, q);
   }
 }
 

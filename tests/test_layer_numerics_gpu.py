@@ -92,6 +92,20 @@ def test_index_rows_with_an_infinity_hold_the_quotients():
     np.testing.assert_array_equal(plain.E4M3[pool[:, :D]], want)
 
 
+def test_index_rows_keep_the_signs_of_zeros():
+    D, bs = 64, 32
+    x = torch.zeros(2, D)
+    x[:, ::3], x[1, 5], x[1, 7] = -0.0, -2.0, -1e-30
+    pool = torch.zeros(2, bs * (D + 4), dtype=torch.uint8, device=dev())
+    seq = torch.ones(2, dtype=torch.int32, device=dev())
+    bt = torch.arange(2, dtype=torch.int32, device=dev())[:, None]
+    q8, _ = idx.index_prepare(x.to(dev()), pool, bt, seq, q=x[:, None].to(dev()), weights=torch.ones(2, 1, device=dev()))
+    clean()
+    want = torch.signbit(x).numpy()
+    assert ((pool.cpu().numpy()[:, :D] >= 0x80) == want).all()
+    assert ((q8.view(torch.uint8).cpu().numpy()[:, 0] >= 0x80) == want).all()
+
+
 def test_index_prepare_writes_the_keys_of_queries_without_heads():
     B, D, bs = 3, 64, 32
     k = torch.randn(B, D, generator=gen(7)).bfloat16().to(dev())
