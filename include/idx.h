@@ -462,8 +462,9 @@ int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, 
 
 /*
  * Attention over the 8-bit K/V cache (layout as for idx_kv_append; the scales may be any finite
- * numbers, value scales below 2^-100 counting as 0; a NaN, or an infinite value scale, makes the rows
- * that see it NaN, lse too).  For row r = b*next_n + t and query head h, with K/V head g = h / (num_heads/kv_heads):
+ * numbers, value scales below 2^-100 counting as 0; a NaN, or an infinite value scale, makes the
+ * rows that see it NaN, lse too).  For row r = b*next_n + t and query head h, with K/V head
+ * g = h / (num_heads/kv_heads):
  *
  *   z_p = softmax_scale * k_scale[page(p)][g] * (q[b,t,h,:] . k[p,g,:])
  *   out[b,t,h,:] = sum_p softmax(z)_p * v_scale[page(p)][g] * v[p,g,:]
@@ -475,9 +476,9 @@ int idx_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, 
  * counts twice).  A row without positions gives zeros and lse = -inf.  What stands in the cache
  * at a position that a row does not see never reaches it, NaN included.
  *
- * Products are exact and sums float32; out is rounded once.  A query element is held exactly, or to
- * 2^-31 of its row's largest magnitude, a weight (softmax times |v_scale|) to 2^-10 of itself with bfloat16
- * and 2^-14 with float16, or to 2^-34 of the row's largest.
+ * Products are exact and sums float32; out is rounded once.  A query element is held exactly, or
+ * to 2^-31 of its row's largest magnitude; a weight (softmax times |v_scale|) to 2^-10 of itself
+ * with bfloat16 and 2^-14 with float16, or to 2^-34 of the row's largest.
  *
  *   q             device [batch][next_n][num_heads][head_dim] of dtype (IDX_DTYPE_F16 or _BF16),
  *                 16-byte aligned, strides in elements, multiples of 8

@@ -425,7 +425,8 @@ def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
     sees positions 0 .. seq_lens[b] - next_n + t.  With ``candidates`` (int32 [B*next_n, slots, 2])
     and ``ranges`` (int32 [2, B*next_n]) as the select leaves them, each row sees only the
     positions stored in its slot range.  Rows that see nothing give zeros.  softmax_scale defaults
-    to D ** -0.5; ``lse`` (float32 [B, next_n, H]) receives the log-sums; ``workspace`` (uint8, at
+    to D ** -0.5; weights are held to 2^-10 of themselves (float16 queries: 2^-14), sums in float32;
+    ``lse`` (float32 [B, next_n, H]) receives the log-sums; ``workspace`` (uint8, at
     least idx_attention_workspace_bytes) is allocated if not given.  Returns out, contiguous
     [B, next_n, H, D] in q's dtype."""
     import torch
