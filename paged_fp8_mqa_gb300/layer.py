@@ -110,20 +110,13 @@ def _index(t, name):
     return t.get_device()
 
 
-def _on_its_device(f):
-    """f with the device of its first argument current: the launch, the SM count and the workspace's
-    size are that device's, whichever is current where f is called."""
-    name = f.__code__.co_varnames[0]
-
-    @functools.wraps(f)
-    def call(*args, **more):
-        import torch
-        index = _index(args[0] if args else more.get(name), name)
-        if index == torch.cuda.current_device():
-            return f(*args, **more)
-        with torch.cuda.device(index):
-            return f(*args, **more)
-    return call
+def _elsewhere(index, f, *args, **more):
+    """f again with device `index`, its tensors', current: the launch, the SM count and the workspace's
+    size are then that device's.  (Each call asks for itself whether it has to: a wrapper around it
+    costs a microsecond.)"""
+    import torch
+    with torch.cuda.device(index):
+        return f(*args, **more)
 
 
 def _tensor(t, name, dims, dtype, index):
@@ -286,7 +279,6 @@ def _recorded_rotary():
     return Rotary.apply
 
 
-@_on_its_device
 def rotary(x, positions, table, *, interleaved: bool = False, rot_offset: int = 0,
            inverse: bool = False, out=None, stream=None):
     """Rotary positions: x [T, H, D] (float32, float16 or bfloat16; any token and head strides) at
@@ -296,9 +288,12 @@ def rotary(x, positions, table, *, interleaved: bool = False, rot_offset: int = 
     the way back, where the table's magnitude is 1, as it is but for "yarn").  Autograd records the
     call where x requires a gradient; with ``out`` nothing is recorded."""
     import torch
-    if out is None and torch.is_grad_enabled() and x.requires_grad:
-        return _recorded_rotary()(x, positions, table, interleaved, rot_offset, inverse, stream)
     index = _index(x, "x")
+    if x.requires_grad and out is None and torch.is_grad_enabled():
+        return _recorded_rotary()(x, positions, table, interleaved, rot_offset, inverse, stream)
+    if index != torch.cuda.current_device():
+        return _elsewhere(index, rotary, x, positions, table, interleaved=interleaved,
+                          rot_offset=rot_offset, inverse=inverse, out=out, stream=stream)
     code, (x_token, x_head, _) = _rows(x, "x", 3, index)
     _tensor(positions, "positions", 1, torch.int32, index)
     T, H, D = x.shape
@@ -325,7 +320,6 @@ def rotary(x, positions, table, *, interleaved: bool = False, rot_offset: int = 
     return out
 
 
-@_on_its_device
 def index_prepare(k, kv_fused, block_tables, seq_lens, *, token_starts=None, q=None, weights=None,
                   table=None, interleaved: bool = False, rot_offset: int = 0, q_out=None,
                   weights_out=None, stream=None):
@@ -339,6 +333,11 @@ def index_prepare(k, kv_fused, block_tables, seq_lens, *, token_starts=None, q=N
     weights float32 [T, H]), which ``logits_fp8`` takes (q viewed as [B, next_n, H, D])."""
     import torch
     index = _index(k, "k")
+    if index != torch.cuda.current_device():
+        return _elsewhere(index, index_prepare, k, kv_fused, block_tables, seq_lens,
+                          token_starts=token_starts, q=q, weights=weights, table=table,
+                          interleaved=interleaved, rot_offset=rot_offset, q_out=q_out,
+                          weights_out=weights_out, stream=stream)
     code, (k_token, _) = _rows(k, "k", 2, index)
     T, D = k.shape
     if _index(kv_fused, "kv_fused") != index or kv_fused.dtype is not torch.uint8:
@@ -388,7 +387,6 @@ def index_prepare(k, kv_fused, block_tables, seq_lens, *, token_starts=None, q=N
     return None if q is None else (q_out, weights_out)
 
 
-@_on_its_device
 def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,
               token_starts=None, table=None, interleaved: bool = False, rot_offset: int = 0,
               stream=None):
@@ -396,7 +394,12 @@ def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, 
     e4m3 [blocks, Hkv, block_size, D], scales float32 [blocks, Hkv] (powers of two).  The T rows
     are placed as in ``index_prepare``.  A block that already holds tokens keeps its scale while
     the new ones fit it; otherwise the scale grows and what it holds is rescaled."""
+    import torch
     index = _index(k, "k")
+    if index != torch.cuda.current_device():
+        return _elsewhere(index, kv_append, k, v, k_pool, v_pool, k_scales, v_scales, block_tables,
+                          seq_lens, token_starts=token_starts, table=table, interleaved=interleaved,
+                          rot_offset=rot_offset, stream=stream)
     code, (k_token, k_head, _) = _rows(k, "k", 3, index)
     v_code, (v_token, v_head, _) = _rows(v, "v", 3, index)
     shape = T, H, D = k.shape
@@ -416,7 +419,6 @@ def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, 
             *scales, _on(stream, index)))
 
 
-@_on_its_device
 def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,
                   softmax_scale: float | None = None, candidates=None, ranges=None, out=None,
                   lse=None, workspace=None, num_sms: int = 0, stream=None):
@@ -431,6 +433,11 @@ def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
     [B, next_n, H, D] in q's dtype."""
     import torch
     index = _index(q, "q")
+    if index != torch.cuda.current_device():
+        return _elsewhere(index, attention_fp8, q, k_pool, v_pool, k_scales, v_scales, block_tables,
+                          seq_lens, softmax_scale=softmax_scale, candidates=candidates,
+                          ranges=ranges, out=out, lse=lse, workspace=workspace, num_sms=num_sms,
+                          stream=stream)
     dtype = q.dtype
     code = _code(dtype)
     if code is None or dtype is torch.float32:
