@@ -349,7 +349,8 @@ int idx_device_status(int32_t *status_out, int32_t clear);
 
 /* =================================================================================================
  * The operators around the indexer: rotary positions, the writers of the two 8-bit pools and the
- * attention over the K/V pool.  The pages have no counterpart to these entry points.
+ * attention over the K/V pool; then heads normalised and rotated at once, and a 4-bit K/V cache.  The
+ * pages have no counterpart to these entry points.
  *
  * New tokens.  idx_index_prepare and idx_kv_append take `tokens` rows, request by request.
  * token_starts: device int32 [batch + 1], non-decreasing: request b's are rows
@@ -498,6 +499,121 @@ int64_t idx_attention_workspace_bytes(int32_t batch, int32_t next_n, int32_t num
 int idx_attention_fp8(const void *q, int64_t q_batch_stride, int64_t q_token_stride,
                       int64_t q_head_stride, int32_t dtype, const uint8_t *k_pool,
                       const uint8_t *v_pool, const float *k_scales, const float *v_scales,
+                      int64_t num_blocks, int32_t block_size, const int32_t *block_tables,
+                      int64_t bt_row_stride, int32_t bt_width, const int32_t *seq_lens,
+                      int64_t seq_lens_stride, int32_t batch, int32_t next_n, int32_t num_heads,
+                      int32_t kv_heads, int32_t head_dim, float softmax_scale,
+                      const int32_t *candidates, int32_t slots, const int32_t *ranges,
+                      int32_t num_sms, void *out, float *lse, void *workspace,
+                      int64_t workspace_bytes, void *stream);
+
+/* -------------------------------------------------------------------------------------------------
+ * Several axes, normalised heads.
+ *
+ * Axes.  Image and video tokens have a position on each of several axes (time, height, width):
+ * positions is device int32 [axes][tokens] with unit token stride and axis_stride elements between
+ * axes (0: the same for all), and pair i of the rotated part is turned by its own axis' position,
+ * the angle of table[positions[pair_axis[i]][t]][i].  pair_axis: host uint8 [rot_dim/2], read before
+ * the call returns, each below axes; not read with axes = 1.  Up to IDX_ROTARY_MAX_AXES axes.  A pair
+ * whose position is past the table stays as it is (IDX_DEV_BAD_POSITION).
+ */
+#define IDX_ROTARY_MAX_AXES 4
+#define IDX_NORM_MAX_DIM 1024
+
+/* idx_rotary by several axes; head_dim at most IDX_NORM_MAX_DIM. */
+int idx_rotary_axes(const void *x, int64_t x_token_stride, int64_t x_head_stride,
+                    const int32_t *positions, int64_t axis_stride, const uint8_t *pair_axis,
+                    int32_t axes, int64_t tokens, int32_t num_heads, int32_t head_dim, int32_t dtype,
+                    const float *table, int32_t max_positions, int32_t rot_dim, int32_t rot_offset,
+                    int32_t interleaved, int32_t inverse, void *out, int64_t out_token_stride,
+                    int64_t out_head_stride, void *stream);
+
+/*
+ * Every head x of q [tokens][q_heads][head_dim] and of k [tokens][k_heads][head_dim] (k_heads = 0:
+ * none) normalised and rotated, in one launch:
+ *
+ *   y = R(x / sqrt(mean(x^2) + eps) * weight)
+ *
+ * in float32 and rounded once.  q and k have dtype, any token and head strides and unit element
+ * stride; the weights [head_dim] (NULL: ones) have weight_dtype, dtype or IDX_DTYPE_F32.  table NULL:
+ * no rotation (positions is not read then).  q_out = q, k_out = k with the same strides work in place;
+ * otherwise outputs and inputs must not overlap.
+ */
+int idx_norm_rotary(const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads,
+                    const void *k, int64_t k_token_stride, int64_t k_head_stride, int32_t k_heads,
+                    int32_t dtype, int64_t tokens, int32_t head_dim, const void *q_weight,
+                    const void *k_weight, int32_t weight_dtype, float eps, const int32_t *positions,
+                    int64_t axis_stride, const uint8_t *pair_axis, int32_t axes, const float *table,
+                    int32_t max_positions, int32_t rot_dim, int32_t rot_offset, int32_t interleaved,
+                    void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void *k_out,
+                    int64_t k_out_token_stride, int64_t k_out_head_stride, void *stream);
+
+/*
+ * Its gradients from q, k and the outputs' gradients (any token and head strides, 0 among them):
+ * q_grad, k_grad (dtype, contiguous) and, where not NULL, q_weight_grad, k_weight_grad (weight_dtype),
+ * each summed over all tokens and heads in an order that does not change from call to call.
+ * workspace: device, 16-byte aligned, idx_norm_rotary_workspace_bytes(head_dim) bytes (-1: a head_dim
+ * that is refused).
+ */
+int64_t idx_norm_rotary_workspace_bytes(int32_t head_dim);
+int idx_norm_rotary_backward(
+    const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads, const void *k,
+    int64_t k_token_stride, int64_t k_head_stride, int32_t k_heads, int32_t dtype, int64_t tokens,
+    int32_t head_dim, const void *q_weight, const void *k_weight, int32_t weight_dtype, float eps,
+    const int32_t *positions, int64_t axis_stride, const uint8_t *pair_axis, int32_t axes,
+    const float *table, int32_t max_positions, int32_t rot_dim, int32_t rot_offset,
+    int32_t interleaved, const void *q_out_grad, int64_t qg_token_stride, int64_t qg_head_stride,
+    const void *k_out_grad, int64_t kg_token_stride, int64_t kg_head_stride, void *q_grad,
+    void *k_grad, void *q_weight_grad, void *k_weight_grad, void *workspace,
+    int64_t workspace_bytes, void *stream);
+
+/* -------------------------------------------------------------------------------------------------
+ * The 4-bit K/V cache.
+ *
+ *   k_pool, v_pool   device uint8 [num_blocks][kv_heads][block_size][head_dim/2]: E2M1 codes (a sign
+ *                    and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6), element 2j in the low half of byte j
+ *   k_scales         device uint8 [num_blocks][kv_heads][block_size][head_dim/32]: UE8M0, 2^(byte-127)
+ *                    for each 32 elements of a key (0xFF: NaN)
+ *   v_scales         device float32 [num_blocks][kv_heads][block_size]: one for each value row
+ *   head_dim         64 or 128; block_size 32, 64 or 128
+ *
+ * idx_kv_append_fp4 writes new keys (rotated) and values, placed as for idx_kv_append: codes rounded to
+ * nearest, ties to the even code.  A key's scale is the least power of two, 2^-100 or more, that brings
+ * its 32 elements to at most 6; a value row's is max(max|v|, 2^-96) / 6, its codes those of
+ * 6 v / max|v|.  Infinities have no say in a scale and are held as +-6; a NaN makes its scale NaN.
+ *
+ * idx_kv_read_fp4 gives back what is held, as dense rows of dtype (for an attention among the tokens of
+ * a prompt, or a cache of another kind): request b's newest tokens, rows [token_starts[b],
+ * token_starts[b+1]) of k_out and v_out [tokens][kv_heads][head_dim], token and head strides in
+ * elements (NULL: its next_n newest).  Rows of no request, before position 0 or without a block become
+ * zeros where clear != 0 and else stay as they were.
+ */
+int idx_kv_append_fp4(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                      int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t tokens,
+                      int32_t kv_heads, int32_t head_dim, const float *table, int32_t max_positions,
+                      int32_t rot_dim, int32_t rot_offset, int32_t interleaved,
+                      const int32_t *token_starts, const int32_t *seq_lens, int64_t seq_lens_stride,
+                      int32_t batch, int32_t next_n, const int32_t *block_tables,
+                      int64_t bt_row_stride, int32_t bt_width, int32_t block_size,
+                      int64_t num_blocks, uint8_t *k_pool, uint8_t *v_pool, uint8_t *k_scales,
+                      float *v_scales, void *stream);
+int idx_kv_read_fp4(const uint8_t *k_pool, const uint8_t *v_pool, const uint8_t *k_scales,
+                    const float *v_scales, int64_t num_blocks, int32_t block_size, int32_t kv_heads,
+                    int32_t head_dim, const int32_t *token_starts, int64_t tokens,
+                    const int32_t *seq_lens, int64_t seq_lens_stride, int32_t batch, int32_t next_n,
+                    const int32_t *block_tables, int64_t bt_row_stride, int32_t bt_width,
+                    int32_t clear, int32_t dtype, void *k_out, int64_t k_token_stride,
+                    int64_t k_head_stride, void *v_out, int64_t v_token_stride, int64_t v_head_stride, void *stream);
+
+/*
+ * idx_attention_fp8 over the 4-bit cache: the same arguments but for the scales, the same rows, extents,
+ * candidates and workspace.  The pools must be 32-byte aligned, the scales 16-byte.  Scales may be any
+ * numbers: a key's NaN, a value's NaN or infinity, makes the rows that see it NaN; value scales below
+ * 2^-100 count as 0.
+ */
+int idx_attention_fp4(const void *q, int64_t q_batch_stride, int64_t q_token_stride,
+                      int64_t q_head_stride, int32_t dtype, const uint8_t *k_pool,
+                      const uint8_t *v_pool, const uint8_t *k_scales, const float *v_scales,
                       int64_t num_blocks, int32_t block_size, const int32_t *block_tables,
                       int64_t bt_row_stride, int32_t bt_width, const int32_t *seq_lens,
                       int64_t seq_lens_stride, int32_t batch, int32_t next_n, int32_t num_heads,

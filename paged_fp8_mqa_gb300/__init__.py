@@ -11,7 +11,8 @@ Low-level names mirror the C ABI (``idx_logits_fp8``, ``idx_threshold_select``,
 check dtypes/devices, and pass pointers, strides and the current CUDA stream through.
 
 The operators around the indexer (rotary positions, the writers of the two 8-bit pools, attention
-over the K/V pool) are bound in ``layer`` and reached from here by the same names.
+over the K/V pool) are bound in ``layer``, normalised and rotated heads in ``heads``, the 4-bit K/V
+cache in ``cache4``; all are reached from here by the same names.
 """
 from __future__ import annotations
 
@@ -417,3 +418,8 @@ from .layer import (IDX_ROTARY_LINEAR, IDX_ROTARY_MAX_DIM, IDX_ROTARY_NONE,  # n
                     idx_attention_workspace_bytes, idx_index_prepare, idx_kv_append, idx_rotary,
                     idx_rotary_frequencies, idx_rotary_table, index_prepare, kv_append, rotary,
                     rotary_table)
+from .heads import (IDX_NORM_MAX_DIM, IDX_ROTARY_MAX_AXES, idx_norm_rotary,  # noqa: E402
+                    idx_norm_rotary_backward, idx_norm_rotary_workspace_bytes, idx_rotary_axes,
+                    norm_rotary, rotary_axes)
+from .cache4 import (attention_fp4, idx_attention_fp4, idx_kv_append_fp4,  # noqa: E402
+                     idx_kv_read_fp4, kv_append_fp4, kv_read_fp4)

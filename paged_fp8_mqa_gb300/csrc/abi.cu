@@ -201,6 +201,21 @@ int encode_rows(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_
   return IDX_OK;
 }
 
+int encode_rows4(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows) {
+  EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return fail(IDX_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[2] = {128, rows};
+  const cuuint64_t strides[1] = {64};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void *>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(IDX_CUDA, "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(r));
+  return IDX_OK;
+}
+
 }  // namespace idx
 
 IDX_EXPORT const char *idx_last_error(void) { return g_error.c_str(); }
@@ -700,7 +715,9 @@ IDX_EXPORT int idx_device_status(int32_t *status_out, int32_t clear) {
   if (e == cudaSuccess) e = idx::mxfp4_status(&c, clear != 0);
   int32_t all = a | b | c;
   for (const auto unit : {idx::rotary_status, idx::index_status, idx::append_status,
-                          idx::attention_d64_status, idx::attention_d128_status}) {
+                          idx::attention_d64_status, idx::attention_d128_status,
+                          idx::attention4_d64_status, idx::attention4_d128_status,
+                          idx::heads_status, idx::kv4_status}) {
     int32_t bits = 0;
     if (e == cudaSuccess) e = unit(&bits, clear != 0);
     all |= bits;

@@ -7,6 +7,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "../../include/idx.h"
 #include "internal.h"
@@ -82,6 +83,107 @@ int check_tokens(const int32_t *token_starts, int64_t tokens, const int32_t *seq
 // Whether rows can be read in pieces of v elements of `size` bytes.
 bool pieces(const void *p, int64_t s0, int64_t s1, int v, int size) {
   return aligned(p, v * size) && s0 % v == 0 && s1 % v == 0;
+}
+
+// Whether every pair lies in whole pieces of eight elements (and its angles can be read two at a time).
+bool heads_in_pieces(const idx::Rotation &r) {
+  return r.table == nullptr || (r.offset % 8 == 0 && r.rot % (r.interleaved ? 8 : 16) == 0 &&
+                                aligned(r.table, 16));
+}
+bool dim_in_pieces(const idx::HeadsArgs &a) {
+  return a.dim % 16 == 0 && a.dim <= 256 && heads_in_pieces(a.r);
+}
+
+// The 4-bit cache's pools.
+int check_kv4(uint8_t *k_pool, uint8_t *v_pool, uint8_t *k_scales, float *v_scales, int32_t dtype,
+              int32_t kv_heads, int32_t head_dim, idx::Kv4Args *a) {
+  if (k_pool == nullptr || v_pool == nullptr || k_scales == nullptr || v_scales == nullptr)
+    return fail(IDX_INVALID_ARG, "k_pool, v_pool, k_scales, v_scales: NULL");
+  if (element_bytes(dtype) == 0)
+    return fail(IDX_UNSUPPORTED, "dtype must be IDX_DTYPE_F32, _F16 or _BF16");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(IDX_UNSUPPORTED, "this build supports head_dim 64 or 128");
+  if (kv_heads < 1 || kv_heads > 4096) return fail(IDX_INVALID_ARG, "kv_heads must be 1 .. 4096");
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(v_scales, 4))
+    return fail(IDX_INVALID_ARG, "k_pool and v_pool must be 16-byte aligned, v_scales 4-byte");
+  a->k_pool = k_pool;
+  a->v_pool = v_pool;
+  a->k_scales = k_scales;
+  a->v_scales = v_scales;
+  a->heads = kv_heads;
+  a->dim = head_dim;
+  return IDX_OK;
+}
+
+// Heads to be rotated by one axis or several (pair_axis: host memory), or not (table == NULL).
+int check_heads(int32_t dtype, int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                const int32_t *positions, int64_t axis_stride, const uint8_t *pair_axis, int32_t axes,
+                const float *table, int32_t max_positions, int32_t rot_dim, int32_t rot_offset,
+                int32_t interleaved, idx::HeadsArgs *a) {
+  if (element_bytes(dtype) == 0)
+    return fail(IDX_UNSUPPORTED, "dtype must be IDX_DTYPE_F32, _F16 or _BF16");
+  if (tokens < 0 || tokens > INT32_MAX || q_heads < 0 || k_heads < 0 || q_heads > 65536 ||
+      k_heads > 65536 || head_dim < 1)
+    return fail(IDX_INVALID_ARG, "negative or too large a size");
+  if (head_dim > IDX_NORM_MAX_DIM)
+    return fail(IDX_UNSUPPORTED, "head_dim above IDX_NORM_MAX_DIM");
+  const int st = check_rotation(table, max_positions, rot_dim, rot_offset, head_dim, &a->r, interleaved);
+  if (st != IDX_OK) return st;
+  a->axes.count = 1;
+  if (table != nullptr) {
+    if (positions == nullptr || !aligned(positions, 4))
+      return fail(IDX_INVALID_ARG, "a table needs positions, 4-byte aligned");
+    if (axes < 1 || axes > IDX_ROTARY_MAX_AXES)
+      return fail(IDX_INVALID_ARG, "axes must be 1 .. IDX_ROTARY_MAX_AXES");
+    if (axes > 1) {
+      if (pair_axis == nullptr || axis_stride < 0)
+        return fail(IDX_INVALID_ARG, "several axes need pair_axis and a stride of 0 or more");
+      for (int i = 0; i < rot_dim / 2; ++i) {
+        if (pair_axis[i] >= axes) return fail(IDX_INVALID_ARG, "pair_axis must be below axes");
+        a->axes.axis[i / 16] |= static_cast<uint32_t>(pair_axis[i]) << (2 * (i % 16));
+      }
+      a->axes.count = axes;
+      a->axes.stride = axis_stride;
+    }
+  }
+  a->positions = positions;
+  a->tokens = tokens;
+  a->heads[0] = q_heads;
+  a->heads[1] = k_heads;
+  a->dim = head_dim;
+  a->sin_sign = 1.0f;
+  return IDX_OK;
+}
+
+int check_norm(int32_t dtype, float eps, const void *q_weight, const void *k_weight,
+               int32_t weight_dtype, idx::HeadsArgs *a) {
+  if (!(eps >= 0.0f) || std::isinf(eps))
+    return fail(IDX_INVALID_ARG, "eps must be finite, 0 or more");
+  if (q_weight != nullptr || k_weight != nullptr) {
+    if (weight_dtype != dtype && weight_dtype != IDX_DTYPE_F32)
+      return fail(IDX_UNSUPPORTED, "weights must have the dtype of q and k, or float32");
+    const int size = element_bytes(weight_dtype);
+    if (!aligned(q_weight, size) || !aligned(k_weight, size))
+      return fail(IDX_INVALID_ARG, "weights must be aligned to their elements");
+  }
+  a->norm = 1;
+  a->eps = eps;
+  a->weight[0] = q_weight;
+  a->weight[1] = k_weight;
+  a->weight_f32 = weight_dtype == IDX_DTYPE_F32;
+  return IDX_OK;
+}
+
+// Rows [tokens][heads][dim] of one operand; whole: still all of them in pieces of eight elements.
+int set_rows(const void *p, int64_t token, int64_t head, int size, const void **to, int64_t *token_to,
+             int64_t *head_to, bool *whole) {
+  if (!aligned(p, size))
+    return fail(IDX_INVALID_ARG, "rows must be aligned to their elements");
+  *to = p;
+  *token_to = token;
+  *head_to = head;
+  *whole = *whole && pieces(p, token, head, 8, size);
+  return IDX_OK;
 }
 
 }  // namespace
@@ -308,16 +410,19 @@ IDX_EXPORT int64_t idx_attention_workspace_bytes(int32_t batch, int32_t next_n, 
   return idx::attention_workspace(batch, next_n, num_heads, kv_heads, head_dim, sms);
 }
 
-IDX_EXPORT int idx_attention_fp8(
+namespace {
+
+// idx_attention_fp8 and (four) idx_attention_fp4.
+int attention(
+    bool four,
     const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
-    int32_t dtype, const uint8_t *k_pool, const uint8_t *v_pool, const float *k_scales,
+    int32_t dtype, const uint8_t *k_pool, const uint8_t *v_pool, const void *k_scales,
     const float *v_scales, int64_t num_blocks, int32_t block_size, const int32_t *block_tables,
     int64_t bt_row_stride, int32_t bt_width, const int32_t *seq_lens, int64_t seq_lens_stride,
     int32_t batch, int32_t next_n, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
     float softmax_scale, const int32_t *candidates, int32_t slots, const int32_t *ranges,
     int32_t num_sms, void *out, float *lse, void *workspace, int64_t workspace_bytes,
     void *stream) {
-  idx::clear_error();
   if (q == nullptr || k_pool == nullptr || v_pool == nullptr || k_scales == nullptr ||
       v_scales == nullptr || block_tables == nullptr || seq_lens == nullptr || out == nullptr)
     return fail(IDX_INVALID_ARG, "q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, "
@@ -350,6 +455,9 @@ IDX_EXPORT int idx_attention_fp8(
       !aligned(workspace, 256))
     return fail(IDX_INVALID_ARG, "pools and out must be 16-byte aligned, candidates 8-byte, "
                                  "workspace 256-byte, the rest 4-byte");
+  if (four && (!aligned(k_pool, 32) || !aligned(v_pool, 32) || !aligned(k_scales, 16) ||
+               !aligned(v_scales, 16)))
+    return fail(IDX_INVALID_ARG, "4-bit pools must be 32-byte aligned, their scales 16-byte");
   int32_t ctas = 0;
   int st = idx::resolve_sms(num_sms, &ctas);
   if (st != IDX_OK) return st;
@@ -388,16 +496,258 @@ IDX_EXPORT int idx_attention_fp8(
   a.lse = lse;
   a.workspace = static_cast<float *>(workspace);
   CUtensorMap k_map{}, v_map{};  // (with candidates the rows are gathered without them)
-  if (candidates == nullptr) {
+  if (candidates == nullptr && !(four && head_dim != 128)) {
     const uint64_t rows = static_cast<uint64_t>(num_blocks) * kv_heads * block_size;
-    st = idx::encode_rows(&k_map, k_pool, rows, static_cast<uint32_t>(head_dim),
-                          static_cast<uint32_t>(block_size));
-    if (st != IDX_OK) return st;
-    st = idx::encode_rows(&v_map, v_pool, rows, static_cast<uint32_t>(head_dim),
-                          static_cast<uint32_t>(block_size));
-    if (st != IDX_OK) return st;
+    const uint32_t box = static_cast<uint32_t>(block_size);
+    for (const auto &m : {std::pair<CUtensorMap *, const uint8_t *>{&k_map, k_pool}, {&v_map, v_pool}}) {
+      st = four ? idx::encode_rows4(m.first, m.second, rows, box)
+                : idx::encode_rows(m.first, m.second, rows, static_cast<uint32_t>(head_dim), box);
+      if (st != IDX_OK) return st;
+    }
   }
-  const auto launch = head_dim == 64 ? idx::launch_attention_d64 : idx::launch_attention_d128;
+  const auto launch = four ? (head_dim == 64 ? idx::launch_attention4_d64 : idx::launch_attention4_d128)
+                           : (head_dim == 64 ? idx::launch_attention_d64 : idx::launch_attention_d128);
   const cudaError_t e = launch(k_map, v_map, a, dtype, ctas, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? IDX_OK : cuda_fail(e, "attention launch");
+}
+
+}  // namespace
+
+IDX_EXPORT int idx_attention_fp8(
+    const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
+    int32_t dtype, const uint8_t *k_pool, const uint8_t *v_pool, const float *k_scales,
+    const float *v_scales, int64_t num_blocks, int32_t block_size, const int32_t *block_tables,
+    int64_t bt_row_stride, int32_t bt_width, const int32_t *seq_lens, int64_t seq_lens_stride,
+    int32_t batch, int32_t next_n, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
+    float softmax_scale, const int32_t *candidates, int32_t slots, const int32_t *ranges,
+    int32_t num_sms, void *out, float *lse, void *workspace, int64_t workspace_bytes,
+    void *stream) {
+  idx::clear_error();
+  return attention(false, q, q_batch_stride, q_token_stride, q_head_stride, dtype, k_pool, v_pool, k_scales,
+                   v_scales, num_blocks, block_size, block_tables, bt_row_stride, bt_width, seq_lens,
+                   seq_lens_stride, batch, next_n, num_heads, kv_heads, head_dim, softmax_scale,
+                   candidates, slots, ranges, num_sms, out, lse, workspace, workspace_bytes, stream);
+}
+
+IDX_EXPORT int idx_attention_fp4(
+    const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
+    int32_t dtype, const uint8_t *k_pool, const uint8_t *v_pool, const uint8_t *k_scales,
+    const float *v_scales, int64_t num_blocks, int32_t block_size, const int32_t *block_tables,
+    int64_t bt_row_stride, int32_t bt_width, const int32_t *seq_lens, int64_t seq_lens_stride,
+    int32_t batch, int32_t next_n, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
+    float softmax_scale, const int32_t *candidates, int32_t slots, const int32_t *ranges,
+    int32_t num_sms, void *out, float *lse, void *workspace, int64_t workspace_bytes,
+    void *stream) {
+  idx::clear_error();
+  return attention(true, q, q_batch_stride, q_token_stride, q_head_stride, dtype, k_pool, v_pool, k_scales,
+                   v_scales, num_blocks, block_size, block_tables, bt_row_stride, bt_width, seq_lens,
+                   seq_lens_stride, batch, next_n, num_heads, kv_heads, head_dim, softmax_scale,
+                   candidates, slots, ranges, num_sms, out, lse, workspace, workspace_bytes, stream);
+}
+
+IDX_EXPORT int idx_kv_append_fp4(const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                                 const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                                 int32_t dtype, int64_t tokens, int32_t kv_heads, int32_t head_dim,
+                                 const float *table, int32_t max_positions, int32_t rot_dim,
+                                 int32_t rot_offset, int32_t interleaved,
+                                 const int32_t *token_starts, const int32_t *seq_lens,
+                                 int64_t seq_lens_stride, int32_t batch, int32_t next_n,
+                                 const int32_t *block_tables, int64_t bt_row_stride,
+                                 int32_t bt_width, int32_t block_size, int64_t num_blocks,
+                                 uint8_t *k_pool, uint8_t *v_pool, uint8_t *k_scales,
+                                 float *v_scales, void *stream) {
+  idx::clear_error();
+  if (k == nullptr || v == nullptr) return fail(IDX_INVALID_ARG, "k, v: NULL");
+  idx::Kv4Args a{};
+  int st = check_kv4(k_pool, v_pool, k_scales, v_scales, dtype, kv_heads, head_dim, &a);
+  if (st != IDX_OK) return st;
+  st = check_tokens(token_starts, tokens, seq_lens, seq_lens_stride, batch, next_n, block_tables,
+                    bt_row_stride, bt_width, block_size, num_blocks, &a.m);
+  if (st != IDX_OK) return st;
+  st = check_rotation(table, max_positions, rot_dim, rot_offset, head_dim, &a.r, interleaved);
+  if (st != IDX_OK) return st;
+  const int size = element_bytes(dtype);
+  if (!aligned(k, size) || !aligned(v, size))
+    return fail(IDX_INVALID_ARG, "k and v must be aligned to their elements");
+  if (tokens == 0 || batch == 0) return IDX_OK;
+  a.k = k;
+  a.v = v;
+  a.k_token = k_token_stride;
+  a.k_head = k_head_stride;
+  a.v_token = v_token_stride;
+  a.v_head = v_head_stride;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  const bool k_pieces = pieces(k, k_token_stride, k_head_stride, 8, size);
+  const bool all = k_pieces && pieces(v, v_token_stride, v_head_stride, 8, size);
+  const cudaError_t e = idx::launch_kv4_append(a, dtype, all, k_pieces && heads_in_pieces(a.r),
+                                               static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? IDX_OK : cuda_fail(e, "kv_append_fp4 launch");
+}
+
+IDX_EXPORT int idx_kv_read_fp4(const uint8_t *k_pool, const uint8_t *v_pool, const uint8_t *k_scales,
+                               const float *v_scales, int64_t num_blocks, int32_t block_size,
+                               int32_t kv_heads, int32_t head_dim, const int32_t *token_starts,
+                               int64_t tokens, const int32_t *seq_lens, int64_t seq_lens_stride,
+                               int32_t batch, int32_t next_n, const int32_t *block_tables,
+                               int64_t bt_row_stride, int32_t bt_width, int32_t clear, int32_t dtype,
+                               void *k_out,
+                               int64_t k_token_stride, int64_t k_head_stride, void *v_out,
+                               int64_t v_token_stride, int64_t v_head_stride, void *stream) {
+  idx::clear_error();
+  if (k_out == nullptr || v_out == nullptr) return fail(IDX_INVALID_ARG, "k_out, v_out: NULL");
+  idx::Kv4Args a{};
+  int st = check_kv4(const_cast<uint8_t *>(k_pool), const_cast<uint8_t *>(v_pool),
+                     const_cast<uint8_t *>(k_scales), const_cast<float *>(v_scales), dtype, kv_heads,
+                     head_dim, &a);
+  if (st != IDX_OK) return st;
+  st = check_tokens(token_starts, tokens, seq_lens, seq_lens_stride, batch, next_n, block_tables,
+                    bt_row_stride, bt_width, block_size, num_blocks, &a.m);
+  if (st != IDX_OK) return st;
+  const int size = element_bytes(dtype);
+  if (!aligned(k_out, size) || !aligned(v_out, size))
+    return fail(IDX_INVALID_ARG, "k_out and v_out must be aligned to their elements");
+  if (tokens == 0 || batch == 0) return IDX_OK;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.k_token = k_token_stride;
+  a.k_head = k_head_stride;
+  a.v_token = v_token_stride;
+  a.v_head = v_head_stride;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  const bool all = pieces(k_out, k_token_stride, k_head_stride, 8, size) &&
+                   pieces(v_out, v_token_stride, v_head_stride, 8, size);
+  const cudaError_t e = idx::launch_kv4_read(a, dtype, all, clear != 0,
+                                             static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? IDX_OK : cuda_fail(e, "kv_read_fp4 launch");
+}
+
+IDX_EXPORT int idx_rotary_axes(const void *x, int64_t x_token_stride, int64_t x_head_stride,
+                               const int32_t *positions, int64_t axis_stride,
+                               const uint8_t *pair_axis, int32_t axes, int64_t tokens,
+                               int32_t num_heads, int32_t head_dim, int32_t dtype,
+                               const float *table, int32_t max_positions, int32_t rot_dim,
+                               int32_t rot_offset, int32_t interleaved, int32_t inverse, void *out,
+                               int64_t out_token_stride, int64_t out_head_stride, void *stream) {
+  idx::clear_error();
+  if (x == nullptr || table == nullptr || positions == nullptr || out == nullptr)
+    return fail(IDX_INVALID_ARG, "x, positions, table, out: NULL");
+  idx::HeadsArgs a{};
+  int st = check_heads(dtype, tokens, num_heads, 0, head_dim, positions, axis_stride, pair_axis, axes,
+                       table, max_positions, rot_dim, rot_offset, interleaved, &a);
+  if (st != IDX_OK) return st;
+  bool whole = true;
+  st = set_rows(x, x_token_stride, x_head_stride, element_bytes(dtype), &a.x[0], &a.x_token[0],
+                &a.x_head[0], &whole);
+  if (st == IDX_OK)
+    st = set_rows(out, out_token_stride, out_head_stride, element_bytes(dtype),
+                  const_cast<const void **>(&a.out[0]), &a.out_token[0], &a.out_head[0], &whole);
+  if (st != IDX_OK) return st;
+  if (tokens == 0 || num_heads == 0) return IDX_OK;
+  a.sin_sign = inverse ? -1.0f : 1.0f;
+  const cudaError_t e = idx::launch_heads(a, dtype, whole && dim_in_pieces(a),
+                                          static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? IDX_OK : cuda_fail(e, "rotary launch");
+}
+
+IDX_EXPORT int idx_norm_rotary(
+    const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads, const void *k,
+    int64_t k_token_stride, int64_t k_head_stride, int32_t k_heads, int32_t dtype, int64_t tokens,
+    int32_t head_dim, const void *q_weight, const void *k_weight, int32_t weight_dtype, float eps,
+    const int32_t *positions, int64_t axis_stride, const uint8_t *pair_axis, int32_t axes,
+    const float *table, int32_t max_positions, int32_t rot_dim, int32_t rot_offset,
+    int32_t interleaved, void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+    void *k_out, int64_t k_out_token_stride, int64_t k_out_head_stride, void *stream) {
+  idx::clear_error();
+  if (q == nullptr || q_out == nullptr || (k_heads > 0 && (k == nullptr || k_out == nullptr)))
+    return fail(IDX_INVALID_ARG, "q, q_out (with k_heads: k, k_out): NULL");
+  idx::HeadsArgs a{};
+  int st = check_heads(dtype, tokens, q_heads, k_heads, head_dim, positions, axis_stride, pair_axis,
+                       axes, table, max_positions, rot_dim, rot_offset, interleaved, &a);
+  if (st == IDX_OK) st = check_norm(dtype, eps, q_weight, k_weight, weight_dtype, &a);
+  if (st != IDX_OK) return st;
+  const int size = element_bytes(dtype);
+  bool whole = true;
+  st = set_rows(q, q_token_stride, q_head_stride, size, &a.x[0], &a.x_token[0], &a.x_head[0], &whole);
+  if (st == IDX_OK)
+    st = set_rows(q_out, q_out_token_stride, q_out_head_stride, size,
+                  const_cast<const void **>(&a.out[0]), &a.out_token[0], &a.out_head[0], &whole);
+  if (st == IDX_OK && k_heads > 0)
+    st = set_rows(k, k_token_stride, k_head_stride, size, &a.x[1], &a.x_token[1], &a.x_head[1], &whole);
+  if (st == IDX_OK && k_heads > 0)
+    st = set_rows(k_out, k_out_token_stride, k_out_head_stride, size,
+                  const_cast<const void **>(&a.out[1]), &a.out_token[1], &a.out_head[1], &whole);
+  if (st != IDX_OK) return st;
+  if (tokens == 0 || q_heads + k_heads == 0) return IDX_OK;
+  const cudaError_t e = idx::launch_heads(a, dtype, whole && dim_in_pieces(a),
+                                          static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? IDX_OK : cuda_fail(e, "norm_rotary launch");
+}
+
+IDX_EXPORT int64_t idx_norm_rotary_workspace_bytes(int32_t head_dim) {
+  idx::clear_error();
+  if (head_dim < 1 || head_dim > IDX_NORM_MAX_DIM) return -1;
+  int32_t sms = 0;
+  if (idx::resolve_sms(0, &sms) != IDX_OK) return -1;
+  return 2ll * idx::heads_blocks(sms) * head_dim * 4;
+}
+
+IDX_EXPORT int idx_norm_rotary_backward(
+    const void *q, int64_t q_token_stride, int64_t q_head_stride, int32_t q_heads, const void *k,
+    int64_t k_token_stride, int64_t k_head_stride, int32_t k_heads, int32_t dtype, int64_t tokens,
+    int32_t head_dim, const void *q_weight, const void *k_weight, int32_t weight_dtype, float eps,
+    const int32_t *positions, int64_t axis_stride, const uint8_t *pair_axis, int32_t axes,
+    const float *table, int32_t max_positions, int32_t rot_dim, int32_t rot_offset,
+    int32_t interleaved, const void *q_out_grad, int64_t qg_token_stride, int64_t qg_head_stride,
+    const void *k_out_grad, int64_t kg_token_stride, int64_t kg_head_stride, void *q_grad,
+    void *k_grad, void *q_weight_grad, void *k_weight_grad, void *workspace,
+    int64_t workspace_bytes, void *stream) {
+  idx::clear_error();
+  if (q == nullptr || q_out_grad == nullptr || q_grad == nullptr ||
+      (k_heads > 0 && (k == nullptr || k_out_grad == nullptr || k_grad == nullptr)))
+    return fail(IDX_INVALID_ARG, "q, q_out_grad, q_grad (with k_heads: k, k_out_grad, k_grad): NULL");
+  idx::HeadsArgs a{};
+  int st = check_heads(dtype, tokens, q_heads, k_heads, head_dim, positions, axis_stride, pair_axis,
+                       axes, table, max_positions, rot_dim, rot_offset, interleaved, &a);
+  if (st == IDX_OK) st = check_norm(dtype, eps, q_weight, k_weight, weight_dtype, &a);
+  if (st != IDX_OK) return st;
+  if ((q_weight_grad != nullptr && q_weight == nullptr) ||
+      (k_weight_grad != nullptr && k_weight == nullptr))
+    return fail(IDX_INVALID_ARG, "a weight's gradient without the weight");
+  const int size = element_bytes(dtype), wsize = element_bytes(weight_dtype);
+  if (!aligned(q_weight_grad, wsize ? wsize : 1) || !aligned(k_weight_grad, wsize ? wsize : 1))
+    return fail(IDX_INVALID_ARG, "the weights' gradients must be aligned to their elements");
+  bool whole = true;
+  const int64_t qt = static_cast<int64_t>(q_heads) * head_dim, kt = static_cast<int64_t>(k_heads) * head_dim;
+  st = set_rows(q, q_token_stride, q_head_stride, size, &a.x[0], &a.x_token[0], &a.x_head[0], &whole);
+  if (st == IDX_OK)
+    st = set_rows(q_out_grad, qg_token_stride, qg_head_stride, size, &a.dy[0], &a.dy_token[0],
+                  &a.dy_head[0], &whole);
+  if (st == IDX_OK)
+    st = set_rows(q_grad, qt, head_dim, size, const_cast<const void **>(&a.out[0]), &a.out_token[0],
+                  &a.out_head[0], &whole);
+  if (st == IDX_OK && k_heads > 0)
+    st = set_rows(k, k_token_stride, k_head_stride, size, &a.x[1], &a.x_token[1], &a.x_head[1], &whole);
+  if (st == IDX_OK && k_heads > 0)
+    st = set_rows(k_out_grad, kg_token_stride, kg_head_stride, size, &a.dy[1], &a.dy_token[1],
+                  &a.dy_head[1], &whole);
+  if (st == IDX_OK && k_heads > 0)
+    st = set_rows(k_grad, kt, head_dim, size, const_cast<const void **>(&a.out[1]), &a.out_token[1],
+                  &a.out_head[1], &whole);
+  if (st != IDX_OK) return st;
+  int32_t sms = 0;
+  st = idx::resolve_sms(0, &sms);
+  if (st != IDX_OK) return st;
+  if (workspace == nullptr || !aligned(workspace, 16) ||
+      workspace_bytes < 2ll * idx::heads_blocks(sms) * head_dim * 4)
+    return fail(IDX_INVALID_ARG, "workspace (16-byte aligned) below "
+                                 "idx_norm_rotary_workspace_bytes(...)");
+  a.dweight[0] = q_weight_grad;
+  a.dweight[1] = k_heads > 0 ? k_weight_grad : nullptr;
+  a.workspace = static_cast<float *>(workspace);
+  a.sin_sign = -1.0f;
+  const cudaError_t e = idx::launch_heads_backward(a, dtype, whole && dim_in_pieces(a), sms,
+                                                   static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? IDX_OK : cuda_fail(e, "norm_rotary_backward launch");
 }

@@ -6,8 +6,8 @@ namespace idx {
 
 cudaError_t launch_attention_d128(const CUtensorMap &k_map, const CUtensorMap &v_map,
                                  const AttentionArgs &a, int dtype, int sms, cudaStream_t stream) {
-  return a.candidates != nullptr ? launch_rows<128, true>(k_map, v_map, a, dtype, sms, stream)
-                                 : launch_rows<128, false>(k_map, v_map, a, dtype, sms, stream);
+  return a.candidates != nullptr ? launch_rows<128, true, false>(k_map, v_map, a, dtype, sms, stream)
+                                 : launch_rows<128, false, false>(k_map, v_map, a, dtype, sms, stream);
 }
 
 cudaError_t attention_d128_status(int32_t *value, bool clear) {
@@ -19,7 +19,7 @@ int64_t attention_workspace(int batch, int next_n, int heads, int kv_heads, int 
   for (const bool f16 : {false, true})
     for (const bool select : {false, true}) {
       const AttnShape s = attn_shape(heads / kv_heads * (select ? 1 : next_n), f16);
-      const int on_sm = dim == 64 ? ctas_for<64, false>(s.r, f16) : ctas_for<128, false>(s.r, f16);
+      const int on_sm = dim == 64 ? ctas_for<64, false, false>(s.r, f16) : ctas_for<128, false, false>(s.r, f16);
       const int64_t groups =
           static_cast<int64_t>(select ? batch * next_n : batch) * kv_heads * s.chunks;
       const int64_t bytes = attn_slots_bytes(static_cast<int64_t>(sms) * on_sm, s.r, dim) +

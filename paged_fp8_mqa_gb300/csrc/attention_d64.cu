@@ -6,8 +6,8 @@ namespace idx {
 
 cudaError_t launch_attention_d64(const CUtensorMap &k_map, const CUtensorMap &v_map,
                                  const AttentionArgs &a, int dtype, int sms, cudaStream_t stream) {
-  return a.candidates != nullptr ? launch_rows<64, true>(k_map, v_map, a, dtype, sms, stream)
-                                 : launch_rows<64, false>(k_map, v_map, a, dtype, sms, stream);
+  return a.candidates != nullptr ? launch_rows<64, true, false>(k_map, v_map, a, dtype, sms, stream)
+                                 : launch_rows<64, false, false>(k_map, v_map, a, dtype, sms, stream);
 }
 
 cudaError_t attention_d64_status(int32_t *value, bool clear) {

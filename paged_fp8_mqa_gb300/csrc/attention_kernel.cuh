@@ -60,11 +60,13 @@ constexpr float kRefNone = -1e30f;             // the reference of a row that ha
 constexpr float kTop = 11.0f, kMost = 15.8f, kUp2 = 8.0f, kUp = 16.0f;
 constexpr float kLeastScale = 7.8886090522101180541e-31f;  // 2^-100: a value scale below it is 0
 
-// One kernel's shape: R rows, PARTS parts a weight, head_dim D.
-template <int D_, int R_, int PARTS_, bool SELECT_>
+// One kernel's shape: R rows, PARTS parts a weight, head_dim D; FP4: the cache in four bits.
+template <int D_, int R_, int PARTS_, bool SELECT_, bool FP4_>
 struct AttnCfg {
   static constexpr int D = D_, R = R_, PARTS = PARTS_;
-  static constexpr bool SELECT = SELECT_;
+  static constexpr bool SELECT = SELECT_, FP4 = FP4_;
+  // Rows by ordinary asynchronous copies, not by the TMA unit (whose 4-bit boxes are 128 elements wide).
+  static constexpr bool COPIES = SELECT || (FP4 && D != 128);
   static constexpr int QPARTS = 3;                    // parts of a query
   // With R = 8 a query's parts stand side by side, in columns that are added when read (the last
   // eight of 32 mean nothing); else each part is a product of its own into the same columns.  (Three
@@ -80,7 +82,9 @@ struct AttnCfg {
   // softmax's registers leave room for.
   static constexpr int LOADERS = !SELECT || R == 32 ? 1 : R == 8 ? 4 : 2;
   static constexpr int THREADS = 32 * (LOADERS + 1 + SOFT_WARPS);
-  static constexpr int COLS = 2 * NS + NO;            // two of S, one of O
+  // Two of S, one of O; with FP4 the keys' scale factors, two tiles of them, and the queries' (1).
+  static constexpr int SFA = 2 * NS + NO, SFB = SFA + 8;
+  static constexpr int COLS = FP4 ? SFB + 4 : SFA;
   static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   // CTAs on an SM, each with a pipeline of its own, so that one's loads and products run beside the
   // other's softmax.  Three of two stages instead of two of three: decode took 1.4 times as long, as
@@ -93,8 +97,9 @@ struct AttnCfg {
   // They take the place of the tile's keys, which have been read by then, where they fit it; else
   // two buffers of their own.
   static constexpr bool OVER_K = P_BYTES <= kTile * D;
-  static constexpr int AUX = kTile * 16;              // a stage's Token records
-  static constexpr int MISC = 48 * R + 3 * D * 4 + 256;
+  static constexpr int SF_BYTES = FP4 ? kTile * 4 : 0;  // a stage's scale factors of the keys
+  static constexpr int AUX = kTile * 16 + SF_BYTES;   // and its Token records
+  static constexpr int MISC = 48 * R + (FP4 ? 0 : 3 * D * 4) + 256;
   static constexpr int FIXED = 1024 + Q_BYTES + (OVER_K ? 0 : 2 * P_BYTES) + MISC;
   static constexpr int ROOM = CTAS == 2 ? 115456 : 231424;
   static constexpr int FIT = (ROOM - FIXED) / (KV_BYTES + AUX);
@@ -122,6 +127,32 @@ __device__ __forceinline__ Token token_of(float k, float v_scale, int pos) {
   t.inv_v = copysignf(1.0f / held, v_scale);
   t.pos = pos;
   return t;
+}
+
+// A key's scale factors (FP4): its bytes, one for each 32 elements.
+template <int D>
+__device__ __forceinline__ uint32_t scale_factors(const void *scales, int64_t row) {
+  if constexpr (D == 128)
+    return __ldg(static_cast<const uint32_t *>(scales) + row);
+  else
+    return __ldg(static_cast<const uint16_t *>(scales) + row);
+}
+// Token::k of a key with these factors: the tensor core applies them; a byte of 0xFF is NaN.
+template <int D>
+__device__ __forceinline__ float unit_of_factors(uint32_t factors, float z_unit) {
+  if constexpr (D != 128) factors |= factors << 16;
+  return __vcmpeq4(factors, 0xFFFFFFFFu) != 0 ? __int_as_float(0x7FC00000) : z_unit;
+}
+
+// 16 elements of a pool's row, from element x on, to shared memory (FP4: eight bytes, the lower half
+// of the 16 that they take there).
+template <bool FP4, int D>
+__device__ __forceinline__ void copy_piece(uint8_t *dst, const uint8_t *pool, int row, int x,
+                                           uint64_t policy) {
+  if constexpr (FP4)
+    cp_async_8(dst, pool + static_cast<int64_t>(row) * (D / 2) + x / 2);
+  else
+    cp_async_16(dst, pool + static_cast<int64_t>(row) * D + x, policy);
 }
 
 // Where the runs' parts of a group are, written by the CTA that has the group's first tile.
@@ -246,6 +277,7 @@ __device__ __forceinline__ uint64_t smem_desc_p(uint32_t saddr) {
 
 constexpr uint32_t kMajorMN_A = 1u << 15, kMajorMN_B = 1u << 16;
 constexpr uint32_t kE5m2_B = 1u << 10;  // (the operands' types are set one by one)
+constexpr uint32_t kE2m1_A = 5u << 7;
 
 // Byte offset of byte x of row n in K-major rows of D bytes with the matching swizzle.
 template <int D>
@@ -372,7 +404,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     return C::OVER_K ? s_kv + stage * C::KV_BYTES : s_p + (tile & 1) * C::P_BYTES;
   };
   Token *s_tok = reinterpret_cast<Token *>(at);      // [stage][kTile]
-  at += C::STAGES * C::AUX;
+  at += C::STAGES * kTile * 16;
+  uint32_t *s_sf = reinterpret_cast<uint32_t *>(at);  // [stage][32][4]: token t's at [t % 32][t / 32]
+  at += C::STAGES * C::SF_BYTES;
   float *s_max = reinterpret_cast<float *>(at);      // [R][4 warps]
   at += R * 16;
   float *s_sum = reinterpret_cast<float *>(at);      // [R][4 warps]
@@ -384,7 +418,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   int *s_row = reinterpret_cast<int *>(at);          // [2][R]: a row's (b, t, h) in line, by segment
   at += 2 * R * 4;
   int *s_nan = reinterpret_cast<int *>(at);          // [3][D]: see below
-  at += 3 * D * 4;
+  if constexpr (!C::FP4) at += 3 * D * 4;
   uint64_t *bars = reinterpret_cast<uint64_t *>(at);
   uint64_t *kv_full = bars, *kv_empty = bars + C::STAGES, *s_full = bars + 2 * C::STAGES,
            *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *drain = q_full + 1;
@@ -398,13 +432,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   const int keys = C::SELECT ? a.batch * a.next_n : a.batch;
 
   if (warp == 0 && lane == 0) {
-    if constexpr (!C::SELECT) {
+    if constexpr (!C::COPIES) {
       prefetch_tensor_map(&k_map);
       prefetch_tensor_map(&v_map);
     }
     for (int i = 0; i < C::STAGES; ++i) {
-      // A loading lane's arrival; with SELECT also one when its copies have landed.
-      mbar_init(&kv_full[i], C::SELECT ? 64 * C::LOADERS : 32);
+      // A loading lane's arrival, and one when its own copies have landed.
+      mbar_init(&kv_full[i], C::COPIES ? 64 * C::LOADERS : 32);
       mbar_init(&kv_empty[i], 1);
     }
     mbar_init(&s_full[0], 1);
@@ -422,7 +456,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     tmem_alloc(s_tmem, C::TMEM);
     tmem_relinquish();
   }
-  for (int i = tid; i < 3 * D; i += C::THREADS) s_nan[i] = 0;
+  if constexpr (!C::FP4)
+    for (int i = tid; i < 3 * D; i += C::THREADS) s_nan[i] = 0;
   griddep_wait();
   griddep_launch_dependents();
 
@@ -553,15 +588,23 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
         if (bad) attn_flag(IDX_DEV_BAD_PAGE);
       };
-      const auto scales = [&](const int (&row)[EACH], float (&ks)[EACH], float (&vs)[EACH]) {
+      // (FP4: a token's own, the keys' a word of scale factors.)
+      using KeyScale = std::conditional_t<C::FP4, uint32_t, float>;
+      const auto scales = [&](const int (&row)[EACH], KeyScale (&ks)[EACH], float (&vs)[EACH]) {
 #pragma unroll
         for (int j = 0; j < EACH; ++j) {
-          ks[j] = row[j] >= 0 ? __ldg(a.k_scales + (row[j] >> shift)) : 0.0f;
-          vs[j] = row[j] >= 0 ? __ldg(a.v_scales + (row[j] >> shift)) : 0.0f;
+          if constexpr (C::FP4) {
+            ks[j] = row[j] >= 0 ? scale_factors<D>(a.k_scales, row[j]) : 0u;
+            vs[j] = row[j] >= 0 ? __ldg(a.v_scales + row[j]) : 0.0f;
+          } else {
+            ks[j] = row[j] >= 0 ? __ldg(static_cast<const float *>(a.k_scales) + (row[j] >> shift)) : 0.0f;
+            vs[j] = row[j] >= 0 ? __ldg(a.v_scales + (row[j] >> shift)) : 0.0f;
+          }
         }
       };
       int row0[EACH], row1[EACH];
-      float ks0[EACH], vs0[EACH], ks1[EACH], vs1[EACH];
+      KeyScale ks0[EACH], ks1[EACH];
+      float vs0[EACH], vs1[EACH];
       positions();
       bool live0 = far.live, live1 = false, primed = false;
       pool_rows(row0);
@@ -583,10 +626,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             const int n = j * kRows + sub;  // lane n's q-th token
             const int row = __shfl_sync(0xffffffffu, row0[q], n);
             if (row < 0) continue;  // (the softmax clears the value row of a token that is not)
-            const int64_t src = static_cast<int64_t>(row) * D + x;
             const uint32_t dst = swizzled<D>(token0 - lane + 32 * q + n, x);
-            cp_async_16(kt + dst, a.k_pool + src, policy);
-            cp_async_16(vt + dst, a.v_pool + src, policy);
+            copy_piece<C::FP4, D>(kt + dst, a.k_pool, row, x, policy);
+            copy_piece<C::FP4, D>(vt + dst, a.v_pool, row, x, policy);
           }
         if (!primed) {  // (the first tile's copies go out before anything waits for the second's ids)
           primed = true;
@@ -596,9 +638,18 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           scales(row1, ks1, vs1);
         }
 #pragma unroll
-        for (int j = 0; j < EACH; ++j)
-          s_tok[stage * kTile + token0 + 32 * j] =
-              token_of(ks0[j] * z_unit, vs0[j], row0[j] >= 0 ? 0 : kNone);
+        for (int j = 0; j < EACH; ++j) {
+          const int t = token0 + 32 * j;
+          float k;
+          if constexpr (C::FP4) {
+            k = unit_of_factors<D>(ks0[j], z_unit);
+            s_sf[(stage * 32 + t % 32) * 4 + t / 32] = ks0[j];
+          } else {
+            k = ks0[j] * z_unit;
+          }
+          s_tok[stage * kTile + t] = token_of(k, vs0[j], row0[j] >= 0 ? 0 : kNone);
+        }
+        if constexpr (C::FP4) fence_proxy_async_shared();
         cp_async_arrive_noinc(&kv_full[stage]);
         mbar_arrive(&kv_full[stage]);
         next_stage();
@@ -612,6 +663,95 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         pool_rows(row1);
         live1 = far.live;
         if (live1) positions();
+      }
+    } else if constexpr (C::FP4) {
+      while (ok && w.next(a, groups, keys)) {
+        const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
+        const int32_t *table = a.block_tables + m.b * a.bt_stride;
+        // A lane reads one page's id, 32 pages ahead of the ones in hand, and looks after four tokens
+        // of a tile, whose scales it reads one tile ahead.
+        const int n_pages = (w.length + a.block_size - 1) >> shift;
+        const int per_tile = kTile >> shift;
+        int first = w.seg_tile * per_tile;  // the page of lane 0
+        const auto ids = [&](int page) {
+          if (page >= n_pages || page >= (w.seg_tile + w.seg_tiles) * per_tile) return -1;
+          const int id = page < a.bt_width ? __ldg(table + page) : -1;
+          if (id >= 0 && id < a.num_blocks) return id;
+          attn_flag(IDX_DEV_BAD_PAGE);
+          return -1;
+        };
+        int id = ids(first + lane), id_next = ids(first + 32 + lane);
+        // The pool's row of this lane's first token in tile i (one of the 64 pages in hand), or -1.
+        const auto row_of = [&](int i) {
+          const int p = i * kTile + lane * 4;
+          const int block =
+              __shfl_sync(0xffffffffu, i * per_tile < first + 32 ? id : id_next, (p >> shift) - first);
+          return block < 0 ? -1 : ((block * a.kv_heads + m.g) << shift) + (p & (a.block_size - 1));
+        };
+        const auto scales = [&](int row, uint32_t (&ks)[4], float4 &vs) {
+          vs = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          ks[0] = ks[1] = ks[2] = ks[3] = 0u;
+          if (row < 0) return;
+          vs = __ldg(reinterpret_cast<const float4 *>(a.v_scales + row));
+          if constexpr (D == 128) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a.k_scales) + row / 4);
+            ks[0] = u.x, ks[1] = u.y, ks[2] = u.z, ks[3] = u.w;
+          } else {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(a.k_scales) + row / 4);
+            ks[0] = u.x & 0xFFFFu, ks[1] = u.x >> 16, ks[2] = u.y & 0xFFFFu, ks[3] = u.y >> 16;
+          }
+        };
+        int row = row_of(w.seg_tile), row_next = -1;
+        uint32_t ks[4], ks_next[4];
+        float4 vs, vs_next;
+        scales(row, ks, vs);
+        const int end = w.seg_tile + w.seg_tiles;
+        for (int i = w.seg_tile; i < end; ++i) {
+          if (i + 1 < end) row_next = row_of(i + 1);
+          else row_next = -1;
+          scales(row_next, ks_next, vs_next);
+          if (!stage_free()) break;
+          uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
+          const int p = i * kTile + lane * 4;
+          if constexpr (C::COPIES) {
+            constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+            const int x = (lane % kLanes) * 16, sub = lane / kLanes;
+#pragma unroll
+            for (int j = 0; j < kTile / kRows; ++j) {
+              const int n = j * kRows + sub;
+              const int r0 = __shfl_sync(0xffffffffu, row, n / 4);
+              if (r0 < 0) continue;
+              copy_piece<true, D>(kt + swizzled<D>(n, x), a.k_pool, r0 + n % 4, x, policy);
+              copy_piece<true, D>(vt + swizzled<D>(n, x), a.v_pool, r0 + n % 4, x, policy);
+            }
+          } else if (row >= 0 && (p & (a.block_size - 1)) == 0) {
+            // (The barrier counts the bytes read, half of those that the rows take here.)
+            mbar_expect_tx(&kv_full[stage], D * a.block_size);
+            tma_load_2d(kt + lane * 4 * D, &k_map, &kv_full[stage], 0, row, policy);
+            tma_load_2d(vt + lane * 4 * D, &v_map, &kv_full[stage], 0, row, policy);
+          }
+          const float v4[4] = {vs.x, vs.y, vs.z, vs.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int t = lane * 4 + j;
+            s_sf[(stage * 32 + t % 32) * 4 + t / 32] = ks[j];
+            s_tok[stage * kTile + t] = token_of(unit_of_factors<D>(ks[j], z_unit), v4[j],
+                                                row >= 0 && p + j < w.length ? p + j : kNone);
+          }
+          fence_proxy_async_shared();
+          if constexpr (C::COPIES) cp_async_arrive_noinc(&kv_full[stage]);
+          mbar_arrive(&kv_full[stage]);
+          next_stage();
+          row = row_next;
+          vs = vs_next;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ks[j] = ks_next[j];
+          if ((i + 1) * per_tile >= first + 32) {
+            first += 32;
+            id = id_next;
+            id_next = ids(first + 32 + lane);
+          }
+        }
       }
     } else {
       while (ok && w.next(a, groups, keys)) {
@@ -633,7 +773,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         float ks = 0.0f, vs = 0.0f, ks_next = 0.0f, vs_next = 0.0f;
         const auto scales = [&](int block, float &k, float &v) {
           const int page = block * a.kv_heads + m.g;
-          k = block >= 0 ? __ldg(a.k_scales + page) : 0.0f;
+          k = block >= 0 ? __ldg(static_cast<const float *>(a.k_scales) + page) : 0.0f;
           v = block >= 0 ? __ldg(a.v_scales + page) : 0.0f;
         };
         scales(id, ks, vs);
@@ -680,23 +820,31 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   } else if (warp == 1) {
     // ============================== MMA issuer ==================================================
     constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, NS) | kE5m2_B;
-    constexpr uint32_t idesc_o = idesc_e4m3_f32(D, C::NO) | kE5m2_B | kMajorMN_A | kMajorMN_B;
+    constexpr uint32_t idesc_o =
+        idesc_e4m3_f32(D, C::NO) | kE5m2_B | kMajorMN_A | kMajorMN_B | (C::FP4 ? kE2m1_A : 0u);
     const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
     const uint32_t o_tmem = tmem + 2 * NS;
     uint32_t tile = 0, seg = 0;
     const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
       const uint64_t k_desc = smem_desc_rows<D>(smem_addr(s_kv + st * C::KV_BYTES));
+      const uint32_t factors = tmem + C::SFA + (n & 1) * 4;
+      if constexpr (C::FP4) tmem_copy_factors(factors, smem_desc_factors(smem_addr(s_sf + st * kTile)));
 #pragma unroll
       for (int part = 0; part < C::PASSES; ++part)
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          mma_f8f6f4(tmem + (n & 1) * NS, k_desc + 2 * k, q_desc + part * (R * D >> 4) + 2 * k,
-                     idesc_s, part + k > 0);
+        for (int k = 0; k < D / 32; ++k) {
+          const uint64_t q_at = q_desc + part * (R * D >> 4) + 2 * k;
+          if constexpr (C::FP4)
+            mma_mxf8f6f4(tmem + (n & 1) * NS, k_desc + 2 * k, q_at, idesc_mx(kTile, NS, k), factors,
+                         tmem + C::SFB, part + k > 0);
+          else
+            mma_f8f6f4(tmem + (n & 1) * NS, k_desc + 2 * k, q_at, idesc_s, part + k > 0);
+        }
       mma_commit(&s_full[n & 1]);
     };
     const auto keys_here = [&]() {
-      // (The selected rows were written by ordinary asynchronous copies.)
-      if constexpr (C::SELECT) fence_proxy_async_shared();
+      // (What ordinary copies and stores wrote.)
+      if constexpr (C::COPIES || C::FP4) fence_proxy_async_shared();
       tc_fence_after_sync();
     };
     // One thread's work: the segment's products; false if a wait gave up.
@@ -767,6 +915,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const auto sync_group = [&]() {
       asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + wg) : "memory");
     };
+    if (C::FP4 && wg == 0) {  // the queries' scale factors: 2^-14, whatever the place
+      constexpr uint32_t f = 0x71717171u;
+      asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(lane_base +
+                                                                                       C::SFB),
+                   "r"(f)
+                   : "memory");
+      tmem_st_wait();
+      tc_fence_before_sync();  // (of the first arrival at q_full)
+    }
     while (w.next(a, groups, keys)) {
       const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
       const int len = C::SELECT ? 0 : w.length;
@@ -807,7 +964,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
           const float up = e > 127 ? __int_as_float(0x7FC00000)  // an infinity: the row is NaN
                                    : __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + min(e, 127)) << 23);
+          const float down =
+              __uint_as_float(static_cast<uint32_t>(127 - (C::FP4 ? 0 : 14) + min(e, 127)) << 23);
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] *= up;
 #pragma unroll
@@ -1010,7 +1168,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // cache, or bytes that were never written): what no row sees becomes 0; in the newest
         // tokens, which only the later draft slots see, a NaN becomes 0 and is noted in s_nan (as
         // this segment's number) for the rows that do see it.
-        if (wg == 0 && !seen) {
+        // (Four bits hold no NaN.)
+        if (!C::FP4 && wg == 0 && !seen) {
           uint8_t *v = s_kv + stage * C::KV_BYTES + kTile * D;
           if (tok.pos == kNone) {
             for (int x = 0; x < D; x += 16)
@@ -1060,7 +1219,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if (lane == r && ((unset >> r) & 1u) == 0) m_run = -(r & 1 ? nref[r / 2].y : nref[r / 2].x);
       // ---- the segment's result ----------------------------------------------------------------------
       // (s_rs and s_ext are not read past the barrier below: the next segment's are written then.)
-      if (!C::SELECT && a.next_n > 1) {
+      if (!C::FP4 && !C::SELECT && a.next_n > 1) {
         for (int u = 0; u < a.next_n - 1; ++u) {
           const bool noted = dim >= 0 && s_nan[u * D + max(dim, 0)] == seg;
           if (!__any_sync(0xffffffffu, noted)) continue;
@@ -1287,37 +1446,37 @@ cudaError_t launch_cfg(const CUtensorMap &k_map, const CUtensorMap &v_map, const
                           dim3(kJoinThreads), 0, stream, a, split, parts);
 }
 
-template <int D, bool SELECT>
+template <int D, bool SELECT, bool FP4>
 cudaError_t launch_rows(const CUtensorMap &k_map, const CUtensorMap &v_map, const AttentionArgs &a,
                         int dtype, int sms, cudaStream_t stream) {
   const bool f16 = dtype == IDX_DTYPE_F16;
   const AttnShape s = attn_shape(a.heads / a.kv_heads * (SELECT ? 1 : a.next_n), f16);
   if (f16) {
     switch (s.r) {
-      case 16: return launch_cfg<AttnCfg<D, 16, 4, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
-      case 32: return launch_cfg<AttnCfg<D, 32, 4, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
-      default: return launch_cfg<AttnCfg<D, 64, 4, SELECT>, __half>(k_map, v_map, a, s, sms, stream);
+      case 16: return launch_cfg<AttnCfg<D, 16, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream);
+      case 32: return launch_cfg<AttnCfg<D, 32, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream);
+      default: return launch_cfg<AttnCfg<D, 64, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream);
     }
   }
   using B = __nv_bfloat16;
   switch (s.r) {
-    case 8: return launch_cfg<AttnCfg<D, 8, 3, SELECT>, B>(k_map, v_map, a, s, sms, stream);
-    case 16: return launch_cfg<AttnCfg<D, 16, 3, SELECT>, B>(k_map, v_map, a, s, sms, stream);
-    case 32: return launch_cfg<AttnCfg<D, 32, 3, SELECT>, B>(k_map, v_map, a, s, sms, stream);
-    default: return launch_cfg<AttnCfg<D, 64, 3, SELECT>, B>(k_map, v_map, a, s, sms, stream);
+    case 8: return launch_cfg<AttnCfg<D, 8, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
+    case 16: return launch_cfg<AttnCfg<D, 16, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
+    case 32: return launch_cfg<AttnCfg<D, 32, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
+    default: return launch_cfg<AttnCfg<D, 64, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
   }
 }
 
 // The CTAs on an SM of the kernel that a shape takes.
-template <int D, bool SELECT>
+template <int D, bool SELECT, bool FP4>
 int ctas_for(int r, bool f16) {
   if (f16)
-    return r == 16 ? AttnCfg<D, 16, 4, SELECT>::CTAS
-                   : r == 32 ? AttnCfg<D, 32, 4, SELECT>::CTAS : AttnCfg<D, 64, 4, SELECT>::CTAS;
-  return r == 8 ? AttnCfg<D, 8, 3, SELECT>::CTAS
-                : r == 16 ? AttnCfg<D, 16, 3, SELECT>::CTAS
-                          : r == 32 ? AttnCfg<D, 32, 3, SELECT>::CTAS
-                                    : AttnCfg<D, 64, 3, SELECT>::CTAS;
+    return r == 16 ? AttnCfg<D, 16, 4, SELECT, FP4>::CTAS
+                   : r == 32 ? AttnCfg<D, 32, 4, SELECT, FP4>::CTAS : AttnCfg<D, 64, 4, SELECT, FP4>::CTAS;
+  return r == 8 ? AttnCfg<D, 8, 3, SELECT, FP4>::CTAS
+                : r == 16 ? AttnCfg<D, 16, 3, SELECT, FP4>::CTAS
+                          : r == 32 ? AttnCfg<D, 32, 3, SELECT, FP4>::CTAS
+                                    : AttnCfg<D, 64, 3, SELECT, FP4>::CTAS;
 }
 
 inline cudaError_t read_attention_status(int32_t *value, bool clear) {

@@ -25,6 +25,9 @@ int resolve_sms(int32_t requested, int32_t *out);
 // 128- or 64-byte swizzle (abi.cu).
 int encode_rows(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes,
                 uint32_t box_rows);
+// A tensor map of `rows` rows of 128 four-bit elements, read `box_rows` at a time: in shared memory 16
+// elements take 16 bytes (the lower eight hold them), rows 128 bytes with the 128-byte swizzle.
+int encode_rows4(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows);
 
 // Launches `kernel` as a programmatic dependent of the previous kernel in `stream`: the launch may
 // be processed while that kernel still runs, so its latency hides behind it.  Every kernel of

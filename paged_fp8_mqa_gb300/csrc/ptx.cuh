@@ -204,6 +204,13 @@ __device__ __forceinline__ void cp_async_16(void *dst, const void *src, uint64_t
                : "memory");
 }
 
+// The same of 8 bytes.
+__device__ __forceinline__ void cp_async_8(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+
 // Arrives on `bar` once every cp.async this thread issued so far has landed; the arrival counts
 // toward the barrier's initial count (.noinc).
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t *bar) {
@@ -327,6 +334,40 @@ __device__ __forceinline__ void mma_f8f6f4(uint32_t d_tmem, uint32_t a_lo, uint3
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %5, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// Block scaling: kind::mxf8f6f4 multiplies 32 elements of a row of A (of B) by the row's scale factor, a
+// power of two in UE8M0.  Instruction descriptor: A = E2M1 (format 5; in shared memory 16 elements take
+// 16 bytes, of which the lower eight hold them), B = E5M2 (1), UE8M0 factors (bit 23); the factors of
+// this product's 32 elements stand in byte `block` of A's words (bits 29-30), in byte 0 of B's.
+__host__ __device__ constexpr uint32_t idesc_mx(uint32_t m, uint32_t n, uint32_t block) {
+  return (5u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24) | (block << 29);
+}
+__device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t a_factors, uint32_t b_factors,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], "
+      "p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_factors), "r"(b_factors), "r"(accumulate)
+      : "memory");
+}
+
+// The factors of 128 rows from shared memory ([32][4] words: row r's word, a byte for each 32
+// elements, at [r % 32][r / 32]) to four columns of all lanes, in order with the products that the same
+// thread issues.
+__device__ __forceinline__ void tmem_copy_factors(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Their descriptor: rows of 16 bytes without swizzle, eight of them 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_factors(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  return d;
 }
 
 // Arrives once on `bar` when every tcgen05 operation this thread issued so far has completed.

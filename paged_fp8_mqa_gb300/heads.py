@@ -1,0 +1,277 @@
+"""Heads rotated by several axes, and queries and keys normalised and rotated at once.
+
+The C-ABI mirrors (``idx_...``) take raw pointers and sizes in the order of ``include/idx.h``, the
+torch-facing functions take tensors; see ``layer``, whose checks they share.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+from .layer import (_D, _F, _I, _L, _P, _SIGNATURES, _c, _check, _code, _elsewhere, _index, _on, _rows,
+                    _table, _tensor)
+
+IDX_ROTARY_MAX_AXES = 4
+IDX_NORM_MAX_DIM = 1024
+
+_ROWS = [_P, _L, _L]
+_TURN = [_P, _L, _P, _I, _P, _I, _I, _I, _I]  # positions, axes, table, pairs
+_NORM = [*_ROWS, _I, *_ROWS, _I, _I, _L, _I, _P, _P, _I, _F, *_TURN]
+_SIGNATURES.update({
+    "idx_rotary_axes": (ctypes.c_int, [*_ROWS, _P, _L, _P, _I, _L, _I, _I, _I, _P, _I, _I, _I, _I, _I,
+                                       *_ROWS, _P]),
+    "idx_norm_rotary": (ctypes.c_int, [*_NORM, *_ROWS, *_ROWS, _P]),
+    "idx_norm_rotary_workspace_bytes": (ctypes.c_int64, [_I]),
+    "idx_norm_rotary_backward": (ctypes.c_int, [*_NORM, *_ROWS, *_ROWS, _P, _P, _P, _P, _P, _L, _P]),
+})
+
+
+def idx_rotary_axes(*args) -> int:
+    return _c("idx_rotary_axes")(*args)
+
+
+def idx_norm_rotary(*args) -> int:
+    return _c("idx_norm_rotary")(*args)
+
+
+def idx_norm_rotary_workspace_bytes(*args) -> int:
+    return int(_c("idx_norm_rotary_workspace_bytes")(*args))
+
+
+def idx_norm_rotary_backward(*args) -> int:
+    return _c("idx_norm_rotary_backward")(*args)
+
+
+def rotary_axes(sections, *, in_turn: bool = False):
+    """The axis of each pair for ``axes=``, from the number of pairs of each axis: one section after
+    the other, or, ``in_turn``, one pair of each axis after the other while it has some left."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= IDX_ROTARY_MAX_AXES or min(left) < 0:
+        raise ValueError(f"sections must be 1 to {IDX_ROTARY_MAX_AXES} numbers of pairs")
+    if not in_turn:
+        return tuple(a for a, n in enumerate(left) for _ in range(n))
+    return tuple(a for i in range(max(left)) for a, n in enumerate(left) if i < n)
+
+
+@functools.lru_cache(maxsize=256)
+def _axis_bytes(axes, count, pairs):
+    """The axes of all pairs as the C entry takes them (host memory)."""
+    if len(axes) != pairs:
+        raise ValueError(f"axes must name an axis for each of the {pairs} pairs, got {len(axes)}")
+    if any(not isinstance(a, int) or not 0 <= a < count for a in axes):
+        raise ValueError(f"axes must be whole numbers below the {count} axes of positions")
+    return (ctypes.c_uint8 * pairs)(*axes)
+
+
+def _turn(positions, axes, rot, T, index):
+    """The arguments (positions, axis stride, pair_axis, axes) of a rotation."""
+    import torch
+    if axes is None:
+        _tensor(positions, "positions", 1, torch.int32, index)
+        if positions.shape[0] != T or not positions.is_contiguous():
+            raise ValueError("positions must be contiguous, one for each token")
+        return positions.data_ptr(), 0, None, 1
+    _tensor(positions, "positions", 2, torch.int32, index)
+    count = positions.shape[0]
+    if positions.shape[1] != T or not 1 <= count <= IDX_ROTARY_MAX_AXES:
+        raise ValueError(f"positions must be [axes, T] with 1 to {IDX_ROTARY_MAX_AXES} axes")
+    axis_stride, unit = positions.stride()
+    if T > 1 and unit != 1:
+        raise ValueError("positions of an axis must be contiguous")
+    pair_axis = _axis_bytes(axes if type(axes) is tuple else tuple(axes), count, rot // 2)
+    return positions.data_ptr(), axis_stride, pair_axis, count
+
+
+def _like(out, x, name, index, made):
+    """The result for x: ``out`` if given, else a new one; and its strides."""
+    import torch
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        made.append(out)
+    else:
+        _tensor(out, name, 3, x.dtype, index)
+        if out.shape != x.shape or (x.shape[2] > 1 and out.stride(2) != 1):
+            raise ValueError(f"{name} must have its input's shape and contiguous rows")
+    return out, out.stride(0), out.stride(1)
+
+
+def rotary_by_axes(x, positions, table, axes, interleaved, rot_offset, inverse, out, stream):
+    """``rotary`` with ``axes`` (on x's device, which is the current one)."""
+    index = _index(x, "x")
+    code, (x_token, x_head, _) = _rows(x, "x", 3, index)
+    T, H, D = x.shape
+    tab, most, rot = _table(table, index)
+    if tab is None:
+        raise TypeError("table must be a CUDA tensor")
+    place, axis_stride, pair_axis, count = _turn(positions, axes, rot, T, index)
+    made = []
+    out, o_token, o_head = _like(out, x, "out", index, made)
+    if not (T and H and D):
+        return out
+    _check(idx_rotary_axes(x.data_ptr(), x_token, x_head, place, axis_stride, pair_axis, count, T, H, D,
+                           code, tab, most, rot, rot_offset, interleaved, inverse, out.data_ptr(),
+                           o_token, o_head, _on(stream, index, *made)))
+    return out
+
+
+def _weight(w, name, code, D, index):
+    """A weight's address and dtype code."""
+    if w is None:
+        return None, None
+    if _index(w, name) != index:
+        raise ValueError(f"{name} is on cuda:{w.get_device()}, not on cuda:{index}")
+    w_code = _code(w.dtype)
+    if w_code not in (code, 0):  # (IDX_DTYPE_F32)
+        raise TypeError(f"{name} must have the dtype of q and k, or float32")
+    if w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{D}]")
+    return w.data_ptr(), w_code
+
+
+def _norm_args(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset, index):
+    """The arguments that the forward and the backward entry share."""
+    code, (q_token, q_head, _) = _rows(q, "q", 3, index)
+    T, H, D = q.shape
+    k_args, k_heads = (None, 0, 0), 0
+    if k is not None:
+        k_code, (k_token, k_head, _) = _rows(k, "k", 3, index)
+        if k_code != code or k.shape[0] != T or k.shape[2] != D:
+            raise TypeError("q and k must have the same dtype, tokens and head_dim")
+        k_heads = k.shape[1]
+        if k_heads:
+            k_args = k.data_ptr(), k_token, k_head
+    elif k_weight is not None:
+        raise ValueError("k_weight without k")
+    qw, qw_code = _weight(q_weight, "q_weight", code, D, index)
+    kw, kw_code = _weight(k_weight, "k_weight", code, D, index)
+    if qw_code is not None and kw_code is not None and qw_code != kw_code:
+        raise TypeError("q_weight and k_weight must have the same dtype")
+    w_code = qw_code if qw_code is not None else kw_code if kw_code is not None else code
+    turn, tab = (None, 0, None, 1), (None, 0, 0)
+    if table is not None:
+        tab = _table(table, index)
+        turn = _turn(positions, axes, tab[2], T, index)
+    elif positions is not None or axes is not None:
+        raise ValueError("positions and axes need a table")
+    return (q.data_ptr(), q_token, q_head, H, *k_args, k_heads, code, T, D, qw, kw, w_code, eps,
+            *turn, *tab, rot_offset, interleaved)
+
+
+def _forward(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset, q_out,
+             k_out, stream):
+    index = _index(q, "q")
+    args = _norm_args(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset,
+                      index)
+    made = []
+    q_to, q_token, q_head = _like(q_out, q, "q_out", index, made)
+    k_to, k_args = None, (None, 0, 0)
+    if k is not None:
+        k_to, k_token, k_head = _like(k_out, k, "k_out", index, made)
+        if k.shape[1]:
+            k_args = k_to.data_ptr(), k_token, k_head
+    T, H, D = q.shape
+    if T and D and H + (0 if k is None else k.shape[1]):
+        # (Without query heads there is nothing at q: any address will do.)
+        q_at = q_to.data_ptr() if H else k_args[0]
+        _check(idx_norm_rotary(*(args if H else (k_args[0], *args[1:])), q_at, q_token, q_head, *k_args,
+                               _on(stream, index, *made)))
+    return q_to, k_to
+
+
+def _backward(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset, q_grad,
+              k_grad):
+    """(dq, dk, dq_weight, dk_weight) from the outputs' gradients."""
+    import torch
+    index = _index(q, "q")
+    if index != torch.cuda.current_device():
+        return _elsewhere(index, _backward, q, k, q_weight, k_weight, positions, table, eps, axes,
+                          interleaved, rot_offset, q_grad, k_grad)
+    args = _norm_args(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset,
+                      index)
+
+    def rows(g, x):
+        if g.dtype != x.dtype:
+            g = g.to(x.dtype)
+        if g.shape[2] > 1 and g.stride(2) != 1:  # (of a sum: one element, expanded)
+            g = g.contiguous()
+        return g
+
+    T, H, D = q.shape
+    dq = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    dqw = None if q_weight is None else torch.empty_like(q_weight)
+    dk = dkw = None
+    k_args, dk_at = (None, 0, 0), None
+    if k is not None:
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        dkw = None if k_weight is None else torch.empty_like(k_weight)
+        k_grad = rows(k_grad, k)
+        k_args = k_grad.data_ptr(), k_grad.stride(0), k_grad.stride(1)
+        dk_at = dk.data_ptr()
+    if not T:  # (sums over nothing)
+        return dq, dk, *(None if w is None else w.zero_() for w in (dqw, dkw))
+    q_grad = rows(q_grad, q)
+    need = idx_norm_rotary_workspace_bytes(D)
+    workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    _check(idx_norm_rotary_backward(
+        *args, q_grad.data_ptr(), q_grad.stride(0), q_grad.stride(1), *k_args, dq.data_ptr(), dk_at,
+        None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
+        workspace.data_ptr(), need, _on(None, index)))
+    return dq, dk, dqw, dkw
+
+
+@functools.cache
+def _recorded():
+    """norm_rotary as a step that autograd records."""
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class NormRotary(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset,
+                    stream):
+            ctx.save_for_backward(q, k, q_weight, k_weight, positions, table)
+            ctx.how = eps, axes, interleaved, rot_offset
+            return _forward(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved,
+                            rot_offset, None, None, stream)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, q_grad, k_grad):
+            return (*_backward(*ctx.saved_tensors, *ctx.how, q_grad, k_grad), *[None] * 7)
+
+    return NormRotary.apply
+
+
+def norm_rotary(q, k, q_weight=None, k_weight=None, positions=None, table=None, *, eps: float = 1e-6,
+                axes=None, interleaved: bool = False, rot_offset: int = 0, q_out=None, k_out=None,
+                stream=None):
+    """Every head of q [T, H, D] and of k [T, Hkv, D] (float32, float16 or bfloat16; any token and head
+    strides, so views of one projection do) over its root mean square, times its weight, and rotated as by
+    ``rotary``: R(x / sqrt(mean(x^2) + eps) * weight), one launch, float32 within, one rounding.
+
+    The weights [D] (their dtype or float32; None: ones) belong to all heads of q and of k.  k may be
+    None.  Without a table nothing is rotated; with ``axes`` (see ``rotary_axes``) positions are
+    int32 [axes, T].  ``q_out=q`` and ``k_out=k`` work in place.  Returns (q, k) normalised.
+
+    Autograd records the call where q, k or a weight requires a gradient; given outputs are refused then.
+    The weights' gradients are sums in an order that does not change from call to call.  The gradients
+    cannot be differentiated again."""
+    import torch
+    index = _index(q, "q")
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                       for t in (q, k, q_weight, k_weight)):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out cannot be given where a gradient is required")
+        if not all(t is None or (t.dim() == 3 and t.shape[1] and t.shape[2]) for t in (q, k)):
+            raise ValueError("a gradient needs heads of q and, where it is given, of k")
+        if index != torch.cuda.current_device():
+            return _elsewhere(index, norm_rotary, q, k, q_weight, k_weight, positions, table, eps=eps,
+                              axes=axes, interleaved=interleaved, rot_offset=rot_offset, stream=stream)
+        return _recorded()(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved,
+                           rot_offset, stream)
+    if index != torch.cuda.current_device():
+        return _elsewhere(index, norm_rotary, q, k, q_weight, k_weight, positions, table, eps=eps,
+                          axes=axes, interleaved=interleaved, rot_offset=rot_offset, q_out=q_out,
+                          k_out=k_out, stream=stream)
+    return _forward(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset,
+                    q_out, k_out, stream)

@@ -263,37 +263,45 @@ def _recorded_rotary():
 
     class Rotary(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, positions, table, interleaved, rot_offset, inverse, stream):
+        def forward(ctx, x, positions, table, axes, interleaved, rot_offset, inverse, stream):
             ctx.save_for_backward(positions, table)
-            ctx.how = dict(interleaved=interleaved, rot_offset=rot_offset, inverse=not inverse)
-            return rotary(x, positions, table, interleaved=interleaved, rot_offset=rot_offset,
-                          inverse=inverse, stream=stream)
+            ctx.how = dict(axes=axes, interleaved=interleaved, rot_offset=rot_offset,
+                           inverse=not inverse)
+            return rotary(x, positions, table, axes=axes, interleaved=interleaved,
+                          rot_offset=rot_offset, inverse=inverse, stream=stream)
 
         @staticmethod
         def backward(ctx, grad):
             positions, table = ctx.saved_tensors
             if grad.shape[-1] > 1 and grad.stride(-1) != 1:  # (of a sum: one element, expanded)
                 grad = grad.contiguous()
-            return (rotary(grad, positions, table, **ctx.how), *[None] * 6)
+            return (rotary(grad, positions, table, **ctx.how), *[None] * 7)
 
     return Rotary.apply
 
 
-def rotary(x, positions, table, *, interleaved: bool = False, rot_offset: int = 0,
+def rotary(x, positions, table, *, axes=None, interleaved: bool = False, rot_offset: int = 0,
            inverse: bool = False, out=None, stream=None):
     """Rotary positions: x [T, H, D] (float32, float16 or bfloat16; any token and head strides) at
     positions (int32 [T]), elements [rot_offset, rot_offset + rot_dim) of each head turned by the
     angles of ``table`` (see ``rotary_table``), in halves or in interleaved pairs.  ``out=x``
     rotates in place.  ``inverse`` turns by the negative angles: the gradient with respect to x (and
     the way back, where the table's magnitude is 1, as it is but for "yarn").  Autograd records the
-    call where x requires a gradient; with ``out`` nothing is recorded."""
+    call where x requires a gradient; with ``out`` nothing is recorded.
+
+    ``axes``, for tokens of images and video, names each pair's axis (rot_dim / 2 whole numbers, see
+    ``rotary_axes``): positions are then int32 [axes, T] (up to 4 axes, D at most 1024), and a pair is
+    turned by the position on its own axis."""
     import torch
     index = _index(x, "x")
     if x.requires_grad and out is None and torch.is_grad_enabled():
-        return _recorded_rotary()(x, positions, table, interleaved, rot_offset, inverse, stream)
+        return _recorded_rotary()(x, positions, table, axes, interleaved, rot_offset, inverse, stream)
     if index != torch.cuda.current_device():
-        return _elsewhere(index, rotary, x, positions, table, interleaved=interleaved,
+        return _elsewhere(index, rotary, x, positions, table, axes=axes, interleaved=interleaved,
                           rot_offset=rot_offset, inverse=inverse, out=out, stream=stream)
+    if axes is not None:
+        from .heads import rotary_by_axes
+        return rotary_by_axes(x, positions, table, axes, interleaved, rot_offset, inverse, out, stream)
     code, (x_token, x_head, _) = _rows(x, "x", 3, index)
     _tensor(positions, "positions", 1, torch.int32, index)
     T, H, D = x.shape
@@ -419,25 +427,10 @@ def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, 
             *scales, _on(stream, index)))
 
 
-def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,
-                  softmax_scale: float | None = None, candidates=None, ranges=None, out=None,
-                  lse=None, workspace=None, num_sms: int = 0, stream=None):
-    """Attention over the 8-bit K/V cache: q [B, next_n, H, D] (float16 or bfloat16; strides that
-    are multiples of 8), pools and scales as for ``kv_append``, H a multiple of Hkv; row (b, t)
-    sees positions 0 .. seq_lens[b] - next_n + t.  With ``candidates`` (int32 [B*next_n, slots, 2])
-    and ``ranges`` (int32 [2, B*next_n]) as the select leaves them, each row sees only the
-    positions stored in its slot range.  Rows that see nothing give zeros.  softmax_scale defaults
-    to D ** -0.5; weights are held to 2^-10 of themselves (float16 queries: 2^-14), sums in float32;
-    ``lse`` (float32 [B, next_n, H]) receives the log-sums; ``workspace`` (uint8, at
-    least idx_attention_workspace_bytes) is allocated if not given.  Returns out, contiguous
-    [B, next_n, H, D] in q's dtype."""
+def _attend(entry, index, q, pools, sizes, block_tables, seq_lens, softmax_scale, candidates, ranges,
+            out, lse, workspace, num_sms, stream):
+    """The attention's call by its C entry: pools, the cache's four addresses; sizes, its (blocks, Hkv, block_size, D)."""
     import torch
-    index = _index(q, "q")
-    if index != torch.cuda.current_device():
-        return _elsewhere(index, attention_fp8, q, k_pool, v_pool, k_scales, v_scales, block_tables,
-                          seq_lens, softmax_scale=softmax_scale, candidates=candidates,
-                          ranges=ranges, out=out, lse=lse, workspace=workspace, num_sms=num_sms,
-                          stream=stream)
     dtype = q.dtype
     code = _code(dtype)
     if code is None or dtype is torch.float32:
@@ -449,12 +442,9 @@ def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
     q_batch, q_token, q_head, q_unit = q.stride()
     if q_unit != 1 and D > 1:
         raise ValueError("q rows must be contiguous")
-    pools = _pool8(k_pool, "k_pool", 4, index), _pool8(v_pool, "v_pool", 4, index)
-    blocks, kv_heads, block_size, dim = k_pool.shape
-    if dim != D or v_pool.shape != k_pool.shape:
-        raise ValueError("k_pool and v_pool must be [blocks, Hkv, block_size, D] for q's D")
-    scales = (_scales(k_scales, "k_scales", (blocks, kv_heads), index),
-              _scales(v_scales, "v_scales", (blocks, kv_heads), index))
+    blocks, kv_heads, block_size, dim = sizes
+    if dim != D:
+        raise ValueError("the pools must have the head_dim of q")
     pages = _requests(block_tables, seq_lens, B, index)
     cand, slots, cand_ranges = None, 0, None
     if candidates is not None:
@@ -496,9 +486,38 @@ def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
     else:
         _tensor(workspace, "workspace", 1, torch.uint8, index)
         need = workspace.shape[0]
-    _check(idx_attention_fp8(
-        q.data_ptr(), q_batch, q_token, q_head, code, *pools, *scales, blocks, block_size, *pages,
+    _check(entry(
+        q.data_ptr(), q_batch, q_token, q_head, code, *pools, blocks, block_size, *pages,
         B, n, H, kv_heads, D, D ** -0.5 if softmax_scale is None else softmax_scale, cand, slots,
         cand_ranges, num_sms, out.data_ptr(), lse_to, workspace.data_ptr(), need,
         _on(stream, index, *made)))
     return out
+
+
+def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,
+                  softmax_scale: float | None = None, candidates=None, ranges=None, out=None,
+                  lse=None, workspace=None, num_sms: int = 0, stream=None):
+    """Attention over the 8-bit K/V cache: q [B, next_n, H, D] (float16 or bfloat16; strides that
+    are multiples of 8), pools and scales as for ``kv_append``, H a multiple of Hkv; row (b, t)
+    sees positions 0 .. seq_lens[b] - next_n + t.  With ``candidates`` (int32 [B*next_n, slots, 2])
+    and ``ranges`` (int32 [2, B*next_n]) as the select leaves them, each row sees only the
+    positions stored in its slot range.  Rows that see nothing give zeros.  softmax_scale defaults
+    to D ** -0.5; weights are held to 2^-10 of themselves (float16 queries: 2^-14), sums in float32;
+    ``lse`` (float32 [B, next_n, H]) receives the log-sums; ``workspace`` (uint8, at
+    least idx_attention_workspace_bytes) is allocated if not given.  Returns out, contiguous
+    [B, next_n, H, D] in q's dtype."""
+    import torch
+    index = _index(q, "q")
+    if index != torch.cuda.current_device():
+        return _elsewhere(index, attention_fp8, q, k_pool, v_pool, k_scales, v_scales, block_tables,
+                          seq_lens, softmax_scale=softmax_scale, candidates=candidates,
+                          ranges=ranges, out=out, lse=lse, workspace=workspace, num_sms=num_sms,
+                          stream=stream)
+    pools = _pool8(k_pool, "k_pool", 4, index), _pool8(v_pool, "v_pool", 4, index)
+    sizes = k_pool.shape
+    if v_pool.shape != sizes:
+        raise ValueError("k_pool and v_pool must be [blocks, Hkv, block_size, D] for q's D")
+    scales = (_scales(k_scales, "k_scales", sizes[:2], index),
+              _scales(v_scales, "v_scales", sizes[:2], index))
+    return _attend(idx_attention_fp8, index, q, (*pools, *scales), sizes, block_tables, seq_lens,
+                   softmax_scale, candidates, ranges, out, lse, workspace, num_sms, stream)
