@@ -78,9 +78,9 @@ struct AttnCfg {
   static constexpr int WG = R == 64 ? 2 : 1;          // softmax warpgroups, R / WG rows each
   static constexpr int RT = R / WG;
   static constexpr int SOFT_WARPS = 4 * WG;
-  // Warps that load: one for whole pages; up to four share the rows of a selection, as many as the
-  // softmax's registers leave room for.
-  static constexpr int LOADERS = !SELECT || R == 32 ? 1 : R == 8 ? 4 : 2;
+  // Warps that load: one for whole pages; up to four share the rows of a selection (FP4: of any tile
+  // that the TMA unit does not bring), as many as the softmax's registers leave room for.
+  static constexpr int LOADERS = !COPIES || R == 32 ? 1 : R == 8 ? 4 : 2;
   static constexpr int THREADS = 32 * (LOADERS + 1 + SOFT_WARPS);
   // Two of S, one of O; with FP4 the keys' scale factors, two tiles of them, and the queries' (1).
   static constexpr int SFA = 2 * NS + NO, SFB = SFA + 8;
@@ -91,21 +91,36 @@ struct AttnCfg {
   // what the next launch needs no longer fits beside them.  64 rows in chunks of 32, two CTAs an SM:
   // one long request 1.07 times as long, a batch of 64 requests with 64 heads on one 1.3 times.
   static constexpr int CTAS = R == 64 ? 1 : 2;
-  static constexpr int KV_BYTES = 2 * kTile * D;
+  static constexpr int T_BYTES = kTile * D;           // a tile of K, or of V, as the products read it
   static constexpr int Q_BYTES = NS * (CAT ? 1 : QPARTS) * D;
   static constexpr int P_BYTES = NO * kTile;          // a tile's weights
   // They take the place of the tile's keys, which have been read by then, where they fit it; else
-  // two buffers of their own.
-  static constexpr bool OVER_K = P_BYTES <= kTile * D;
-  static constexpr int SF_BYTES = FP4 ? kTile * 4 : 0;  // a stage's scale factors of the keys
-  static constexpr int AUX = kTile * 16 + SF_BYTES;   // and its Token records
+  // they have buffers of their own.  (FP4: always, see below.)
+  static constexpr bool OVER_K = !FP4 && P_BYTES <= kTile * D;
+  static constexpr int P_BUFS = OVER_K ? 0 : !FP4 || R == 64 ? 2 : 1;
+  // What a stage of K (its scale factors, FP4) and of V (its Token records) holds besides.
+  static constexpr int K_AUX = FP4 ? kTile * 4 : 0;
+  static constexpr int V_AUX = kTile * (FP4 ? 8 : 16);
   static constexpr int MISC = 48 * R + (FP4 ? 0 : 3 * D * 4) + 256;
-  static constexpr int FIXED = 1024 + Q_BYTES + (OVER_K ? 0 : 2 * P_BYTES) + MISC;
+  static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_BYTES + MISC;
   static constexpr int ROOM = CTAS == 2 ? 115456 : 231424;
-  static constexpr int FIT = (ROOM - FIXED) / (KV_BYTES + AUX);
-  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
-  static constexpr int SMEM = FIXED + STAGES * (KV_BYTES + AUX);
-  static_assert(STAGES >= 2 && SMEM <= 232448, "fits the 227 KiB per-CTA limit");
+  static constexpr int LEFT = ROOM - FIXED;
+  // FP4 copies land as they lie in the pool, K and V and what goes with them, and are spread by the
+  // warp that asked for them: what is in flight takes half the room that the products need.
+  static constexpr int RAW_BYTES = COPIES && FP4 ? kTile * (D + 16) : 0;
+  // Stages of K and of V.  In 8 bits they are the same ones.  In four, a tile takes the room of 8 bits
+  // for half the bytes, so that stages are what bounds the loads in flight: a key's is given back as soon
+  // as its scores are there, long before its values' is.
+  static constexpr int VS8 = LEFT / (2 * T_BYTES + V_AUX);
+  static constexpr int KS = !FP4 ? (VS8 > 6 ? 6 : VS8) : COPIES && D == 128 && R != 64 ? 1 : R == 64 && !COPIES ? 3 : 2;
+  static constexpr int K_ROOM = KS * (T_BYTES + K_AUX);
+  static constexpr int VS4 = COPIES ? 2 : (LEFT - K_ROOM) / (T_BYTES + V_AUX);
+  static constexpr int VS = !FP4 ? KS : VS4 > 6 ? 6 : VS4;
+  static constexpr int V_ROOM = VS * (T_BYTES + V_AUX);
+  static constexpr int RAW_FIT = RAW_BYTES == 0 ? 0 : (LEFT - K_ROOM - V_ROOM) / (RAW_BYTES + !RAW_BYTES);
+  static constexpr int RAW = RAW_FIT > 6 ? 6 : RAW_FIT;
+  static constexpr int SMEM = FIXED + K_ROOM + V_ROOM + RAW * RAW_BYTES;
+  static_assert(VS >= 2 && (RAW_BYTES == 0 || RAW >= 1) && SMEM <= 232448, "fits the 227 KiB per-CTA limit");
   static_assert(Q_BYTES % 1024 == 0 && (!CAT || PARTS == 3), "aligned; eight rows: three parts");
 };
 
@@ -115,6 +130,11 @@ struct alignas(16) Token {
   float log_v;   // log2|v_scale|
   float inv_v;   // 1 / |v_scale|, with v_scale's sign
   int32_t pos;   // its position (0 with SELECT), or kNone
+};
+// The same with FP4, as the loaders leave it; the rest is the position's softmax thread's work.
+struct alignas(8) Token4 {
+  float v_scale;  // NaN where the key's scale is
+  int32_t pos;
 };
 
 __device__ __forceinline__ Token token_of(float k, float v_scale, int pos) {
@@ -129,30 +149,11 @@ __device__ __forceinline__ Token token_of(float k, float v_scale, int pos) {
   return t;
 }
 
-// A key's scale factors (FP4): its bytes, one for each 32 elements.
+// A byte of 0xFF among a key's factors is NaN, which its rows' weights take from the value scale.
 template <int D>
-__device__ __forceinline__ uint32_t scale_factors(const void *scales, int64_t row) {
-  if constexpr (D == 128)
-    return __ldg(static_cast<const uint32_t *>(scales) + row);
-  else
-    return __ldg(static_cast<const uint16_t *>(scales) + row);
-}
-// Token::k of a key with these factors: the tensor core applies them; a byte of 0xFF is NaN.
-template <int D>
-__device__ __forceinline__ float unit_of_factors(uint32_t factors, float z_unit) {
+__device__ __forceinline__ float scale_of(uint32_t factors, float v_scale) {
   if constexpr (D != 128) factors |= factors << 16;
-  return __vcmpeq4(factors, 0xFFFFFFFFu) != 0 ? __int_as_float(0x7FC00000) : z_unit;
-}
-
-// 16 elements of a pool's row, from element x on, to shared memory (FP4: eight bytes, the lower half
-// of the 16 that they take there).
-template <bool FP4, int D>
-__device__ __forceinline__ void copy_piece(uint8_t *dst, const uint8_t *pool, int row, int x,
-                                           uint64_t policy) {
-  if constexpr (FP4)
-    cp_async_8(dst, pool + static_cast<int64_t>(row) * (D / 2) + x / 2);
-  else
-    cp_async_16(dst, pool + static_cast<int64_t>(row) * D + x, policy);
+  return __vcmpeq4(factors, 0xFFFFFFFFu) != 0 ? __int_as_float(0x7FC00000) : v_scale;
 }
 
 // Where the runs' parts of a group are, written by the CTA that has the group's first tile.
@@ -305,6 +306,19 @@ __device__ __forceinline__ int tiles_for(int length) {
   return length / kTile + (length % kTile != 0);
 }
 
+// A place in a ring of N stages, and the parity of its present use.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // A CTA's run over the line: the segments (group, first tile, tiles) in order.  Every warp walks
 // its own copy, all its lanes together: keys without positions are passed over 32 at a time.
 template <bool SELECT>
@@ -394,19 +408,28 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   extern __shared__ uint8_t s_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(s_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint8_t *s_kv = base;                              // [stage][K tile, V tile]
-  uint8_t *s_q = s_kv + C::STAGES * C::KV_BYTES;     // [QPARTS * R][D], K-major, swizzled
+  // K tiles and V tiles, in 8 bits side by side in one stage.
+  const auto k_tile = [&](int st) { return base + st * (C::FP4 ? 1 : 2) * C::T_BYTES; };
+  const auto v_tile = [&](int st) {
+    return C::FP4 ? base + (C::KS + st) * C::T_BYTES : base + (2 * st + 1) * C::T_BYTES;
+  };
+  uint8_t *s_q = base + (C::KS + C::VS) * C::T_BYTES;  // [QPARTS * R][D], K-major, swizzled
   uint8_t *at = s_q + C::Q_BYTES;
   // A tile's weights, [NO / 16][kTile][16].
   uint8_t *s_p = at;
-  if constexpr (!C::OVER_K) at += 2 * C::P_BYTES;
+  at += C::P_BUFS * C::P_BYTES;
   const auto weights_of = [&](uint32_t tile, int stage) {
-    return C::OVER_K ? s_kv + stage * C::KV_BYTES : s_p + (tile & 1) * C::P_BYTES;
+    return C::OVER_K ? k_tile(stage) : s_p + (C::P_BUFS == 2 ? tile & 1 : 0) * C::P_BYTES;
   };
-  Token *s_tok = reinterpret_cast<Token *>(at);      // [stage][kTile]
-  at += C::STAGES * kTile * 16;
-  uint32_t *s_sf = reinterpret_cast<uint32_t *>(at);  // [stage][32][4]: token t's at [t % 32][t / 32]
-  at += C::STAGES * C::SF_BYTES;
+  uint8_t *s_raw_kv = at;                            // [RAW][kTile][D / 2 of K, D / 2 of V]
+  at += C::RAW * kTile * D;
+  uint4 *s_raw_aux = reinterpret_cast<uint4 *>(at);  // [RAW][kTile]: factors, value scale, pos, row
+  at += C::RAW * (C::RAW_BYTES - kTile * D);
+  Token *s_tok = reinterpret_cast<Token *>(at);      // [stage of V][kTile]
+  Token4 *s_tok4 = reinterpret_cast<Token4 *>(at);
+  at += C::VS * C::V_AUX;
+  uint32_t *s_sf = reinterpret_cast<uint32_t *>(at);  // [stage of K][32][4]: token t's at [t % 32][t / 32]
+  at += C::KS * C::K_AUX;
   float *s_max = reinterpret_cast<float *>(at);      // [R][4 warps]
   at += R * 16;
   float *s_sum = reinterpret_cast<float *>(at);      // [R][4 warps]
@@ -420,8 +443,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   int *s_nan = reinterpret_cast<int *>(at);          // [3][D]: see below
   if constexpr (!C::FP4) at += 3 * D * 4;
   uint64_t *bars = reinterpret_cast<uint64_t *>(at);
-  uint64_t *kv_full = bars, *kv_empty = bars + C::STAGES, *s_full = bars + 2 * C::STAGES,
-           *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2, *drain = q_full + 1;
+  uint64_t *k_full = bars, *k_empty = k_full + C::KS, *v_full = C::FP4 ? k_empty + C::KS : k_full,
+           *v_empty = C::FP4 ? v_full + C::VS : k_empty, *s_full = v_empty + C::VS, *p_full = s_full + 2,
+           *pv_done = p_full + 2, *q_full = pv_done + 2, *drain = q_full + 1;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(drain + 1);
   __shared__ int64_t s_scan[C::THREADS / 32];
   __shared__ int64_t s_begin;  // the run's first tile within its key
@@ -436,11 +460,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       prefetch_tensor_map(&k_map);
       prefetch_tensor_map(&v_map);
     }
-    for (int i = 0; i < C::STAGES; ++i) {
-      // A loading lane's arrival, and one when its own copies have landed.
-      mbar_init(&kv_full[i], C::COPIES ? 64 * C::LOADERS : 32);
-      mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < C::KS; ++i) {
+      // A loading lane's arrival, and (SELECT in 8 bits) one when its own copies have landed.
+      mbar_init(&k_full[i], (C::SELECT && !C::FP4 ? 64 : 32) * C::LOADERS);
+      mbar_init(&k_empty[i], 1);
     }
+    if constexpr (C::FP4)
+      for (int i = 0; i < C::VS; ++i) {
+        mbar_init(&v_full[i], 32 * C::LOADERS);
+        mbar_init(&v_empty[i], 1);
+      }
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     // (Two, as the softmax may finish a tile before the issuer has seen the one before.)
@@ -516,27 +545,25 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     w.tile = static_cast<int>(at0 - static_cast<int64_t>(w.group) * w.tiles);
   }
   bool ok = true;
-  uint32_t issued = 0;  // producer: tiles whose copies were started; MMA: nothing
-  int stage = 0;
-  uint32_t phase = 0;
+  uint32_t issued_k = 0, issued_v = 0;  // loaders: tiles whose copies were started
+  Ring<C::KS> kr;
+  Ring<C::VS> vr;  // (in 8 bits the same as kr, and not used)
 
   if (warp == 0 || warp >= 2 + C::SOFT_WARPS) {
     // ============================== loaders =====================================================
     const uint64_t policy = l2_policy_evict_first();
     const int shift = a.block_size == 32 ? 5 : a.block_size == 64 ? 6 : 7;
     const float z_unit = a.scale * 1.4426950408889634f;  // scores in units of ln 2
-    const auto stage_free = [&]() {
-      ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], phase ^ 1, kWaitNs));
+    const auto free_now = [&](uint64_t *empty, uint32_t phase) {
+      ok = __all_sync(0xffffffffu, mbar_wait(empty, phase ^ 1, kWaitNs));
       return ok;
     };
+    const auto stage_free = [&]() { return free_now(&k_empty[kr.at], kr.phase); };
     const auto next_stage = [&]() {
-      ++issued;
-      if (++stage == C::STAGES) {
-        stage = 0;
-        phase ^= 1;
-      }
+      ++issued_k;
+      kr.advance();
     };
-    if constexpr (C::SELECT) {
+    if constexpr (C::COPIES) {
       // A lane looks after EACH tokens of a tile, 32 apart: position, then page, then the page's
       // scales, each read one tile further ahead than the next (segments and all), so that a tile
       // pays for one memory round trip and not for three.
@@ -558,16 +585,20 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           if (!far.live) return;
           const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
           far.table = a.block_tables + m.b * a.bt_stride;
-          far.extent = __ldg(a.seq_lens + m.b * a.sl_stride) - a.next_n + m.t_select + 1;
           far.g = m.g;
-          cand = a.candidates + w.key * a.cand_stride + max(0, __ldg(a.ranges + w.key));
+          if constexpr (C::SELECT) {
+            far.extent = __ldg(a.seq_lens + m.b * a.sl_stride) - a.next_n + m.t_select + 1;
+            cand = a.candidates + w.key * a.cand_stride + max(0, __ldg(a.ranges + w.key));
+          } else {
+            far.extent = w.length;
+          }
           slot = w.seg_tile * kTile;
           end = min((w.seg_tile + w.seg_tiles) * kTile, w.length);
         }
 #pragma unroll
         for (int j = 0; j < EACH; ++j) {
           const int s = slot + token0 + 32 * j;
-          far.pos[j] = s < end ? __ldg(&cand[s].x) : -1;
+          far.pos[j] = s >= end ? -1 : C::SELECT ? __ldg(&cand[s].x) : s;
         }
         slot += kTile;
       };
@@ -590,79 +621,182 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       };
       // (FP4: a token's own, the keys' a word of scale factors.)
       using KeyScale = std::conditional_t<C::FP4, uint32_t, float>;
-      const auto scales = [&](const int (&row)[EACH], KeyScale (&ks)[EACH], float (&vs)[EACH]) {
+      if constexpr (C::FP4) {
+        // 16 bytes a lane and copy, as they lie in the pool, RAW tiles ahead; each lane spreads what it
+        // asked for itself, 16 elements to the lower half of 16 bytes, with the swizzle that the products
+        // expect.  (Copies of eight bytes, which need no spreading, go through L1, of which there is
+        // hardly any left: the serving mix took 160 us.)
+        constexpr int kLanes = D / 32, kRows = 32 / kLanes;
+        const int piece = lane % kLanes, sub = lane / kLanes;
+        Ring<C::RAW> in, out;
+        int row0[EACH], row1[EACH], pos0[EACH], pos1[EACH];
+        const auto rows = [&](int (&row)[EACH], int (&pos)[EACH]) {
+          pool_rows(row);
 #pragma unroll
-        for (int j = 0; j < EACH; ++j) {
-          if constexpr (C::FP4) {
-            ks[j] = row[j] >= 0 ? scale_factors<D>(a.k_scales, row[j]) : 0u;
-            vs[j] = row[j] >= 0 ? __ldg(a.v_scales + row[j]) : 0.0f;
-          } else {
+          for (int j = 0; j < EACH; ++j) pos[j] = row[j] < 0 ? kNone : C::SELECT ? 0 : far.pos[j];
+        };
+        const auto issue = [&]() {
+          uint8_t *raw = s_raw_kv + in.at * (kTile * D) + piece * 16;
+#pragma unroll
+          for (int q = 0; q < EACH; ++q) {
+            const int t0 = token0 - lane + 32 * q;
+#pragma unroll
+            for (int j = 0; j < 32 / kRows; ++j) {
+              const int n = j * kRows + sub;  // lane n's q-th token
+              const int row = __shfl_sync(0xffffffffu, row0[q], n);
+              if (row < 0) continue;  // (any code is a number, and its weight will be 0)
+              const int64_t src = static_cast<int64_t>(row) * (D / 2) + piece * 16;
+              cp_async_16(raw + (t0 + n) * D, a.k_pool + src, policy);
+              cp_async_16(raw + (t0 + n) * D + D / 2, a.v_pool + src, policy);
+            }
+            uint32_t *aux = reinterpret_cast<uint32_t *>(s_raw_aux + in.at * kTile + t0 + lane);
+            if (row0[q] >= 0) {
+              cp_async_4(aux, static_cast<const uint8_t *>(a.k_scales) +
+                                  (D == 128 ? static_cast<int64_t>(row0[q]) : row0[q] >> 1) * 4);
+              cp_async_4(aux + 1, a.v_scales + row0[q]);
+            }
+            *reinterpret_cast<int2 *>(aux + 2) = make_int2(pos0[q], row0[q]);
+          }
+          in.advance();
+        };
+        const auto spread = [&](uint8_t *tile, int half) {
+          const uint8_t *raw = s_raw_kv + out.at * (kTile * D) + half * (D / 2) + piece * 16;
+#pragma unroll
+          for (int q = 0; q < EACH; ++q)
+#pragma unroll
+            for (int j = 0; j < 32 / kRows; ++j) {
+              const int t = token0 - lane + 32 * q + j * kRows + sub;
+              const uint4 u = *reinterpret_cast<const uint4 *>(raw + t * D);
+              *reinterpret_cast<uint2 *>(tile + swizzled<D>(t, piece * 32)) = make_uint2(u.x, u.y);
+              *reinterpret_cast<uint2 *>(tile + swizzled<D>(t, piece * 32 + 16)) = make_uint2(u.z, u.w);
+            }
+        };
+        // A tile that has landed, to the stages.
+        const auto hand_over = [&]() {
+          uint4 aux[EACH];
+#pragma unroll
+          for (int q = 0; q < EACH; ++q) {
+            aux[q] = s_raw_aux[out.at * kTile + token0 + 32 * q];
+            if (D != 128) aux[q].x = aux[q].w & 1 ? aux[q].x >> 16 : aux[q].x & 0xFFFFu;
+          }
+          if (!stage_free()) return false;
+          spread(k_tile(kr.at), 0);
+#pragma unroll
+          for (int q = 0; q < EACH; ++q) {
+            const int t = token0 + 32 * q;
+            s_sf[(kr.at * 32 + t % 32) * 4 + t / 32] = aux[q].x;
+          }
+          fence_proxy_async_shared();
+          mbar_arrive(&k_full[kr.at]);
+          next_stage();
+          if (!free_now(&v_empty[vr.at], vr.phase)) return false;
+          spread(v_tile(vr.at), 1);
+#pragma unroll
+          for (int q = 0; q < EACH; ++q)
+            s_tok4[vr.at * kTile + token0 + 32 * q] =
+                Token4{scale_of<D>(aux[q].x, __uint_as_float(aux[q].y)), static_cast<int>(aux[q].z)};
+          fence_proxy_async_shared();
+          mbar_arrive(&v_full[vr.at]);
+          ++issued_v;
+          vr.advance();
+          out.advance();
+          return true;
+        };
+        positions();
+        bool live0 = far.live;
+        rows(row0, pos0);
+        if (live0) positions();
+        int ahead = 0;  // tiles asked for and not handed over
+        bool ending = false;
+        while (live0 || ahead > 0) {
+          if (live0) {
+            issue();
+            ++ahead;
+            rows(row1, pos1);
+            const bool live1 = far.live;
+            if (live1) positions();
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) {
+              row0[j] = row1[j];
+              pos0[j] = pos1[j];
+            }
+            live0 = live1;
+          }
+          // A group a round, empty ones too, so that RAW - 1 groups follow the oldest of the tiles ahead
+          // when it is waited for.
+          cp_async_commit();
+          if (!live0 && !ending) {
+            ending = true;
+            for (int i = ahead; i < C::RAW; ++i) cp_async_commit();
+          }
+          if (ahead == C::RAW || ending) {
+            cp_async_wait_group<C::RAW - 1>();
+            if (!hand_over()) break;
+            --ahead;
+          }
+        }
+        cp_async_wait_all();
+      } else {
+        const auto scales = [&](const int (&row)[EACH], float (&ks)[EACH], float (&vs)[EACH]) {
+#pragma unroll
+          for (int j = 0; j < EACH; ++j) {
             ks[j] = row[j] >= 0 ? __ldg(static_cast<const float *>(a.k_scales) + (row[j] >> shift)) : 0.0f;
             vs[j] = row[j] >= 0 ? __ldg(a.v_scales + (row[j] >> shift)) : 0.0f;
           }
-        }
-      };
-      int row0[EACH], row1[EACH];
-      KeyScale ks0[EACH], ks1[EACH];
-      float vs0[EACH], vs1[EACH];
-      positions();
-      bool live0 = far.live, live1 = false, primed = false;
-      pool_rows(row0);
-      scales(row0, ks0, vs0);
-      if (live0) positions();
-      // 16 bytes a lane and copy: a warp's copy is 512 / D rows of K or of V, stored with the swizzle
-      // that the products expect.  (As gathers of four rows by the TMA unit, 64 a tile, a tile took
-      // 2.1 us to issue, and the serving mix's 343 MB of selected rows 176 us.)
-      constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-      const int x = (lane % kLanes) * 16, sub = lane / kLanes;
-      while (live0) {
-        if (primed) scales(row1, ks1, vs1);
-        if (!stage_free()) break;
-        uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
+        };
+        int row0[EACH], row1[EACH];
+        float ks0[EACH], vs0[EACH], ks1[EACH], vs1[EACH];
+        positions();
+        bool live0 = far.live, live1 = false, primed = false;
+        pool_rows(row0);
+        scales(row0, ks0, vs0);
+        if (live0) positions();
+        // 16 bytes a lane and copy: a warp's copy is 512 / D rows of K or of V, stored with the swizzle
+        // that the products expect.  (As gathers of four rows by the TMA unit, 64 a tile, a tile took
+        // 2.1 us to issue, and the serving mix's 343 MB of selected rows 176 us.)
+        constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+        const int x = (lane % kLanes) * 16, sub = lane / kLanes;
+        while (live0) {
+          if (primed) scales(row1, ks1, vs1);
+          if (!stage_free()) break;
+          uint8_t *kt = k_tile(kr.at), *vt = v_tile(kr.at);
 #pragma unroll
-        for (int q = 0; q < EACH; ++q)
+          for (int q = 0; q < EACH; ++q)
 #pragma unroll
-          for (int j = 0; j < 32 / kRows; ++j) {
-            const int n = j * kRows + sub;  // lane n's q-th token
-            const int row = __shfl_sync(0xffffffffu, row0[q], n);
-            if (row < 0) continue;  // (the softmax clears the value row of a token that is not)
-            const uint32_t dst = swizzled<D>(token0 - lane + 32 * q + n, x);
-            copy_piece<C::FP4, D>(kt + dst, a.k_pool, row, x, policy);
-            copy_piece<C::FP4, D>(vt + dst, a.v_pool, row, x, policy);
+            for (int j = 0; j < 32 / kRows; ++j) {
+              const int n = j * kRows + sub;  // lane n's q-th token
+              const int row = __shfl_sync(0xffffffffu, row0[q], n);
+              if (row < 0) continue;  // (the softmax clears the value row of a token that is not)
+              const int64_t src = static_cast<int64_t>(row) * D + x;
+              const uint32_t dst = swizzled<D>(token0 - lane + 32 * q + n, x);
+              cp_async_16(kt + dst, a.k_pool + src, policy);
+              cp_async_16(vt + dst, a.v_pool + src, policy);
+            }
+          if (!primed) {  // (the first tile's copies go out before anything waits for the second's ids)
+            primed = true;
+            pool_rows(row1);
+            live1 = far.live;
+            if (live1) positions();
+            scales(row1, ks1, vs1);
           }
-        if (!primed) {  // (the first tile's copies go out before anything waits for the second's ids)
-          primed = true;
+#pragma unroll
+          for (int j = 0; j < EACH; ++j)
+            s_tok[kr.at * kTile + token0 + 32 * j] =
+                token_of(ks0[j] * z_unit, vs0[j], row0[j] >= 0 ? 0 : kNone);
+          cp_async_arrive_noinc(&k_full[kr.at]);
+          mbar_arrive(&k_full[kr.at]);
+          next_stage();
+#pragma unroll
+          for (int j = 0; j < EACH; ++j) {
+            row0[j] = row1[j];
+            ks0[j] = ks1[j];
+            vs0[j] = vs1[j];
+          }
+          live0 = live1;
           pool_rows(row1);
           live1 = far.live;
           if (live1) positions();
-          scales(row1, ks1, vs1);
         }
-#pragma unroll
-        for (int j = 0; j < EACH; ++j) {
-          const int t = token0 + 32 * j;
-          float k;
-          if constexpr (C::FP4) {
-            k = unit_of_factors<D>(ks0[j], z_unit);
-            s_sf[(stage * 32 + t % 32) * 4 + t / 32] = ks0[j];
-          } else {
-            k = ks0[j] * z_unit;
-          }
-          s_tok[stage * kTile + t] = token_of(k, vs0[j], row0[j] >= 0 ? 0 : kNone);
-        }
-        if constexpr (C::FP4) fence_proxy_async_shared();
-        cp_async_arrive_noinc(&kv_full[stage]);
-        mbar_arrive(&kv_full[stage]);
-        next_stage();
-#pragma unroll
-        for (int j = 0; j < EACH; ++j) {
-          row0[j] = row1[j];
-          ks0[j] = ks1[j];
-          vs0[j] = vs1[j];
-        }
-        live0 = live1;
-        pool_rows(row1);
-        live1 = far.live;
-        if (live1) positions();
       }
     } else if constexpr (C::FP4) {
       while (ok && w.next(a, groups, keys)) {
@@ -693,13 +827,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           ks[0] = ks[1] = ks[2] = ks[3] = 0u;
           if (row < 0) return;
           vs = __ldg(reinterpret_cast<const float4 *>(a.v_scales + row));
-          if constexpr (D == 128) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a.k_scales) + row / 4);
-            ks[0] = u.x, ks[1] = u.y, ks[2] = u.z, ks[3] = u.w;
-          } else {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(a.k_scales) + row / 4);
-            ks[0] = u.x & 0xFFFFu, ks[1] = u.x >> 16, ks[2] = u.y & 0xFFFFu, ks[3] = u.y >> 16;
-          }
+          const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a.k_scales) + row / 4);
+          ks[0] = u.x, ks[1] = u.y, ks[2] = u.z, ks[3] = u.w;
         };
         int row = row_of(w.seg_tile), row_next = -1;
         uint32_t ks[4], ks_next[4];
@@ -710,38 +839,35 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           if (i + 1 < end) row_next = row_of(i + 1);
           else row_next = -1;
           scales(row_next, ks_next, vs_next);
-          if (!stage_free()) break;
-          uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
           const int p = i * kTile + lane * 4;
-          if constexpr (C::COPIES) {
-            constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-            const int x = (lane % kLanes) * 16, sub = lane / kLanes;
-#pragma unroll
-            for (int j = 0; j < kTile / kRows; ++j) {
-              const int n = j * kRows + sub;
-              const int r0 = __shfl_sync(0xffffffffu, row, n / 4);
-              if (r0 < 0) continue;
-              copy_piece<true, D>(kt + swizzled<D>(n, x), a.k_pool, r0 + n % 4, x, policy);
-              copy_piece<true, D>(vt + swizzled<D>(n, x), a.v_pool, r0 + n % 4, x, policy);
-            }
-          } else if (row >= 0 && (p & (a.block_size - 1)) == 0) {
+          const bool page = row >= 0 && (p & (a.block_size - 1)) == 0;  // (this lane's first token begins one)
+          if (!stage_free()) break;
+          if (page) {
             // (The barrier counts the bytes read, half of those that the rows take here.)
-            mbar_expect_tx(&kv_full[stage], D * a.block_size);
-            tma_load_2d(kt + lane * 4 * D, &k_map, &kv_full[stage], 0, row, policy);
-            tma_load_2d(vt + lane * 4 * D, &v_map, &kv_full[stage], 0, row, policy);
+            mbar_expect_tx(&k_full[kr.at], D / 2 * a.block_size);
+            tma_load_2d(k_tile(kr.at) + lane * 4 * D, &k_map, &k_full[kr.at], 0, row, policy);
           }
-          const float v4[4] = {vs.x, vs.y, vs.z, vs.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int t = lane * 4 + j;
-            s_sf[(stage * 32 + t % 32) * 4 + t / 32] = ks[j];
-            s_tok[stage * kTile + t] = token_of(unit_of_factors<D>(ks[j], z_unit), v4[j],
-                                                row >= 0 && p + j < w.length ? p + j : kNone);
+            s_sf[(kr.at * 32 + t % 32) * 4 + t / 32] = ks[j];
           }
           fence_proxy_async_shared();
-          if constexpr (C::COPIES) cp_async_arrive_noinc(&kv_full[stage]);
-          mbar_arrive(&kv_full[stage]);
+          mbar_arrive(&k_full[kr.at]);
           next_stage();
+          if (!free_now(&v_empty[vr.at], vr.phase)) break;
+          if (page) {
+            mbar_expect_tx(&v_full[vr.at], D / 2 * a.block_size);
+            tma_load_2d(v_tile(vr.at) + lane * 4 * D, &v_map, &v_full[vr.at], 0, row, policy);
+          }
+          const float v4[4] = {vs.x, vs.y, vs.z, vs.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s_tok4[vr.at * kTile + lane * 4 + j] = Token4{
+                scale_of<D>(ks[j], v4[j]), row >= 0 && p + j < w.length ? p + j : kNone};
+          mbar_arrive(&v_full[vr.at]);
+          ++issued_v;
+          vr.advance();
           row = row_next;
           vs = vs_next;
 #pragma unroll
@@ -796,19 +922,19 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           tok.log_v = __shfl_sync(0xffffffffu, mine.log_v, from);
           tok.inv_v = __shfl_sync(0xffffffffu, mine.inv_v, from);
           if (!stage_free()) break;
-          uint8_t *kt = s_kv + stage * C::KV_BYTES, *vt = kt + kTile * D;
+          uint8_t *kt = k_tile(kr.at), *vt = v_tile(kr.at);
           if (block >= 0 && (p & (a.block_size - 1)) == 0) {
             const int row = (block * a.kv_heads + m.g) << shift;
-            mbar_expect_tx(&kv_full[stage], 2 * D * a.block_size);
-            tma_load_2d(kt + lane * 4 * D, &k_map, &kv_full[stage], 0, row, policy);
-            tma_load_2d(vt + lane * 4 * D, &v_map, &kv_full[stage], 0, row, policy);
+            mbar_expect_tx(&k_full[kr.at], 2 * D * a.block_size);
+            tma_load_2d(kt + lane * 4 * D, &k_map, &k_full[kr.at], 0, row, policy);
+            tma_load_2d(vt + lane * 4 * D, &v_map, &k_full[kr.at], 0, row, policy);
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             tok.pos = block >= 0 && p + j < w.length ? p + j : kNone;
-            s_tok[stage * kTile + lane * 4 + j] = tok;
+            s_tok[kr.at * kTile + lane * 4 + j] = tok;
           }
-          mbar_arrive(&kv_full[stage]);
+          mbar_arrive(&k_full[kr.at]);
           next_stage();
           if (fetch) {
             scales(id_next, ks_next, vs_next);
@@ -826,7 +952,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const uint32_t o_tmem = tmem + 2 * NS;
     uint32_t tile = 0, seg = 0;
     const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
-      const uint64_t k_desc = smem_desc_rows<D>(smem_addr(s_kv + st * C::KV_BYTES));
+      const uint64_t k_desc = smem_desc_rows<D>(smem_addr(k_tile(st)));
       const uint32_t factors = tmem + C::SFA + (n & 1) * 4;
       if constexpr (C::FP4) tmem_copy_factors(factors, smem_desc_factors(smem_addr(s_sf + st * kTile)));
 #pragma unroll
@@ -841,6 +967,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             mma_f8f6f4(tmem + (n & 1) * NS, k_desc + 2 * k, q_at, idesc_s, part + k > 0);
         }
       mma_commit(&s_full[n & 1]);
+      if constexpr (C::FP4) mma_commit(&k_empty[st]);
     };
     const auto keys_here = [&]() {
       // (What ordinary copies and stores wrote.)
@@ -854,29 +981,31 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       bool ahead = false;  // S of the tile has been issued already
       for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
         if (!ahead) {
-          if (!mbar_wait(&kv_full[stage], phase, kWaitNs)) return false;
+          if (!mbar_wait(&k_full[kr.at], kr.phase, kWaitNs)) return false;
           keys_here();
-          scores(tile, stage);
+          scores(tile, kr.at);
         }
         // The next tile's scores, if its keys are here, before this tile's weights are.
-        const int next = stage + 1 == C::STAGES ? 0 : stage + 1;
-        const uint32_t next_phase = next == 0 ? phase ^ 1 : phase;
-        ahead = i + 1 < w.seg_tiles && mbar_try_wait(&kv_full[next], next_phase);
+        Ring<C::KS> next = kr;
+        next.advance();
+        ahead = i + 1 < w.seg_tiles && mbar_try_wait(&k_full[next.at], next.phase);
         if (ahead) {
           keys_here();
-          scores(tile + 1, next);
+          scores(tile + 1, next.at);
         }
         if (!mbar_wait(&p_full[tile & 1], (tile >> 1) & 1, kWaitNs)) return false;
+        if (C::FP4 && !mbar_wait(&v_full[vr.at], vr.phase, kWaitNs)) return false;
+        if constexpr (C::FP4 && C::COPIES) fence_proxy_async_shared();
         tc_fence_after_sync();
-        const uint64_t v_desc = smem_desc_mn<D>(smem_addr(s_kv + stage * C::KV_BYTES + kTile * D));
-        const uint64_t p_desc = smem_desc_p(smem_addr(weights_of(tile, stage)));
+        const uint64_t v_desc = smem_desc_mn<D>(smem_addr(v_tile(C::FP4 ? vr.at : kr.at)));
+        const uint64_t p_desc = smem_desc_p(smem_addr(weights_of(tile, kr.at)));
 #pragma unroll
         for (int k = 0; k < kTile / 32; ++k)
           mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o, i + k > 0);
         mma_commit(&pv_done[tile & 1]);
-        mma_commit(&kv_empty[stage]);
-        stage = next;
-        phase = next_phase;
+        mma_commit(C::FP4 ? &v_empty[vr.at] : &k_empty[kr.at]);
+        kr = next;
+        vr.advance();
       }
       return true;
     };
@@ -895,6 +1024,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     // The thread's dimension of the output, or -1 (M = 64: 16 lanes of each quarter).
     const int dim = D == 128 ? token : lane < 16 ? quarter * 16 + lane : -1;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const float z_unit = a.scale * 1.4426950408889634f;  // (FP4: what the tokens' keys share)
     uint32_t tile = 0;
     int seg = 0;
     // Once a wait has given up the warp goes on without waiting, so that the barriers below (which
@@ -1004,10 +1134,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       // Positions below this are seen by every row of the segment.
       const int all_see = C::SELECT ? kNone : len - a.next_n + 1 + (slot_head<C>(a, m, 0).x);
       for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
-        wait(&kv_full[stage], phase);
+        wait(C::FP4 ? &v_full[vr.at] : &k_full[kr.at], C::FP4 ? vr.phase : kr.phase);
         wait(&s_full[tile & 1], (tile >> 1) & 1);
         tc_fence_after_sync();
-        const Token tok = s_tok[stage * kTile + token];
+        Token tok;
+        if constexpr (C::FP4) {
+          const Token4 t4 = s_tok4[vr.at * kTile + token];
+          tok = token_of(z_unit, t4.v_scale, t4.pos);
+        } else {
+          tok = s_tok[kr.at * kTile + token];
+        }
         float2 y[RT / 2];  // the weights' logarithms
         {
           uint32_t v[RT];
@@ -1122,8 +1258,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // ---- weights, their parts, the running sums ------------------------------------------------
         // The weights' buffer was last read by the product two tiles ago.  (In the place of the keys
         // they need not wait; but whoever waits for a barrier has to see all its phases.)
-        if (tile >= 2) wait(&pv_done[tile & 1], ((tile >> 1) - 1) & 1);
-        uint8_t *sp = weights_of(tile, stage) + token * 16;
+        if constexpr (C::P_BUFS == 1) {
+          if (tile >= 1) wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
+        } else {
+          if (tile >= 2) wait(&pv_done[tile & 1], ((tile >> 1) - 1) & 1);
+        }
+        uint8_t *sp = weights_of(tile, kr.at) + token * 16;
         const float inv_v = fabsf(tok.inv_v);
         // The weights of a position whose value scale is negative or 0 (as good as): rare, so asked
         // of the whole warp.
@@ -1170,7 +1310,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // this segment's number) for the rows that do see it.
         // (Four bits hold no NaN.)
         if (!C::FP4 && wg == 0 && !seen) {
-          uint8_t *v = s_kv + stage * C::KV_BYTES + kTile * D;
+          uint8_t *v = v_tile(kr.at);
           if (tok.pos == kNone) {
             for (int x = 0; x < D; x += 16)
               *reinterpret_cast<uint4 *>(v + token * D + x) = make_uint4(0, 0, 0, 0);
@@ -1191,10 +1331,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[tile & 1]);
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
+        kr.advance();
+        vr.advance();
       }
       // ---- the segment's sums ------------------------------------------------------------------------
       wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
@@ -1306,12 +1444,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     // A wait gave up: let the copies and products in flight end before the memory is given back.
     if (!ok) attn_flag(IDX_DEV_WAIT_TIMEOUT);
     if (warp == 0 && lane == 0) {
-      const uint32_t tail = issued < C::STAGES ? issued : C::STAGES;
-      for (uint32_t d = 1; d <= tail; ++d) {
-        const uint32_t n = issued - d;
-        if (!mbar_wait(&kv_full[n % C::STAGES], (n / C::STAGES) & 1, kWaitNs))
-          attn_flag(IDX_DEV_WAIT_TIMEOUT);
-      }
+      const auto landed = [&](uint64_t *full, uint32_t issued, uint32_t stages) {
+        const uint32_t tail = issued < stages ? issued : stages;
+        for (uint32_t d = 1; d <= tail; ++d) {
+          const uint32_t n = issued - d;
+          if (!mbar_wait(&full[n % stages], (n / stages) & 1, kWaitNs)) attn_flag(IDX_DEV_WAIT_TIMEOUT);
+        }
+      };
+      landed(k_full, issued_k, C::KS);
+      if constexpr (C::FP4) landed(v_full, issued_v, C::VS);
     }
   }
   if (warp == 1 && lane == 0 && !mbar_wait(drain, 0, kWaitNs)) attn_flag(IDX_DEV_WAIT_TIMEOUT);

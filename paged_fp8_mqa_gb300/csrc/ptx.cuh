@@ -204,13 +204,6 @@ __device__ __forceinline__ void cp_async_16(void *dst, const void *src, uint64_t
                : "memory");
 }
 
-// The same of 8 bytes.
-__device__ __forceinline__ void cp_async_8(void *dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(dst)),
-               "l"(reinterpret_cast<uint64_t>(src))
-               : "memory");
-}
-
 // Arrives on `bar` once every cp.async this thread issued so far has landed; the arrival counts
 // toward the barrier's initial count (.noinc).
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t *bar) {
