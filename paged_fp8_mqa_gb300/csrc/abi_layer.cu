@@ -171,6 +171,8 @@ int check_norm(int32_t dtype, float eps, const void *q_weight, const void *k_wei
   a->weight[0] = q_weight;
   a->weight[1] = k_weight;
   a->weight_f32 = weight_dtype == IDX_DTYPE_F32;
+  a->weight_pieces = aligned(q_weight, 8 * element_bytes(weight_dtype)) &&
+                     aligned(k_weight, 8 * element_bytes(weight_dtype));
   return IDX_OK;
 }
 
@@ -690,7 +692,7 @@ IDX_EXPORT int64_t idx_norm_rotary_workspace_bytes(int32_t head_dim) {
   if (head_dim < 1 || head_dim > IDX_NORM_MAX_DIM) return -1;
   int32_t sms = 0;
   if (idx::resolve_sms(0, &sms) != IDX_OK) return -1;
-  return 2ll * idx::heads_blocks(sms) * head_dim * 4;
+  return (idx::heads_blocks(sms) + 1ll) * head_dim * 4;
 }
 
 IDX_EXPORT int idx_norm_rotary_backward(
@@ -740,7 +742,7 @@ IDX_EXPORT int idx_norm_rotary_backward(
   st = idx::resolve_sms(0, &sms);
   if (st != IDX_OK) return st;
   if (workspace == nullptr || !aligned(workspace, 16) ||
-      workspace_bytes < 2ll * idx::heads_blocks(sms) * head_dim * 4)
+      workspace_bytes < (idx::heads_blocks(sms) + 1ll) * head_dim * 4)
     return fail(IDX_INVALID_ARG, "workspace (16-byte aligned) below "
                                  "idx_norm_rotary_workspace_bytes(...)");
   a.dweight[0] = q_weight_grad;

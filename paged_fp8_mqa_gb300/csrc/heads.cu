@@ -12,8 +12,8 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "pieces.cuh"
 #include "ptx.cuh"
-#include "rows.cuh"
 
 namespace idx {
 
@@ -21,7 +21,8 @@ __device__ int g_heads_status;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kFewWarps = 8192;
 constexpr int kMaxDim = IDX_NORM_MAX_DIM;
 
 __device__ __forceinline__ int axis_of(const Axes &x, int pair) {
@@ -37,55 +38,12 @@ __device__ __forceinline__ bool angle_of(const HeadsArgs &a, int64_t t, int pair
   return true;
 }
 
-// 1 / sqrt(v): the approximation and one step of Newton's method (where v is a positive number).
-__device__ __forceinline__ float inv_sqrt(float v) {
-  const float r = rsqrtf(v);
-  return v > 1e-37f && v < 1e37f ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
-}
-
-// A lane's two pieces of a head of D = 16 * (lanes at work) elements, and how they are turned.
-struct Pieces {
-  int at[2];        // their first elements
-  bool on[2];       // rotated
-  bool across;      // halves: element j of the first with element j of the second; else within each
-  float2 cs[8];     // the angles of the lane's pairs
-  uint32_t valid;   // bit j: pair j's position is in the table
-};
-
-// Where lane l's pieces lie (which does not depend on the token), and the pairs of their angles 0 and 4.
-__device__ __forceinline__ void place_pieces(const Rotation &r, int l, Pieces &p, int (&pair)[2]) {
-  const int off = r.offset, rot = r.table != nullptr ? r.rot : 0;
-  p.across = !r.interleaved;
-  if (r.interleaved) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      p.at[s] = 16 * l + 8 * s;
-      p.on[s] = p.at[s] >= off && p.at[s] < off + rot;
-      pair[s] = (p.at[s] - off) >> 1;
-    }
-  } else if (l < rot / 16) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      p.at[s] = off + 8 * l + s * (rot >> 1);
-      p.on[s] = true;
-      pair[s] = 8 * l + 4 * s;
-    }
-  } else {  // what is not rotated, piece after piece
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int e = 16 * l - rot + 8 * s;
-      p.at[s] = e < off ? e : e + rot;
-      p.on[s] = false;
-      pair[s] = 0;
-    }
-  }
-}
-
+template <bool ADJ>
 __device__ __forceinline__ Pieces pieces_of(const HeadsArgs &a, int64_t t, int l) {
   Pieces p;
   const int half = a.r.rot >> 1;
   int pair[2];
-  place_pieces(a.r, l, p, pair);
+  place_pieces<ADJ>(a.r, a.dim, l, p, pair);
   p.valid = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) p.cs[j] = make_float2(1.0f, 0.0f);
@@ -117,50 +75,30 @@ __device__ __forceinline__ Pieces pieces_of(const HeadsArgs &a, int64_t t, int l
   return p;
 }
 
-// v, the lane's 16 elements, turned.  A pair that is not turned stays to the bit (a product with a
-// sine of 0 would make an infinity's partner NaN).
-__device__ __forceinline__ void turn(const Pieces &p, float (&v)[2][8]) {
-  if (p.across) {
-    if (p.valid == 0xFFu) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = v[0][j], y = v[1][j];
-        v[0][j] = turn_a(x, y, p.cs[j]);
-        v[1][j] = turn_b(x, y, p.cs[j]);
-      }
-    } else if (p.valid != 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = v[0][j], y = v[1][j];
-        const bool go = (p.valid >> j) & 1u;
-        v[0][j] = go ? turn_a(x, y, p.cs[j]) : x;
-        v[1][j] = go ? turn_b(x, y, p.cs[j]) : y;
-      }
-    }
-  } else if (p.valid != 0) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = v[s][2 * j], y = v[s][2 * j + 1];
-        const bool go = (p.valid >> (4 * s + j)) & 1u;
-        v[s][2 * j] = go ? turn_a(x, y, p.cs[4 * s + j]) : x;
-        v[s][2 * j + 1] = go ? turn_b(x, y, p.cs[4 * s + j]) : y;
-      }
-  }
+// 1 / sqrt(v): the approximation and one step of Newton's method (where v is a positive number).
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  return v > 1e-37f && v < 1e37f ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
 }
 
-// The lane's 16 weights in float32 (1 without).
-template <typename T>
+// The lane's 16 weights in float32 (1 without), as the elements are unpacked.
+template <bool ADJ, typename T>
 __device__ __forceinline__ void weights_of(const HeadsArgs &a, int kind, const Pieces &p,
-                                           float (&w)[2][8]) {
+                                           float2 (&w)[2][4]) {
+  if (a.weight[kind] == nullptr) {
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      w[s][j] = a.weight[kind] == nullptr ? 1.0f
-                : a.weight_f32 ? __ldg(static_cast<const float *>(a.weight[kind]) + p.at[s] + j)
-                               : to_f32(static_cast<const T *>(a.weight[kind])[p.at[s] + j]);
+    for (int j = 0; j < 4; ++j) w[0][j] = w[1][j] = make_float2(1.0f, 1.0f);
+  } else if (a.weight_f32) {
+    const float *at = static_cast<const float *>(a.weight[kind]);
+    const Piece<float, 8> two[2] = {load_whole(at + p.at[0], a.weight_pieces),
+                                    load_whole(at + p.at[1], a.weight_pieces)};
+    unpack<ADJ, float>(two, w);
+  } else {
+    const T *at = static_cast<const T *>(a.weight[kind]);
+    const Piece<T, 8> two[2] = {load_whole(at + p.at[0], a.weight_pieces),
+                                load_whole(at + p.at[1], a.weight_pieces)};
+    unpack<ADJ, T>(two, w);
+  }
 }
 
 template <int W>
@@ -170,71 +108,111 @@ __device__ __forceinline__ float sum_lanes(float x) {
   return x;
 }
 
-// W lanes (a power of two, 16 elements a lane; those past dim idle) walk HEADS heads of one token, of q
-// or of k, all of them asked for at once.
-template <typename T, int W, int HEADS>
-__global__ void __launch_bounds__(kThreads) k_heads(const __grid_constant__ HeadsArgs a,
-                                                    int64_t first_token) {
+// W lanes (a power of two, 16 elements a lane; those past dim idle) walk `walk` heads of one token, of q or
+// of k, AHEAD heads asked for before they are needed.
+template <typename T, int W, bool ADJ, int AHEAD, bool NORM, int BLOCKS>
+__global__ void __launch_bounds__(kThreads, BLOCKS)
+    k_heads(const __grid_constant__ HeadsArgs a, int64_t first_token, int walk) {
   griddep_wait();
   griddep_launch_dependents();
-  const int chunks_q = (a.heads[0] + HEADS - 1) / HEADS;
-  const int chunks = chunks_q + (a.heads[1] + HEADS - 1) / HEADS;
+  const int chunks_q = (a.heads[0] + walk - 1) / walk;
+  const int chunks = chunks_q + (a.heads[1] + walk - 1) / walk;
   const uint32_t id = blockIdx.x * (kThreads / W) + threadIdx.x / W;
   const uint32_t tok = id / chunks;
   const int64_t t = first_token + tok;
   // (Past the last token or element: the last, and nothing is stored, so that the shuffles find all
   // their lanes.)
   const int lanes = a.dim / 16;
-  const bool live = t < a.tokens && static_cast<int>(threadIdx.x % W) < lanes;
+  const bool idle = static_cast<int>(threadIdx.x % W) >= lanes;
+  const bool live = t < a.tokens && !idle;
   const int64_t tt = min(t, a.tokens - 1);
   const int l = min(static_cast<int>(threadIdx.x % W), lanes - 1);
   int chunk = id - tok * chunks;
   const int kind = chunk >= chunks_q;
   if (kind) chunk -= chunks_q;
-  const int h0 = chunk * HEADS, n = min(HEADS, a.heads[kind] - h0);
-  const T *x = static_cast<const T *>(a.x[kind]) + tt * a.x_token[kind] + h0 * a.x_head[kind];
-  T *out = static_cast<T *>(a.out[kind]) + tt * a.out_token[kind] + h0 * a.out_head[kind];
-  const Pieces p = pieces_of(a, tt, l);
-  Piece<T, 8> own[HEADS][2];
+  const int h0 = chunk * walk, n = min(walk, a.heads[kind] - h0);
+  const int rounds = __reduce_max_sync(0xffffffffu, n);  // (the same for the whole warp)
+  const int64_t x_head = a.x_head[kind], out_head = a.out_head[kind];
+  const T *x = static_cast<const T *>(a.x[kind]) + tt * a.x_token[kind] + h0 * x_head;
+  T *out = static_cast<T *>(a.out[kind]) + tt * a.out_token[kind] + h0 * out_head;
+  const Pieces p = pieces_of<ADJ>(a, tt, l);
+  Piece<T, 8> own[AHEAD][2];
 #pragma unroll
-  for (int h = 0; h < HEADS; ++h)
+  for (int d = 0; d < AHEAD; ++d)
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      own[h][s] = load_piece<T, 8>(x + min(h, n - 1) * a.x_head[kind] + p.at[s]);
+      own[d][s] = load_piece<T, 8>(x + min(d, n - 1) * x_head + p.at[s]);
   if (live && h0 == 0 && kind == (a.heads[0] == 0) &&
       p.valid != ((p.on[0] ? 0x0Fu : 0u) | (p.on[1] ? 0xF0u : 0u)))
     atomicOr(&g_heads_status, IDX_DEV_BAD_POSITION);
-  float w[2][8];
-  if (a.norm) weights_of<T>(a, kind, p, w);
+  // Turned and (NORM) weighted: y0 = own[0] v0 - cross[0] v1, y1 = own[1] v1 + cross[1] v0.
+  float2 own_f[NORM ? 2 : 1][4], cross[NORM ? 2 : 1][4];
+  angles_of(p, own_f[0], cross[0]);
+  const uint32_t valid = p.valid;
+  if constexpr (NORM) {
+    float2 w[2][4];
+    weights_of<ADJ, T>(a, kind, p, w);
 #pragma unroll
-  for (int h = 0; h < HEADS; ++h) {
-    float v[2][8];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) piece_f32<T, 8>(own[h][s], v[s]);
-    if (a.norm) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[s][j], v[s][j], ss);
-      if (static_cast<int>(threadIdx.x % W) >= lanes) ss = 0.0f;
-      const float r = inv_sqrt(sum_lanes<W>(ss) / static_cast<float>(a.dim) + a.eps);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[s][j] = v[s][j] * r * w[s][j];
+    for (int j = 0; j < 4; ++j) {
+      const float2 c = own_f[0][j], n = cross[0][j];
+      own_f[0][j] = __fmul2_rn(c, w[0][j]);
+      own_f[1][j] = __fmul2_rn(c, w[1][j]);
+      cross[0][j] = __fmul2_rn(n, minus(w[1][j]));
+      cross[1][j] = __fmul2_rn(n, w[0][j]);
     }
-    const bool untouched = !a.norm && p.valid == 0;
-    if (!untouched) {
-      turn(p, v);
+  }
+  const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  const int at0 = p.at[0], at1 = p.at[1];
+  const T *next = x + AHEAD * x_head;
+  for (int r0 = 0; r0 < rounds; r0 += AHEAD) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+    for (int d = 0; d < AHEAD; ++d) {
+      const int h = r0 + d;
+      if (h >= rounds) break;
+      const bool store = live && h < n;
+      if (NORM || valid != 0) {
+        float2 v[2][4];
+        unpack<ADJ, T>(own[d], v);
+        if constexpr (NORM) {
+          float2 sq = __fmul2_rn(v[0][0], v[0][0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) own[h][s].e[j] = from_f32<T>(v[s][j]);
+          for (int j = 1; j < 4; ++j) sq = __ffma2_rn(v[0][j], v[0][j], sq);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sq = __ffma2_rn(v[1][j], v[1][j], sq);
+          const float ss = sum_lanes<W>(idle ? 0.0f : sq.x + sq.y);
+          const float r = inv_sqrt(fmaf(ss, inv_dim, a.eps));
+          const float2 r2 = make_float2(r, r);
+          const bool odd = !(r > 0.0f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = v[0][j], y = v[1][j];
+            v[0][j] = __fmul2_rn(__ffma2_rn(x, own_f[0][j], __fmul2_rn(y, cross[0][j])), r2);
+            v[1][j] = __fmul2_rn(__ffma2_rn(y, own_f[1][j], __fmul2_rn(x, cross[1][j])), r2);
+            if (odd) {
+              // The row holds something that is not finite (or too large to be squared): what is not
+              // turned must not meet its neighbour, not even times 0.
+              const float2 a0 = __fmul2_rn(__fmul2_rn(x, r2), own_f[0][j]);
+              const float2 a1 = __fmul2_rn(__fmul2_rn(y, r2), own_f[1][j]);
+              if (!((valid >> (2 * j)) & 1u)) v[0][j].x = a0.x, v[1][j].x = a1.x;
+              if (!((valid >> (2 * j + 1)) & 1u)) v[0][j].y = a0.y, v[1][j].y = a1.y;
+            }
+          }
+        } else {
+          turn(valid, own_f[0], cross[0], v);
+        }
+        pack<ADJ, T>(v, own[d]);
+      }
+      if (store) {
+        store_piece<T, 8>(out + at0, own[d][0]);
+        store_piece<T, 8>(out + at1, own[d][1]);
+      }
+      out += out_head;
+      if (h + AHEAD < n) {  // (past the last: what is there, which is stored nowhere)
+        own[d][0] = load_piece<T, 8>(next + at0);
+        own[d][1] = load_piece<T, 8>(next + at1);
+      }
+      next += x_head;
     }
-    if (live && h < n)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) store_piece<T, 8>(out + h * a.out_head[kind] + p.at[s], own[h][s]);
   }
 }
 
@@ -301,118 +279,134 @@ __global__ void __launch_bounds__(32 * kAnyWarps) k_heads_any(const __grid_const
   }
 }
 
-// The gradients: blocks y = 0 take q's heads, y = 1 k's, W lanes a head, two heads of a token at a
-// time.  A lane's 16 elements of the weight's gradient stay in its registers over all its heads; a block
-// leaves its sums in the workspace and a second launch adds the blocks', in order.
-template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) k_heads_backward(const __grid_constant__ HeadsArgs a) {
+// How the gradients' blocks are shared: the first `q` of them take q's heads, the others k's, `walk`
+// heads of a token at a time.
+struct BackwardSplit {
+  int32_t q, k, walk;
+};
+
+// The gradients, W lanes a head.  8192 tokens of 32 + 8 heads of 128 (252 MB) take 60 us, 37 at the copy rate:
+// 128 registers leave 16 warps an SM (three blocks of them 63 us, five 82).  A lane's 16 elements of the weight's gradient stay in its registers over
+// all its heads; a block leaves its sums in the workspace and a second launch adds the blocks', in order.
+template <typename T, int W, bool ADJ>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
+    k_heads_backward(const __grid_constant__ HeadsArgs a, const BackwardSplit split) {
   constexpr int GROUPS = kThreads / W;
   extern __shared__ float s_sum[];  // [GROUPS][16 * W]
   griddep_wait();
   griddep_launch_dependents();
-  const int kind = blockIdx.y, heads = a.heads[kind], lanes = a.dim / 16;
+  const int kind = static_cast<int>(blockIdx.x) >= split.q;
+  const int block = blockIdx.x - (kind ? split.q : 0), blocks = kind ? split.k : split.q;
+  const int heads = a.heads[kind], lanes = a.dim / 16, walk = split.walk;
   const int group = threadIdx.x / W, lw = threadIdx.x % W, l = min(lw, lanes - 1);
   const bool live_lane = lw < lanes;
-  constexpr int HEADS = 2;
-  const int chunks = (heads + HEADS - 1) / HEADS;
-  const int64_t items = a.tokens * chunks;
-  float dw[2][8];
+  const int chunks = (heads + walk - 1) / walk;
+  const int64_t items = a.tokens * chunks, step = static_cast<int64_t>(blocks) * GROUPS;
+  const int64_t x_head = a.x_head[kind], dy_head = a.dy_head[kind], out_head = a.out_head[kind];
+  Pieces p;
+  int pair[2];
+  place_pieces<ADJ>(a.r, a.dim, l, p, pair);
+  const int at0 = p.at[0], at1 = p.at[1];
+  float2 dw[2][4], w[2][4];
+  weights_of<ADJ, T>(a, kind, p, w);
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[s][j] = 0.0f;
-  float w[2][8];
-  bool first = true;
-  // All groups of a warp make the same number of rounds.
-  const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * GROUPS; i0 < items; i0 += step) {
-    const int64_t i = i0 + group;
-    const bool live = i < items;
-    const int64_t at = min(i, items - 1);
-    const int64_t t = at / chunks;
-    const int h0 = static_cast<int>(at - t * chunks) * HEADS, n = min(HEADS, heads - h0);
-    const T *x = static_cast<const T *>(a.x[kind]) + t * a.x_token[kind] + h0 * a.x_head[kind];
-    const T *dy = static_cast<const T *>(a.dy[kind]) + t * a.dy_token[kind] + h0 * a.dy_head[kind];
-    T *out = static_cast<T *>(a.out[kind]) + t * a.out_token[kind] + h0 * a.out_head[kind];
-    const Pieces p = pieces_of(a, t, l);
-    Piece<T, 8> px[HEADS][2], pg[HEADS][2];
-#pragma unroll
-    for (int h = 0; h < HEADS; ++h)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        px[h][s] = load_piece<T, 8>(x + min(h, n - 1) * a.x_head[kind] + p.at[s]);
-        pg[h][s] = load_piece<T, 8>(dy + min(h, n - 1) * a.dy_head[kind] + p.at[s]);
+    for (int j = 0; j < 4; ++j) dw[s][j] = make_float2(0.0f, 0.0f);
+  const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  // (All groups of a warp make the same number of rounds, so that the shuffles find all their lanes.)
+  for (int64_t i0 = static_cast<int64_t>(block) * GROUPS; i0 < items; i0 += step) {
+    const int64_t i = i0 + group, at = min(i, items - 1), t = at / chunks;
+    const int h0 = static_cast<int>(at - t * chunks) * walk, n = min(walk, heads - h0);
+    const int rounds = __reduce_max_sync(0xffffffffu, n);
+    const T *x = static_cast<const T *>(a.x[kind]) + t * a.x_token[kind] + h0 * x_head;
+    const T *dy = static_cast<const T *>(a.dy[kind]) + t * a.dy_token[kind] + h0 * dy_head;
+    T *out = static_cast<T *>(a.out[kind]) + t * a.out_token[kind] + h0 * out_head;
+    Piece<T, 8> px[2], pg[2];
+    px[0] = load_piece<T, 8>(x + at0);
+    px[1] = load_piece<T, 8>(x + at1);
+    pg[0] = load_piece<T, 8>(dy + at0);
+    pg[1] = load_piece<T, 8>(dy + at1);
+    float2 c[4], m[4];
+    p = pieces_of<ADJ>(a, t, l);
+    angles_of(p, c, m);
+    for (int h = 0; h < rounds; ++h) {
+      float2 v[2][4], g[2][4];
+      unpack<ADJ, T>(px, v);
+      unpack<ADJ, T>(pg, g);
+      x += x_head;
+      dy += dy_head;
+      if (h + 1 < n) {
+        px[0] = load_piece<T, 8>(x + at0);
+        px[1] = load_piece<T, 8>(x + at1);
+        pg[0] = load_piece<T, 8>(dy + at0);
+        pg[1] = load_piece<T, 8>(dy + at1);
       }
-    if (first) {
-      weights_of<T>(a, kind, p, w);
-      first = false;
-    }
-#pragma unroll
-    for (int h = 0; h < HEADS; ++h) {
-      float v[2][8], g[2][8];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        piece_f32<T, 8>(px[h][s], v[s]);
-        piece_f32<T, 8>(pg[h][s], g[s]);
-      }
-      turn(p, g);
-      float ss = 0.0f, dot = 0.0f;
+      turn(p.valid, c, m, g);
+      float2 sq = make_float2(0.0f, 0.0f), sd = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ss = fmaf(v[s][j], v[s][j], ss);
-          dot = fmaf(g[s][j] * w[s][j], v[s][j], dot);
+        for (int j = 0; j < 4; ++j) {
+          sq = __ffma2_rn(v[s][j], v[s][j], sq);
+          sd = __ffma2_rn(__fmul2_rn(g[s][j], w[s][j]), v[s][j], sd);
         }
-      if (!live_lane) ss = dot = 0.0f;
-      const float dim = static_cast<float>(a.dim);
-      const float r = inv_sqrt(sum_lanes<W>(ss) / dim + a.eps);
-      const float c = sum_lanes<W>(dot) * r / dim;  // mean(g w x r)
-      if (!live || h >= n) continue;
-      Piece<T, 8> o[2];
+      const float ss = sum_lanes<W>(live_lane ? sq.x + sq.y : 0.0f);
+      const float dot = sum_lanes<W>(live_lane ? sd.x + sd.y : 0.0f);
+      const float r = inv_sqrt(fmaf(ss, inv_dim, a.eps));
+      const float mean = -dot * r * inv_dim;  // -mean(g w x r)
+      if (i < items && h < n) {
+        const float2 r2 = make_float2(r, r), k2 = make_float2(mean, mean);
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float unit = v[s][j] * r;
-          dw[s][j] = fmaf(g[s][j], unit, dw[s][j]);
-          o[s].e[j] = from_f32<T>(r * fmaf(g[s][j], w[s][j], -unit * c));
+          for (int j = 0; j < 4; ++j) {
+            const float2 unit = __fmul2_rn(v[s][j], r2);
+            dw[s][j] = __ffma2_rn(g[s][j], unit, dw[s][j]);
+            v[s][j] = __fmul2_rn(__ffma2_rn(g[s][j], w[s][j], __fmul2_rn(unit, k2)), r2);
+          }
+        if (live_lane) {
+          Piece<T, 8> o[2];
+          pack<ADJ, T>(v, o);
+          store_piece<T, 8>(out + at0, o[0]);
+          store_piece<T, 8>(out + at1, o[1]);
         }
-      if (live_lane)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) store_piece<T, 8>(out + h * a.out_head[kind] + p.at[s], o[s]);
+      }
+      out += out_head;
     }
   }
   if (a.dweight[kind] == nullptr) return;
-  Pieces p;
-  int pair[2];
-  place_pieces(a.r, l, p, pair);
   if (live_lane)
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s_sum[group * (16 * W) + p.at[s] + j] = dw[s][j];
+      for (int j = 0; j < 4; ++j) {
+        s_sum[group * (16 * W) + element_at<ADJ>(p, s, j, 0)] = dw[s][j].x;
+        s_sum[group * (16 * W) + element_at<ADJ>(p, s, j, 1)] = dw[s][j].y;
+      }
   __syncthreads();
   for (int d = threadIdx.x; d < a.dim; d += kThreads) {
     float sum = 0.0f;
     for (int g = 0; g < GROUPS; ++g) sum += s_sum[g * (16 * W) + d];
-    a.workspace[(static_cast<int64_t>(kind) * gridDim.x + blockIdx.x) * a.dim + d] = sum;
+    a.workspace[static_cast<int64_t>(blockIdx.x) * a.dim + d] = sum;
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kAnyWarps)
-    k_heads_backward_any(const __grid_constant__ HeadsArgs a) {
+    k_heads_backward_any(const __grid_constant__ HeadsArgs a, const BackwardSplit split) {
   extern __shared__ float s_any[];  // [warps][dim] of g, then of the weight's gradient
   griddep_wait();
   griddep_launch_dependents();
-  const int kind = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kind = static_cast<int>(blockIdx.x) >= split.q;
+  const int block = blockIdx.x - (kind ? split.q : 0), blocks = kind ? split.k : split.q;
   float *g = s_any + warp * a.dim, *dw = s_any + (kAnyWarps + warp) * a.dim;
   for (int d = lane; d < a.dim; d += 32) dw[d] = 0.0f;
   const int64_t rows = a.tokens * a.heads[kind];
   const float dim = static_cast<float>(a.dim);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAnyWarps + warp; i < rows;
-       i += static_cast<int64_t>(gridDim.x) * kAnyWarps) {
+  for (int64_t i = static_cast<int64_t>(block) * kAnyWarps + warp; i < rows;
+       i += static_cast<int64_t>(blocks) * kAnyWarps) {
     const int64_t t = i / a.heads[kind];
     const int h = static_cast<int>(i - t * a.heads[kind]);
     const T *x = static_cast<const T *>(a.x[kind]) + t * a.x_token[kind] + h * a.x_head[kind];
@@ -451,35 +445,44 @@ __global__ void __launch_bounds__(32 * kAnyWarps)
   for (int d = threadIdx.x; d < a.dim; d += 32 * kAnyWarps) {
     float sum = 0.0f;
     for (int w = 0; w < kAnyWarps; ++w) sum += s_any[(kAnyWarps + w) * a.dim + d];
-    a.workspace[(static_cast<int64_t>(kind) * gridDim.x + blockIdx.x) * a.dim + d] = sum;
+    a.workspace[static_cast<int64_t>(blockIdx.x) * a.dim + d] = sum;
   }
 }
 
-// The blocks' sums of a weight's gradient, in order and in 64 bits: a warp an element, block (x, kind).
+// The blocks' sums of a weight's gradient, in order and in 64 bits: 32 elements a block (x, kind), a warp
+// every 32nd row of them.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_weight_gradient(const __grid_constant__ HeadsArgs a,
-                                                              int blocks) {
+__global__ void __launch_bounds__(1024) k_weight_gradient(const __grid_constant__ HeadsArgs a,
+                                                          const BackwardSplit split) {
+  __shared__ double s_part[32][33];
   griddep_wait();
   griddep_launch_dependents();
-  const int kind = blockIdx.y, lane = threadIdx.x & 31;
-  const int d = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (a.dweight[kind] == nullptr || d >= a.dim) return;
+  const int kind = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int d = blockIdx.x * 32 + lane;
+  if (a.dweight[kind] == nullptr) return;
+  const int begin = kind ? split.q : 0, end = begin + (kind ? split.k : split.q);
   double sum = 0.0;
-  for (int b = lane; b < blocks; b += 32)
-    sum += a.workspace[(static_cast<int64_t>(kind) * blocks + b) * a.dim + d];
+  if (d < a.dim) {
+#pragma unroll 4
+    for (int b = begin + warp; b < end; b += 32) sum += a.workspace[static_cast<int64_t>(b) * a.dim + d];
+  }
+  s_part[warp][lane] = sum;
+  __syncthreads();
+  sum = s_part[lane][warp];  // element `warp` of the block's, part `lane`
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane != 0) return;
+  const int e = blockIdx.x * 32 + warp;
+  if (lane != 0 || e >= a.dim) return;
   if (a.weight_f32)
-    static_cast<float *>(a.dweight[kind])[d] = static_cast<float>(sum);
+    static_cast<float *>(a.dweight[kind])[e] = static_cast<float>(sum);
   else
-    static_cast<T *>(a.dweight[kind])[d] = from_f32<T>(static_cast<float>(sum));
+    static_cast<T *>(a.dweight[kind])[e] = from_f32<T>(static_cast<float>(sum));
 }
 
-template <typename T, int W, int HEADS>
-cudaError_t launch_walk(const HeadsArgs &a, cudaStream_t stream) {
+template <typename T, int W, bool ADJ, int AHEAD, bool NORM, int BLOCKS = 1>
+cudaError_t launch_walk(const HeadsArgs &a, int walk, cudaStream_t stream) {
   constexpr int GROUPS = kThreads / W;
-  const int64_t chunks = (a.heads[0] + HEADS - 1) / HEADS + (a.heads[1] + HEADS - 1) / HEADS;
+  const int64_t chunks = (a.heads[0] + walk - 1) / walk + (a.heads[1] + walk - 1) / walk;
   // The group's number is 32 bits wide: more tokens than fit it go in several launches.
   const int64_t most = (INT64_C(1) << 30) / chunks;
   for (int64_t t = 0; t < a.tokens; t += most) {
@@ -487,27 +490,40 @@ cudaError_t launch_walk(const HeadsArgs &a, cudaStream_t stream) {
     HeadsArgs part = a;
     part.tokens = t + n;
     const unsigned blocks = static_cast<unsigned>((n * chunks + GROUPS - 1) / GROUPS);
-    const cudaError_t e = launch_dependent(k_heads<T, W, HEADS>, dim3(blocks), dim3(kThreads), 0,
-                                           stream, part, t);
+    const cudaError_t e = launch_dependent(k_heads<T, W, ADJ, AHEAD, NORM, BLOCKS>, dim3(blocks), dim3(kThreads), 0,
+                                           stream, part, t, walk);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-// Four heads a group where that still leaves some thousands of warps, else one.
-template <typename T, int W>
+// As many heads a group as leave some thousands of warps, 16 at most; a small call takes one head a group.
+template <typename T, int W, bool ADJ>
 cudaError_t launch_pieces(const HeadsArgs &a, cudaStream_t stream) {
-  const int64_t warps = a.tokens * (a.heads[0] + a.heads[1]) * W / 32;
-  return warps > 16384 ? launch_walk<T, W, 4>(a, stream) : launch_walk<T, W, 1>(a, stream);
+  int walk = 16;
+  while (walk > 1 && a.tokens * ((a.heads[0] + a.heads[1]) / walk) * W / 32 < kFewWarps) walk /= 2;
+  // Heads asked for ahead, and blocks of 128 threads that an SM holds (see k_heads).
+  constexpr int AHEAD = sizeof(T) == 2 ? 3 : 2, TURN_AHEAD = sizeof(T) == 2 ? 4 : 2;
+  constexpr int BLOCKS = sizeof(T) == 2 ? 6 : 4;
+  if (a.norm)
+    return walk == 1 ? launch_walk<T, W, ADJ, 1, true>(a, 1, stream)
+                     : launch_walk<T, W, ADJ, AHEAD, true, BLOCKS>(a, walk, stream);
+  return walk == 1 ? launch_walk<T, W, ADJ, 1, false>(a, 1, stream)
+                   : launch_walk<T, W, ADJ, TURN_AHEAD, false, BLOCKS>(a, walk, stream);
 }
 
 template <typename T>
 cudaError_t launch(const HeadsArgs &a, bool pieces, cudaStream_t stream) {
   if (pieces) {
     const int lanes = a.dim / 16;
-    if (lanes <= 4) return launch_pieces<T, 4>(a, stream);
-    if (lanes <= 8) return launch_pieces<T, 8>(a, stream);
-    return launch_pieces<T, 16>(a, stream);
+    if (a.r.interleaved) {
+      if (lanes <= 4) return launch_pieces<T, 4, true>(a, stream);
+      if (lanes <= 8) return launch_pieces<T, 8, true>(a, stream);
+      return launch_pieces<T, 16, true>(a, stream);
+    }
+    if (lanes <= 4) return launch_pieces<T, 4, false>(a, stream);
+    if (lanes <= 8) return launch_pieces<T, 8, false>(a, stream);
+    return launch_pieces<T, 16, false>(a, stream);
   }
   const int64_t rows = a.tokens * (a.heads[0] + a.heads[1]);
   const int64_t blocks = (rows + kAnyWarps - 1) / kAnyWarps;
@@ -516,33 +532,47 @@ cudaError_t launch(const HeadsArgs &a, bool pieces, cudaStream_t stream) {
 }
 
 template <typename T, int W>
-cudaError_t launch_backward_pieces(const HeadsArgs &a, int blocks, cudaStream_t stream) {
-  return launch_dependent(k_heads_backward<T, W>, dim3(blocks, a.heads[1] > 0 ? 2 : 1),
-                          dim3(kThreads), kThreads * 16 * 4, stream, a);
+cudaError_t launch_backward_pieces(const HeadsArgs &a, const BackwardSplit &s, cudaStream_t stream) {
+  return a.r.interleaved ? launch_dependent(k_heads_backward<T, W, true>, dim3(s.q + s.k),
+                                            dim3(kThreads), kThreads * 16 * 4, stream, a, s)
+                         : launch_dependent(k_heads_backward<T, W, false>, dim3(s.q + s.k),
+                                            dim3(kThreads), kThreads * 16 * 4, stream, a, s);
 }
 
 template <typename T>
 cudaError_t launch_backward(const HeadsArgs &a, bool pieces, int sms, cudaStream_t stream) {
-  const int blocks = heads_blocks(sms);
-  const int lanes = a.dim / 16;
+  // Blocks in proportion to the heads of q and of k, no more than there are heads for.
+  const int lanes = a.dim / 16, width = lanes <= 4 ? 4 : lanes <= 8 ? 8 : 16;
+  const int at_once = pieces ? kThreads / width : kAnyWarps;
+  const int64_t all = heads_blocks(sms), heads = a.heads[0] + a.heads[1];
+  BackwardSplit s;
+  s.walk = 8;
+  while (pieces && s.walk > 1 && a.tokens * heads < all * at_once * s.walk) s.walk /= 2;
+  if (!pieces) s.walk = 1;
+  const auto blocks = [&](int h) {
+    const int64_t share = all * h / heads, need = (a.tokens * ((h + s.walk - 1) / s.walk) + at_once - 1) / at_once;
+    return static_cast<int>(h == 0 ? 0 : need < share ? need : share > 0 ? share : 1);
+  };
+  s.k = blocks(a.heads[1]);
+  s.q = blocks(a.heads[0]);
   cudaError_t e;
   if (!pieces)
-    e = launch_dependent(k_heads_backward_any<T>, dim3(blocks, a.heads[1] > 0 ? 2 : 1),
-                         dim3(32 * kAnyWarps), 2 * kAnyWarps * a.dim * 4, stream, a);
-  else if (lanes <= 4)
-    e = launch_backward_pieces<T, 4>(a, blocks, stream);
-  else if (lanes <= 8)
-    e = launch_backward_pieces<T, 8>(a, blocks, stream);
+    e = launch_dependent(k_heads_backward_any<T>, dim3(s.q + s.k), dim3(32 * kAnyWarps),
+                         2 * kAnyWarps * a.dim * 4, stream, a, s);
+  else if (width == 4)
+    e = launch_backward_pieces<T, 4>(a, s, stream);
+  else if (width == 8)
+    e = launch_backward_pieces<T, 8>(a, s, stream);
   else
-    e = launch_backward_pieces<T, 16>(a, blocks, stream);
+    e = launch_backward_pieces<T, 16>(a, s, stream);
   if (e != cudaSuccess || (a.dweight[0] == nullptr && a.dweight[1] == nullptr)) return e;
-  return launch_dependent(k_weight_gradient<T>, dim3((a.dim + 7) / 8, a.heads[1] > 0 ? 2 : 1),
-                          dim3(kThreads), 0, stream, a, blocks);
+  return launch_dependent(k_weight_gradient<T>, dim3((a.dim + 31) / 32, a.heads[1] > 0 ? 2 : 1),
+                          dim3(1024), 0, stream, a, s);
 }
 
 }  // namespace
 
-int heads_blocks(int sms) { return 2 * sms; }
+int heads_blocks(int sms) { return 4 * sms; }
 
 cudaError_t launch_heads(const HeadsArgs &a, int dtype, bool pieces, cudaStream_t stream) {
   switch (dtype) {

@@ -12,8 +12,8 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "pieces.cuh"
 #include "ptx.cuh"
-#include "rows.cuh"
 
 namespace idx {
 
@@ -147,8 +147,194 @@ __device__ __forceinline__ Spot spot_of(const Kv4Args &a, int t, int lane) {
   return s;
 }
 
-// A warp takes one token and ROUNDS times 32 * 8 / D of its 2 * heads rows (the keys, then the values),
-// eight elements a lane; all its rows are asked for at once, before the token's place is known.
+// The larger of two magnitudes; a NaN wins.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// The largest finite magnitude of four pairs, or NaN.
+__device__ __forceinline__ float finite_or_nan(const float2 (&v)[4]) {
+  float f[8];
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = v[j].x;
+    f[2 * j + 1] = v[j].y;
+    nan |= v[j].x != v[j].x || v[j].y != v[j].y;
+  }
+  return nan ? __int_as_float(0x7FC00000) : largest_finite(f, 0.0f);
+}
+__device__ __forceinline__ float largest_of(const float2 (&v)[4]) {
+  float m = max_nan(fabsf(v[0].x), fabsf(v[0].y));
+#pragma unroll
+  for (int j = 1; j < 4; ++j) m = max_nan(m, max_nan(fabsf(v[j].x), fabsf(v[j].y)));
+  return m;
+}
+__device__ __forceinline__ uint32_t codes_of(const float2 (&v)[4]) {
+  const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+  return e2m1x8(f);
+}
+
+// 6 v / amax, correctly rounded: the quotient's remainder times the reciprocal (within 2^-22 of it) added,
+// so that what lies halfway between two codes stays there.
+__device__ __forceinline__ float2 six_over(float2 v, float2 minus_m, float2 inv) {
+  const float2 x = __fmul2_rn(v, make_float2(6.0f, 6.0f)), q = __fmul2_rn(x, inv);
+  return __ffma2_rn(__ffma2_rn(q, minus_m, x), inv, q);
+}
+// x / 6, correctly rounded in the same way.
+__device__ __forceinline__ float sixth(float x) {
+  constexpr float k = 1.0f / 6.0f;
+  const float q = x * k;
+  return fmaf(fmaf(-q, 6.0f, x), k, q);
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Rows whose pairs lie in whole pieces and whose pieces, four lanes' together, are a key's groups of 32.  A
+// warp takes one token and ROUNDS rounds of 512 / D of its heads, the keys' first, then the values', and
+// asks for all of them before the token's place is known; the values are done before the keys, whose angles
+// come meanwhile.
+//
+// 34,000 tokens of 8 heads of 128 (176 MB) take 45 us, 26 at the copy rate: an instruction-bound and a
+// latency-bound half.  With eight elements a lane, whose partners another lane holds, and scalar arithmetic
+// 80 us; two rounds a warp 48; several tokens a warp, one after the other, the next one's rows asked for
+// ahead, 61 to 71 (fewer warps fit).
+constexpr int kPieceThreads = 128;
+template <typename T, int D, bool ADJ, int ROUNDS>
+__global__ void __launch_bounds__(kPieceThreads, ROUNDS == 1 ? 1 : 5)
+    k_kv4_append_pieces(const Kv4Args a) {
+  constexpr int W = D / 16, AT_ONCE = 32 / W;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, l = lane % W, group = lane / W;
+  const int t = blockIdx.x * (kPieceThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.m.tokens) return;
+  const int half = (a.heads + AT_ONCE - 1) / AT_ONCE;  // rounds of keys, and of values
+  const int first = blockIdx.y * ROUNDS;
+  Pieces p;
+  int pair[2];
+  place_pieces<ADJ>(a.r, D, l, p, pair);
+  Piece<T, 8> own[ROUNDS][2];
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    // (Past the last: that one again, so that no branch parts the loads.)
+    const int r = min(first + i, 2 * half - 1);
+    const bool is_k = r < half;
+    const int h = min((is_k ? r : r - half) * AT_ONCE + group, a.heads - 1);
+    const T *x = static_cast<const T *>(is_k ? a.k : a.v) + t * (is_k ? a.k_token : a.v_token) +
+                 h * (is_k ? a.k_head : a.v_head);
+    own[i][0] = load_piece<T, 8>(x + p.at[0]);
+    own[i][1] = load_piece<T, 8>(x + p.at[1]);
+  }
+  const Spot s = spot_of(a, t, lane);
+  if (s.page < 0) return;
+  uint32_t valid = 0;
+  float2 c[4], n[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = n[j] = make_float2(0.0f, 0.0f);
+  if (a.r.table != nullptr && first < half) {
+    if (s.pos < a.r.max_positions) {
+      const float2 *row = a.r.table + static_cast<int64_t>(s.pos) * (a.r.rot >> 1);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (p.on[e]) {
+          valid |= 0xFu << (4 * e);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float4 two = __ldg(reinterpret_cast<const float4 *>(row + pair[e] + 2 * j));
+            c[2 * e + j] = make_float2(two.x, two.z);
+            n[2 * e + j] = make_float2(two.y, two.w);
+          }
+        }
+    } else if (lane == 0) {
+      atomicOr(&g_kv4_status, IDX_DEV_BAD_POSITION);
+    }
+  }
+  // The row of the lane's first head in this token's place.
+  const int64_t row0 =
+      (s.page * a.heads + group) * a.block_size + (s.pos & (a.block_size - 1));
+#pragma unroll
+  for (int i = ROUNDS - 1; i >= 0; --i) {
+    const int r = first + i;
+    const bool is_k = r < half;  // (the same for the whole warp)
+    const int h0 = (is_k ? r : r - half) * AT_ONCE;
+    const bool live = h0 + group < a.heads;
+    const int64_t row = row0 + h0 * a.block_size;
+    if (r >= 2 * half) continue;
+    float2 v[2][4];
+    if (is_k) {
+      unpack<ADJ, T>(own[i], v);
+      turn(valid, c, n, v);
+      float2 u[2][4];  // the pieces' elements in order
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = v[0][2 * e + (j >> 1)], g = v[1][2 * e + (j >> 1)];
+          u[e][j] = !ADJ ? v[e][j] : j & 1 ? make_float2(f.y, g.y) : make_float2(f.x, g.x);
+        }
+      float m[2] = {largest_of(u[0]), largest_of(u[1])};
+      if (__any_sync(0xffffffffu, m[0] == kInf || m[1] == kInf))
+        m[0] = finite_or_nan(u[0]), m[1] = finite_or_nan(u[1]);
+      uint8_t *to = a.k_pool + row * (D / 2), *scale = a.k_scales + row * (D / 32);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[e] = max_nan(m[e], __shfl_xor_sync(0xffffffffu, m[e], 1));
+        m[e] = max_nan(m[e], __shfl_xor_sync(0xffffffffu, m[e], 2));
+        // (Of a NaN, whose bits are past an infinity's: 0xFF, and codes that mean nothing.)
+        const int exponent = min(key_exponent(m[e]), 127);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+        const float2 up2 = make_float2(up, up);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[e][j] = __fmul2_rn(u[e][j], up2);
+        const uint32_t codes = codes_of(u[e]);
+        if (live) {
+          *reinterpret_cast<uint32_t *>(to + p.at[e] / 2) = codes;
+          if ((lane & 3) == 0) scale[p.at[e] / 32] = m[e] != m[e] ? 255 : static_cast<uint8_t>(exponent + 127);
+        }
+      }
+    } else {
+      unpack<false, T>(own[i], v);
+      float m = max_nan(largest_of(v[0]), largest_of(v[1]));
+      const bool odd = __any_sync(0xffffffffu, m > 1.2676506002282294e30f);  // past 2^100
+      if (odd) m = max_nan(finite_or_nan(v[0]), finite_or_nan(v[1]));
+#pragma unroll
+      for (int o = 1; o < W; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const bool nan = m != m;
+      m = fmaxf(m, kLeastMax);  // (of a NaN: kLeastMax; the row's scale says what it is)
+      if (live && l == 0) a.v_scales[row] = nan ? __int_as_float(0x7FC00000) : sixth(m);
+      if (odd) {
+        // Infinities to the largest; rows past 2^100 2^64 down, so that six times them is finite.
+        const float down = m > 1.2676506002282294e30f ? 5.421010862427522e-20f : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[e][j].x = fminf(fmaxf(v[e][j].x, -m), m) * down;
+            v[e][j].y = fminf(fmaxf(v[e][j].y, -m), m) * down;
+          }
+        m *= down;
+      }
+      const float inv = reciprocal(m);
+      const float2 inv2 = make_float2(inv, inv), m2 = make_float2(-m, -m);
+      uint8_t *to = a.v_pool + row * (D / 2);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[e][j] = six_over(v[e][j], m2, inv2);
+        const uint32_t codes = codes_of(v[e]);
+        if (live) *reinterpret_cast<uint32_t *>(to + p.at[e] / 2) = codes;
+      }
+    }
+  }
+}
+
+// Any other rotated part, strides or alignment: a warp takes one token and ROUNDS times 32 * 8 / D of its
+// 2 * heads rows (the keys, then the values), eight elements a lane, the partners read from memory.
 template <typename T, int D, int ROUNDS>
 __global__ void __launch_bounds__(kThreads) k_kv4_append(const Kv4Args a, bool pieces, bool turns) {
   constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
@@ -287,9 +473,30 @@ inline dim3 grid_of(const Kv4Args &a, int rows) {
               static_cast<unsigned>((2 * a.heads + rows - 1) / rows));
 }
 
+template <typename T, int D, bool ADJ>
+cudaError_t append_pieces(const Kv4Args &a, cudaStream_t stream) {
+  constexpr int AT_ONCE = 512 / D;
+  const int rounds = 2 * ((a.heads + AT_ONCE - 1) / AT_ONCE);
+  constexpr int WARPS = kPieceThreads / 32;
+  const auto grid = [&](int each) {
+    return dim3(static_cast<unsigned>((a.m.tokens + WARPS - 1) / WARPS),
+                static_cast<unsigned>((rounds + each - 1) / each));
+  };
+  // (As with many(): a small call is one chain of latencies.)
+  return static_cast<int64_t>(a.m.tokens) * rounds > 16384
+             ? launch_dependent(k_kv4_append_pieces<T, D, ADJ, 4>, grid(4), dim3(kPieceThreads), 0, stream, a)
+             : launch_dependent(k_kv4_append_pieces<T, D, ADJ, 1>, grid(1), dim3(kPieceThreads), 0, stream, a);
+}
+
 template <typename T, int D>
 cudaError_t append(const Kv4Args &a, bool pieces, bool turns, cudaStream_t stream) {
   constexpr int AT_ONCE = 256 / D;
+  // Where four lanes' pieces are a key's groups of 32 (see place_pieces).
+  const bool adjacent = a.r.table != nullptr && a.r.interleaved;
+  if (pieces && turns &&
+      (a.r.table == nullptr || adjacent ||
+       (a.r.offset % 32 == 0 && a.r.rot % 64 == 0 && (D - a.r.rot) % 64 == 0)))
+    return adjacent ? append_pieces<T, D, true>(a, stream) : append_pieces<T, D, false>(a, stream);
   return many(a, AT_ONCE)
              ? launch_dependent(k_kv4_append<T, D, 4>, grid_of(a, 4 * AT_ONCE), dim3(kThreads), 0,
                                 stream, a, pieces, turns)

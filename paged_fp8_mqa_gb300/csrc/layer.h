@@ -144,6 +144,7 @@ struct HeadsArgs {
   void *dweight[2];       // backward, nullable
   int32_t heads[2];
   int32_t weight_f32;     // the weights are float32, whatever x is
+  int32_t weight_pieces;  // they may be read eight at a time
   int32_t norm;           // 0: only rotated
   float eps;
   const int32_t *positions;
@@ -152,7 +153,7 @@ struct HeadsArgs {
   Rotation r;  // table == nullptr: none
   Axes axes;
   float sin_sign;
-  float *workspace;       // backward: heads_blocks(...) partial sums of [dim] for each of q and k
+  float *workspace;       // backward: heads_blocks(...) + 1 partial sums of [dim]
 };
 // pieces: everything may be read eight elements at a time and pairs lie in whole pieces.
 cudaError_t launch_heads(const HeadsArgs &a, int dtype, bool pieces, cudaStream_t stream);
