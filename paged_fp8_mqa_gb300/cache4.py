@@ -35,9 +35,22 @@ def _cache(k_pool, v_pool, k_scales, v_scales, index):
     """The cache's addresses (k_pool, v_pool, k_scales, v_scales) and sizes (blocks, heads, block_size,
     D)."""
     import torch
-    for t, name, dims, dtype in ((k_pool, "k_pool", 4, torch.uint8), (v_pool, "v_pool", 4, torch.uint8),
-                                 (k_scales, "k_scales", 4, torch.uint8),
-                                 (v_scales, "v_scales", 3, torch.float32)):
+    u8 = torch.uint8
+    try:  # (the usual case at once; what is wrong with any other is said below)
+        shape = blocks, heads, block_size, half = k_pool.shape
+        if (k_pool.dtype is u8 and v_pool.dtype is u8 and k_scales.dtype is u8
+                and v_scales.dtype is torch.float32 and v_pool.shape == shape
+                and k_scales.shape == (blocks, heads, block_size, half // 16)
+                and v_scales.shape == (blocks, heads, block_size)
+                and k_pool.get_device() == v_pool.get_device() == k_scales.get_device()
+                == v_scales.get_device() == index and k_pool.is_contiguous() and v_pool.is_contiguous()
+                and k_scales.is_contiguous() and v_scales.is_contiguous()):
+            return ((k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr()),
+                    (blocks, heads, block_size, 2 * half))
+    except (AttributeError, ValueError):
+        pass
+    for t, name, dims, dtype in ((k_pool, "k_pool", 4, u8), (v_pool, "v_pool", 4, u8),
+                                 (k_scales, "k_scales", 4, u8), (v_scales, "v_scales", 3, torch.float32)):
         _tensor(t, name, dims, dtype, index)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -49,7 +62,7 @@ def _cache(k_pool, v_pool, k_scales, v_scales, index):
         raise ValueError("k_scales must be [blocks, Hkv, block_size, D / 32], v_scales [blocks, Hkv, "
                          "block_size]")
     return ((k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr()),
-            (blocks, heads, block_size, 2 * half))
+            (*rows, 2 * half))
 
 
 def kv_append_fp4(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, *,

@@ -86,12 +86,13 @@ def _like(out, x, name, index, made):
     """The result for x: ``out`` if given, else a new one; and its strides."""
     import torch
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        shape = x.shape
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
         made.append(out)
-    else:
-        _tensor(out, name, 3, x.dtype, index)
-        if out.shape != x.shape or (x.shape[2] > 1 and out.stride(2) != 1):
-            raise ValueError(f"{name} must have its input's shape and contiguous rows")
+        return out, shape[1] * shape[2], shape[2]
+    _tensor(out, name, 3, x.dtype, index)
+    if out.shape != x.shape or (x.shape[2] > 1 and out.stride(2) != 1):
+        raise ValueError(f"{name} must have its input's shape and contiguous rows")
     return out, out.stride(0), out.stride(1)
 
 
@@ -132,62 +133,67 @@ def _norm_args(q, k, q_weight, k_weight, positions, table, eps, axes, interleave
     """The arguments that the forward and the backward entry share."""
     code, (q_token, q_head, _) = _rows(q, "q", 3, index)
     T, H, D = q.shape
-    k_args, k_heads = (None, 0, 0), 0
+    k_at, k_token, k_head, k_heads = None, 0, 0, 0
     if k is not None:
         k_code, (k_token, k_head, _) = _rows(k, "k", 3, index)
-        if k_code != code or k.shape[0] != T or k.shape[2] != D:
+        k_T, k_heads, k_D = k.shape
+        if k_code != code or k_T != T or k_D != D:
             raise TypeError("q and k must have the same dtype, tokens and head_dim")
-        k_heads = k.shape[1]
-        if k_heads:
-            k_args = k.data_ptr(), k_token, k_head
+        k_at = k.data_ptr() if k_heads else None
     elif k_weight is not None:
         raise ValueError("k_weight without k")
-    qw, qw_code = _weight(q_weight, "q_weight", code, D, index)
-    kw, kw_code = _weight(k_weight, "k_weight", code, D, index)
-    if qw_code is not None and kw_code is not None and qw_code != kw_code:
-        raise TypeError("q_weight and k_weight must have the same dtype")
-    w_code = qw_code if qw_code is not None else kw_code if kw_code is not None else code
-    turn, tab = (None, 0, None, 1), (None, 0, 0)
+    if q_weight is not None and k_weight is not None and q_weight.dtype is k_weight.dtype \
+            and q_weight.shape == k_weight.shape == (D,) and q_weight.get_device() == index \
+            and k_weight.get_device() == index and q_weight.is_contiguous() and k_weight.is_contiguous() \
+            and _code(q_weight.dtype) in (code, 0):
+        qw, kw, w_code = q_weight.data_ptr(), k_weight.data_ptr(), _code(q_weight.dtype)
+    else:
+        qw, qw_code = _weight(q_weight, "q_weight", code, D, index)
+        kw, kw_code = _weight(k_weight, "k_weight", code, D, index)
+        if qw_code is not None and kw_code is not None and qw_code != kw_code:
+            raise TypeError("q_weight and k_weight must have the same dtype")
+        w_code = qw_code if qw_code is not None else kw_code if kw_code is not None else code
     if table is not None:
-        tab = _table(table, index)
-        turn = _turn(positions, axes, tab[2], T, index)
-    elif positions is not None or axes is not None:
+        tab, most, rot = _table(table, index)
+        at, axis_stride, pair_axis, count = _turn(positions, axes, rot, T, index)
+        return (q.data_ptr(), q_token, q_head, H, k_at, k_token, k_head, k_heads, code, T, D, qw, kw,
+                w_code, eps, at, axis_stride, pair_axis, count, tab, most, rot, rot_offset, interleaved)
+    if positions is not None or axes is not None:
         raise ValueError("positions and axes need a table")
-    return (q.data_ptr(), q_token, q_head, H, *k_args, k_heads, code, T, D, qw, kw, w_code, eps,
-            *turn, *tab, rot_offset, interleaved)
+    return (q.data_ptr(), q_token, q_head, H, k_at, k_token, k_head, k_heads, code, T, D, qw, kw, w_code,
+            eps, None, 0, None, 1, None, 0, 0, rot_offset, interleaved)
 
 
-def _forward(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset, q_out,
-             k_out, stream):
-    index = _index(q, "q")
-    args = _norm_args(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset,
-                      index)
+def _forward(index, args, q, k, q_out, k_out, stream):
+    """The call with the arguments that _norm_args made."""
     made = []
     q_to, q_token, q_head = _like(q_out, q, "q_out", index, made)
-    k_to, k_args = None, (None, 0, 0)
+    k_to, k_at, k_token, k_head = None, None, 0, 0
     if k is not None:
         k_to, k_token, k_head = _like(k_out, k, "k_out", index, made)
-        if k.shape[1]:
-            k_args = k_to.data_ptr(), k_token, k_head
-    T, H, D = q.shape
-    if T and D and H + (0 if k is None else k.shape[1]):
+        k_at = k_to.data_ptr() if args[7] else None
+    if args[9] and args[10] and args[3] + args[7]:
         # (Without query heads there is nothing at q: any address will do.)
-        q_at = q_to.data_ptr() if H else k_args[0]
-        _check(idx_norm_rotary(*(args if H else (k_args[0], *args[1:])), q_at, q_token, q_head, *k_args,
+        q_at = q_to.data_ptr() if args[3] else k_at
+        if not args[3]:
+            args = (k_at, *args[1:])
+        _check(idx_norm_rotary(*args, q_at, q_token, q_head, k_at, k_token, k_head,
                                _on(stream, index, *made)))
     return q_to, k_to
 
 
 def _backward(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset, q_grad,
-              k_grad):
-    """(dq, dk, dq_weight, dk_weight) from the outputs' gradients."""
+              k_grad, args=None):
+    """(dq, dk, dq_weight, dk_weight) from the outputs' gradients.  args: those of the forward call, if
+    the tensors are still the ones that it had."""
     import torch
     index = _index(q, "q")
     if index != torch.cuda.current_device():
         return _elsewhere(index, _backward, q, k, q_weight, k_weight, positions, table, eps, axes,
-                          interleaved, rot_offset, q_grad, k_grad)
-    args = _norm_args(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset,
-                      index)
+                          interleaved, rot_offset, q_grad, k_grad, args)
+    if args is None or args[0] != q.data_ptr():
+        args = _norm_args(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset,
+                          index)
 
     def rows(g, x):
         if g.dtype != x.dtype:
@@ -196,27 +202,35 @@ def _backward(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved
             g = g.contiguous()
         return g
 
-    T, H, D = q.shape
-    dq = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    empty, dtype, device = torch.empty, q.dtype, q.device
+    T, D = args[9], args[10]
+    dq = empty(q.shape, dtype=dtype, device=device)
+    dk = None if k is None else empty(k.shape, dtype=dtype, device=device)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
-    dk = dkw = None
-    k_args, dk_at = (None, 0, 0), None
-    if k is not None:
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        dkw = None if k_weight is None else torch.empty_like(k_weight)
-        k_grad = rows(k_grad, k)
-        k_args = k_grad.data_ptr(), k_grad.stride(0), k_grad.stride(1)
-        dk_at = dk.data_ptr()
+    dkw = None if k_weight is None else torch.empty_like(k_weight)
     if not T:  # (sums over nothing)
         return dq, dk, *(None if w is None else w.zero_() for w in (dqw, dkw))
     q_grad = rows(q_grad, q)
-    need = idx_norm_rotary_workspace_bytes(D)
-    workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    qg_token, qg_head, _ = q_grad.stride()
+    kg, kg_token, kg_head, dk_at = None, 0, 0, None
+    if k is not None:
+        k_grad = rows(k_grad, k)
+        kg_token, kg_head, _ = k_grad.stride()
+        kg, dk_at = k_grad.data_ptr(), dk.data_ptr()
+    need = _workspaces.get((index, D))
+    if need is None:
+        need = idx_norm_rotary_workspace_bytes(D)
+        if need > 0:
+            _workspaces[index, D] = need
+    workspace = empty(max(need, 1), dtype=torch.uint8, device=device)
     _check(idx_norm_rotary_backward(
-        *args, q_grad.data_ptr(), q_grad.stride(0), q_grad.stride(1), *k_args, dq.data_ptr(), dk_at,
+        *args, q_grad.data_ptr(), qg_token, qg_head, kg, kg_token, kg_head, dq.data_ptr(), dk_at,
         None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
         workspace.data_ptr(), need, _on(None, index)))
     return dq, dk, dqw, dkw
+
+
+_workspaces: dict = {}  # sizes, by device and head_dim
 
 
 @functools.cache
@@ -229,15 +243,24 @@ def _recorded():
         @staticmethod
         def forward(ctx, q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset,
                     stream):
+            index = q.get_device()
+            args = _norm_args(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved,
+                              rot_offset, index)
             ctx.save_for_backward(q, k, q_weight, k_weight, positions, table)
             ctx.how = eps, axes, interleaved, rot_offset
-            return _forward(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved,
-                            rot_offset, None, None, stream)
+            ctx.args = args
+            return _forward(index, args, q, k, None, None, stream)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, q_grad, k_grad):
-            return (*_backward(*ctx.saved_tensors, *ctx.how, q_grad, k_grad), *[None] * 7)
+            saved = ctx.saved_tensors
+            # (Hooks on what is saved may have put other tensors in their place.)
+            a = ctx.args
+            at = [None if t is None else t.data_ptr() for t in saved]
+            same = at == [a[0], a[4], a[11], a[12], a[15], a[19]] and saved[0].stride()[:2] == a[1:3] \
+                and (saved[1] is None or saved[1].stride()[:2] == a[5:7])
+            return (*_backward(*saved, *ctx.how, q_grad, k_grad, a if same else None), *[None] * 7)
 
     return NormRotary.apply
 
@@ -258,8 +281,9 @@ def norm_rotary(q, k, q_weight=None, k_weight=None, positions=None, table=None, 
     cannot be differentiated again."""
     import torch
     index = _index(q, "q")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (q, k, q_weight, k_weight)):
+    if (q.requires_grad or (k is not None and k.requires_grad)
+            or (q_weight is not None and q_weight.requires_grad)
+            or (k_weight is not None and k_weight.requires_grad)) and torch.is_grad_enabled():
         if q_out is not None or k_out is not None:
             raise ValueError("q_out and k_out cannot be given where a gradient is required")
         if not all(t is None or (t.dim() == 3 and t.shape[1] and t.shape[2]) for t in (q, k)):
@@ -273,5 +297,5 @@ def norm_rotary(q, k, q_weight=None, k_weight=None, positions=None, table=None, 
         return _elsewhere(index, norm_rotary, q, k, q_weight, k_weight, positions, table, eps=eps,
                           axes=axes, interleaved=interleaved, rot_offset=rot_offset, q_out=q_out,
                           k_out=k_out, stream=stream)
-    return _forward(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset,
-                    q_out, k_out, stream)
+    args = _norm_args(q, k, q_weight, k_weight, positions, table, eps, axes, interleaved, rot_offset, index)
+    return _forward(index, args, q, k, q_out, k_out, stream)
