@@ -98,9 +98,10 @@ struct AttnCfg {
   // they have buffers of their own.  (FP4: always, see below.)
   static constexpr bool OVER_K = !FP4 && P_BYTES <= kTile * D;
   static constexpr int P_BUFS = OVER_K ? 0 : !FP4 || R == 64 ? 2 : 1;
-  // What a stage of K (its scale factors, FP4) and of V (its Token records) holds besides.
+  // What a stage of K (its scale factors, FP4) and of V holds besides: Token records, or (FP4, by the
+  // TMA unit) value scales, scale factors and which of the tokens are there.
   static constexpr int K_AUX = FP4 ? kTile * 4 : 0;
-  static constexpr int V_AUX = kTile * (FP4 ? 8 : 16);
+  static constexpr int V_AUX = FP4 ? kTile * 8 + (COPIES ? 0 : 16) : kTile * 16;
   static constexpr int MISC = 48 * R + (FP4 ? 0 : 3 * D * 4) + 256;
   static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_BYTES + MISC;
   static constexpr int ROOM = CTAS == 2 ? 115456 : 231424;
@@ -112,7 +113,7 @@ struct AttnCfg {
   // for half the bytes, so that stages are what bounds the loads in flight: a key's is given back as soon
   // as its scores are there, long before its values' is.
   static constexpr int VS8 = LEFT / (2 * T_BYTES + V_AUX);
-  static constexpr int KS = !FP4 ? (VS8 > 6 ? 6 : VS8) : COPIES && D == 128 && R != 64 ? 1 : R == 64 && !COPIES ? 3 : 2;
+  static constexpr int KS = !FP4 ? (VS8 > 6 ? 6 : VS8) : COPIES && D == 128 && R != 64 && R != 8 ? 1 : R == 64 && !COPIES ? 3 : 2;
   static constexpr int K_ROOM = KS * (T_BYTES + K_AUX);
   static constexpr int VS4 = COPIES ? 2 : (LEFT - K_ROOM) / (T_BYTES + V_AUX);
   static constexpr int VS = !FP4 ? KS : VS4 > 6 ? 6 : VS4;
@@ -427,6 +428,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   at += C::RAW * (C::RAW_BYTES - kTile * D);
   Token *s_tok = reinterpret_cast<Token *>(at);      // [stage of V][kTile]
   Token4 *s_tok4 = reinterpret_cast<Token4 *>(at);
+  uint32_t *s_aux = reinterpret_cast<uint32_t *>(at);
   at += C::VS * C::V_AUX;
   uint32_t *s_sf = reinterpret_cast<uint32_t *>(at);  // [stage of K][32][4]: token t's at [t % 32][t / 32]
   at += C::KS * C::K_AUX;
@@ -461,13 +463,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       prefetch_tensor_map(&v_map);
     }
     for (int i = 0; i < C::KS; ++i) {
-      // A loading lane's arrival, and (SELECT in 8 bits) one when its own copies have landed.
-      mbar_init(&k_full[i], (C::SELECT && !C::FP4 ? 64 : 32) * C::LOADERS);
+      // A loading lane's arrival, and one when its own copies have landed, where they go straight to
+      // the stage (of a selection in 8 bits, of the scales in 4).
+      mbar_init(&k_full[i], C::COPIES == C::FP4 ? 32 * C::LOADERS : 64 * C::LOADERS);
       mbar_init(&k_empty[i], 1);
     }
     if constexpr (C::FP4)
       for (int i = 0; i < C::VS; ++i) {
-        mbar_init(&v_full[i], 32 * C::LOADERS);
+        mbar_init(&v_full[i], C::COPIES ? 32 * C::LOADERS : 64);
         mbar_init(&v_empty[i], 1);
       }
     mbar_init(&s_full[0], 1);
@@ -619,8 +622,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
         if (bad) attn_flag(IDX_DEV_BAD_PAGE);
       };
-      // (FP4: a token's own, the keys' a word of scale factors.)
-      using KeyScale = std::conditional_t<C::FP4, uint32_t, float>;
       if constexpr (C::FP4) {
         // 16 bytes a lane and copy, as they lie in the pool, RAW tiles ahead; each lane spreads what it
         // asked for itself, 16 elements to the lower half of 16 bytes, with the swizzle that the products
@@ -629,11 +630,35 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         constexpr int kLanes = D / 32, kRows = 32 / kLanes;
         const int piece = lane % kLanes, sub = lane / kLanes;
         Ring<C::RAW> in, out;
-        int row0[EACH], row1[EACH], pos0[EACH], pos1[EACH];
-        const auto rows = [&](int (&row)[EACH], int (&pos)[EACH]) {
-          pool_rows(row);
+        int row0[EACH], pos0[EACH];
+        // Each read of the chain position -> page has a tile's time to come back.
+        Ahead mid{};                 // a tile whose pages are being read
+        int id_mid[EACH];
+        const auto pages = [&]() {   // of far's tile
+          mid = far;
 #pragma unroll
-          for (int j = 0; j < EACH; ++j) pos[j] = row[j] < 0 ? kNone : C::SELECT ? 0 : far.pos[j];
+          for (int j = 0; j < EACH; ++j) {
+            const int blk = mid.pos[j] >> shift;
+            const bool seen = mid.live && mid.pos[j] >= 0 && mid.pos[j] < mid.extent;
+            if (!seen) mid.pos[j] = -1;
+            id_mid[j] = seen && blk < a.bt_width ? __ldg(mid.table + blk) : -1;
+          }
+        };
+        const auto rows = [&](int (&row)[EACH], int (&pos)[EACH]) {  // of mid's tile
+          bool bad = false;
+#pragma unroll
+          for (int j = 0; j < EACH; ++j) {
+            row[j] = -1;
+            pos[j] = kNone;
+            if (mid.pos[j] < 0) continue;
+            if (id_mid[j] >= 0 && id_mid[j] < a.num_blocks) {
+              row[j] = ((id_mid[j] * a.kv_heads + mid.g) << shift) + (mid.pos[j] & (a.block_size - 1));
+              pos[j] = C::SELECT ? 0 : mid.pos[j];
+            } else {
+              bad = true;
+            }
+          }
+          if (bad) attn_flag(IDX_DEV_BAD_PAGE);
         };
         const auto issue = [&]() {
           uint8_t *raw = s_raw_kv + in.at * (kTile * D) + piece * 16;
@@ -703,24 +728,22 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           return true;
         };
         positions();
-        bool live0 = far.live;
+        pages();
+        if (far.live) positions();
+        bool live0 = mid.live;
         rows(row0, pos0);
-        if (live0) positions();
+        pages();
+        if (far.live) positions();
         int ahead = 0;  // tiles asked for and not handed over
         bool ending = false;
         while (live0 || ahead > 0) {
           if (live0) {
             issue();
             ++ahead;
-            rows(row1, pos1);
-            const bool live1 = far.live;
-            if (live1) positions();
-#pragma unroll
-            for (int j = 0; j < EACH; ++j) {
-              row0[j] = row1[j];
-              pos0[j] = pos1[j];
-            }
-            live0 = live1;
+            live0 = mid.live;
+            rows(row0, pos0);
+            pages();
+            if (far.live) positions();
           }
           // A group a round, empty ones too, so that RAW - 1 groups follow the oldest of the tiles ahead
           // when it is waited for.
@@ -802,8 +825,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       while (ok && w.next(a, groups, keys)) {
         const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
         const int32_t *table = a.block_tables + m.b * a.bt_stride;
-        // A lane reads one page's id, 32 pages ahead of the ones in hand, and looks after four tokens
-        // of a tile, whose scales it reads one tile ahead.
+        // A lane reads one page's id, 32 pages ahead of the ones in hand.  All else of a tile is copied
+        // without passing through a register (a tile's scales, read one tile ahead, held the loader up
+        // for a memory round trip at every tile: decode 228 us).
         const int n_pages = (w.length + a.block_size - 1) >> shift;
         const int per_tile = kTile >> shift;
         int first = w.seg_tile * per_tile;  // the page of lane 0
@@ -815,70 +839,55 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           return -1;
         };
         int id = ids(first + lane), id_next = ids(first + 32 + lane);
-        // The pool's row of this lane's first token in tile i (one of the 64 pages in hand), or -1.
-        const auto row_of = [&](int i) {
-          const int p = i * kTile + lane * 4;
-          const int block =
-              __shfl_sync(0xffffffffu, i * per_tile < first + 32 ? id : id_next, (p >> shift) - first);
-          return block < 0 ? -1 : ((block * a.kv_heads + m.g) << shift) + (p & (a.block_size - 1));
-        };
-        const auto scales = [&](int row, uint32_t (&ks)[4], float4 &vs) {
-          vs = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          ks[0] = ks[1] = ks[2] = ks[3] = 0u;
-          if (row < 0) return;
-          vs = __ldg(reinterpret_cast<const float4 *>(a.v_scales + row));
-          const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a.k_scales) + row / 4);
-          ks[0] = u.x, ks[1] = u.y, ks[2] = u.z, ks[3] = u.w;
-        };
-        int row = row_of(w.seg_tile), row_next = -1;
-        uint32_t ks[4], ks_next[4];
-        float4 vs, vs_next;
-        scales(row, ks, vs);
         const int end = w.seg_tile + w.seg_tiles;
         for (int i = w.seg_tile; i < end; ++i) {
-          if (i + 1 < end) row_next = row_of(i + 1);
-          else row_next = -1;
-          scales(row_next, ks_next, vs_next);
-          const int p = i * kTile + lane * 4;
-          const bool page = row >= 0 && (p & (a.block_size - 1)) == 0;  // (this lane's first token begins one)
-          if (!stage_free()) break;
-          if (page) {
-            // (The barrier counts the bytes read, half of those that the rows take here.)
-            mbar_expect_tx(&k_full[kr.at], D / 2 * a.block_size);
-            tma_load_2d(k_tile(kr.at) + lane * 4 * D, &k_map, &k_full[kr.at], 0, row, policy);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int t = lane * 4 + j;
-            s_sf[(kr.at * 32 + t % 32) * 4 + t / 32] = ks[j];
-          }
-          fence_proxy_async_shared();
-          mbar_arrive(&k_full[kr.at]);
-          next_stage();
-          if (!free_now(&v_empty[vr.at], vr.phase)) break;
-          if (page) {
-            mbar_expect_tx(&v_full[vr.at], D / 2 * a.block_size);
-            tma_load_2d(v_tile(vr.at) + lane * 4 * D, &v_map, &v_full[vr.at], 0, row, policy);
-          }
-          const float v4[4] = {vs.x, vs.y, vs.z, vs.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            s_tok4[vr.at * kTile + lane * 4 + j] = Token4{
-                scale_of<D>(ks[j], v4[j]), row >= 0 && p + j < w.length ? p + j : kNone};
-          mbar_arrive(&v_full[vr.at]);
-          ++issued_v;
-          vr.advance();
-          row = row_next;
-          vs = vs_next;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) ks[j] = ks_next[j];
-          if ((i + 1) * per_tile >= first + 32) {
+          if (i * per_tile >= first + 32) {
             first += 32;
             id = id_next;
             id_next = ids(first + 32 + lane);
           }
+          // The pool's row of token t of the tile, or -1.
+          const auto row_of = [&](int t) {
+            const int block = __shfl_sync(0xffffffffu, id, i * per_tile + (t >> shift) - first);
+            return block < 0 ? -1 : ((block * a.kv_heads + m.g) << shift) + (t & (a.block_size - 1));
+          };
+          const int row4 = row_of(lane * 4);  // of four tokens
+          const bool page = row4 >= 0 && ((lane * 4) & (a.block_size - 1)) == 0;  // (they begin one)
+          if (!stage_free()) break;
+          if (page) {
+            // (The barrier counts the bytes read, half of those that the rows take here.)
+            mbar_expect_tx(&k_full[kr.at], D / 2 * a.block_size);
+            tma_load_2d(k_tile(kr.at) + lane * 4 * D, &k_map, &k_full[kr.at], 0, row4, policy);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = row_of(32 * j + lane);
+            if (row >= 0)
+              cp_async_4(s_sf + (kr.at * 32 + lane) * 4 + j,
+                         static_cast<const uint32_t *>(a.k_scales) + row);
+          }
+          cp_async_arrive_noinc(&k_full[kr.at]);
+          mbar_arrive(&k_full[kr.at]);
+          next_stage();
+          if (!free_now(&v_empty[vr.at], vr.phase)) break;
+          uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
+          if (page) {
+            mbar_expect_tx(&v_full[vr.at], D / 2 * a.block_size);
+            tma_load_2d(v_tile(vr.at) + lane * 4 * D, &v_map, &v_full[vr.at], 0, row4, policy);
+          }
+          if (row4 >= 0) {
+            cp_async_16(aux + lane * 4, a.v_scales + row4, policy);
+            cp_async_16(aux + kTile + lane * 4, static_cast<const uint32_t *>(a.k_scales) + row4, policy);
+          }
+          const unsigned there = __ballot_sync(0xffffffffu, row4 >= 0);
+          if (lane == 0) aux[2 * kTile] = there;  // (bit t / 4: token t's page is there)
+          cp_async_arrive_noinc(&v_full[vr.at]);
+          mbar_arrive(&v_full[vr.at]);
+          ++issued_v;
+          vr.advance();
         }
       }
+      cp_async_wait_all();
     } else {
       while (ok && w.next(a, groups, keys)) {
         const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
@@ -951,9 +960,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
     const uint32_t o_tmem = tmem + 2 * NS;
     uint32_t tile = 0, seg = 0;
+    const bool leader = elect_one();
+    const auto all_wait = [&](uint64_t *bar, uint32_t parity, uint64_t limit) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit)) != 0;
+    };
     const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
       const uint64_t k_desc = smem_desc_rows<D>(smem_addr(k_tile(st)));
       const uint32_t factors = tmem + C::SFA + (n & 1) * 4;
+      if (!leader) return;
       if constexpr (C::FP4) tmem_copy_factors(factors, smem_desc_factors(smem_addr(s_sf + st * kTile)));
 #pragma unroll
       for (int part = 0; part < C::PASSES; ++part)
@@ -974,47 +988,49 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       if constexpr (C::COPIES || C::FP4) fence_proxy_async_shared();
       tc_fence_after_sync();
     };
-    // One thread's work: the segment's products; false if a wait gave up.
+    // The segment's products; false if a wait gave up.  The whole warp walks through it, so that the
+    // descriptors are the warp's and not one thread's; one thread issues.
     const auto segment = [&]() {
-      if (!mbar_wait(q_full, seg & 1, kWaitNs)) return false;
+      if (!all_wait(q_full, seg & 1, kWaitNs)) return false;
       tc_fence_after_sync();
       bool ahead = false;  // S of the tile has been issued already
       for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
         if (!ahead) {
-          if (!mbar_wait(&k_full[kr.at], kr.phase, kWaitNs)) return false;
+          if (!all_wait(&k_full[kr.at], kr.phase, kWaitNs)) return false;
           keys_here();
           scores(tile, kr.at);
         }
         // The next tile's scores, if its keys are here, before this tile's weights are.
         Ring<C::KS> next = kr;
         next.advance();
-        ahead = i + 1 < w.seg_tiles && mbar_try_wait(&k_full[next.at], next.phase);
+        ahead = i + 1 < w.seg_tiles && __all_sync(0xffffffffu, mbar_try_wait(&k_full[next.at], next.phase));
         if (ahead) {
           keys_here();
           scores(tile + 1, next.at);
         }
-        if (!mbar_wait(&p_full[tile & 1], (tile >> 1) & 1, kWaitNs)) return false;
-        if (C::FP4 && !mbar_wait(&v_full[vr.at], vr.phase, kWaitNs)) return false;
+        if (!all_wait(&p_full[tile & 1], (tile >> 1) & 1, kWaitNs)) return false;
+        if (C::FP4 && !all_wait(&v_full[vr.at], vr.phase, kWaitNs)) return false;
         if constexpr (C::FP4 && C::COPIES) fence_proxy_async_shared();
         tc_fence_after_sync();
         const uint64_t v_desc = smem_desc_mn<D>(smem_addr(v_tile(C::FP4 ? vr.at : kr.at)));
         const uint64_t p_desc = smem_desc_p(smem_addr(weights_of(tile, kr.at)));
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < kTile / 32; ++k)
-          mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o, i + k > 0);
-        mma_commit(&pv_done[tile & 1]);
-        mma_commit(C::FP4 ? &v_empty[vr.at] : &k_empty[kr.at]);
+          for (int k = 0; k < kTile / 32; ++k)
+            mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o, i + k > 0);
+          mma_commit(&pv_done[tile & 1]);
+          mma_commit(C::FP4 ? &v_empty[vr.at] : &k_empty[kr.at]);
+        }
         kr = next;
         vr.advance();
       }
       return true;
     };
     while (ok && w.next(a, groups, keys)) {
-      if (lane == 0) ok = segment();
-      ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
+      ok = segment();
       ++seg;
     }
-    if (lane == 0) mma_commit(drain);
+    if (leader) mma_commit(drain);
     __syncwarp();
   } else {
     // ============================== softmax =====================================================
@@ -1139,7 +1155,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         tc_fence_after_sync();
         Token tok;
         if constexpr (C::FP4) {
-          const Token4 t4 = s_tok4[vr.at * kTile + token];
+          Token4 t4;
+          if constexpr (C::COPIES) {
+            t4 = s_tok4[vr.at * kTile + token];
+          } else {
+            const uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
+            const int p = (w.seg_tile + i) * kTile + token;
+            t4.v_scale = scale_of<D>(aux[kTile + token], __uint_as_float(aux[token]));
+            t4.pos = ((aux[2 * kTile] >> (token / 4)) & 1u) != 0 && p < len ? p : kNone;
+          }
           tok = token_of(z_unit, t4.v_scale, t4.pos);
         } else {
           tok = s_tok[kr.at * kTile + token];
