@@ -113,7 +113,7 @@ struct AttnCfg {
   // for half the bytes, so that stages are what bounds the loads in flight: a key's is given back as soon
   // as its scores are there, long before its values' is.
   static constexpr int VS8 = LEFT / (2 * T_BYTES + V_AUX);
-  static constexpr int KS = !FP4 ? (VS8 > 6 ? 6 : VS8) : COPIES && D == 128 && R != 64 && R != 8 ? 1 : R == 64 && !COPIES ? 3 : 2;
+  static constexpr int KS = !FP4 ? (VS8 > 6 ? 6 : VS8) : COPIES && D == 128 && R != 64 ? 1 : R == 64 && !COPIES ? 3 : 2;
   static constexpr int K_ROOM = KS * (T_BYTES + K_AUX);
   static constexpr int VS4 = COPIES ? 2 : (LEFT - K_ROOM) / (T_BYTES + V_AUX);
   static constexpr int VS = !FP4 ? KS : VS4 > 6 ? 6 : VS4;
@@ -846,40 +846,43 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             id = id_next;
             id_next = ids(first + 32 + lane);
           }
-          // The pool's row of token t of the tile, or -1.
-          const auto row_of = [&](int t) {
+          // The pool's row of the first token of the page that holds token t of the tile, or -1.
+          const auto page_of = [&](int t) {
             const int block = __shfl_sync(0xffffffffu, id, i * per_tile + (t >> shift) - first);
-            return block < 0 ? -1 : ((block * a.kv_heads + m.g) << shift) + (t & (a.block_size - 1));
+            return block < 0 ? -1 : (block * a.kv_heads + m.g) << shift;
           };
-          const int row4 = row_of(lane * 4);  // of four tokens
-          const bool page = row4 >= 0 && ((lane * 4) & (a.block_size - 1)) == 0;  // (they begin one)
+          const int in_page = (lane * 4) & (a.block_size - 1);
+          const int page4 = page_of(lane * 4);  // of four tokens
+          const bool begins = page4 >= 0 && in_page == 0;
           if (!stage_free()) break;
-          if (page) {
+          if (begins) {
             // (The barrier counts the bytes read, half of those that the rows take here.)
             mbar_expect_tx(&k_full[kr.at], D / 2 * a.block_size);
-            tma_load_2d(k_tile(kr.at) + lane * 4 * D, &k_map, &k_full[kr.at], 0, row4, policy);
+            tma_load_2d(k_tile(kr.at) + lane * 4 * D, &k_map, &k_full[kr.at], 0, page4, policy);
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int row = row_of(32 * j + lane);
-            if (row >= 0)
+            const int page = page_of(32 * j);
+            if (page >= 0)
               cp_async_4(s_sf + (kr.at * 32 + lane) * 4 + j,
-                         static_cast<const uint32_t *>(a.k_scales) + row);
+                         static_cast<const uint32_t *>(a.k_scales) + page +
+                             ((32 * j) & (a.block_size - 1)) + lane);
           }
           cp_async_arrive_noinc(&k_full[kr.at]);
           mbar_arrive(&k_full[kr.at]);
           next_stage();
           if (!free_now(&v_empty[vr.at], vr.phase)) break;
           uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
-          if (page) {
+          if (begins) {
             mbar_expect_tx(&v_full[vr.at], D / 2 * a.block_size);
-            tma_load_2d(v_tile(vr.at) + lane * 4 * D, &v_map, &v_full[vr.at], 0, row4, policy);
+            tma_load_2d(v_tile(vr.at) + lane * 4 * D, &v_map, &v_full[vr.at], 0, page4, policy);
           }
-          if (row4 >= 0) {
-            cp_async_16(aux + lane * 4, a.v_scales + row4, policy);
-            cp_async_16(aux + kTile + lane * 4, static_cast<const uint32_t *>(a.k_scales) + row4, policy);
+          if (page4 >= 0) {
+            cp_async_16(aux + lane * 4, a.v_scales + page4 + in_page, policy);
+            cp_async_16(aux + kTile + lane * 4,
+                        static_cast<const uint32_t *>(a.k_scales) + page4 + in_page, policy);
           }
-          const unsigned there = __ballot_sync(0xffffffffu, row4 >= 0);
+          const unsigned there = __ballot_sync(0xffffffffu, page4 >= 0);
           if (lane == 0) aux[2 * kTile] = there;  // (bit t / 4: token t's page is there)
           cp_async_arrive_noinc(&v_full[vr.at]);
           mbar_arrive(&v_full[vr.at]);
