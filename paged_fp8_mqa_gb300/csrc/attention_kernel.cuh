@@ -98,9 +98,10 @@ struct AttnCfg {
   // they have buffers of their own.  (FP4: always, see below.)
   static constexpr bool OVER_K = !FP4 && P_BYTES <= kTile * D;
   static constexpr int P_BUFS = OVER_K ? 0 : !FP4 || R == 64 ? 2 : 1;
-  // What a stage of K (its scale factors, FP4) and of V holds besides: Token records, or (FP4, by the
-  // TMA unit) value scales, scale factors and which of the tokens are there.
-  static constexpr int K_AUX = FP4 ? kTile * 4 : 0;
+  // What a stage of K (FP4: its scale factors, where they are used and, by the TMA unit, as they came)
+  // and of V holds besides: Token records, or (FP4, by the TMA unit) value scales, scale factors and
+  // which of the tokens are there.
+  static constexpr int K_AUX = !FP4 ? 0 : COPIES ? kTile * 4 : kTile * 8;
   static constexpr int V_AUX = FP4 ? kTile * 8 + (COPIES ? 0 : 16) : kTile * 16;
   static constexpr int MISC = 48 * R + (FP4 ? 0 : 3 * D * 4) + 256;
   static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_BYTES + MISC;
@@ -430,7 +431,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   Token4 *s_tok4 = reinterpret_cast<Token4 *>(at);
   uint32_t *s_aux = reinterpret_cast<uint32_t *>(at);
   at += C::VS * C::V_AUX;
-  uint32_t *s_sf = reinterpret_cast<uint32_t *>(at);  // [stage of K][32][4]: token t's at [t % 32][t / 32]
+  // [stage of K][32][4]: token t's at [t % 32][t / 32]; by the TMA unit each followed by [kTile].
+  uint32_t *s_sf = reinterpret_cast<uint32_t *>(at);
   at += C::KS * C::K_AUX;
   float *s_max = reinterpret_cast<float *>(at);      // [R][4 warps]
   at += R * 16;
@@ -463,14 +465,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       prefetch_tensor_map(&v_map);
     }
     for (int i = 0; i < C::KS; ++i) {
-      // A loading lane's arrival, and one when its own copies have landed, where they go straight to
-      // the stage (of a selection in 8 bits, of the scales in 4).
-      mbar_init(&k_full[i], C::COPIES == C::FP4 ? 32 * C::LOADERS : 64 * C::LOADERS);
+      // A loading lane's arrival, and (SELECT) one when its own copies have landed; with FP4 one for each
+      // loading warp (thirty-two of a warp, one after the other on one word, are what takes time).
+      mbar_init(&k_full[i], C::FP4 ? C::LOADERS : (C::SELECT ? 64 : 32) * C::LOADERS);
       mbar_init(&k_empty[i], 1);
     }
     if constexpr (C::FP4)
       for (int i = 0; i < C::VS; ++i) {
-        mbar_init(&v_full[i], C::COPIES ? 32 * C::LOADERS : 64);
+        mbar_init(&v_full[i], C::LOADERS);
         mbar_init(&v_empty[i], 1);
       }
     mbar_init(&s_full[0], 1);
@@ -712,7 +714,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             s_sf[(kr.at * 32 + t % 32) * 4 + t / 32] = aux[q].x;
           }
           fence_proxy_async_shared();
-          mbar_arrive(&k_full[kr.at]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[kr.at]);
           next_stage();
           if (!free_now(&v_empty[vr.at], vr.phase)) return false;
           spread(v_tile(vr.at), 1);
@@ -721,7 +724,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             s_tok4[vr.at * kTile + token0 + 32 * q] =
                 Token4{scale_of<D>(aux[q].x, __uint_as_float(aux[q].y)), static_cast<int>(aux[q].z)};
           fence_proxy_async_shared();
-          mbar_arrive(&v_full[vr.at]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_full[vr.at]);
           ++issued_v;
           vr.advance();
           out.advance();
@@ -826,8 +830,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
         const int32_t *table = a.block_tables + m.b * a.bt_stride;
         // A lane reads one page's id, 32 pages ahead of the ones in hand.  All else of a tile is copied
-        // without passing through a register (a tile's scales, read one tile ahead, held the loader up
-        // for a memory round trip at every tile: decode 228 us).
+        // by the lanes that begin a page, in bulk: the loader's instructions are what paces the tiles.
         const int n_pages = (w.length + a.block_size - 1) >> shift;
         const int per_tile = kTile >> shift;
         int first = w.seg_tile * per_tile;  // the page of lane 0
@@ -846,51 +849,40 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             id = id_next;
             id_next = ids(first + 32 + lane);
           }
-          // The pool's row of the first token of the page that holds token t of the tile, or -1.
-          const auto page_of = [&](int t) {
-            const int block = __shfl_sync(0xffffffffu, id, i * per_tile + (t >> shift) - first);
-            return block < 0 ? -1 : (block * a.kv_heads + m.g) << shift;
-          };
-          const int in_page = (lane * 4) & (a.block_size - 1);
-          const int page4 = page_of(lane * 4);  // of four tokens
-          const bool begins = page4 >= 0 && in_page == 0;
+          // The pool's row of the first token of the page that holds this lane's four tokens, or -1.
+          const int block = __shfl_sync(0xffffffffu, id, i * per_tile + ((lane * 4) >> shift) - first);
+          const int page4 = block < 0 ? -1 : (block * a.kv_heads + m.g) << shift;
+          const bool begins = page4 >= 0 && ((lane * 4) & (a.block_size - 1)) == 0;
+          const int bytes = D / 2 * a.block_size, words = 4 * a.block_size;
           if (!stage_free()) break;
           if (begins) {
             // (The barrier counts the bytes read, half of those that the rows take here.)
-            mbar_expect_tx(&k_full[kr.at], D / 2 * a.block_size);
+            mbar_expect_tx(&k_full[kr.at], bytes + words);
             tma_load_2d(k_tile(kr.at) + lane * 4 * D, &k_map, &k_full[kr.at], 0, page4, policy);
+            bulk_load(s_sf + (kr.at * 2 + 1) * kTile + lane * 4,
+                      static_cast<const uint32_t *>(a.k_scales) + page4, words, &k_full[kr.at], policy);
           }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int page = page_of(32 * j);
-            if (page >= 0)
-              cp_async_4(s_sf + (kr.at * 32 + lane) * 4 + j,
-                         static_cast<const uint32_t *>(a.k_scales) + page +
-                             ((32 * j) & (a.block_size - 1)) + lane);
-          }
-          cp_async_arrive_noinc(&k_full[kr.at]);
-          mbar_arrive(&k_full[kr.at]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[kr.at]);
           next_stage();
           if (!free_now(&v_empty[vr.at], vr.phase)) break;
           uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
           if (begins) {
-            mbar_expect_tx(&v_full[vr.at], D / 2 * a.block_size);
+            mbar_expect_tx(&v_full[vr.at], bytes + 2 * words);
             tma_load_2d(v_tile(vr.at) + lane * 4 * D, &v_map, &v_full[vr.at], 0, page4, policy);
-          }
-          if (page4 >= 0) {
-            cp_async_16(aux + lane * 4, a.v_scales + page4 + in_page, policy);
-            cp_async_16(aux + kTile + lane * 4,
-                        static_cast<const uint32_t *>(a.k_scales) + page4 + in_page, policy);
+            bulk_load(aux + lane * 4, a.v_scales + page4, words, &v_full[vr.at], policy);
+            bulk_load(aux + kTile + lane * 4, static_cast<const uint32_t *>(a.k_scales) + page4, words,
+                      &v_full[vr.at], policy);
           }
           const unsigned there = __ballot_sync(0xffffffffu, page4 >= 0);
-          if (lane == 0) aux[2 * kTile] = there;  // (bit t / 4: token t's page is there)
-          cp_async_arrive_noinc(&v_full[vr.at]);
-          mbar_arrive(&v_full[vr.at]);
+          if (lane == 0) {
+            aux[2 * kTile] = there;  // (bit t / 4: token t's page is there)
+            mbar_arrive(&v_full[vr.at]);
+          }
           ++issued_v;
           vr.advance();
         }
       }
-      cp_async_wait_all();
     } else {
       while (ok && w.next(a, groups, keys)) {
         const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
@@ -964,14 +956,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const uint32_t o_tmem = tmem + 2 * NS;
     uint32_t tile = 0, seg = 0;
     const bool leader = elect_one();
-    const auto all_wait = [&](uint64_t *bar, uint32_t parity, uint64_t limit) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit)) != 0;
+    const auto all_wait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs)) != 0;
     };
     const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
       const uint64_t k_desc = smem_desc_rows<D>(smem_addr(k_tile(st)));
       const uint32_t factors = tmem + C::SFA + (n & 1) * 4;
       if (!leader) return;
-      if constexpr (C::FP4) tmem_copy_factors(factors, smem_desc_factors(smem_addr(s_sf + st * kTile)));
+      if constexpr (C::FP4) tmem_copy_factors(factors, smem_desc_factors(smem_addr(s_sf + st * (C::K_AUX / 4))));
 #pragma unroll
       for (int part = 0; part < C::PASSES; ++part)
 #pragma unroll
@@ -986,34 +978,50 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       mma_commit(&s_full[n & 1]);
       if constexpr (C::FP4) mma_commit(&k_empty[st]);
     };
-    const auto keys_here = [&]() {
+    const auto keys_here = [&](int st) {
+      if constexpr (C::FP4 && !C::COPIES) {
+        // Their scale factors, which came in the tokens' order, to where the tensor core expects them.
+        const uint4 u = *reinterpret_cast<const uint4 *>(s_sf + (st * 2 + 1) * kTile + lane * 4);
+        uint32_t *to = s_sf + st * 2 * kTile + (lane % 8) * 16 + lane / 8;
+        to[0] = u.x, to[4] = u.y, to[8] = u.z, to[12] = u.w;
+      }
       // (What ordinary copies and stores wrote.)
       if constexpr (C::COPIES || C::FP4) fence_proxy_async_shared();
+      __syncwarp();
       tc_fence_after_sync();
     };
     // The segment's products; false if a wait gave up.  The whole warp walks through it, so that the
     // descriptors are the warp's and not one thread's; one thread issues.
     const auto segment = [&]() {
-      if (!all_wait(q_full, seg & 1, kWaitNs)) return false;
+      if (!all_wait(q_full, seg & 1)) return false;
       tc_fence_after_sync();
       bool ahead = false;  // S of the tile has been issued already
       for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
         if (!ahead) {
-          if (!all_wait(&k_full[kr.at], kr.phase, kWaitNs)) return false;
-          keys_here();
+          if (!all_wait(&k_full[kr.at], kr.phase)) return false;
+          keys_here(kr.at);
           scores(tile, kr.at);
         }
-        // The next tile's scores, if its keys are here, before this tile's weights are.
+        // The next tile's scores as soon as its keys are here, this tile's sum as soon as its weights are.
         Ring<C::KS> next = kr;
         next.advance();
-        ahead = i + 1 < w.seg_tiles && __all_sync(0xffffffffu, mbar_try_wait(&k_full[next.at], next.phase));
-        if (ahead) {
-          keys_here();
-          scores(tile + 1, next.at);
+        ahead = i + 1 >= w.seg_tiles;
+        uint64_t begin = 0;
+        for (;;) {
+          if (!ahead && __all_sync(0xffffffffu, mbar_test_wait(&k_full[next.at], next.phase))) {
+            ahead = true;
+            keys_here(next.at);
+            scores(tile + 1, next.at);
+          }
+          if (__all_sync(0xffffffffu, mbar_try_wait_sleep(&p_full[tile & 1], (tile >> 1) & 1, ahead ? 100000u : 100u)))
+            break;
+          const uint64_t now = global_timer_ns();
+          if (begin == 0) begin = now;
+          if (now - begin > kWaitNs) return false;
         }
-        if (!all_wait(&p_full[tile & 1], (tile >> 1) & 1, kWaitNs)) return false;
-        if (C::FP4 && !all_wait(&v_full[vr.at], vr.phase, kWaitNs)) return false;
-        if constexpr (C::FP4 && C::COPIES) fence_proxy_async_shared();
+        ahead = ahead && i + 1 < w.seg_tiles;
+        if (C::FP4 && !all_wait(&v_full[vr.at], vr.phase)) return false;
+        if constexpr (C::FP4) fence_proxy_async_shared();
         tc_fence_after_sync();
         const uint64_t v_desc = smem_desc_mn<D>(smem_addr(v_tile(C::FP4 ? vr.at : kr.at)));
         const uint64_t p_desc = smem_desc_p(smem_addr(weights_of(tile, kr.at)));
