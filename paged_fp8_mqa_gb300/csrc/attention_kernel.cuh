@@ -97,7 +97,9 @@ struct AttnCfg {
   // They take the place of the tile's keys, which have been read by then, where they fit it; else
   // they have buffers of their own.  (FP4: always, see below.)
   static constexpr bool OVER_K = !FP4 && P_BYTES <= kTile * D;
-  static constexpr int P_BUFS = OVER_K ? 0 : !FP4 || R == 64 ? 2 : 1;
+  // With two buffers a tile's weights need not wait for the product of the tile before, and S of this
+  // tile, which was issued after the product of the tile before that, says that theirs is free.
+  static constexpr int P_BUFS = OVER_K ? 0 : FP4 && (R == 32 || (R < 32 && COPIES && D == 128)) ? 1 : 2;
   // What a stage of K (FP4: its scale factors, where they are used and, by the TMA unit, as they came)
   // and of V holds besides: Token records, or (FP4, by the TMA unit) value scales, scale factors and
   // which of the tokens are there.
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   const auto weights_of = [&](uint32_t tile, int stage) {
     return C::OVER_K ? k_tile(stage) : s_p + (C::P_BUFS == 2 ? tile & 1 : 0) * C::P_BYTES;
   };
-  uint8_t *s_raw_kv = at;                            // [RAW][kTile][D / 2 of K, D / 2 of V]
+  uint8_t *s_raw_kv = at;                            // [RAW][K, V][kTile][D / 2]
   at += C::RAW * kTile * D;
   uint4 *s_raw_aux = reinterpret_cast<uint4 *>(at);  // [RAW][kTile]: factors, value scale, pos, row
   at += C::RAW * (C::RAW_BYTES - kTile * D);
@@ -465,14 +467,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       prefetch_tensor_map(&v_map);
     }
     for (int i = 0; i < C::KS; ++i) {
-      // A loading lane's arrival, and (SELECT) one when its own copies have landed; with FP4 one for each
-      // loading warp (thirty-two of a warp, one after the other on one word, are what takes time).
-      mbar_init(&k_full[i], C::FP4 ? C::LOADERS : (C::SELECT ? 64 : 32) * C::LOADERS);
+      // A loading lane's arrival, and (SELECT) one when its own copies have landed.  With FP4 one for each
+      // loading warp, or the loader's and one for each lane's copies (of scales).
+      mbar_init(&k_full[i], !C::FP4 ? (C::SELECT ? 64 : 32) * C::LOADERS : C::COPIES ? C::LOADERS : 33);
       mbar_init(&k_empty[i], 1);
     }
     if constexpr (C::FP4)
       for (int i = 0; i < C::VS; ++i) {
-        mbar_init(&v_full[i], C::LOADERS);
+        mbar_init(&v_full[i], C::COPIES ? C::LOADERS : 33);
         mbar_init(&v_empty[i], 1);
       }
     mbar_init(&s_full[0], 1);
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           if (bad) attn_flag(IDX_DEV_BAD_PAGE);
         };
         const auto issue = [&]() {
-          uint8_t *raw = s_raw_kv + in.at * (kTile * D) + piece * 16;
+          uint8_t *raw = s_raw_kv + in.at * (kTile * D) + piece * 16;  // (K rows, then V rows)
 #pragma unroll
           for (int q = 0; q < EACH; ++q) {
             const int t0 = token0 - lane + 32 * q;
@@ -673,8 +675,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               const int row = __shfl_sync(0xffffffffu, row0[q], n);
               if (row < 0) continue;  // (any code is a number, and its weight will be 0)
               const int64_t src = static_cast<int64_t>(row) * (D / 2) + piece * 16;
-              cp_async_16(raw + (t0 + n) * D, a.k_pool + src, policy);
-              cp_async_16(raw + (t0 + n) * D + D / 2, a.v_pool + src, policy);
+              cp_async_16(raw + (t0 + n) * (D / 2), a.k_pool + src, policy);
+              cp_async_16(raw + (kTile + t0 + n) * (D / 2), a.v_pool + src, policy);
             }
             uint32_t *aux = reinterpret_cast<uint32_t *>(s_raw_aux + in.at * kTile + t0 + lane);
             if (row0[q] >= 0) {
@@ -687,13 +689,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           in.advance();
         };
         const auto spread = [&](uint8_t *tile, int half) {
-          const uint8_t *raw = s_raw_kv + out.at * (kTile * D) + half * (D / 2) + piece * 16;
+          const uint8_t *raw = s_raw_kv + (out.at * 2 + half) * (kTile * D / 2) + piece * 16;
 #pragma unroll
           for (int q = 0; q < EACH; ++q)
 #pragma unroll
             for (int j = 0; j < 32 / kRows; ++j) {
               const int t = token0 - lane + 32 * q + j * kRows + sub;
-              const uint4 u = *reinterpret_cast<const uint4 *>(raw + t * D);
+              const uint4 u = *reinterpret_cast<const uint4 *>(raw + t * (D / 2));
               *reinterpret_cast<uint2 *>(tile + swizzled<D>(t, piece * 32)) = make_uint2(u.x, u.y);
               *reinterpret_cast<uint2 *>(tile + swizzled<D>(t, piece * 32 + 16)) = make_uint2(u.z, u.w);
             }
@@ -826,11 +828,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
       }
     } else if constexpr (C::FP4) {
+      const bool leader = elect_one();
       while (ok && w.next(a, groups, keys)) {
         const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
         const int32_t *table = a.block_tables + m.b * a.bt_stride;
         // A lane reads one page's id, 32 pages ahead of the ones in hand.  All else of a tile is copied
-        // by the lanes that begin a page, in bulk: the loader's instructions are what paces the tiles.
+        // without passing through a register, and the copies of pages are one thread's with the warp's
+        // operands (as many threads' they come one after the other, each with operands of its own): the
+        // loader's instructions are what paces the tiles.
         const int n_pages = (w.length + a.block_size - 1) >> shift;
         const int per_tile = kTile >> shift;
         int first = w.seg_tile * per_tile;  // the page of lane 0
@@ -852,37 +857,43 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           // The pool's row of the first token of the page that holds this lane's four tokens, or -1.
           const int block = __shfl_sync(0xffffffffu, id, i * per_tile + ((lane * 4) >> shift) - first);
           const int page4 = block < 0 ? -1 : (block * a.kv_heads + m.g) << shift;
-          const bool begins = page4 >= 0 && ((lane * 4) & (a.block_size - 1)) == 0;
-          const int bytes = D / 2 * a.block_size, words = 4 * a.block_size;
+          const unsigned there = __ballot_sync(0xffffffffu, page4 >= 0);  // bit t / 4: token t's page is there
+          const int bytes = (D / 2) * 4 * __popc(there);
+          const int row4 = page4 + ((lane * 4) & (a.block_size - 1));
           if (!stage_free()) break;
-          if (begins) {
-            // (The barrier counts the bytes read, half of those that the rows take here.)
-            mbar_expect_tx(&k_full[kr.at], bytes + words);
-            tma_load_2d(k_tile(kr.at) + lane * 4 * D, &k_map, &k_full[kr.at], 0, page4, policy);
-            bulk_load(s_sf + (kr.at * 2 + 1) * kTile + lane * 4,
-                      static_cast<const uint32_t *>(a.k_scales) + page4, words, &k_full[kr.at], policy);
+          // (The barrier counts the bytes read, half of those that the rows take here.)
+          if (leader) mbar_arrive_expect_tx(&k_full[kr.at], bytes);
+          for (int pg = 0; pg < per_tile; ++pg) {
+            const int row = __shfl_sync(0xffffffffu, page4, pg << (shift - 2));
+            if (leader && row >= 0)
+              tma_load_2d(k_tile(kr.at) + (pg << shift) * D, &k_map, &k_full[kr.at], 0, row, policy);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[kr.at]);
+          if (page4 >= 0)
+            cp_async_16(s_sf + (kr.at * 2 + 1) * kTile + lane * 4,
+                        static_cast<const uint32_t *>(a.k_scales) + row4, policy);
+          cp_async_arrive_noinc(&k_full[kr.at]);
           next_stage();
           if (!free_now(&v_empty[vr.at], vr.phase)) break;
           uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
-          if (begins) {
-            mbar_expect_tx(&v_full[vr.at], bytes + 2 * words);
-            tma_load_2d(v_tile(vr.at) + lane * 4 * D, &v_map, &v_full[vr.at], 0, page4, policy);
-            bulk_load(aux + lane * 4, a.v_scales + page4, words, &v_full[vr.at], policy);
-            bulk_load(aux + kTile + lane * 4, static_cast<const uint32_t *>(a.k_scales) + page4, words,
-                      &v_full[vr.at], policy);
+          if (leader) {
+            aux[2 * kTile] = there;
+            mbar_arrive_expect_tx(&v_full[vr.at], bytes);
           }
-          const unsigned there = __ballot_sync(0xffffffffu, page4 >= 0);
-          if (lane == 0) {
-            aux[2 * kTile] = there;  // (bit t / 4: token t's page is there)
-            mbar_arrive(&v_full[vr.at]);
+          for (int pg = 0; pg < per_tile; ++pg) {
+            const int row = __shfl_sync(0xffffffffu, page4, pg << (shift - 2));
+            if (leader && row >= 0)
+              tma_load_2d(v_tile(vr.at) + (pg << shift) * D, &v_map, &v_full[vr.at], 0, row, policy);
           }
+          if (page4 >= 0) {
+            cp_async_16(aux + lane * 4, a.v_scales + row4, policy);
+            cp_async_16(aux + kTile + lane * 4, static_cast<const uint32_t *>(a.k_scales) + row4, policy);
+          }
+          cp_async_arrive_noinc(&v_full[vr.at]);
           ++issued_v;
           vr.advance();
         }
       }
+      cp_async_wait_all();
     } else {
       while (ok && w.next(a, groups, keys)) {
         const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
@@ -1293,7 +1304,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // ---- weights, their parts, the running sums ------------------------------------------------
         // The weights' buffer was last read by the product two tiles ago.  (In the place of the keys
         // they need not wait; but whoever waits for a barrier has to see all its phases.)
-        if constexpr (C::P_BUFS == 1) {
+        if constexpr (C::FP4 && C::P_BUFS == 2) {
+        } else if constexpr (C::P_BUFS == 1) {
           if (tile >= 1) wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
         } else {
           if (tile >= 2) wait(&pv_done[tile & 1], ((tile >> 1) - 1) & 1);
