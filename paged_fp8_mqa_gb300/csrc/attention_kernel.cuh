@@ -80,7 +80,9 @@ struct AttnCfg {
   static constexpr int SOFT_WARPS = 4 * WG;
   // Warps that load: one for whole pages; up to four share the rows of a selection (FP4: of any tile
   // that the TMA unit does not bring), as many as the softmax's registers leave room for.
-  static constexpr int LOADERS = !COPIES || R == 32 ? 1 : R == 8 ? 4 : 2;
+  // In four bits whole pages have two, one for keys and one for values, where there is room: what holds
+  // a loader up is handing its copies to the TMA unit.
+  static constexpr int LOADERS = !COPIES ? (FP4 && R <= 16 ? 2 : 1) : R == 32 ? 1 : R == 8 ? 4 : 2;
   static constexpr int THREADS = 32 * (LOADERS + 1 + SOFT_WARPS);
   // Two of S, one of O; with FP4 the keys' scale factors, two tiles of them, and the queries' (1).
   static constexpr int SFA = 2 * NS + NO, SFB = SFA + 8;
@@ -828,7 +830,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
       }
     } else if constexpr (C::FP4) {
-      const bool leader = elect_one();
+      const bool leader = elect_one(), keys_too = C::LOADERS == 1 || warp == 0,
+                 values_too = C::LOADERS == 1 || warp != 0;
       while (ok && w.next(a, groups, keys)) {
         const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
         const int32_t *table = a.block_tables + m.b * a.bt_stride;
@@ -860,37 +863,41 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           const unsigned there = __ballot_sync(0xffffffffu, page4 >= 0);  // bit t / 4: token t's page is there
           const int bytes = (D / 2) * 4 * __popc(there);
           const int row4 = page4 + ((lane * 4) & (a.block_size - 1));
-          if (!stage_free()) break;
-          // (The barrier counts the bytes read, half of those that the rows take here.)
-          if (leader) mbar_arrive_expect_tx(&k_full[kr.at], bytes);
-          for (int pg = 0; pg < per_tile; ++pg) {
-            const int row = __shfl_sync(0xffffffffu, page4, pg << (shift - 2));
-            if (leader && row >= 0)
-              tma_load_2d(k_tile(kr.at) + (pg << shift) * D, &k_map, &k_full[kr.at], 0, row, policy);
+          if (keys_too) {
+            if (!stage_free()) break;
+            // (The barrier counts the bytes read, half of those that the rows take here.)
+            if (leader) mbar_arrive_expect_tx(&k_full[kr.at], bytes);
+            for (int pg = 0; pg < per_tile; ++pg) {
+              const int row = __shfl_sync(0xffffffffu, page4, pg << (shift - 2));
+              if (leader && row >= 0)
+                tma_load_2d(k_tile(kr.at) + (pg << shift) * D, &k_map, &k_full[kr.at], 0, row, policy);
+            }
+            if (page4 >= 0)
+              cp_async_16(s_sf + (kr.at * 2 + 1) * kTile + lane * 4,
+                          static_cast<const uint32_t *>(a.k_scales) + row4, policy);
+            cp_async_arrive_noinc(&k_full[kr.at]);
+            next_stage();
           }
-          if (page4 >= 0)
-            cp_async_16(s_sf + (kr.at * 2 + 1) * kTile + lane * 4,
-                        static_cast<const uint32_t *>(a.k_scales) + row4, policy);
-          cp_async_arrive_noinc(&k_full[kr.at]);
-          next_stage();
-          if (!free_now(&v_empty[vr.at], vr.phase)) break;
-          uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
-          if (leader) {
-            aux[2 * kTile] = there;
-            mbar_arrive_expect_tx(&v_full[vr.at], bytes);
+          if (values_too) {
+            if (!free_now(&v_empty[vr.at], vr.phase)) break;
+            uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
+            if (leader) {
+              aux[2 * kTile] = there;
+              mbar_arrive_expect_tx(&v_full[vr.at], bytes);
+            }
+            for (int pg = 0; pg < per_tile; ++pg) {
+              const int row = __shfl_sync(0xffffffffu, page4, pg << (shift - 2));
+              if (leader && row >= 0)
+                tma_load_2d(v_tile(vr.at) + (pg << shift) * D, &v_map, &v_full[vr.at], 0, row, policy);
+            }
+            if (page4 >= 0) {
+              cp_async_16(aux + lane * 4, a.v_scales + row4, policy);
+              cp_async_16(aux + kTile + lane * 4, static_cast<const uint32_t *>(a.k_scales) + row4, policy);
+            }
+            cp_async_arrive_noinc(&v_full[vr.at]);
+            ++issued_v;
+            vr.advance();
           }
-          for (int pg = 0; pg < per_tile; ++pg) {
-            const int row = __shfl_sync(0xffffffffu, page4, pg << (shift - 2));
-            if (leader && row >= 0)
-              tma_load_2d(v_tile(vr.at) + (pg << shift) * D, &v_map, &v_full[vr.at], 0, row, policy);
-          }
-          if (page4 >= 0) {
-            cp_async_16(aux + lane * 4, a.v_scales + row4, policy);
-            cp_async_16(aux + kTile + lane * 4, static_cast<const uint32_t *>(a.k_scales) + row4, policy);
-          }
-          cp_async_arrive_noinc(&v_full[vr.at]);
-          ++issued_v;
-          vr.advance();
         }
       }
       cp_async_wait_all();
@@ -1490,7 +1497,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   if (__syncthreads_or(!ok)) {
     // A wait gave up: let the copies and products in flight end before the memory is given back.
     if (!ok) attn_flag(IDX_DEV_WAIT_TIMEOUT);
-    if (warp == 0 && lane == 0) {
+    if ((warp == 0 || warp >= 2 + C::SOFT_WARPS) && lane == 0) {
       const auto landed = [&](uint64_t *full, uint32_t issued, uint32_t stages) {
         const uint32_t tail = issued < stages ? issued : stages;
         for (uint32_t d = 1; d <= tail; ++d) {
