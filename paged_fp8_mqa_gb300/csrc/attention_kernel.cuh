@@ -143,6 +143,7 @@ struct alignas(8) Token4 {
   int32_t pos;
 };
 
+template <bool APPROX = false>
 __device__ __forceinline__ Token token_of(float k, float v_scale, int pos) {
   Token t;
   const float held = fmaxf(fabsf(v_scale), kLeastScale);
@@ -150,7 +151,8 @@ __device__ __forceinline__ Token token_of(float k, float v_scale, int pos) {
   // (A NaN makes the weight one in the rows that see the position, and only in those: a weight of 0
   // meets inv_v, which stays a number.)
   t.log_v = v_scale == v_scale ? __log2f(held) : v_scale;
-  t.inv_v = copysignf(1.0f / held, v_scale);
+  // (APPROX: to one unit or so, as good as the sum that it goes into; past 2^125 it would be 0.)
+  t.inv_v = copysignf(APPROX && held < 4.2e37f ? __fdividef(1.0f, held) : 1.0f / held, v_scale);
   t.pos = pos;
   return t;
 }
@@ -1139,7 +1141,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
           const float up = e > 127 ? __int_as_float(0x7FC00000)  // an infinity: the row is NaN
                                    : __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-          const float down =
+          const float down =  // (times softmax_scale log2(e) with FP4: -100 <= e, so that it stays normal)
               __uint_as_float(static_cast<uint32_t>(127 - (C::FP4 ? 0 : 14) + min(e, 127)) << 23);
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[j] *= up;
@@ -1155,7 +1157,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             }
           }
           if (x == 0) {
-            s_rs[r] = down;
+            s_rs[r] = C::FP4 ? down * z_unit : down;
             s_row[(seg & 1) * R + r] = (m.b * a.next_n + th.x) * a.heads + th.y;
             s_ext[r] = r >= m.rows ? 0 : C::SELECT ? 1 : max(0, len - a.next_n + th.x + 1);
           }
@@ -1179,32 +1181,43 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       // Positions below this are seen by every row of the segment.
       const int all_see = C::SELECT ? kNone : len - a.next_n + 1 + (slot_head<C>(a, m, 0).x);
       for (int i = 0; i < w.seg_tiles; ++i, ++tile) {
-        wait(C::FP4 ? &v_full[vr.at] : &k_full[kr.at], C::FP4 ? vr.phase : kr.phase);
-        wait(&s_full[tile & 1], (tile >> 1) & 1);
+        {
+          // (Usually both are through: asked for at once, as each answer takes its time.)
+          uint64_t *there = C::FP4 ? &v_full[vr.at] : &k_full[kr.at];
+          const uint32_t use = C::FP4 ? vr.phase : kr.phase;
+          const bool v_there = mbar_test_wait(there, use);
+          const bool s_there = mbar_test_wait(&s_full[tile & 1], (tile >> 1) & 1);
+          if (!__all_sync(0xffffffffu, v_there && s_there)) {
+            wait(there, use);
+            wait(&s_full[tile & 1], (tile >> 1) & 1);
+          }
+        }
         tc_fence_after_sync();
         Token tok;
-        if constexpr (C::FP4) {
-          Token4 t4;
-          if constexpr (C::COPIES) {
-            t4 = s_tok4[vr.at * kTile + token];
-          } else {
-            const uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
-            const int p = (w.seg_tile + i) * kTile + token;
-            t4.v_scale = scale_of<D>(aux[kTile + token], __uint_as_float(aux[token]));
-            t4.pos = ((aux[2 * kTile] >> (token / 4)) & 1u) != 0 && p < len ? p : kNone;
-          }
-          tok = token_of(z_unit, t4.v_scale, t4.pos);
-        } else {
-          tok = s_tok[kr.at * kTile + token];
-        }
         float2 y[RT / 2];  // the weights' logarithms
         {
-          uint32_t v[RT];
+          uint32_t v[RT], u[C::CAT ? RT : 8], t[C::CAT ? RT : 8];
           tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + r0, v);
           if constexpr (C::CAT) {
-            uint32_t u[RT], t[RT];
             tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + R, u);
             tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + 2 * R, t);
+          }
+          // (While they come: what the position brings.)
+          if constexpr (C::FP4) {
+            Token4 t4;
+            if constexpr (C::COPIES) {
+              t4 = s_tok4[vr.at * kTile + token];
+            } else {
+              const uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
+              const int p = (w.seg_tile + i) * kTile + token;
+              t4.v_scale = scale_of<D>(aux[kTile + token], __uint_as_float(aux[token]));
+              t4.pos = ((aux[2 * kTile] >> (token / 4)) & 1u) != 0 && p < len ? p : kNone;
+            }
+            tok = token_of<true>(1.0f, t4.v_scale, t4.pos);
+          } else {
+            tok = s_tok[kr.at * kTile + token];
+          }
+          if constexpr (C::CAT) {
             tmem_ld_wait();
             reg_fence(v);
             reg_fence(u);
@@ -1229,8 +1242,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             for (int h = 0; h < 2; ++h) {
               const float2 s2 = make_float2(__uint_as_float(v[2 * (r + h)]),
                                             __uint_as_float(v[2 * (r + h) + 1]));
-              y[r + h] = __ffma2_rn(s2, __fmul2_rn(h ? make_float2(f.z, f.w) : make_float2(f.x, f.y), k2),
-                                    __fadd2_rn(lv2, nref[r + h]));
+              const float2 unit = h ? make_float2(f.z, f.w) : make_float2(f.x, f.y);
+              // (FP4: the tensor core has applied the key's scale, and unit holds the rest.)
+              y[r + h] = __ffma2_rn(s2, C::FP4 ? unit : __fmul2_rn(unit, k2), __fadd2_rn(lv2, nref[r + h]));
             }
           }
         }
