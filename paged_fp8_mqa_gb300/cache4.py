@@ -130,12 +130,17 @@ def kv_read_fp4(k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, toke
             raise TypeError("k_out and v_out must have the same dtype, the one asked for")
         if k_out.shape != (tokens, H, D) or v_out.shape != (tokens, H, D):
             raise ValueError("k_out and v_out must be [tokens, Hkv, D]")
+        if (tokens > 1 and not (k_token and v_token)) or (H > 1 and not (k_head and v_head)):
+            raise ValueError("k_out and v_out must not repeat rows (expanded tensors)")
     starts, lens, stride, batch, next_n, tables, row_stride, width = _tokens(
         block_tables, seq_lens, token_starts, tokens, index)
+    if tokens and not batch:
+        raise ValueError("tokens of no request")
     if tokens and H and D:
         _check(idx_kv_read_fp4(*pools, blocks, block_size, H, D, starts, tokens, lens, stride, batch,
                                next_n, tables, row_stride, width, bool(made), code,
-                               k_out.data_ptr(), k_token, k_head, v_out.data_ptr(), v_token, v_head, _on(stream, index, *made)))
+                               k_out.data_ptr(), k_token, k_head, v_out.data_ptr(), v_token, v_head,
+                               _on(stream, index, *made)))
     return k_out, v_out
 
 

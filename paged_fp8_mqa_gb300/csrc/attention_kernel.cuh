@@ -1037,7 +1037,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             break;
           const uint64_t now = global_timer_ns();
           if (begin == 0) begin = now;
-          if (now - begin > kWaitNs) return false;
+          if (__any_sync(0xffffffffu, now - begin > kWaitNs)) return false;
         }
         ahead = ahead && i + 1 < w.seg_tiles;
         if (C::FP4 && !all_wait(&v_full[vr.at], vr.phase)) return false;

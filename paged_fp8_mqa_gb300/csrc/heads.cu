@@ -555,8 +555,10 @@ cudaError_t launch_backward(const HeadsArgs &a, bool pieces, int sms, cudaStream
   };
   s.k = blocks(a.heads[1]);
   s.q = blocks(a.heads[0]);
-  cudaError_t e;
-  if (!pieces)
+  cudaError_t e = cudaSuccess;
+  if (s.q + s.k == 0)
+    ;  // (no tokens: the weights' gradients are sums over nothing)
+  else if (!pieces)
     e = launch_dependent(k_heads_backward_any<T>, dim3(s.q + s.k), dim3(32 * kAnyWarps),
                          2 * kAnyWarps * a.dim * 4, stream, a, s);
   else if (width == 4)

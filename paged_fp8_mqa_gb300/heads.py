@@ -91,9 +91,12 @@ def _like(out, x, name, index, made):
         made.append(out)
         return out, shape[1] * shape[2], shape[2]
     _tensor(out, name, 3, x.dtype, index)
-    if out.shape != x.shape or (x.shape[2] > 1 and out.stride(2) != 1):
+    token, head, unit = out.stride()
+    if out.shape != x.shape or (x.shape[2] > 1 and unit != 1):
         raise ValueError(f"{name} must have its input's shape and contiguous rows")
-    return out, out.stride(0), out.stride(1)
+    if (x.shape[0] > 1 and token == 0) or (x.shape[1] > 1 and head == 0):
+        raise ValueError(f"{name} must not repeat rows (an expanded tensor)")
+    return out, token, head
 
 
 def rotary_by_axes(x, positions, table, axes, interleaved, rot_offset, inverse, out, stream):

@@ -575,3 +575,37 @@ def test_a_decode_step_norms_appends_and_attends():
     kk, _ = idx.kv_read_fp4(*cache, bt, seq, tokens=3, dtype=torch.float32)
     scale = 2.0 ** torch.ceil(torch.log2(k.float().unflatten(-1, (-1, 32)).abs().amax(-1, keepdim=True) / 6))
     assert ((kk - k.float()).unflatten(-1, (-1, 32)).abs() <= scale).all()
+
+
+def test_refusals_of_tensors():
+    g = gen(1)
+    cache = empty_cache(4, 2, 32, 64, g)
+    kp, vp, ks, vs = cache
+    x = torch.randn(3, 2, 64, generator=g).bfloat16().to(dev())
+    bt = torch.zeros(3, 1, dtype=torch.int32, device=dev())
+    seq = torch.ones(3, dtype=torch.int32, device=dev())
+    starts = torch.zeros(1, dtype=torch.int32, device=dev())
+    wide = torch.zeros(3, 1, 2, 64, dtype=torch.bfloat16, device=dev())
+    for bad, error in (
+            (lambda: idx.kv_append_fp4(x, x.half(), *cache, bt, seq), TypeError),
+            (lambda: idx.kv_append_fp4(x, x, kp.float(), vp, ks, vs, bt, seq), TypeError),
+            (lambda: idx.kv_append_fp4(x, x, kp, vp, ks[..., :1], vs, bt, seq), ValueError),
+            (lambda: idx.kv_append_fp4(x, x, kp, vp, ks, vs[:, :1].expand(4, 2, 32), bt, seq), ValueError),
+            (lambda: idx.kv_append_fp4(x, x, kp, vp[:3], ks, vs, bt, seq), ValueError),
+            (lambda: idx.kv_append_fp4(x[:, :1], x[:, :1], *cache, bt, seq), ValueError),
+            (lambda: idx.kv_append_fp4(x, x, *cache, bt[:1].expand(3, 1), seq), ValueError),
+            (lambda: idx.kv_append_fp4(x[:2], x[:2], *cache, bt, seq), ValueError),
+            (lambda: idx.kv_read_fp4(*cache, bt, seq, tokens=4), ValueError),
+            (lambda: idx.kv_read_fp4(*cache, bt[:0], seq[:0], starts, tokens=4), ValueError),
+            (lambda: idx.kv_read_fp4(*cache, bt, seq, tokens=3, dtype=torch.float64), TypeError),
+            (lambda: idx.kv_read_fp4(*cache, bt, seq, tokens=3, k_out=x), ValueError),
+            (lambda: idx.kv_read_fp4(*cache, bt, seq, tokens=3, k_out=x, v_out=x[:1].expand(3, 2, 64)), ValueError),
+            (lambda: idx.attention_fp4(wide.float(), *cache, bt, seq), TypeError),
+            (lambda: idx.attention_fp4(wide[..., :32], *cache, bt, seq), ValueError),
+            (lambda: idx.attention_fp4(torch.cat([wide] * 5, 1), *cache, bt, seq), idx.IdxError),
+            (lambda: idx.attention_fp4(wide[:, :, :1], *cache, bt, seq), idx.IdxError)):
+        with pytest.raises(error):
+            bad()
+    torch.cuda.synchronize()
+    k, v = idx.kv_read_fp4(*cache, bt, seq, torch.zeros(4, dtype=torch.int32, device=dev()), tokens=0)
+    assert k.shape == (0, 2, 64) and v.dtype == torch.bfloat16

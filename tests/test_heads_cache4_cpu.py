@@ -176,3 +176,49 @@ def test_host_tensors_are_refused():
               lambda: idx.attention_fp4(x[:, None], *cache, bt, sl)):
         with pytest.raises(TypeError, match="CUDA"):
             f()
+
+
+@pytest.mark.parametrize("call", ["axes", "norm", "append", "read", "attention"])
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_run_on_their_tensors_device(call, current, monkeypatch):
+    """Tensors said to be on device 1, with device 0 or 1 current: every C call is made with 1 current."""
+    from paged_fp8_mqa_gb300 import cache4, heads, layer
+    now, entered, seen = [current], [], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+            entered.append(self.index)
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    def c_call(*_):
+        seen.append(now[0])
+        return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for module in (layer, heads, cache4):
+        monkeypatch.setattr(module, "_index", lambda t, name: 1)
+        monkeypatch.setattr(module, "_on", lambda *a: 0)
+    monkeypatch.setattr(layer, "_sizes", {})
+    monkeypatch.setattr(layer, "idx_attention_workspace_bytes", c_call)
+    for module, name in ((heads, "idx_rotary_axes"), (heads, "idx_norm_rotary"), (cache4, "idx_kv_append_fp4"),
+                         (cache4, "idx_kv_read_fp4"), (cache4, "idx_attention_fp4")):
+        monkeypatch.setattr(module, name, c_call)
+    i32 = torch.int32
+    x, table = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(8, 32, 2)
+    pos, bt, sl = torch.zeros(2, 2, dtype=i32), torch.zeros(2, 1, dtype=i32), torch.ones(2, dtype=i32)
+    cache = (torch.zeros(2, 4, 32, 32, dtype=torch.uint8), torch.zeros(2, 4, 32, 32, dtype=torch.uint8),
+             torch.zeros(2, 4, 32, 2, dtype=torch.uint8), torch.zeros(2, 4, 32))
+    {"axes": lambda: idx.rotary(x, pos, table, axes=[0, 1] * 16),
+     "norm": lambda: idx.norm_rotary(x, x, None, None, pos, table, axes=[0, 1] * 16),
+     "append": lambda: idx.kv_append_fp4(x, x, *cache, bt, sl),
+     "read": lambda: idx.kv_read_fp4(*cache, bt, sl, tokens=2),
+     "attention": lambda: idx.attention_fp4(x[:, None], *cache, bt, sl)}[call]()
+    assert seen == [1] * (2 if call == "attention" else 1)
+    assert entered == ([1] if current == 0 else []) and now == [current]

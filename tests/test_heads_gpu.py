@@ -338,3 +338,51 @@ def test_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(grads, eager)) and torch.equal(out[0], want[0])
+
+
+def test_refusals_of_tensors():
+    q, k, w, pos, table, how, _ = heads_case(6, 4, 2, 64, 32, 0, False, 1, "f32", "f32", "plain")
+    two = pos.expand(2, 6)
+    axes = idx.rotary_axes((8, 8))
+    for bad, error in (
+            (lambda: idx.norm_rotary(q, k.half(), *w, pos, table), TypeError),
+            (lambda: idx.norm_rotary(q, k[:5], *w, pos, table), TypeError),
+            (lambda: idx.norm_rotary(q, k, w[0][:32], w[1], pos, table), ValueError),
+            (lambda: idx.norm_rotary(q, k, w[0].half(), w[1], pos, table), TypeError),
+            (lambda: idx.norm_rotary(q, k, w[0].bfloat16(), w[1].half(), pos, table), TypeError),
+            (lambda: idx.norm_rotary(q, None, w[0], w[1], pos, table), ValueError),
+            (lambda: idx.norm_rotary(q, k, *w, pos), ValueError),
+            (lambda: idx.norm_rotary(q, k, *w, pos[:5], table), ValueError),
+            (lambda: idx.norm_rotary(q, k, *w, two, table), ValueError),
+            (lambda: idx.norm_rotary(q, k, *w, pos, table, axes=axes), ValueError),
+            (lambda: idx.norm_rotary(q, k, *w, two, table, axes=axes[:-1]), ValueError),
+            (lambda: idx.norm_rotary(q, k, *w, two.t().contiguous().t(), table, axes=axes), ValueError),
+            (lambda: idx.norm_rotary(q, k, *w, pos, table, q_out=k), ValueError),
+            (lambda: idx.norm_rotary(q, k, *w, pos, table, q_out=q[:1].expand(6, 4, 64)), ValueError),
+            (lambda: idx.norm_rotary(q, k, *w, pos, table, rot_offset=40), idx.IdxError),
+            (lambda: idx.norm_rotary(q, k, *w, pos, table, eps=-1.0), idx.IdxError),
+            (lambda: idx.norm_rotary(q.requires_grad_(), k, *w, pos, table, q_out=torch.empty_like(q)), ValueError),
+            (lambda: idx.norm_rotary(torch.zeros(2, 1, 1040, device=dev())), None),
+            (lambda: idx.norm_rotary(torch.zeros(2, 1, 1040, device=dev()), None), idx.IdxError),
+            (lambda: idx.rotary(k, two.expand(5, 2, 6)[0], table, axes=axes), None),
+            (lambda: idx.rotary(k, pos.expand(5, 6), table, axes=axes), ValueError)):
+        if error is None:
+            continue
+        with pytest.raises(error):
+            bad()
+    torch.cuda.synchronize()
+
+
+def test_c_entry_of_the_gradients_without_tokens():
+    """No tokens: the weights' gradients are zeros."""
+    w = torch.ones(64, device=dev())
+    g = [torch.full((64,), 5.0, device=dev()) for _ in range(2)]
+    need = idx.idx_norm_rotary_workspace_bytes(64)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev())
+    p = w.data_ptr()
+    rows = (p, 128, 64)
+    assert idx.idx_norm_rotary_backward(*rows, 2, *rows, 1, idx.IDX_DTYPE_F32, 0, 64, p, p, idx.IDX_DTYPE_F32,
+                                        1e-6, None, 0, None, 1, None, 0, 0, 0, 0, *rows, *rows, p, p,
+                                        g[0].data_ptr(), g[1].data_ptr(), ws.data_ptr(), need, None) == 0
+    clean()
+    assert (g[0] == 0).all() and (g[1] == 0).all()
