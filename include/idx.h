@@ -603,7 +603,8 @@ int idx_kv_read_fp4(const uint8_t *k_pool, const uint8_t *v_pool, const uint8_t 
                     const int32_t *seq_lens, int64_t seq_lens_stride, int32_t batch, int32_t next_n,
                     const int32_t *block_tables, int64_t bt_row_stride, int32_t bt_width,
                     int32_t clear, int32_t dtype, void *k_out, int64_t k_token_stride,
-                    int64_t k_head_stride, void *v_out, int64_t v_token_stride, int64_t v_head_stride, void *stream);
+                    int64_t k_head_stride, void *v_out, int64_t v_token_stride, int64_t v_head_stride,
+                    void *stream);
 
 /*
  * idx_attention_fp8 over the 4-bit cache: the same arguments but for the scales, the same rows, extents,

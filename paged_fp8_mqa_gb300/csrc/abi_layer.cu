@@ -609,7 +609,8 @@ IDX_EXPORT int idx_kv_read_fp4(const uint8_t *k_pool, const uint8_t *v_pool, con
   const int size = element_bytes(dtype);
   if (!aligned(k_out, size) || !aligned(v_out, size))
     return fail(IDX_INVALID_ARG, "k_out and v_out must be aligned to their elements");
-  if (tokens == 0 || batch == 0) return IDX_OK;
+  if (tokens == 0) return IDX_OK;
+  if (batch == 0) return fail(IDX_INVALID_ARG, "tokens of no request");
   a.k_out = k_out;
   a.v_out = v_out;
   a.k_token = k_token_stride;

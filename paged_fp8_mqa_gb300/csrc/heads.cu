@@ -285,9 +285,10 @@ struct BackwardSplit {
   int32_t q, k, walk;
 };
 
-// The gradients, W lanes a head.  8192 tokens of 32 + 8 heads of 128 (252 MB) take 60 us, 37 at the copy rate:
-// 128 registers leave 16 warps an SM (three blocks of them 63 us, five 82).  A lane's 16 elements of the weight's gradient stay in its registers over
-// all its heads; a block leaves its sums in the workspace and a second launch adds the blocks', in order.
+// The gradients, W lanes a head.  8192 tokens of 32 + 8 heads of 128 (252 MB) take 60 us, 37 at the copy
+// rate: 128 registers leave 16 warps an SM (three blocks of them 63 us, five 82).  A lane's 16 elements of
+// the weight's gradient stay in its registers over all its heads; a block leaves its sums in the workspace
+// and a second launch adds the blocks', in order.
 template <typename T, int W, bool ADJ>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     k_heads_backward(const __grid_constant__ HeadsArgs a, const BackwardSplit split) {
@@ -544,7 +545,7 @@ cudaError_t launch_backward(const HeadsArgs &a, bool pieces, int sms, cudaStream
   // Blocks in proportion to the heads of q and of k, no more than there are heads for.
   const int lanes = a.dim / 16, width = lanes <= 4 ? 4 : lanes <= 8 ? 8 : 16;
   const int at_once = pieces ? kThreads / width : kAnyWarps;
-  const int64_t all = heads_blocks(sms), heads = a.heads[0] + a.heads[1];
+  const int64_t all = heads_blocks(sms), heads = a.heads[0] + a.heads[1] + (a.heads[0] + a.heads[1] == 0);
   BackwardSplit s;
   s.walk = 8;
   while (pieces && s.walk > 1 && a.tokens * heads < all * at_once * s.walk) s.walk /= 2;
@@ -557,7 +558,7 @@ cudaError_t launch_backward(const HeadsArgs &a, bool pieces, int sms, cudaStream
   s.q = blocks(a.heads[0]);
   cudaError_t e = cudaSuccess;
   if (s.q + s.k == 0)
-    ;  // (no tokens: the weights' gradients are sums over nothing)
+    ;  // (no tokens or no heads: the weights' gradients are sums over nothing)
   else if (!pieces)
     e = launch_dependent(k_heads_backward_any<T>, dim3(s.q + s.k), dim3(32 * kAnyWarps),
                          2 * kAnyWarps * a.dim * 4, stream, a, s);

@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const Kv4Args a, bool p
   }
 }
 
-// The rows back: a warp's token and rows as above.
+// The rows back: a warp's token and rows as above, all its loads before its first store.  34,000 tokens of 8
+// heads of 128 (176 MB) take 37 us, 26 at the copy rate; two rounds a warp 45, eight 41, sixteen 50.
 template <typename T, int D, int ROUNDS>
 __global__ void __launch_bounds__(kThreads) k_kv4_read(const Kv4Args a, bool pieces, bool clear) {
   constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;

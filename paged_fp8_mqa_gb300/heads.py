@@ -78,7 +78,7 @@ def _turn(positions, axes, rot, T, index):
     axis_stride, unit = positions.stride()
     if T > 1 and unit != 1:
         raise ValueError("positions of an axis must be contiguous")
-    pair_axis = _axis_bytes(axes if type(axes) is tuple else tuple(axes), count, rot // 2)
+    pair_axis = _axis_bytes(axes, count, rot // 2)
     return positions.data_ptr(), axis_stride, pair_axis, count
 
 
@@ -284,6 +284,8 @@ def norm_rotary(q, k, q_weight=None, k_weight=None, positions=None, table=None, 
     cannot be differentiated again."""
     import torch
     index = _index(q, "q")
+    if axes is not None and type(axes) is not tuple:
+        axes = tuple(axes)
     if (q.requires_grad or (k is not None and k.requires_grad)
             or (q_weight is not None and q_weight.requires_grad)
             or (k_weight is not None and k_weight.requires_grad)) and torch.is_grad_enabled():

@@ -294,6 +294,8 @@ def rotary(x, positions, table, *, axes=None, interleaved: bool = False, rot_off
     turned by the position on its own axis."""
     import torch
     index = _index(x, "x")
+    if axes is not None and type(axes) is not tuple:
+        axes = tuple(axes)
     if x.requires_grad and out is None and torch.is_grad_enabled():
         return _recorded_rotary()(x, positions, table, axes, interleaved, rot_offset, inverse, stream)
     if index != torch.cuda.current_device():
@@ -429,7 +431,8 @@ def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, 
 
 def _attend(entry, index, q, pools, sizes, block_tables, seq_lens, softmax_scale, candidates, ranges,
             out, lse, workspace, num_sms, stream):
-    """The attention's call by its C entry: pools, the cache's four addresses; sizes, its (blocks, Hkv, block_size, D)."""
+    """The attention's call by its C entry: pools, the cache's four addresses; sizes, its (blocks, Hkv,
+    block_size, D)."""
     import torch
     dtype = q.dtype
     code = _code(dtype)

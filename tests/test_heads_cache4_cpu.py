@@ -133,7 +133,7 @@ def test_kv_append_fp4_refused(over, code):
     assert call(idx.idx_kv_append_fp4, args, over) == code, idx.idx_last_error()
 
 
-@pytest.mark.parametrize("over,code", PLACES)
+@pytest.mark.parametrize("over,code", PLACES + [(dict(batch=0, token_starts=FAKE), 1)])
 def test_kv_read_fp4_refused(over, code):
     args = dict(**POOLS, num_blocks=10, block_size=64, heads=8, dim=128, token_starts=None, tokens=4,
                 seq_lens=FAKE, seq_stride=1, batch=2, next_n=2, tables=FAKE, table_stride=16, width=16,

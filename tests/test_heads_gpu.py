@@ -386,3 +386,29 @@ def test_c_entry_of_the_gradients_without_tokens():
                                         g[0].data_ptr(), g[1].data_ptr(), ws.data_ptr(), need, None) == 0
     clean()
     assert (g[0] == 0).all() and (g[1] == 0).all()
+
+
+def test_c_entry_of_the_gradients_without_heads():
+    """No heads: the same."""
+    w = torch.ones(64, device=dev())
+    g = torch.full((64,), 5.0, device=dev())
+    need = idx.idx_norm_rotary_workspace_bytes(64)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev())
+    p = w.data_ptr()
+    rows, none = (p, 64, 64), (None, 0, 0)
+    assert idx.idx_norm_rotary_backward(*rows, 0, *none, 0, idx.IDX_DTYPE_F32, 3, 64, p, None, idx.IDX_DTYPE_F32,
+                                        1e-6, None, 0, None, 1, None, 0, 0, 0, 0, *rows, *none, p, None,
+                                        g.data_ptr(), None, ws.data_ptr(), need, None) == 0
+    clean()
+    assert (g == 0).all()
+
+
+def test_axes_that_can_be_read_only_once():
+    q, k, w, pos, table, how, ph = heads_case(5, 4, 2, 64, 32, 0, False, 3, "f32", "f32")
+    want = [torch.autograd.grad(y, x, torch.ones_like(y)) for x in (q.detach().requires_grad_(),) for y in
+            (idx.norm_rotary(x, None, w[0], None, pos, table, **how)[0], idx.rotary(x, pos, table, **how))]
+    x = q.detach().requires_grad_()
+    for f, (dx,) in zip((lambda axes: idx.norm_rotary(x, None, w[0], None, pos, table, axes=axes)[0],
+                         lambda axes: idx.rotary(x, pos, table, axes=axes)), want):
+        y = f(a for a in how["axes"])
+        assert torch.equal(torch.autograd.grad(y, x, torch.ones_like(y))[0], dx)
