@@ -619,9 +619,11 @@ IDX_EXPORT int idx_kv_read_fp4(const uint8_t *k_pool, const uint8_t *v_pool, con
   a.v_head = v_head_stride;
   a.num_blocks = num_blocks;
   a.block_size = block_size;
-  const bool all = pieces(k_out, k_token_stride, k_head_stride, 8, size) &&
-                   pieces(v_out, v_token_stride, v_head_stride, 8, size);
-  const cudaError_t e = idx::launch_kv4_read(a, dtype, all, clear != 0,
+  const auto at_once = [&](int bytes) {
+    return pieces(k_out, k_token_stride, k_head_stride, bytes / size, size) &&
+           pieces(v_out, v_token_stride, v_head_stride, bytes / size, size);
+  };
+  const cudaError_t e = idx::launch_kv4_read(a, dtype, at_once(8 * size), at_once(32), clear != 0,
                                              static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? IDX_OK : cuda_fail(e, "kv_read_fp4 launch");
 }

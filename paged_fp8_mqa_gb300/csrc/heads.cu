@@ -285,8 +285,8 @@ struct BackwardSplit {
   int32_t q, k, walk;
 };
 
-// The gradients, W lanes a head.  8192 tokens of 32 + 8 heads of 128 (252 MB) take 60 us, 37 at the copy
-// rate: 128 registers leave 16 warps an SM (three blocks of them 63 us, five 82).  A lane's 16 elements of
+// The gradients, W lanes a head.  8192 tokens of 32 + 8 heads of 128 (252 MB) take 53 us with the second
+// launch, 37 at the copy rate: 128 registers leave 16 warps an SM (three blocks of them 3 us more, five 22).  A lane's 16 elements of
 // the weight's gradient stay in its registers over all its heads; a block leaves its sums in the workspace
 // and a second launch adds the blocks', in order.
 template <typename T, int W, bool ADJ>
@@ -450,34 +450,51 @@ __global__ void __launch_bounds__(32 * kAnyWarps)
   }
 }
 
-// The blocks' sums of a weight's gradient, in order and in 64 bits: 32 elements a block (x, kind), a warp
-// every 32nd row of them.
+// A sum and what its roundings left out (exact for each addition).
+struct Sum2 {
+  float sum, rest;
+};
+__device__ __forceinline__ void add2(Sum2 &s, float x) {
+  const float t = __fadd_rn(s.sum, x), y = __fsub_rn(t, s.sum);
+  s.rest = __fadd_rn(s.rest, __fadd_rn(__fsub_rn(s.sum, __fsub_rn(t, y)), __fsub_rn(x, y)));
+  s.sum = t;
+}
+
+// The blocks' sums of a weight's gradient, in order and in two floats: 32 elements a block (x, kind), a warp
+// every 32nd row of them.  (In 64 bits, whose units are few, the two launches took 60 us for 53.)
 template <typename T>
 __global__ void __launch_bounds__(1024) k_weight_gradient(const __grid_constant__ HeadsArgs a,
                                                           const BackwardSplit split) {
-  __shared__ double s_part[32][33];
+  __shared__ Sum2 s_part[32][33];
   griddep_wait();
   griddep_launch_dependents();
   const int kind = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = blockIdx.x * 32 + lane;
   if (a.dweight[kind] == nullptr) return;
   const int begin = kind ? split.q : 0, end = begin + (kind ? split.k : split.q);
-  double sum = 0.0;
+  Sum2 sum{0.0f, 0.0f};
   if (d < a.dim) {
 #pragma unroll 4
-    for (int b = begin + warp; b < end; b += 32) sum += a.workspace[static_cast<int64_t>(b) * a.dim + d];
+    for (int b = begin + warp; b < end; b += 32) add2(sum, a.workspace[static_cast<int64_t>(b) * a.dim + d]);
   }
   s_part[warp][lane] = sum;
   __syncthreads();
   sum = s_part[lane][warp];  // element `warp` of the block's, part `lane`
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    const float other = __shfl_xor_sync(0xffffffffu, sum.sum, o);
+    const float rest = __shfl_xor_sync(0xffffffffu, sum.rest, o);
+    add2(sum, other);
+    sum.rest += rest;
+  }
   const int e = blockIdx.x * 32 + warp;
   if (lane != 0 || e >= a.dim) return;
+  // (Of an infinite sum the rest is NaN.)
+  const float all = fabsf(sum.sum) < __int_as_float(0x7F800000) ? sum.sum + sum.rest : sum.sum;
   if (a.weight_f32)
-    static_cast<float *>(a.dweight[kind])[e] = static_cast<float>(sum);
+    static_cast<float *>(a.dweight[kind])[e] = all;
   else
-    static_cast<T *>(a.dweight[kind])[e] = from_f32<T>(static_cast<float>(sum));
+    static_cast<T *>(a.dweight[kind])[e] = from_f32<T>(all);
 }
 
 template <typename T, int W, bool ADJ, int AHEAD, bool NORM, int BLOCKS = 1>

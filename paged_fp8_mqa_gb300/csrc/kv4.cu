@@ -416,51 +416,79 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const Kv4Args a, bool p
   }
 }
 
-// The rows back: a warp's token and rows as above, all its loads before its first store.  34,000 tokens of 8
-// heads of 128 (176 MB) take 37 us, 26 at the copy rate; two rounds a warp 45, eight 41, sixteen 50.
+// 16 elements of a row: in stores of 32 bytes (wide), of 16, or one by one.
+enum Store { kByOne, kInPieces, kWide };
+template <typename T>
+__device__ __forceinline__ void store16(T *out, const Piece<T, 8> (&p)[2], int how) {
+  if (how == kWide) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+    for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + j * (32 / sizeof(T))),
+                   "r"(w[8 * j]), "r"(w[8 * j + 1]), "r"(w[8 * j + 2]), "r"(w[8 * j + 3]), "r"(w[8 * j + 4]),
+                   "r"(w[8 * j + 5]), "r"(w[8 * j + 6]), "r"(w[8 * j + 7])
+                   : "memory");
+  } else if (how == kInPieces) {
+    store_piece<T, 8>(out, p[0]);
+    store_piece<T, 8>(out + 8, p[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) out[j] = p[j >> 3].e[j & 7];
+  }
+}
+
+// The rows back: a warp takes one token and ROUNDS times 512 / D of its 2 * heads rows (the keys, then the
+// values), 16 elements a lane, all its loads before its first store.  34,000 tokens of 8 heads of 128
+// (176 MB) take 31 us, 26 at the copy rate; one round a warp 36, two 34, eight 33 (eight elements
+// a lane in 16-byte stores 37).
 template <typename T, int D, int ROUNDS>
-__global__ void __launch_bounds__(kThreads) k_kv4_read(const Kv4Args a, bool pieces, bool clear) {
-  constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
+__global__ void __launch_bounds__(kThreads) k_kv4_read(const Kv4Args a, int how, bool clear) {
+  constexpr int LANES = D / 16, AT_ONCE = 32 / LANES;
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, l = lane % LANES;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= a.m.tokens) return;
-  const int first = blockIdx.y * ROUNDS * AT_ONCE + lane / LANES, d = (lane % LANES) * 8;
+  const int first = blockIdx.y * ROUNDS * AT_ONCE + lane / LANES;
   const Spot s = spot_of(a, t, lane);
   if (s.page < 0 && !clear) return;
-  const int in_page = s.pos & (a.block_size - 1);
-  uint32_t codes[ROUNDS];
+  uint2 codes[ROUNDS];
   float scale[ROUNDS];
 #pragma unroll
   for (int i = 0; i < ROUNDS; ++i) {
-    const int n = min(first + i * AT_ONCE, 2 * a.heads - 1);
-    const bool is_k = n < a.heads;
-    codes[i] = 0;
+    codes[i] = make_uint2(0, 0);
     scale[i] = 0.0f;
-    if (s.page < 0) continue;
-    const int64_t row = (s.page * a.heads + (is_k ? n : n - a.heads)) * a.block_size + in_page;
-    codes[i] = *reinterpret_cast<const uint32_t *>((is_k ? a.k_pool : a.v_pool) + row * (D / 2) + d / 2);
-    scale[i] = is_k ? ue8m0(a.k_scales[row * (D / 32) + d / 32]) : a.v_scales[row];
+  }
+  if (s.page >= 0) {
+    const int64_t row0 = s.page * a.heads * a.block_size + (s.pos & (a.block_size - 1));
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int n = min(first + i * AT_ONCE, 2 * a.heads - 1);
+      const bool is_k = n < a.heads;
+      const int64_t row = row0 + (is_k ? n : n - a.heads) * a.block_size;
+      codes[i] = *reinterpret_cast<const uint2 *>((is_k ? a.k_pool : a.v_pool) + row * (D / 2) + l * 8);
+      scale[i] = is_k ? ue8m0(a.k_scales[row * (D / 32) + l / 2]) : a.v_scales[row];
+    }
   }
 #pragma unroll
   for (int i = 0; i < ROUNDS; ++i) {
     const int n = first + i * AT_ONCE;
     if (n >= 2 * a.heads) return;
     const bool is_k = n < a.heads;
-    float v[8];
-    e2m1x8_to_f32(codes[i], v);
-    Piece<T, 8> p;
+    Piece<T, 8> p[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p.e[j] = from_f32<T>(v[j] * scale[i]);
-    T *out = static_cast<T *>(is_k ? a.k_out : a.v_out) + t * (is_k ? a.k_token : a.v_token) +
-             (is_k ? n * a.k_head : (n - a.heads) * a.v_head) + d;
-    if (pieces) {
-      store_piece<T, 8>(out, p);
-    } else {
+    for (int e = 0; e < 2; ++e) {
+      float v[8];
+      e2m1x8_to_f32(e ? codes[i].y : codes[i].x, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) out[j] = p.e[j];
+      for (int j = 0; j < 8; j += 2) {
+        const float2 f = __fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(scale[i], scale[i]));
+        put_two<T>(p[e], j, f.x, f.y);
+      }
     }
+    store16<T>(static_cast<T *>(is_k ? a.k_out : a.v_out) + t * (is_k ? a.k_token : a.v_token) +
+                   (is_k ? n * a.k_head : (n - a.heads) * a.v_head) + l * 16,
+               p, how);
   }
 }
 
@@ -506,12 +534,12 @@ cudaError_t append(const Kv4Args &a, bool pieces, bool turns, cudaStream_t strea
 }
 
 template <typename T, int D>
-cudaError_t read(const Kv4Args &a, bool pieces, bool clear, cudaStream_t stream) {
-  constexpr int AT_ONCE = 256 / D;
+cudaError_t read(const Kv4Args &a, int how, bool clear, cudaStream_t stream) {
+  constexpr int AT_ONCE = 512 / D;
   return many(a, AT_ONCE) ? launch_dependent(k_kv4_read<T, D, 4>, grid_of(a, 4 * AT_ONCE),
-                                             dim3(kThreads), 0, stream, a, pieces, clear)
+                                             dim3(kThreads), 0, stream, a, how, clear)
                           : launch_dependent(k_kv4_read<T, D, 1>, grid_of(a, AT_ONCE), dim3(kThreads),
-                                             0, stream, a, pieces, clear);
+                                             0, stream, a, how, clear);
 }
 
 template <typename T>
@@ -519,8 +547,8 @@ cudaError_t append_dim(const Kv4Args &a, bool pieces, bool turns, cudaStream_t s
   return a.dim == 64 ? append<T, 64>(a, pieces, turns, stream) : append<T, 128>(a, pieces, turns, stream);
 }
 template <typename T>
-cudaError_t read_dim(const Kv4Args &a, bool pieces, bool clear, cudaStream_t stream) {
-  return a.dim == 64 ? read<T, 64>(a, pieces, clear, stream) : read<T, 128>(a, pieces, clear, stream);
+cudaError_t read_dim(const Kv4Args &a, int how, bool clear, cudaStream_t stream) {
+  return a.dim == 64 ? read<T, 64>(a, how, clear, stream) : read<T, 128>(a, how, clear, stream);
 }
 
 }  // namespace
@@ -534,12 +562,13 @@ cudaError_t launch_kv4_append(const Kv4Args &a, int dtype, bool pieces, bool tur
   }
 }
 
-cudaError_t launch_kv4_read(const Kv4Args &a, int dtype, bool pieces, bool clear,
+cudaError_t launch_kv4_read(const Kv4Args &a, int dtype, bool pieces, bool wide, bool clear,
                             cudaStream_t stream) {
+  const int how = wide ? kWide : pieces ? kInPieces : kByOne;
   switch (dtype) {
-    case IDX_DTYPE_F32: return read_dim<float>(a, pieces, clear, stream);
-    case IDX_DTYPE_F16: return read_dim<__half>(a, pieces, clear, stream);
-    default: return read_dim<__nv_bfloat16>(a, pieces, clear, stream);
+    case IDX_DTYPE_F32: return read_dim<float>(a, how, clear, stream);
+    case IDX_DTYPE_F16: return read_dim<__half>(a, how, clear, stream);
+    default: return read_dim<__nv_bfloat16>(a, how, clear, stream);
   }
 }
 

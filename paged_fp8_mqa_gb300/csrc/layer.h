@@ -179,8 +179,9 @@ struct Kv4Args {
 // pieces: rows may be read (written) eight elements at a time; turns: the rotated part too.
 cudaError_t launch_kv4_append(const Kv4Args &a, int dtype, bool pieces, bool turns,
                               cudaStream_t stream);
-// clear: rows that hold nothing become zeros.
-cudaError_t launch_kv4_read(const Kv4Args &a, int dtype, bool pieces, bool clear, cudaStream_t stream);
+// pieces, wide: rows may be written 16, 32 bytes at a time; clear: rows that hold nothing become zeros.
+cudaError_t launch_kv4_read(const Kv4Args &a, int dtype, bool pieces, bool wide, bool clear,
+                            cudaStream_t stream);
 
 // Device-side status words (IDX_DEV_* bits) of the translation units above.
 cudaError_t rotary_status(int32_t *value, bool clear);
