@@ -1,4 +1,4 @@
-// attention_kernel.cuh -- attention over the 8-bit K/V cache: for row (b, t) and query head h with
+// attention_kernel.cuh -- attention over the 8-bit and the 4-bit K/V cache: for row (b, t) and query head h with
 // K/V head g = h / (heads / kv_heads),
 //   z_p = scale * ks[page(p), g] * (q . k_p),  out = sum_p softmax(z)_p * vs[page(p), g] * v_p
 // over the positions p <= seq_lens[b] - next_n + t, or over those of them that the select stored
@@ -35,6 +35,31 @@
 // The tiles of all (request, K/V head) groups in one line are cut into equal runs, one for each CTA
 // of the grid; a group that a run's end cuts leaves partial sums in the workspace and a second
 // launch joins them in order.  Every wait has a limit; nothing waits on another CTA.
+//
+// The 4-bit cache (FP4) is not converted either.  A key's scales, one for each 32 elements, are what the
+// tensor core's block scaling takes: S^T = K Q^T is kind::mxf8f6f4 with K as e2m1 and its scale bytes copied
+// from shared to tensor memory, Q's parts as e5m2 with the constant scale 2^-14; so S comes scaled and
+// only softmax_scale is left to the rows.  A value row's float32 scale goes into the weight, as a block's
+// does above, and O^T = V^T P^T is kind::f8f6f4 with V as e2m1.  Both read e2m1 from the padded layout, a
+// byte an element, sixteen of them in every sixteen, which the TMA unit writes from the packed rows: a tile
+// takes as much shared memory, and as many of its cycles, as in 8 bits, for half the bytes of memory.
+//   * The TMA unit pads rows of 128 elements.  Selected rows, and rows of 64, are fetched packed, 16 bytes
+//     a copy, into a ring of their own and spread by the warp that asked for them.
+//   * Keys and values have rings of their own: a key's stage is free once its scores are there, a tile's
+//     worth of time before its values' is, and stages are what bounds the loads in flight.
+//   * Scales: with whole pages by bulk copies (a page's are one run), with selected rows beside the rows.
+//     What a position's scales give its weights (a logarithm, a reciprocal) its softmax thread works out while
+//     its scores come.
+//   * The MMA warp waits on the next tile's keys and on this tile's weights at once (test_wait and a short
+//     try_wait in turn): scores of the next tile go ahead of the product of this one when they can.
+// What bounds it, head_dim 128, whole pages (DRAM rates of the copy): with few rows (64 requests of
+// 1K..32K, 8 rows: 218 us for 173) the shared memory's port, 312 cycles for a tile's writes, 161 for each read
+// by the tensor core, and what separates them, of 870 that a tile takes on an SM; with 32 rows (draft
+// verification, 179 us for 87) the same with three reads of K and the weights' parts, and the softmax warps'
+// latency.  Selected rows: 64-byte rows and their scales from places of their own, of which DRAM moves twice
+// what is used (serving mix, 102 us for 27).  From L2 instead of DRAM decode takes 208 us.  Not kept:
+// prefetches into L2 by any unit (231 to 273 us), softmax warpgroups in turn on tiles (228 for 219), two or
+// more loading warps a ring (220), 8-byte copies of selected rows (serving 160 us).
 #pragma once
 
 #include <cuda_runtime.h>
