@@ -498,9 +498,11 @@ int attention(
   a.lse = lse;
   a.workspace = static_cast<float *>(workspace);
   CUtensorMap k_map{}, v_map{};  // (with candidates the rows are gathered without them)
-  if (candidates == nullptr && !(four && head_dim != 128)) {
-    const uint64_t rows = static_cast<uint64_t>(num_blocks) * kv_heads * block_size;
-    const uint32_t box = static_cast<uint32_t>(block_size);
+  if (candidates == nullptr) {
+    // (Rows of 128 elements in four bits: two tokens' of 64.)
+    const int tokens = four ? 128 / head_dim : 1;
+    const uint64_t rows = static_cast<uint64_t>(num_blocks) * kv_heads * (block_size / tokens);
+    const uint32_t box = static_cast<uint32_t>(block_size / tokens);
     for (const auto &m : {std::pair<CUtensorMap *, const uint8_t *>{&k_map, k_pool}, {&v_map, v_pool}}) {
       st = four ? idx::encode_rows4(m.first, m.second, rows, box)
                 : idx::encode_rows(m.first, m.second, rows, static_cast<uint32_t>(head_dim), box);

@@ -43,8 +43,9 @@
 // does above, and O^T = V^T P^T is kind::f8f6f4 with V as e2m1.  Both read e2m1 from the padded layout, a
 // byte an element, sixteen of them in every sixteen, which the TMA unit writes from the packed rows: a tile
 // takes as much shared memory, and as many of its cycles, as in 8 bits, for half the bytes of memory.
-//   * The TMA unit pads rows of 128 elements.  Selected rows, and rows of 64, are fetched packed, 16 bytes
-//     a copy, into a ring of their own and spread by the warp that asked for them.
+//   * The TMA unit pads rows of 128 elements.  Rows of 64 come to it two tokens at a time (PAIRS).  Selected
+//     rows, and rows of 64 where more than 16 rows of queries share them, are fetched packed, 16 bytes a
+//     copy, into a ring of their own and spread by the warp that asked for them.
 //   * Keys and values have rings of their own: a key's stage is free once its scores are there, a tile's
 //     worth of time before its values' is, and stages are what bounds the loads in flight.
 //   * Scales: with whole pages by bulk copies (a page's are one run), with selected rows beside the rows.
@@ -90,8 +91,16 @@ template <int D_, int R_, int PARTS_, bool SELECT_, bool FP4_>
 struct AttnCfg {
   static constexpr int D = D_, R = R_, PARTS = PARTS_;
   static constexpr bool SELECT = SELECT_, FP4 = FP4_;
-  // Rows by ordinary asynchronous copies, not by the TMA unit (whose 4-bit boxes are 128 elements wide).
-  static constexpr bool COPIES = SELECT || (FP4 && D != 128);
+  // Whole pages of rows of 64 in four bits, by the TMA unit, whose 4-bit boxes are 128 elements wide: two
+  // tokens a row.  A tile is then 256 positions, the first tokens of the pairs and the second ones, which have
+  // columns of S, weights and sums of their own; a softmax thread takes both positions of a pair, whose
+  // chains run side by side.  (Each by itself, tile after tile: 101 us for 78 with 32 requests of 4K..64K, 32
+  // heads on 4; rows by ordinary copies 133.  More rows have no columns for two of O.)
+  static constexpr bool PAIRS = FP4 && !SELECT && D == 64 && R <= 16;
+  static constexpr int SUBS = PAIRS ? 2 : 1, POS = kTile * SUBS;  // positions of a row, and of a tile
+  static constexpr int ROW = PAIRS ? 128 : D;         // bytes of a tile's row
+  // Rows by ordinary asynchronous copies, not by the TMA unit.
+  static constexpr bool COPIES = SELECT || (FP4 && D != 128 && !PAIRS);
   static constexpr int QPARTS = 3;                    // parts of a query
   // With R = 8 a query's parts stand side by side, in columns that are added when read (the last
   // eight of 32 mean nothing); else each part is a product of its own into the same columns.  (Three
@@ -109,8 +118,9 @@ struct AttnCfg {
   // a loader up is handing its copies to the TMA unit.
   static constexpr int LOADERS = !COPIES ? (FP4 && R <= 16 ? 2 : 1) : R == 32 ? 1 : R == 8 ? 4 : 2;
   static constexpr int THREADS = 32 * (LOADERS + 1 + SOFT_WARPS);
-  // Two of S, one of O; with FP4 the keys' scale factors, two tiles of them, and the queries' (1).
-  static constexpr int SFA = 2 * NS + NO, SFB = SFA + 8;
+  // Two of S, one of O (PAIRS: O of either token's weights with both tokens' values; half of each is
+  // used); with FP4 the keys' scale factors, two tiles of them, and the queries' (1).
+  static constexpr int OUT = 2 * SUBS * NS, SFA = OUT + SUBS * NO, SFB = SFA + 8;
   static constexpr int COLS = FP4 ? SFB + 4 : SFA;
   static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   // CTAs on an SM, each with a pipeline of its own, so that one's loads and products run beside the
@@ -118,9 +128,9 @@ struct AttnCfg {
   // what the next launch needs no longer fits beside them.  64 rows in chunks of 32, two CTAs an SM:
   // one long request 1.07 times as long, a batch of 64 requests with 64 heads on one 1.3 times.
   static constexpr int CTAS = R == 64 ? 1 : 2;
-  static constexpr int T_BYTES = kTile * D;           // a tile of K, or of V, as the products read it
+  static constexpr int T_BYTES = kTile * ROW;         // a tile of K, or of V, as the products read it
   static constexpr int Q_BYTES = NS * (CAT ? 1 : QPARTS) * D;
-  static constexpr int P_BYTES = NO * kTile;          // a tile's weights
+  static constexpr int P_BYTES = SUBS * NO * kTile;   // a tile's weights
   // They take the place of the tile's keys, which have been read by then, where they fit it; else
   // they have buffers of their own.  (FP4: always, see below.)
   static constexpr bool OVER_K = !FP4 && P_BYTES <= kTile * D;
@@ -131,7 +141,7 @@ struct AttnCfg {
   // and of V holds besides: Token records, or (FP4, by the TMA unit) value scales, scale factors and
   // which of the tokens are there.
   static constexpr int K_AUX = !FP4 ? 0 : COPIES ? kTile * 4 : kTile * 8;
-  static constexpr int V_AUX = FP4 ? kTile * 8 + (COPIES ? 0 : 16) : kTile * 16;
+  static constexpr int V_AUX = FP4 ? kTile * 4 * (SUBS + 1) + (COPIES ? 0 : 16) : kTile * 16;
   static constexpr int MISC = 48 * R + (FP4 ? 0 : 3 * D * 4) + 256;
   static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_BYTES + MISC;
   static constexpr int ROOM = CTAS == 2 ? 115456 : 231424;
@@ -152,6 +162,7 @@ struct AttnCfg {
   static constexpr int RAW = RAW_FIT > 6 ? 6 : RAW_FIT;
   static constexpr int SMEM = FIXED + K_ROOM + V_ROOM + RAW * RAW_BYTES;
   static_assert(VS >= 2 && (RAW_BYTES == 0 || RAW >= 1) && SMEM <= 232448, "fits the 227 KiB per-CTA limit");
+  static_assert(!PAIRS || (WG == 1 && R * D * 4 <= P_BUFS * P_BYTES), "room for the second tokens' sums");
   static_assert(Q_BYTES % 1024 == 0 && (!CAT || PARTS == 3), "aligned; eight rows: three parts");
 };
 
@@ -324,19 +335,20 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t n, uint32_t x) {
 
 // Keys of the line of groups: a request (all its draft slots see one list of positions), or with
 // SELECT a row.  Each has kv_heads * chunks groups.
-template <bool SELECT>
+template <class C>
 __device__ __forceinline__ int key_length(const AttentionArgs &a, int key) {
-  if constexpr (SELECT) {
+  if constexpr (C::SELECT) {
     const int rows = a.batch * a.next_n;
     const int lo = max(0, __ldg(a.ranges + key));
     return max(0, min(__ldg(a.ranges + rows + key), a.slots) - lo);
   } else {
-    return max(0, min(__ldg(a.seq_lens + key * a.sl_stride), INT_MAX - kTile));
+    return max(0, min(__ldg(a.seq_lens + key * a.sl_stride), INT_MAX - C::POS));
   }
 }
 
+template <class C>
 __device__ __forceinline__ int tiles_for(int length) {
-  return length / kTile + (length % kTile != 0);
+  return length / C::POS + (length % C::POS != 0);
 }
 
 // A place in a ring of N stages, and the parity of its present use.
@@ -354,7 +366,7 @@ struct Ring {
 
 // A CTA's run over the line: the segments (group, first tile, tiles) in order.  Every warp walks
 // its own copy, all its lanes together: keys without positions are passed over 32 at a time.
-template <bool SELECT>
+template <class C>
 struct Walk {
   int64_t left;  // tiles of the run not yet handed out
   int key, group, tile, length, tiles;
@@ -368,7 +380,7 @@ struct Walk {
         group = 0;
         const int lane = threadIdx.x & 31;
         for (;;) {
-          const int n = key + 1 + lane < keys ? key_length<SELECT>(a, key + 1 + lane) : 0;
+          const int n = key + 1 + lane < keys ? key_length<C>(a, key + 1 + lane) : 0;
           const unsigned some = __ballot_sync(0xffffffffu, n > 0);
           if (some != 0) {
             const int at = __ffs(some) - 1;
@@ -379,7 +391,7 @@ struct Walk {
           key += 32;
           if (key >= keys) return false;  // (lengths that changed under the call)
         }
-        tiles = tiles_for(length);
+        tiles = tiles_for<C>(length);
       }
     }
     seg_tile = tile;
@@ -448,7 +460,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   };
   uint8_t *s_q = base + (C::KS + C::VS) * C::T_BYTES;  // [QPARTS * R][D], K-major, swizzled
   uint8_t *at = s_q + C::Q_BYTES;
-  // A tile's weights, [NO / 16][kTile][16].
+  // A tile's weights, [SUBS][NO / 16][kTile][16].
   uint8_t *s_p = at;
   at += C::P_BUFS * C::P_BYTES;
   const auto weights_of = [&](uint32_t tile, int stage) {
@@ -530,7 +542,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   const int per = (keys + C::THREADS - 1) / C::THREADS;
   const int k_lo = min(tid * per, keys), k_hi = min(k_lo + per, keys);
   int64_t mine = 0;
-  for (int k = k_lo; k < k_hi; ++k) mine += tiles_for(key_length<C::SELECT>(a, k));
+  for (int k = k_lo; k < k_hi; ++k) mine += tiles_for<C>(key_length<C>(a, k));
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -557,7 +569,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   }
   if (f0 < f1 && f0 >= before * groups && f0 < (before + mine) * groups) {
     for (int k = k_lo; k < k_hi; ++k) {
-      const int n = tiles_for(key_length<C::SELECT>(a, k));
+      const int n = tiles_for<C>(key_length<C>(a, k));
       if (f0 < (before + n) * groups) {
         s_key = k;
         s_begin = f0 - before * groups;
@@ -569,13 +581,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   __syncthreads();
 
   const uint32_t tmem = *s_tmem;
-  Walk<C::SELECT> w;
+  Walk<C> w;
   w.left = f1 - f0;
   w.seg_tile = w.seg_tiles = 0;
   if (w.left > 0) {
     w.key = s_key;
-    w.length = key_length<C::SELECT>(a, w.key);
-    w.tiles = tiles_for(w.length);
+    w.length = key_length<C>(a, w.key);
+    w.tiles = tiles_for<C>(w.length);
     const int64_t at0 = s_begin;
     w.group = at0 < INT_MAX ? static_cast<int>(at0) / w.tiles : static_cast<int>(at0 / w.tiles);
     w.tile = static_cast<int>(at0 - static_cast<int64_t>(w.group) * w.tiles);
@@ -859,6 +871,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     } else if constexpr (C::FP4) {
       const bool leader = elect_one(), keys_too = C::LOADERS == 1 || warp == 0,
                  values_too = C::LOADERS == 1 || warp != 0;
+      const int sh = C::PAIRS ? shift - 1 : shift;  // rows of a page, of tokens or pairs of them
       while (ok && w.next(a, groups, keys)) {
         const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
         const int32_t *table = a.block_tables + m.b * a.bt_stride;
@@ -867,7 +880,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // operands (as many threads' they come one after the other, each with operands of its own): the
         // loader's instructions are what paces the tiles.
         const int n_pages = (w.length + a.block_size - 1) >> shift;
-        const int per_tile = kTile >> shift;
+        const int per_tile = kTile >> sh;
         int first = w.seg_tile * per_tile;  // the page of lane 0
         const auto ids = [&](int page) {
           if (page >= n_pages || page >= (w.seg_tile + w.seg_tiles) * per_tile) return -1;
@@ -884,20 +897,20 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             id = id_next;
             id_next = ids(first + 32 + lane);
           }
-          // The pool's row of the first token of the page that holds this lane's four tokens, or -1.
-          const int block = __shfl_sync(0xffffffffu, id, i * per_tile + ((lane * 4) >> shift) - first);
-          const int page4 = block < 0 ? -1 : (block * a.kv_heads + m.g) << shift;
-          const unsigned there = __ballot_sync(0xffffffffu, page4 >= 0);  // bit t / 4: token t's page is there
-          const int bytes = (D / 2) * 4 * __popc(there);
-          const int row4 = page4 + ((lane * 4) & (a.block_size - 1));
+          // The pool's first row of the page that holds this lane's four rows, or -1.
+          const int block = __shfl_sync(0xffffffffu, id, i * per_tile + ((lane * 4) >> sh) - first);
+          const int page4 = block < 0 ? -1 : (block * a.kv_heads + m.g) << sh;
+          const unsigned there = __ballot_sync(0xffffffffu, page4 >= 0);  // bit r / 4: row r's page is there
+          const int bytes = (C::ROW / 2) * 4 * __popc(there);
+          const int row4 = page4 + ((lane * 4) & ((1 << sh) - 1));
           if (keys_too) {
             if (!stage_free()) break;
             // (The barrier counts the bytes read, half of those that the rows take here.)
             if (leader) mbar_arrive_expect_tx(&k_full[kr.at], bytes);
             for (int pg = 0; pg < per_tile; ++pg) {
-              const int row = __shfl_sync(0xffffffffu, page4, pg << (shift - 2));
+              const int row = __shfl_sync(0xffffffffu, page4, pg << (sh - 2));
               if (leader && row >= 0)
-                tma_load_2d(k_tile(kr.at) + (pg << shift) * D, &k_map, &k_full[kr.at], 0, row, policy);
+                tma_load_2d(k_tile(kr.at) + (pg << sh) * C::ROW, &k_map, &k_full[kr.at], 0, row, policy);
             }
             if (page4 >= 0)
               cp_async_16(s_sf + (kr.at * 2 + 1) * kTile + lane * 4,
@@ -909,17 +922,19 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             if (!free_now(&v_empty[vr.at], vr.phase)) break;
             uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
             if (leader) {
-              aux[2 * kTile] = there;
+              aux[C::POS + kTile] = there;
               mbar_arrive_expect_tx(&v_full[vr.at], bytes);
             }
             for (int pg = 0; pg < per_tile; ++pg) {
-              const int row = __shfl_sync(0xffffffffu, page4, pg << (shift - 2));
+              const int row = __shfl_sync(0xffffffffu, page4, pg << (sh - 2));
               if (leader && row >= 0)
-                tma_load_2d(v_tile(vr.at) + (pg << shift) * D, &v_map, &v_full[vr.at], 0, row, policy);
+                tma_load_2d(v_tile(vr.at) + (pg << sh) * C::ROW, &v_map, &v_full[vr.at], 0, row, policy);
             }
             if (page4 >= 0) {
-              cp_async_16(aux + lane * 4, a.v_scales + row4, policy);
-              cp_async_16(aux + kTile + lane * 4, static_cast<const uint32_t *>(a.k_scales) + row4, policy);
+#pragma unroll
+              for (int j = 0; j < C::SUBS; ++j)
+                cp_async_16(aux + lane * 4 * C::SUBS + j * 4, a.v_scales + row4 * C::SUBS + j * 4, policy);
+              cp_async_16(aux + C::POS + lane * 4, static_cast<const uint32_t *>(a.k_scales) + row4, policy);
             }
             cp_async_arrive_noinc(&v_full[vr.at]);
             ++issued_v;
@@ -996,30 +1011,33 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     // ============================== MMA issuer ==================================================
     constexpr uint32_t idesc_s = idesc_e4m3_f32(kTile, NS) | kE5m2_B;
     constexpr uint32_t idesc_o =
-        idesc_e4m3_f32(D, C::NO) | kE5m2_B | kMajorMN_A | kMajorMN_B | (C::FP4 ? kE2m1_A : 0u);
+        idesc_e4m3_f32(C::ROW, C::NO) | kE5m2_B | kMajorMN_A | kMajorMN_B | (C::FP4 ? kE2m1_A : 0u);
     const uint64_t q_desc = smem_desc_rows<D>(smem_addr(s_q));
-    const uint32_t o_tmem = tmem + 2 * NS;
+    const uint32_t o_tmem = tmem + C::OUT;
     uint32_t tile = 0, seg = 0;
     const bool leader = elect_one();
     const auto all_wait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs)) != 0;
     };
     const auto scores = [&](uint32_t n, int st) {  // S of tile n of the run, from stage st
-      const uint64_t k_desc = smem_desc_rows<D>(smem_addr(k_tile(st)));
+      const uint64_t k_desc = smem_desc_rows<C::ROW>(smem_addr(k_tile(st)));
       const uint32_t factors = tmem + C::SFA + (n & 1) * 4;
       if (!leader) return;
       if constexpr (C::FP4) tmem_copy_factors(factors, smem_desc_factors(smem_addr(s_sf + st * (C::K_AUX / 4))));
 #pragma unroll
-      for (int part = 0; part < C::PASSES; ++part)
+      for (int sub = 0; sub < C::SUBS; ++sub)
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const uint64_t q_at = q_desc + part * (R * D >> 4) + 2 * k;
-          if constexpr (C::FP4)
-            mma_mxf8f6f4(tmem + (n & 1) * NS, k_desc + 2 * k, q_at, idesc_mx(kTile, NS, k), factors,
-                         tmem + C::SFB, part + k > 0);
-          else
-            mma_f8f6f4(tmem + (n & 1) * NS, k_desc + 2 * k, q_at, idesc_s, part + k > 0);
-        }
+        for (int part = 0; part < C::PASSES; ++part)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            const uint32_t to = tmem + ((n & 1) * C::SUBS + sub) * NS;
+            const uint64_t k_at = k_desc + sub * (D >> 4) + 2 * k, q_at = q_desc + part * (R * D >> 4) + 2 * k;
+            if constexpr (C::FP4)
+              mma_mxf8f6f4(to, k_at, q_at, idesc_mx(kTile, NS, sub * (D / 32) + k), factors, tmem + C::SFB,
+                           part + k > 0);
+            else
+              mma_f8f6f4(to, k_at, q_at, idesc_s, part + k > 0);
+          }
       mma_commit(&s_full[n & 1]);
       if constexpr (C::FP4) mma_commit(&k_empty[st]);
     };
@@ -1068,12 +1086,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if (C::FP4 && !all_wait(&v_full[vr.at], vr.phase)) return false;
         if constexpr (C::FP4) fence_proxy_async_shared();
         tc_fence_after_sync();
-        const uint64_t v_desc = smem_desc_mn<D>(smem_addr(v_tile(C::FP4 ? vr.at : kr.at)));
+        const uint64_t v_desc = smem_desc_mn<C::ROW>(smem_addr(v_tile(C::FP4 ? vr.at : kr.at)));
         const uint64_t p_desc = smem_desc_p(smem_addr(weights_of(tile, kr.at)));
         if (leader) {
 #pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
-            mma_f8f6f4(o_tmem, v_desc + k * (32 * D >> 4), p_desc + k * (512 >> 4), idesc_o, i + k > 0);
+          for (int sub = 0; sub < C::SUBS; ++sub)
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+              mma_f8f6f4(o_tmem + sub * C::NO, v_desc + k * (32 * C::ROW >> 4),
+                         p_desc + sub * (C::NO * kTile >> 4) + k * (512 >> 4), idesc_o, i + k > 0);
           mma_commit(&pv_done[tile & 1]);
           mma_commit(C::FP4 ? &v_empty[vr.at] : &k_empty[kr.at]);
         }
@@ -1093,8 +1114,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const int wg = (warp - 2) >> 2, quarter = warp & 3;
     const int r0 = wg * RT;                      // the thread's rows
     const int token = quarter * 32 + lane;       // the thread's position in the tile
-    // The thread's dimension of the output, or -1 (M = 64: 16 lanes of each quarter).
-    const int dim = D == 128 ? token : lane < 16 ? quarter * 16 + lane : -1;
+    // The thread's dimension of the output, or -1 (M = 64: 16 lanes of each quarter; PAIRS: the first tokens'
+    // values, to which the second tokens' sums are added).
+    const int dim = C::ROW == 128 ? (token < D ? token : -1) : lane < 16 ? quarter * 16 + lane : -1;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float z_unit = a.scale * 1.4426950408889634f;  // (FP4: what the tokens' keys share)
     uint32_t tile = 0;
@@ -1218,81 +1240,100 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
         }
         tc_fence_after_sync();
-        Token tok;
-        float2 y[RT / 2];  // the weights' logarithms
+        Token tok[C::SUBS];
+        float2 y[C::SUBS][RT / 2];  // the weights' logarithms
         {
-          uint32_t v[RT], u[C::CAT ? RT : 8], t[C::CAT ? RT : 8];
-          tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + r0, v);
-          if constexpr (C::CAT) {
-            tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + R, u);
-            tmem_ld_cols<RT>(lane_base + (tile & 1) * NS + 2 * R, t);
+          uint32_t v[C::SUBS][RT], u[C::SUBS][C::CAT ? RT : 8], t[C::SUBS][C::CAT ? RT : 8];
+#pragma unroll
+          for (int sub = 0; sub < C::SUBS; ++sub) {
+            const uint32_t s_at = lane_base + ((tile & 1) * C::SUBS + sub) * NS;
+            tmem_ld_cols<RT>(s_at + r0, v[sub]);
+            if constexpr (C::CAT) {
+              tmem_ld_cols<RT>(s_at + R, u[sub]);
+              tmem_ld_cols<RT>(s_at + 2 * R, t[sub]);
+            }
           }
           // (While they come: what the position brings.)
-          if constexpr (C::FP4) {
-            Token4 t4;
-            if constexpr (C::COPIES) {
-              t4 = s_tok4[vr.at * kTile + token];
+#pragma unroll
+          for (int sub = 0; sub < C::SUBS; ++sub) {
+            if constexpr (C::FP4) {
+              Token4 t4;
+              if constexpr (C::COPIES) {
+                t4 = s_tok4[vr.at * kTile + token];
+              } else {
+                const uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
+                const int p = (w.seg_tile + i) * C::POS + token * C::SUBS + sub;
+                uint32_t factors = aux[C::POS + token];
+                if constexpr (C::PAIRS) factors = (factors >> (16 * sub)) & 0xFFFFu;
+                t4.v_scale = scale_of<D>(factors, __uint_as_float(aux[token * C::SUBS + sub]));
+                t4.pos = ((aux[C::POS + kTile] >> (token / 4)) & 1u) != 0 && p < len ? p : kNone;
+              }
+              tok[sub] = token_of<true>(1.0f, t4.v_scale, t4.pos);
             } else {
-              const uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
-              const int p = (w.seg_tile + i) * kTile + token;
-              t4.v_scale = scale_of<D>(aux[kTile + token], __uint_as_float(aux[token]));
-              t4.pos = ((aux[2 * kTile] >> (token / 4)) & 1u) != 0 && p < len ? p : kNone;
+              tok[sub] = s_tok[kr.at * kTile + token];
             }
-            tok = token_of<true>(1.0f, t4.v_scale, t4.pos);
-          } else {
-            tok = s_tok[kr.at * kTile + token];
           }
-          if constexpr (C::CAT) {
-            tmem_ld_wait();
-            reg_fence(v);
-            reg_fence(u);
-            reg_fence(t);
+          tmem_ld_wait();
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-              v[r] = __float_as_uint(__uint_as_float(v[r]) +
-                                     (__uint_as_float(u[r]) + __uint_as_float(t[r])));
-          } else {
-            tmem_ld_wait();
-            reg_fence(v);
-          }
-          const float2 k2 = make_float2(tok.k, tok.k), lv2 = make_float2(tok.log_v, tok.log_v);
+          for (int sub = 0; sub < C::SUBS; ++sub) {
+            reg_fence(v[sub]);
+            if constexpr (C::CAT) {
+              reg_fence(u[sub]);
+              reg_fence(t[sub]);
 #pragma unroll
-          for (int r = 0; r < RT / 2; r += 2) {
-            float4 f;
-            if constexpr (kHoldRs)
-              f = make_float4(rs[r].x, rs[r].y, rs[r + 1].x, rs[r + 1].y);
-            else
-              f = *reinterpret_cast<const float4 *>(rs_at + r);
+              for (int r = 0; r < RT; ++r)
+                v[sub][r] = __float_as_uint(__uint_as_float(v[sub][r]) +
+                                            (__uint_as_float(u[sub][r]) + __uint_as_float(t[sub][r])));
+            }
+            const float2 k2 = make_float2(tok[sub].k, tok[sub].k);
+            const float2 lv2 = make_float2(tok[sub].log_v, tok[sub].log_v);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float2 s2 = make_float2(__uint_as_float(v[2 * (r + h)]),
-                                            __uint_as_float(v[2 * (r + h) + 1]));
-              const float2 unit = h ? make_float2(f.z, f.w) : make_float2(f.x, f.y);
-              // (FP4: the tensor core has applied the key's scale, and unit holds the rest.)
-              y[r + h] = __ffma2_rn(s2, C::FP4 ? unit : __fmul2_rn(unit, k2), __fadd2_rn(lv2, nref[r + h]));
+            for (int r = 0; r < RT / 2; r += 2) {
+              float4 f;
+              if constexpr (kHoldRs)
+                f = make_float4(rs[r].x, rs[r].y, rs[r + 1].x, rs[r + 1].y);
+              else
+                f = *reinterpret_cast<const float4 *>(rs_at + r);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float2 s2 = make_float2(__uint_as_float(v[sub][2 * (r + h)]),
+                                              __uint_as_float(v[sub][2 * (r + h) + 1]));
+                const float2 unit = h ? make_float2(f.z, f.w) : make_float2(f.x, f.y);
+                // (FP4: the tensor core has applied the key's scale, and unit holds the rest.)
+                y[sub][r + h] = __ffma2_rn(s2, C::FP4 ? unit : __fmul2_rn(unit, k2),
+                                           __fadd2_rn(lv2, nref[r + h]));
+              }
             }
           }
         }
-        const bool seen = tok.pos < all_see;
-        if (!__all_sync(0xffffffffu, seen)) {
-          if (!seen) {
+        bool all_seen = true;
 #pragma unroll
-            for (int r = 0; r < RT / 2; ++r) {
-              if (tok.pos >= s_ext[r0 + 2 * r]) y[r].x = -INFINITY;
-              if (tok.pos >= s_ext[r0 + 2 * r + 1]) y[r].y = -INFINITY;
+        for (int sub = 0; sub < C::SUBS; ++sub) all_seen = all_seen && tok[sub].pos < all_see;
+        if (!__all_sync(0xffffffffu, all_seen)) {
+#pragma unroll
+          for (int sub = 0; sub < C::SUBS; ++sub)
+            if (!(tok[sub].pos < all_see)) {
+#pragma unroll
+              for (int r = 0; r < RT / 2; ++r) {
+                if (tok[sub].pos >= s_ext[r0 + 2 * r]) y[sub][r].x = -INFINITY;
+                if (tok[sub].pos >= s_ext[r0 + 2 * r + 1]) y[sub][r].y = -INFINITY;
+              }
             }
-          }
         }
-        float most = fmaxf(y[0].x, y[0].y);
+        // The larger of a row's logarithms at the thread's positions.
+        const auto top = [&](int r) {
+          float x = r & 1 ? y[0][r / 2].y : y[0][r / 2].x;
 #pragma unroll
-        for (int r = 1; r < RT / 2; ++r) most = fmaxf(most, fmaxf(y[r].x, y[r].y));
+          for (int sub = 1; sub < C::SUBS; ++sub) x = fmaxf(x, r & 1 ? y[sub][r / 2].y : y[sub][r / 2].x);
+          return x;
+        };
+        float most = top(0);
+#pragma unroll
+        for (int r = 1; r < RT; ++r) most = fmaxf(most, top(r));
         bool move = most > kMost;
         if (unset != 0) {
 #pragma unroll
-          for (int r = 0; r < RT / 2; ++r) {
-            move |= ((unset >> (2 * r)) & 1u) != 0 && y[r].x != -INFINITY;
-            move |= ((unset >> (2 * r + 1)) & 1u) != 0 && y[r].y != -INFINITY;
-          }
+          for (int r = 0; r < RT; ++r) move |= ((unset >> r) & 1u) != 0 && top(r) != -INFINITY;
         }
         if (any_of_group(move)) {
           // Some weight would leave e5m2's range, or a row sees its first position: the references
@@ -1300,7 +1341,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           float mine = -INFINITY;  // lane r: row r0 + r
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
-            const float x = warp_max(r & 1 ? y[r / 2].y : y[r / 2].x);
+            const float x = warp_max(top(r));
             if (lane == r) mine = x;
           }
           if (lane < RT) s_max[(r0 + lane) * 4 + quarter] = mine;
@@ -1324,7 +1365,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           for (int r = 0; r < RT / 2; ++r) {
             const float2 d = make_float2(-__shfl_sync(0xffffffffu, up, 2 * r),
                                          -__shfl_sync(0xffffffffu, up, 2 * r + 1));
-            y[r] = __fadd2_rn(y[r], d);
+#pragma unroll
+            for (int sub = 0; sub < C::SUBS; ++sub) y[sub][r] = __fadd2_rn(y[sub][r], d);
             nref[r] = __fadd2_rn(nref[r], d);
             sum[r].x *= __shfl_sync(0xffffffffu, keep, 2 * r);
             sum[r].y *= __shfl_sync(0xffffffffu, keep, 2 * r + 1);
@@ -1333,8 +1375,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
             tc_fence_after_sync();
 #pragma unroll 1
-            for (int part = 0; part < PARTS; ++part) {
-              const uint32_t o_at = lane_base + 2 * NS + part * R + r0;
+            for (int part = 0; part < PARTS * C::SUBS; ++part) {
+              const uint32_t o_at =
+                  lane_base + C::OUT + (part < PARTS ? part * R : C::NO + (part - PARTS) * R) + r0;
               uint32_t v[RT];
               tmem_ld_cols<RT>(o_at, v);
               tmem_ld_wait();
@@ -1356,45 +1399,48 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         } else {
           if (tile >= 2) wait(&pv_done[tile & 1], ((tile >> 1) - 1) & 1);
         }
-        uint8_t *sp = weights_of(tile, kr.at) + token * 16;
-        const float inv_v = fabsf(tok.inv_v);
-        // The weights of a position whose value scale is negative or 0 (as good as): rare, so asked
-        // of the whole warp.
-        const bool odd = __any_sync(0xffffffffu, tok.inv_v < 0.0f || inv_v >= 1.0f / kLeastScale);
-        const uint32_t flip = tok.inv_v < 0.0f ? 0x80808080u : 0u;
-        const uint32_t live = inv_v < 1.0f / kLeastScale ? 0xFFFFFFFFu : 0u;
-        uint32_t bytes[PARTS][4];
-        const float2 inv2 = make_float2(inv_v, inv_v);
 #pragma unroll
-        for (int r = 0; r < RT; r += 4) {
-          float2 p[2];
+        for (int sub = 0; sub < C::SUBS; ++sub) {
+          uint8_t *sp = weights_of(tile, kr.at) + sub * (C::NO * kTile) + token * 16;
+          const float inv_v = fabsf(tok[sub].inv_v);
+          // The weights of a position whose value scale is negative or 0 (as good as): rare, so asked
+          // of the whole warp.
+          const bool odd = __any_sync(0xffffffffu, tok[sub].inv_v < 0.0f || inv_v >= 1.0f / kLeastScale);
+          const uint32_t flip = tok[sub].inv_v < 0.0f ? 0x80808080u : 0u;
+          const uint32_t live = inv_v < 1.0f / kLeastScale ? 0xFFFFFFFFu : 0u;
+          uint32_t bytes[PARTS][4];
+          const float2 inv2 = make_float2(inv_v, inv_v);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            p[j] = make_float2(fast_exp2(y[r / 2 + j].x), fast_exp2(y[r / 2 + j].y));
-            sum[r / 2 + j] = __ffma2_rn(p[j], inv2, sum[r / 2 + j]);
-          }
-          uint32_t four[PARTS];
-          weight_parts<PARTS>(p[0], p[1], four);
+          for (int r = 0; r < RT; r += 4) {
+            float2 p[2];
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part) bytes[part][(r / 4) % 4] = four[part];
-          if (odd && (r % 16 == 12 || r + 4 == RT)) {
-#pragma unroll
-            for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-              for (int q = 0; q < (RT < 16 ? RT / 4 : 4); ++q)
-                bytes[part][q] = (bytes[part][q] & live) ^ flip;
-          }
-          if constexpr (C::CAT) {  // a group of 16 n: the first two parts of the eight rows; then the third
-            if (r == 4) {
-              *reinterpret_cast<uint4 *>(sp) =
-                  make_uint4(bytes[0][0], bytes[0][1], bytes[1][0], bytes[1][1]);
-              *reinterpret_cast<uint2 *>(sp + kTile * 16) = make_uint2(bytes[2][0], bytes[2][1]);
+            for (int j = 0; j < 2; ++j) {
+              p[j] = make_float2(fast_exp2(y[sub][r / 2 + j].x), fast_exp2(y[sub][r / 2 + j].y));
+              sum[r / 2 + j] = __ffma2_rn(p[j], inv2, sum[r / 2 + j]);
             }
-          } else if (r % 16 == 12) {
+            uint32_t four[PARTS];
+            weight_parts<PARTS>(p[0], p[1], four);
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
-              *reinterpret_cast<uint4 *>(sp + (part * R + r0 + r - 12) / 16 * (kTile * 16)) =
-                  make_uint4(bytes[part][0], bytes[part][1], bytes[part][2], bytes[part][3]);
+            for (int part = 0; part < PARTS; ++part) bytes[part][(r / 4) % 4] = four[part];
+            if (odd && (r % 16 == 12 || r + 4 == RT)) {
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                for (int q = 0; q < (RT < 16 ? RT / 4 : 4); ++q)
+                  bytes[part][q] = (bytes[part][q] & live) ^ flip;
+            }
+            if constexpr (C::CAT) {  // a group of 16 n: the first two parts of the eight rows; then the third
+              if (r == 4) {
+                *reinterpret_cast<uint4 *>(sp) =
+                    make_uint4(bytes[0][0], bytes[0][1], bytes[1][0], bytes[1][1]);
+                *reinterpret_cast<uint2 *>(sp + kTile * 16) = make_uint2(bytes[2][0], bytes[2][1]);
+              }
+            } else if (r % 16 == 12) {
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part)
+                *reinterpret_cast<uint4 *>(sp + (part * R + r0 + r - 12) / 16 * (kTile * 16)) =
+                    make_uint4(bytes[part][0], bytes[part][1], bytes[part][2], bytes[part][3]);
+            }
           }
         }
         // A value that some row does not see must not meet its weight of 0 as a NaN (a code of the
@@ -1402,9 +1448,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // tokens, which only the later draft slots see, a NaN becomes 0 and is noted in s_nan (as
         // this segment's number) for the rows that do see it.
         // (Four bits hold no NaN.)
-        if (!C::FP4 && wg == 0 && !seen) {
+        if (!C::FP4 && wg == 0 && !all_seen) {
           uint8_t *v = v_tile(kr.at);
-          if (tok.pos == kNone) {
+          if (tok[0].pos == kNone) {
             for (int x = 0; x < D; x += 16)
               *reinterpret_cast<uint4 *>(v + token * D + x) = make_uint4(0, 0, 0, 0);
           } else {
@@ -1415,7 +1461,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               for (int e = 0; e < 4; ++e)
                 if (((four >> (8 * e)) & 0x7F) == 0x7F) {
                   v[at4 + e] = 0;
-                  s_nan[(len - 1 - tok.pos) * D + x + e] = seg;
+                  s_nan[(len - 1 - tok[0].pos) * D + x + e] = seg;
                 }
             }
           }
@@ -1434,7 +1480,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
       for (int part = PARTS - 1; part >= 0; --part) {
         uint32_t v[RT];
-        tmem_ld_cols<RT>(lane_base + 2 * NS + part * R + r0, v);
+        // (PAIRS: the upper lanes' are the second tokens' dimensions, and the second tiles' weights'.)
+        tmem_ld_cols<RT>(lane_base + C::OUT + (C::PAIRS && token >= D ? C::NO : 0) + part * R + r0, v);
         tmem_ld_wait();
         reg_fence(v);
 #pragma unroll
@@ -1476,7 +1523,22 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         for (int o = RT; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
         if (lane < RT) s_sum[(r0 + lane) * 4 + quarter] = v[0];
       }
+      // (The weights' place is free: their products are done, and the next segment's come after its
+      // queries, for which every warp waits.)
+      float *half = reinterpret_cast<float *>(s_p);
+      if constexpr (C::PAIRS) {
+        if (token >= D) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) half[r * D + token - D] = acc[r];
+        }
+      }
       sync_group();
+      if constexpr (C::PAIRS) {
+        if (token < D) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[r] += half[r * D + token];
+        }
+      }
       float l = 0.0f;  // lane r: the sum of row r0 + r
       if (lane < RT) {
         const float4 t4 = *reinterpret_cast<const float4 *>(s_sum + (r0 + lane) * 4);
@@ -1520,7 +1582,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
   // Keys without positions: their rows are zeros, their groups have no parts.
   for (int k = blockIdx.x; k < keys; k += gridDim.x) {
-    if (key_length<C::SELECT>(a, k) > 0) continue;
+    if (key_length<C>(a, k) > 0) continue;
     for (int g = tid; g < groups; g += C::THREADS)
       parts[static_cast<int64_t>(k) * groups + g] = GroupParts{0, 0};
     const int slots = C::SELECT ? 1 : a.next_n;

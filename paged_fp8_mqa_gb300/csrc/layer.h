@@ -113,8 +113,8 @@ cudaError_t launch_attention_d64(const CUtensorMap &k_map, const CUtensorMap &v_
                                  const AttentionArgs &a, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_attention_d128(const CUtensorMap &k_map, const CUtensorMap &v_map,
                                   const AttentionArgs &a, int dtype, int sms, cudaStream_t stream);
-// The same over a cache held in four bits (k_map, v_map: rows of 128 elements; not read with
-// head_dim 64 either).
+// The same over a cache held in four bits (k_map, v_map: rows of 128 elements, with head_dim 64 two
+// tokens').
 cudaError_t launch_attention4_d64(const CUtensorMap &k_map, const CUtensorMap &v_map,
                                   const AttentionArgs &a, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_attention4_d128(const CUtensorMap &k_map, const CUtensorMap &v_map,
