@@ -16,16 +16,17 @@ cudaError_t attention_d128_status(int32_t *value, bool clear) {
 
 int64_t attention_workspace(int batch, int next_n, int heads, int kv_heads, int dim, int sms) {
   int64_t most = 0;
-  for (const bool f16 : {false, true})
-    for (const bool select : {false, true}) {
-      const AttnShape s = attn_shape(heads / kv_heads * (select ? 1 : next_n), f16);
-      const int on_sm = dim == 64 ? ctas_for<64, false, false>(s.r, f16) : ctas_for<128, false, false>(s.r, f16);
-      const int64_t groups =
-          static_cast<int64_t>(select ? batch * next_n : batch) * kv_heads * s.chunks;
-      const int64_t bytes = attn_slots_bytes(static_cast<int64_t>(sms) * on_sm, s.r, dim) +
-                            groups * static_cast<int64_t>(sizeof(GroupParts));
-      if (bytes > most) most = bytes;
-    }
+  for (const bool four : {false, true})
+    for (const bool f16 : {false, true})
+      for (const bool select : {false, true}) {
+        const AttnShape s = attn_shape(heads / kv_heads * (select ? 1 : next_n), f16,
+                                       most_rows(dim, select, four));
+        const int64_t groups =
+            static_cast<int64_t>(select ? batch * next_n : batch) * kv_heads * s.chunks;
+        const int64_t bytes = attn_slots_bytes(static_cast<int64_t>(sms) * ctas_for(s.r), s.r, dim) +
+                              groups * static_cast<int64_t>(sizeof(GroupParts));
+        if (bytes > most) most = bytes;
+      }
   return most;
 }
 

@@ -44,8 +44,8 @@
 // byte an element, sixteen of them in every sixteen, which the TMA unit writes from the packed rows: a tile
 // takes as much shared memory, and as many of its cycles, as in 8 bits, for half the bytes of memory.
 //   * The TMA unit pads rows of 128 elements.  Rows of 64 come to it two tokens at a time (PAIRS).  Selected
-//     rows, and rows of 64 where more than 16 rows of queries share them, are fetched packed, 16 bytes a
-//     copy, into a ring of their own and spread by the warp that asked for them.
+//     rows are fetched packed, 16 bytes a copy, into a ring of their own and spread by the warp that asked
+//     for them.
 //   * Keys and values have rings of their own: a key's stage is free once its scores are there, a tile's
 //     worth of time before its values' is, and stages are what bounds the loads in flight.
 //   * Scales: with whole pages by bulk copies (a page's are one run), with selected rows beside the rows.
@@ -95,12 +95,10 @@ struct AttnCfg {
   // tokens a row.  A tile is then 256 positions, the first tokens of the pairs and the second ones, which have
   // columns of S, weights and sums of their own; a softmax thread takes both positions of a pair, whose
   // chains run side by side.  (Each by itself, tile after tile: 101 us for 78 with 32 requests of 4K..64K, 32
-  // heads on 4; rows by ordinary copies 133.  More rows have no columns for two of O.)
-  static constexpr bool PAIRS = FP4 && !SELECT && D == 64 && R <= 16;
+  // heads on 4; rows by ordinary copies 133.  More than 16 rows have no columns for two of O.)
+  static constexpr bool PAIRS = FP4 && !SELECT && D == 64;
   static constexpr int SUBS = PAIRS ? 2 : 1, POS = kTile * SUBS;  // positions of a row, and of a tile
   static constexpr int ROW = PAIRS ? 128 : D;         // bytes of a tile's row
-  // Rows by ordinary asynchronous copies, not by the TMA unit.
-  static constexpr bool COPIES = SELECT || (FP4 && D != 128 && !PAIRS);
   static constexpr int QPARTS = 3;                    // parts of a query
   // With R = 8 a query's parts stand side by side, in columns that are added when read (the last
   // eight of 32 mean nothing); else each part is a product of its own into the same columns.  (Three
@@ -112,11 +110,11 @@ struct AttnCfg {
   static constexpr int WG = R == 64 ? 2 : 1;          // softmax warpgroups, R / WG rows each
   static constexpr int RT = R / WG;
   static constexpr int SOFT_WARPS = 4 * WG;
-  // Warps that load: one for whole pages; up to four share the rows of a selection (FP4: of any tile
-  // that the TMA unit does not bring), as many as the softmax's registers leave room for.
+  // Warps that load: one for whole pages; up to four share the rows of a selection, as many as the
+  // softmax's registers leave room for.
   // In four bits whole pages have two, one for keys and one for values, where there is room: what holds
   // a loader up is handing its copies to the TMA unit.
-  static constexpr int LOADERS = !COPIES ? (FP4 && R <= 16 ? 2 : 1) : R == 32 ? 1 : R == 8 ? 4 : 2;
+  static constexpr int LOADERS = !SELECT ? (FP4 && R <= 16 ? 2 : 1) : R == 32 ? 1 : R == 8 ? 4 : 2;
   static constexpr int THREADS = 32 * (LOADERS + 1 + SOFT_WARPS);
   // Two of S, one of O (PAIRS: O of either token's weights with both tokens' values; half of each is
   // used); with FP4 the keys' scale factors, two tiles of them, and the queries' (1).
@@ -127,7 +125,7 @@ struct AttnCfg {
   // other's softmax.  Three of two stages instead of two of three: decode took 1.4 times as long, as
   // what the next launch needs no longer fits beside them.  64 rows in chunks of 32, two CTAs an SM:
   // one long request 1.07 times as long, a batch of 64 requests with 64 heads on one 1.3 times.
-  static constexpr int CTAS = R == 64 ? 1 : 2;
+  static constexpr int CTAS = R == 64 ? 1 : 2;        // (ctas_for, for the workspace, says the same)
   static constexpr int T_BYTES = kTile * ROW;         // a tile of K, or of V, as the products read it
   static constexpr int Q_BYTES = NS * (CAT ? 1 : QPARTS) * D;
   static constexpr int P_BYTES = SUBS * NO * kTile;   // a tile's weights
@@ -136,26 +134,26 @@ struct AttnCfg {
   static constexpr bool OVER_K = !FP4 && P_BYTES <= kTile * D;
   // With two buffers a tile's weights need not wait for the product of the tile before, and S of this
   // tile, which was issued after the product of the tile before that, says that theirs is free.
-  static constexpr int P_BUFS = OVER_K ? 0 : FP4 && (R == 32 || (R < 32 && COPIES && D == 128)) ? 1 : 2;
+  static constexpr int P_BUFS = OVER_K ? 0 : FP4 && (R == 32 || (R < 32 && SELECT && D == 128)) ? 1 : 2;
   // What a stage of K (FP4: its scale factors, where they are used and, by the TMA unit, as they came)
   // and of V holds besides: Token records, or (FP4, by the TMA unit) value scales, scale factors and
   // which of the tokens are there.
-  static constexpr int K_AUX = !FP4 ? 0 : COPIES ? kTile * 4 : kTile * 8;
-  static constexpr int V_AUX = FP4 ? kTile * 4 * (SUBS + 1) + (COPIES ? 0 : 16) : kTile * 16;
+  static constexpr int K_AUX = !FP4 ? 0 : SELECT ? kTile * 4 : kTile * 8;
+  static constexpr int V_AUX = FP4 ? kTile * 4 * (SUBS + 1) + (SELECT ? 0 : 16) : kTile * 16;
   static constexpr int MISC = 48 * R + (FP4 ? 0 : 3 * D * 4) + 256;
   static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_BYTES + MISC;
   static constexpr int ROOM = CTAS == 2 ? 115456 : 231424;
   static constexpr int LEFT = ROOM - FIXED;
   // FP4 copies land as they lie in the pool, K and V and what goes with them, and are spread by the
   // warp that asked for them: what is in flight takes half the room that the products need.
-  static constexpr int RAW_BYTES = COPIES && FP4 ? kTile * (D + 16) : 0;
+  static constexpr int RAW_BYTES = SELECT && FP4 ? kTile * (D + 16) : 0;
   // Stages of K and of V.  In 8 bits they are the same ones.  In four, a tile takes the room of 8 bits
   // for half the bytes, so that stages are what bounds the loads in flight: a key's is given back as soon
   // as its scores are there, long before its values' is.
   static constexpr int VS8 = LEFT / (2 * T_BYTES + V_AUX);
-  static constexpr int KS = !FP4 ? (VS8 > 6 ? 6 : VS8) : COPIES && D == 128 && R != 64 ? 1 : R == 64 && !COPIES ? 3 : 2;
+  static constexpr int KS = !FP4 ? (VS8 > 6 ? 6 : VS8) : SELECT && D == 128 && R != 64 ? 1 : R == 64 && !SELECT ? 3 : 2;
   static constexpr int K_ROOM = KS * (T_BYTES + K_AUX);
-  static constexpr int VS4 = COPIES ? 2 : (LEFT - K_ROOM) / (T_BYTES + V_AUX);
+  static constexpr int VS4 = SELECT ? 2 : (LEFT - K_ROOM) / (T_BYTES + V_AUX);
   static constexpr int VS = !FP4 ? KS : VS4 > 6 ? 6 : VS4;
   static constexpr int V_ROOM = VS * (T_BYTES + V_AUX);
   static constexpr int RAW_FIT = RAW_BYTES == 0 ? 0 : (LEFT - K_ROOM - V_ROOM) / (RAW_BYTES + !RAW_BYTES);
@@ -503,19 +501,19 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   const int keys = C::SELECT ? a.batch * a.next_n : a.batch;
 
   if (warp == 0 && lane == 0) {
-    if constexpr (!C::COPIES) {
+    if constexpr (!C::SELECT) {
       prefetch_tensor_map(&k_map);
       prefetch_tensor_map(&v_map);
     }
     for (int i = 0; i < C::KS; ++i) {
       // A loading lane's arrival, and (SELECT) one when its own copies have landed.  With FP4 one for each
       // loading warp, or the loader's and one for each lane's copies (of scales).
-      mbar_init(&k_full[i], !C::FP4 ? (C::SELECT ? 64 : 32) * C::LOADERS : C::COPIES ? C::LOADERS : 33);
+      mbar_init(&k_full[i], !C::FP4 ? (C::SELECT ? 64 : 32) * C::LOADERS : C::SELECT ? C::LOADERS : 33);
       mbar_init(&k_empty[i], 1);
     }
     if constexpr (C::FP4)
       for (int i = 0; i < C::VS; ++i) {
-        mbar_init(&v_full[i], C::COPIES ? C::LOADERS : 33);
+        mbar_init(&v_full[i], C::SELECT ? C::LOADERS : 33);
         mbar_init(&v_empty[i], 1);
       }
     mbar_init(&s_full[0], 1);
@@ -611,7 +609,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       ++issued_k;
       kr.advance();
     };
-    if constexpr (C::COPIES) {
+    if constexpr (C::SELECT) {
       // A lane looks after EACH tokens of a tile, 32 apart: position, then page, then the page's
       // scales, each read one tile further ahead than the next (segments and all), so that a tile
       // pays for one memory round trip and not for three.
@@ -634,19 +632,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           const RowMap m = rows_of<C>(a, w.key, w.group, split.chunks, split.chunk_rows);
           far.table = a.block_tables + m.b * a.bt_stride;
           far.g = m.g;
-          if constexpr (C::SELECT) {
-            far.extent = __ldg(a.seq_lens + m.b * a.sl_stride) - a.next_n + m.t_select + 1;
-            cand = a.candidates + w.key * a.cand_stride + max(0, __ldg(a.ranges + w.key));
-          } else {
-            far.extent = w.length;
-          }
+          far.extent = __ldg(a.seq_lens + m.b * a.sl_stride) - a.next_n + m.t_select + 1;
+          cand = a.candidates + w.key * a.cand_stride + max(0, __ldg(a.ranges + w.key));
           slot = w.seg_tile * kTile;
           end = min((w.seg_tile + w.seg_tiles) * kTile, w.length);
         }
 #pragma unroll
         for (int j = 0; j < EACH; ++j) {
           const int s = slot + token0 + 32 * j;
-          far.pos[j] = s >= end ? -1 : C::SELECT ? __ldg(&cand[s].x) : s;
+          far.pos[j] = s >= end ? -1 : __ldg(&cand[s].x);
         }
         slot += kTile;
       };
@@ -698,7 +692,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             if (mid.pos[j] < 0) continue;
             if (id_mid[j] >= 0 && id_mid[j] < a.num_blocks) {
               row[j] = ((id_mid[j] * a.kv_heads + mid.g) << shift) + (mid.pos[j] & (a.block_size - 1));
-              pos[j] = C::SELECT ? 0 : mid.pos[j];
+              pos[j] = 0;
             } else {
               bad = true;
             }
@@ -1042,14 +1036,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       if constexpr (C::FP4) mma_commit(&k_empty[st]);
     };
     const auto keys_here = [&](int st) {
-      if constexpr (C::FP4 && !C::COPIES) {
+      if constexpr (C::FP4 && !C::SELECT) {
         // Their scale factors, which came in the tokens' order, to where the tensor core expects them.
         const uint4 u = *reinterpret_cast<const uint4 *>(s_sf + (st * 2 + 1) * kTile + lane * 4);
         uint32_t *to = s_sf + st * 2 * kTile + (lane % 8) * 16 + lane / 8;
         to[0] = u.x, to[4] = u.y, to[8] = u.z, to[12] = u.w;
       }
       // (What ordinary copies and stores wrote.)
-      if constexpr (C::COPIES || C::FP4) fence_proxy_async_shared();
+      if constexpr (C::SELECT || C::FP4) fence_proxy_async_shared();
       __syncwarp();
       tc_fence_after_sync();
     };
@@ -1258,7 +1252,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           for (int sub = 0; sub < C::SUBS; ++sub) {
             if constexpr (C::FP4) {
               Token4 t4;
-              if constexpr (C::COPIES) {
+              if constexpr (C::SELECT) {
                 t4 = s_tok4[vr.at * kTile + token];
               } else {
                 const uint32_t *aux = s_aux + vr.at * (C::V_AUX / 4);
@@ -1701,13 +1695,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-// Rows that share a K/V head, cut into chunks of at most 64, and the kernel's R for a chunk.
+// Rows that share a K/V head, cut into chunks of at most `most`, and the kernel's R for a chunk.
 struct AttnShape {
   int chunks, chunk_rows, r;
 };
-inline AttnShape attn_shape(int rows, bool f16) {
+inline AttnShape attn_shape(int rows, bool f16, int most) {
   AttnShape s;
-  s.chunks = (rows + 63) / 64;
+  s.chunks = (rows + most - 1) / most;
   s.chunk_rows = (rows + s.chunks - 1) / s.chunks;
   s.r = s.chunk_rows <= 8 && !f16 ? 8 : s.chunk_rows <= 16 ? 16 : s.chunk_rows <= 32 ? 32 : 64;
   return s;
@@ -1742,38 +1736,40 @@ cudaError_t launch_cfg(const CUtensorMap &k_map, const CUtensorMap &v_map, const
                           dim3(kJoinThreads), 0, stream, a, split, parts);
 }
 
+// Rows in a chunk: 64, or with PAIRS 16, as many as have columns for two of O (draft verification with 32
+// rows of 64 in two chunks 204 us, in one by ordinary copies 249).
+constexpr int most_rows(int dim, bool select, bool four) { return four && dim == 64 && !select ? 16 : 64; }
+
 template <int D, bool SELECT, bool FP4>
 cudaError_t launch_rows(const CUtensorMap &k_map, const CUtensorMap &v_map, const AttentionArgs &a,
                         int dtype, int sms, cudaStream_t stream) {
   const bool f16 = dtype == IDX_DTYPE_F16;
-  const AttnShape s = attn_shape(a.heads / a.kv_heads * (SELECT ? 1 : a.next_n), f16);
-  if (f16) {
-    switch (s.r) {
-      case 16: return launch_cfg<AttnCfg<D, 16, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream);
-      case 32: return launch_cfg<AttnCfg<D, 32, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream);
-      default: return launch_cfg<AttnCfg<D, 64, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream);
-    }
-  }
+  constexpr int MOST = most_rows(D, SELECT, FP4);
+  const AttnShape s = attn_shape(a.heads / a.kv_heads * (SELECT ? 1 : a.next_n), f16, MOST);
   using B = __nv_bfloat16;
-  switch (s.r) {
-    case 8: return launch_cfg<AttnCfg<D, 8, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
-    case 16: return launch_cfg<AttnCfg<D, 16, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
-    case 32: return launch_cfg<AttnCfg<D, 32, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
-    default: return launch_cfg<AttnCfg<D, 64, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
+  if constexpr (MOST == 16) {
+    return f16 ? launch_cfg<AttnCfg<D, 16, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream)
+               : s.r == 8 ? launch_cfg<AttnCfg<D, 8, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream)
+                          : launch_cfg<AttnCfg<D, 16, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
+  } else {
+    if (f16) {
+      switch (s.r) {
+        case 16: return launch_cfg<AttnCfg<D, 16, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream);
+        case 32: return launch_cfg<AttnCfg<D, 32, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream);
+        default: return launch_cfg<AttnCfg<D, 64, 4, SELECT, FP4>, __half>(k_map, v_map, a, s, sms, stream);
+      }
+    }
+    switch (s.r) {
+      case 8: return launch_cfg<AttnCfg<D, 8, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
+      case 16: return launch_cfg<AttnCfg<D, 16, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
+      case 32: return launch_cfg<AttnCfg<D, 32, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
+      default: return launch_cfg<AttnCfg<D, 64, 3, SELECT, FP4>, B>(k_map, v_map, a, s, sms, stream);
+    }
   }
 }
 
-// The CTAs on an SM of the kernel that a shape takes.
-template <int D, bool SELECT, bool FP4>
-int ctas_for(int r, bool f16) {
-  if (f16)
-    return r == 16 ? AttnCfg<D, 16, 4, SELECT, FP4>::CTAS
-                   : r == 32 ? AttnCfg<D, 32, 4, SELECT, FP4>::CTAS : AttnCfg<D, 64, 4, SELECT, FP4>::CTAS;
-  return r == 8 ? AttnCfg<D, 8, 3, SELECT, FP4>::CTAS
-                : r == 16 ? AttnCfg<D, 16, 3, SELECT, FP4>::CTAS
-                          : r == 32 ? AttnCfg<D, 32, 3, SELECT, FP4>::CTAS
-                                    : AttnCfg<D, 64, 3, SELECT, FP4>::CTAS;
-}
+// The CTAs on an SM of the kernel that takes chunks of r rows (see AttnCfg).
+inline int ctas_for(int r) { return r == 64 ? 1 : 2; }
 
 inline cudaError_t read_attention_status(int32_t *value, bool clear) {
   cudaError_t e = cudaMemcpyFromSymbol(value, g_attention_status, sizeof(int32_t));

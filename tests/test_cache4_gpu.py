@@ -484,6 +484,23 @@ def test_attention_flags_bad_pages():
         check_attention(c, out, lse, [[p for p in row if p < 96] for row in picked])
 
 
+@pytest.mark.parametrize("H,bs,name,n", [(8, 32, "bf16", 1), (16, 64, "bf16", 1), (17, 128, "f16", 1),
+                                         (9, 32, "bf16", 4), (32, 64, "bf16", 2), (16, 32, "f16", 1)])
+def test_attention_where_two_tokens_share_a_row(H, bs, name, n):
+    """head_dim 64: lengths that end at the first and the second token of a pair and around a tile of 256, one
+    chunk of 16 rows and several, a page of the middle that is not there."""
+    clean()
+    c = attention_case([255, 256, 2, 1, 511, 512, 513], n, H, 1, 64, bs, name, 90 + H)
+    check_attention(c, *run_attention(c))
+    clean()
+    c["bt"][5, 1] = -1
+    out, lse = run_attention(c)
+    clean(idx.IDX_DEV_BAD_PAGE)
+    there = [[p for p in range(m - n + t + 1) if b != 5 or p // bs != 1] for b, m in enumerate(c["lens"])
+             for t in range(n)]
+    check_attention(c, out, lse, there)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_attention_and_reader_past_32_bits_of_a_pool(D):
     bs = 128
