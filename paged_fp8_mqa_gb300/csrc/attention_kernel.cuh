@@ -60,7 +60,9 @@
 // latency.  Selected rows: 64-byte rows and their scales from places of their own, of which DRAM moves twice
 // what is used (serving mix, 102 us for 27).  From L2 instead of DRAM decode takes 208 us.  Not kept:
 // prefetches into L2 by any unit (231 to 273 us), softmax warpgroups in turn on tiles (228 for 219), two or
-// more loading warps a ring (220), 8-byte copies of selected rows (serving 160 us).
+// more loading warps a ring (220), two tiles' positions a softmax thread as with PAIRS (261: the stages that
+// two tiles hold are missed by the loads), with 32 rows two buffers of weights and a stage of values fewer
+// (draft verification 197 for 178), 8-byte copies of selected rows (serving 160 us).
 #pragma once
 
 #include <cuda_runtime.h>
