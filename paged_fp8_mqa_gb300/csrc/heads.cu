@@ -285,8 +285,9 @@ struct BackwardSplit {
   int32_t q, k, walk;
 };
 
-// The gradients, W lanes a head.  8192 tokens of 32 + 8 heads of 128 (252 MB) take 53 us with the second
-// launch, 37 at the copy rate: 128 registers leave 16 warps an SM (three blocks of them 3 us more, five 22).  A lane's 16 elements of
+// The gradients, W lanes a head.  8192 tokens of 32 + 8 heads of 128 (252 MB) take 51 us with the second
+// launch, 37 at the copy rate: 128 registers leave 16 warps an SM (three blocks of them 3 us more, five 22).
+// Walks of two heads 55 us, of eight 52; loads three heads ahead through shared memory 50.5, not worth it.  A lane's 16 elements of
 // the weight's gradient stay in its registers over all its heads; a block leaves its sums in the workspace
 // and a second launch adds the blocks', in order.
 template <typename T, int W, bool ADJ>
@@ -461,7 +462,7 @@ __device__ __forceinline__ void add2(Sum2 &s, float x) {
 }
 
 // The blocks' sums of a weight's gradient, in order and in two floats: 32 elements a block (x, kind), a warp
-// every 32nd row of them.  (In 64 bits, whose units are few, the two launches took 60 us for 53.)
+// every 32nd row of them.  (In 64 bits, whose units are few, the two launches took 60 us for 53, as they were then.)
 template <typename T>
 __global__ void __launch_bounds__(1024) k_weight_gradient(const __grid_constant__ HeadsArgs a,
                                                           const BackwardSplit split) {
@@ -564,7 +565,7 @@ cudaError_t launch_backward(const HeadsArgs &a, bool pieces, int sms, cudaStream
   const int at_once = pieces ? kThreads / width : kAnyWarps;
   const int64_t all = heads_blocks(sms), heads = a.heads[0] + a.heads[1] + (a.heads[0] + a.heads[1] == 0);
   BackwardSplit s;
-  s.walk = 8;
+  s.walk = 4;
   while (pieces && s.walk > 1 && a.tokens * heads < all * at_once * s.walk) s.walk /= 2;
   if (!pieces) s.walk = 1;
   const auto blocks = [&](int h) {
