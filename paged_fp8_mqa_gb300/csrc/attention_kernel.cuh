@@ -40,15 +40,15 @@
 // tensor core's block scaling takes: S^T = K Q^T is kind::mxf8f6f4 with K as e2m1 and its scale bytes copied
 // from shared to tensor memory, Q's parts as e5m2 with the constant scale 2^-14; so S comes scaled and
 // only softmax_scale is left to the rows.  A value row's float32 scale goes into the weight, as a block's
-// does above, and O^T = V^T P^T is kind::f8f6f4 with V as e2m1.  Both read e2m1 from the padded layout, a
-// byte an element, sixteen of them in every sixteen, which the TMA unit writes from the packed rows: a tile
-// takes as much shared memory, and as many of its cycles, as in 8 bits, for half the bytes of memory.
+// does above, and O^T = V^T P^T is kind::f8f6f4 with V as e2m1.  Both read e2m1 from the padded layout (16
+// elements in the lower eight of 16 bytes), which the TMA unit writes from the packed rows: a tile takes as
+// much shared memory, and as many of its cycles, as in 8 bits, for half the bytes of memory.
 //   * The TMA unit pads rows of 128 elements.  Rows of 64 come to it two tokens at a time (PAIRS).  Selected
 //     rows are fetched packed, 16 bytes a copy, into a ring of their own and spread by the warp that asked
 //     for them.
 //   * Keys and values have rings of their own: a key's stage is free once its scores are there, a tile's
 //     worth of time before its values' is, and stages are what bounds the loads in flight.
-//   * Scales: with whole pages by bulk copies (a page's are one run), with selected rows beside the rows.
+//   * Scales come by asynchronous copies, with whole pages four rows' at a time, with selected rows a row's.
 //     What a position's scales give its weights (a logarithm, a reciprocal) its softmax thread works out while
 //     its scores come.
 //   * The MMA warp waits on the next tile's keys and on this tile's weights at once (test_wait and a short
