@@ -165,14 +165,14 @@ int check_norm(int32_t dtype, float eps, const void *q_weight, const void *k_wei
     const int size = element_bytes(weight_dtype);
     if (!aligned(q_weight, size) || !aligned(k_weight, size))
       return fail(IDX_INVALID_ARG, "weights must be aligned to their elements");
+    // (Without weights weight_dtype says nothing: any value will do.)
+    a->weight_f32 = weight_dtype == IDX_DTYPE_F32;
+    a->weight_pieces = aligned(q_weight, 8 * size) && aligned(k_weight, 8 * size);
   }
   a->norm = 1;
   a->eps = eps;
   a->weight[0] = q_weight;
   a->weight[1] = k_weight;
-  a->weight_f32 = weight_dtype == IDX_DTYPE_F32;
-  a->weight_pieces = aligned(q_weight, 8 * element_bytes(weight_dtype)) &&
-                     aligned(k_weight, 8 * element_bytes(weight_dtype));
   return IDX_OK;
 }
 

@@ -106,6 +106,18 @@ def test_norm_rotary_backward_refused(over, code):
     assert call(idx.idx_norm_rotary_backward, args, over) == code, idx.idx_last_error()
 
 
+@pytest.mark.parametrize("weight_dtype", [0, 3, 9, -1, 1 << 30])
+def test_without_weights_their_dtype_is_not_read(weight_dtype):
+    """No weights: any weight_dtype is accepted (nothing is launched without tokens)."""
+    over = dict(q_weight=None, k_weight=None, weight_dtype=weight_dtype)
+    args = dict(NORM, q_out=FAKE, qo_token=256, qo_head=128, k_out=FAKE, ko_token=128, ko_head=128, stream=None)
+    assert call(idx.idx_norm_rotary, args, dict(over, tokens=0)) == 0, idx.idx_last_error()
+    args = dict(NORM, gq=FAKE, gq_token=256, gq_head=128, gk=FAKE, gk_token=128, gk_head=128, dq=FAKE,
+                dk=FAKE, dqw=None, dkw=None, workspace=None, workspace_bytes=0, stream=None)
+    # (Refused for the workspace, or where there is no device, after the weights have been looked at.)
+    assert call(idx.idx_norm_rotary_backward, args, over) in (1, 3), idx.idx_last_error()
+
+
 def test_norm_rotary_workspace_refused():
     assert idx.idx_norm_rotary_workspace_bytes(0) == -1 and idx.idx_norm_rotary_workspace_bytes(1025) == -1
 
