@@ -751,7 +751,7 @@ IDX_EXPORT int idx_norm_rotary_backward(
     return fail(IDX_INVALID_ARG, "workspace (16-byte aligned) below "
                                  "idx_norm_rotary_workspace_bytes(...)");
   a.dweight[0] = q_weight_grad;
-  a.dweight[1] = k_heads > 0 ? k_weight_grad : nullptr;
+  a.dweight[1] = k_weight_grad;
   a.workspace = static_cast<float *>(workspace);
   a.sin_sign = -1.0f;
   const cudaError_t e = idx::launch_heads_backward(a, dtype, whole && dim_in_pieces(a), sms,

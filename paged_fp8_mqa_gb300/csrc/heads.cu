@@ -587,7 +587,7 @@ cudaError_t launch_backward(const HeadsArgs &a, bool pieces, int sms, cudaStream
   else
     e = launch_backward_pieces<T, 16>(a, s, stream);
   if (e != cudaSuccess || (a.dweight[0] == nullptr && a.dweight[1] == nullptr)) return e;
-  return launch_dependent(k_weight_gradient<T>, dim3((a.dim + 31) / 32, a.heads[1] > 0 ? 2 : 1),
+  return launch_dependent(k_weight_gradient<T>, dim3((a.dim + 31) / 32, a.dweight[1] != nullptr ? 2 : 1),
                           dim3(1024), 0, stream, a, s);
 }
 

@@ -412,3 +412,26 @@ def test_axes_that_can_be_read_only_once():
                          lambda axes: idx.rotary(x, pos, table, axes=axes)), want):
         y = f(a for a in how["axes"])
         assert torch.equal(torch.autograd.grad(y, x, torch.ones_like(y))[0], dx)
+
+
+@pytest.mark.parametrize("name,wname", [("f32", "f32"), ("bf16", "f32"), ("f16", "f16")])
+def test_c_entry_of_the_gradients_without_keys_heads(name, wname):
+    """No heads of k, whose weight and its gradient are given: the sum over nothing is 0, q's is its own."""
+    T, H, D = 5, 3, 64
+    x, g = (torch.randn(T, H, D, generator=gen(i)).to(DTYPES[name]).to(dev()) for i in (1, 2))
+    w = torch.ones(D, dtype=DTYPES[wname], device=dev())
+    dqw, dkw = (torch.full((D,), 5.0, dtype=w.dtype, device=dev()) for _ in range(2))
+    dx = torch.empty_like(x)
+    need = idx.idx_norm_rotary_workspace_bytes(D)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev())
+    rows = lambda t: (t.data_ptr(), H * D, D)  # noqa: E731
+    none, code = (None, 0, 0), {"f32": idx.IDX_DTYPE_F32, "f16": idx.IDX_DTYPE_F16, "bf16": idx.IDX_DTYPE_BF16}
+    for want_q in (True, False):
+        assert idx.idx_norm_rotary_backward(
+            *rows(x), H, *none, 0, code[name], T, D, w.data_ptr(), w.data_ptr(), code[wname], 1e-6, None, 0,
+            None, 1, None, 0, 0, 0, 0, *rows(g), *none, dx.data_ptr(), None,
+            dqw.data_ptr() if want_q else None, dkw.data_ptr(), ws.data_ptr(), need, None) == 0
+        clean()
+        assert (dkw == 0).all()
+        check_gradients(x, w, g, dx, dqw, (None, None, None, False, 0), name, wname)
+        dkw.fill_(5.0)
