@@ -176,11 +176,29 @@ __device__ __forceinline__ uint32_t codes_of(const float2 (&v)[4]) {
   return e2m1x8(f);
 }
 
-// 6 v / amax, correctly rounded: the quotient's remainder times the reciprocal (within 2^-22 of it) added,
-// so that what lies halfway between two codes stays there.
+// 6 v / amax of 16-bit elements (6 v is exact), correctly rounded by Markstein's correction: the quotient's
+// remainder times the reciprocal (within 2^-22 of it) added, so that what lies halfway between two codes
+// stays there, and nothing else comes to lie there (their quotients are 2^-18 from a border or on it).
 __device__ __forceinline__ float2 six_over(float2 v, float2 minus_m, float2 inv) {
   const float2 x = __fmul2_rn(v, make_float2(6.0f, 6.0f)), q = __fmul2_rn(x, inv);
   return __ffma2_rn(__ffma2_rn(q, minus_m, x), inv, q);
+}
+// The same of any element, float32 ones too: 6 v is taken in two parts, and a quotient that is not a float is
+// rounded to one with an odd last bit, so that it stays on its side of every border between codes
+// (which are even floats, and may be as near as 2^-26).  Below the first border, 0.25, it may be off.
+template <typename T>
+__device__ __forceinline__ float six_over(float v, float m, float inv) {
+  const float x = 6.0f * v;
+  float q = x * inv;
+  if constexpr (sizeof(T) == 2) return fmaf(fmaf(-q, m, x), inv, q);
+  const float low = fmaf(6.0f, v, -x);
+  q = fmaf(fmaf(-q, m, x) + low, inv, q);
+  // The remainder's sign: both terms are exact, or as good as that where the first is the larger.
+  const float rest = fmaf(-q, m, x) + low;
+  const uint32_t bits = __float_as_uint(q);
+  if (rest != 0.0f && (bits & 1u) == 0 && fabsf(q) >= 0.25f)
+    q = __uint_as_float((rest > 0.0f) == (q > 0.0f) ? bits + 1u : bits - 1u);
+  return q;
 }
 // x / 6, correctly rounded in the same way.
 __device__ __forceinline__ float sixth(float x) {
@@ -325,7 +343,12 @@ __global__ void __launch_bounds__(kPieceThreads, ROUNDS == 1 ? 1 : 5)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[e][j] = six_over(v[e][j], m2, inv2);
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(T) == 2)
+            v[e][j] = six_over(v[e][j], m2, inv2);
+          else
+            v[e][j] = make_float2(six_over<T>(v[e][j].x, m, inv), six_over<T>(v[e][j].y, m, inv));
+        }
         const uint32_t codes = codes_of(v[e]);
         if (live) *reinterpret_cast<uint32_t *>(to + p.at[e] / 2) = codes;
       }
@@ -399,17 +422,13 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const Kv4Args a, bool p
       if ((lane & 3) == 0)
         a.k_scales[row * (D / 32) + d / 32] = odd ? 255 : static_cast<uint8_t>(e + 127);
     } else {
-      // The codes of 6 v / amax, correctly rounded (the remainder times the reciprocal), so that what
-      // lies halfway between two codes stays there; rows past 2^100 are brought down first.
+      // The codes of 6 v / amax; rows past 2^100 are brought down first.
       amax = fmaxf(amax, kLeastMax);
       const float down = amax > 1.2676506002282294e30f ? 5.421010862427522e-20f : 1.0f;  // 2^-64
       const float m = amax * down, inv = __frcp_rn(m);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = 6.0f * (fminf(fmaxf(v[j], -amax), amax) * down);
-        const float q = x * inv;
-        v[j] = fmaf(fmaf(-q, m, x), inv, q);
-      }
+      for (int j = 0; j < 8; ++j)
+        v[j] = six_over<T>(fminf(fmaxf(v[j], -amax), amax) * down, m, inv);
       if (d == 0) a.v_scales[row] = odd ? __int_as_float(0x7FC00000) : __fdiv_rn(amax, 6.0f);
     }
     *reinterpret_cast<uint32_t *>((is_k ? a.k_pool : a.v_pool) + row * (D / 2) + d / 2) = e2m1x8(v);

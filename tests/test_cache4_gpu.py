@@ -626,3 +626,47 @@ def test_refusals_of_tensors():
     torch.cuda.synchronize()
     k, v = idx.kv_read_fp4(*cache, bt, seq, torch.zeros(4, dtype=torch.int32, device=dev()), tokens=0)
     assert k.shape == (0, 2, 64) and v.dtype == torch.bfloat16
+
+
+def codes_of_quotients(v, most):
+    """Indices of the nearest values to 6 v / most, ties to the even code, by exact fractions."""
+    from fractions import Fraction
+    values = [Fraction(float(x)) for x in plain4.E2M1[:8]]
+    out = []
+    for x in v:
+        y = min(abs(6 * Fraction(float(x)) / Fraction(float(most))), 6)
+        i = min(range(8), key=lambda c: (abs(values[c] - y), c % 2))
+        out.append(8 + i if x < 0 else i)
+    return out
+
+
+@pytest.mark.parametrize("layout", ["plain", "odd"])
+@pytest.mark.parametrize("D,shift", [(64, 0), (128, -118), (64, 103)])
+def test_float32_values_next_to_a_border(D, shift, layout):
+    """Float32 elements whose quotient lies on a border between two codes, or within 2^-21 of it, where a
+    quotient rounded to float32 would lie on it: the code is the exact quotient's."""
+    g = np.random.default_rng(D + shift)
+    rows = []
+    for _ in range(200):
+        most = int(g.integers(2 ** 23, 2 ** 24)) // 12 * 12 + int(g.integers(2)) * int(g.integers(12))
+        most = min(max(most, 2 ** 23), 2 ** 24 - 1)
+        row = [float(most)]
+        for border in plain4.BORDERS:
+            at = np.float32(border * most / 6)
+            row += [np.nextafter(at, np.float32(0)), at, -at, np.nextafter(at, np.float32(2 ** 25))]
+        rows.append(row + [0.0] * (D - len(row)))
+    # (One that rounds to a tie both in 6 v and in the quotient.)
+    rows[0][:2] = [13421820.0, 5592425.0]
+    v = torch.tensor(np.array(rows, dtype=np.float32) * np.float32(2.0 ** shift))[:, None]
+    wide = torch.zeros(200, 1, D + 3)
+    wide[:, :, :D] = v
+    given = v.to(dev()) if layout == "plain" else wide.to(dev())[:, :, :D]
+    cache = empty_cache(7, 1, 32, D, gen(0))
+    bt = torch.arange(7, dtype=torch.int32, device=dev())[None]
+    clean()
+    idx.kv_append_fp4(given, given, *cache, bt, torch.tensor([200], dtype=torch.int32, device=dev()))
+    clean()
+    got = plain4.codes_of(u8(cache[1]))[:, 0].reshape(-1, D)[:200]
+    want = np.array([codes_of_quotients(row, max(row)) for row in v[:, 0].numpy()])
+    # (A zero's code has no sign.)
+    assert (np.where(v[:, 0].numpy() == 0, 0, got) == want).all()
