@@ -252,6 +252,7 @@ def _recorded():
             ctx.save_for_backward(q, k, q_weight, k_weight, positions, table)
             ctx.how = eps, axes, interleaved, rot_offset
             ctx.args = args
+            ctx.places = None if positions is None else positions.stride()
             return _forward(index, args, q, k, None, None, stream)
 
         @staticmethod
@@ -260,9 +261,12 @@ def _recorded():
             saved = ctx.saved_tensors
             # (Hooks on what is saved may have put other tensors in their place.)
             a = ctx.args
+            q, k, q_weight, k_weight, positions, table = saved
             at = [None if t is None else t.data_ptr() for t in saved]
-            same = at == [a[0], a[4], a[11], a[12], a[15], a[19]] and saved[0].stride()[:2] == a[1:3] \
-                and (saved[1] is None or saved[1].stride()[:2] == a[5:7])
+            same = at == [a[0], a[4], a[11], a[12], a[15], a[19]] and q.stride()[:2] == a[1:3] \
+                and (k is None or k.stride()[:2] == a[5:7]) \
+                and (positions is None or positions.stride() == ctx.places) \
+                and all(t is None or t.is_contiguous() for t in (q_weight, k_weight, table))
             return (*_backward(*saved, *ctx.how, q_grad, k_grad, a if same else None), *[None] * 7)
 
     return NormRotary.apply

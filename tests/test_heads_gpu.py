@@ -435,3 +435,54 @@ def test_c_entry_of_the_gradients_without_keys_heads(name, wname):
         assert (dkw == 0).all()
         check_gradients(x, w, g, dx, dqw, (None, None, None, False, 0), name, wname)
         dkw.fill_(5.0)
+
+
+@pytest.mark.parametrize("kind", ["the same", "copies", "on the host", "positions moved", "q moved", "weight moved"])
+def test_gradients_with_hooks_on_what_is_saved(kind):
+    """Tensors that hooks put in the place of the saved ones are read as they lie: at other addresses, or at the
+    same ones with other strides."""
+    clean()
+    T, H, Hkv, D = 9, 4, 2, 64
+    q, k, w, _, table, how, ph = heads_case(T, H, Hkv, D, 32, 0, False, 2, "f32", "f32")
+    g = gen(3)
+    room = torch.randint(500, (2 * (T + 7),), generator=g, dtype=torch.int32).to(dev())
+    pos = room.view(2, T + 7)[:, :T]
+    wide = torch.empty(T * H * 2 * D, device=dev())
+    wide_q = wide.view(T, H, 2 * D)[:, :, :D].copy_(q)
+    wide_w = torch.empty(2 * D, device=dev())
+    wide_w[:D] = w[0]
+    grads = [torch.randn(t.shape, generator=g).to(dev()) for t in (q, k)]
+    leaves = [t.detach().requires_grad_() for t in (wide_q, k, wide_w[:D], w[1])]
+    call = lambda: idx.norm_rotary(*leaves, pos, table, **how)  # noqa: E731
+    want = torch.autograd.grad(call(), leaves, grads)
+    ph = (pos.tolist(), *ph[1:])
+    check_gradients(q, w[0], grads[0], want[0], want[2], ph, "f32", "f32")
+
+    def pack(t):
+        moved = {"positions moved": pos, "q moved": wide_q, "weight moved": wide_w}.get(kind)
+        if kind == "copies" or (moved is not None and t.data_ptr() == moved.data_ptr()):
+            return t.clone()
+        return t.cpu() if kind == "on the host" else t
+
+    def unpack(t):
+        if kind == "on the host":
+            return t.to(dev())
+        if kind == "positions moved" and t.dtype == torch.int32:
+            return room[:2 * T].copy_(t.reshape(-1)).view(2, T)
+        if kind == "q moved" and t.dim() == 3 and t.shape[1:] == (H, D) and t.data_ptr() != wide.data_ptr():
+            return wide[:T * H * D].copy_(t.reshape(-1)).view(T, H, D)
+        if kind == "weight moved" and t.dim() == 1 and t.data_ptr() != w[1].data_ptr():
+            wide_w[::2] = t
+            return wide_w[::2]
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, unpack):
+        out = call()
+    if kind == "weight moved":
+        with pytest.raises(ValueError, match="contiguous"):  # (as a call with such a weight)
+            torch.autograd.grad(out, leaves, grads)
+        return
+    with torch.no_grad():
+        got = torch.autograd.grad(out, leaves, grads)
+    clean()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
