@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from .layer import (_D, _F, _I, _L, _P, _SIGNATURES, _c, _check, _code, _elsewhere, _index, _on, _rows,
+from .layer import (_F, _I, _L, _P, _SIGNATURES, _c, _check, _code, _elsewhere, _index, _no_tangents, _on, _rows,
                     _table, _tensor)
 
 IDX_ROTARY_MAX_AXES = 4
@@ -285,13 +285,14 @@ def norm_rotary(q, k, q_weight=None, k_weight=None, positions=None, table=None, 
 
     Autograd records the call where q, k or a weight requires a gradient; given outputs are refused then.
     The weights' gradients are sums in an order that does not change from call to call.  The gradients
-    cannot be differentiated again.  A backward pass may be captured into a CUDA graph; no eager graph of the
+    cannot be differentiated again, and forward-mode gradients are refused.  A backward pass may be captured into a CUDA graph; no eager graph of the
     same leaves (an output kept from a warm-up step) may live then, as autograd would wait for the stream
     that it ran on."""
     import torch
     index = _index(q, "q")
     if axes is not None and type(axes) is not tuple:
         axes = tuple(axes)
+    _no_tangents("norm_rotary", q, k, q_weight, k_weight)
     if (q.requires_grad or (k is not None and k.requires_grad)
             or (q_weight is not None and q_weight.requires_grad)
             or (k_weight is not None and k_weight.requires_grad)) and torch.is_grad_enabled():

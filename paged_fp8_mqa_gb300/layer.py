@@ -119,6 +119,15 @@ def _elsewhere(index, f, *args, **more):
         return f(*args, **more)
 
 
+def _no_tangents(name, *tensors):
+    """Forward-mode gradients are not computed: a dual tensor is refused, so that its tangent is not lost
+    without a word (it need not require a gradient, and its address can be read)."""
+    import torch
+    ad = torch.autograd.forward_ad
+    if ad._current_level >= 0 and any(t is not None and ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{name} has no forward-mode gradient")
+
+
 def _tensor(t, name, dims, dtype, index):
     """A CUDA tensor of dtype on device `index` with `dims` dimensions.  (One test for the usual
     case: a call's checks are a good part of its time on the host.)"""
@@ -287,7 +296,7 @@ def rotary(x, positions, table, *, axes=None, interleaved: bool = False, rot_off
     angles of ``table`` (see ``rotary_table``), in halves or in interleaved pairs.  ``out=x``
     rotates in place.  ``inverse`` turns by the negative angles: the gradient with respect to x (and
     the way back, where the table's magnitude is 1, as it is but for "yarn").  Autograd records the
-    call where x requires a gradient; with ``out`` nothing is recorded.
+    call where x requires a gradient; with ``out`` nothing is recorded.  Forward-mode gradients are refused.
 
     ``axes``, for tokens of images and video, names each pair's axis (rot_dim / 2 whole numbers, see
     ``rotary_axes``): positions are then int32 [axes, T] (up to 4 axes, D at most 1024), and a pair is
@@ -296,6 +305,7 @@ def rotary(x, positions, table, *, axes=None, interleaved: bool = False, rot_off
     index = _index(x, "x")
     if axes is not None and type(axes) is not tuple:
         axes = tuple(axes)
+    _no_tangents("rotary", x)
     if x.requires_grad and out is None and torch.is_grad_enabled():
         return _recorded_rotary()(x, positions, table, axes, interleaved, rot_offset, inverse, stream)
     if index != torch.cuda.current_device():

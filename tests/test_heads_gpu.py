@@ -486,3 +486,28 @@ def test_gradients_with_hooks_on_what_is_saved(kind):
         got = torch.autograd.grad(out, leaves, grads)
     clean()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_forward_mode_gradients_are_refused():
+    """A dual tensor, which does not require a gradient, is refused where its tangent would be lost; what has
+    no tangent runs while a dual level is open."""
+    from torch.autograd import forward_ad
+    q, k, w, pos, table, how, _ = heads_case(5, 4, 2, 64, 32, 0, False, 3, "f32", "f32", "plain")
+    want = idx.norm_rotary(q, k, *w, pos, table, **how)
+    turned_q = idx.rotary(q, pos, table, **how)
+    with forward_ad.dual_level():
+        dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for at in range(4):
+            args = [q, k, *w]
+            args[at] = dual(args[at])
+            with torch.no_grad(), pytest.raises(NotImplementedError, match="norm_rotary"):
+                idx.norm_rotary(*args, pos, table, **how)
+        for more in (dict(how), dict(how, out=torch.empty_like(q))):
+            with pytest.raises(NotImplementedError, match="rotary"):
+                idx.rotary(dual(q), pos, table, **more)
+        with pytest.raises(NotImplementedError, match="rotary"):
+            idx.rotary(dual(q), pos[0].contiguous(), table)
+        assert all(torch.equal(a, b) for a, b in zip(idx.norm_rotary(q, k, *w, pos, table, **how), want))
+        assert torch.equal(idx.rotary(q, pos, table, **how), turned_q)
+        assert idx.norm_rotary(q, None, None, None)[1] is None
+    torch.cuda.synchronize()
