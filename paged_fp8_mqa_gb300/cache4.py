@@ -7,9 +7,10 @@ float32 scale.  The C-ABI mirrors (``idx_...``) take raw pointers and sizes in t
 from __future__ import annotations
 
 import ctypes
+import functools
 
-from .layer import (_F, _I, _L, _P, _SIGNATURES, _attend, _c, _check, _code, _elsewhere, _index, _on,
-                    _rows, _table, _tensor, _tokens)
+from .layer import (_F, _I, _L, _P, _SIGNATURES, _attend, _c, _check, _code, _elsewhere, _ending, _index,
+                    _no_tangents, _on, _rows, _table, _tensor, _tokens)
 
 _SIGNATURES.update({
     "idx_kv_append_fp4": _SIGNATURES["idx_kv_append"],
@@ -148,9 +149,15 @@ def attention_fp4(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
                   softmax_scale: float | None = None, candidates=None, ranges=None, out=None,
                   lse=None, workspace=None, num_sms: int = 0, stream=None):
     """``attention_fp8`` over the 4-bit cache (pools and scales as for ``kv_append_fp4``): the same
-    queries, extents, candidates, outputs and workspace."""
+    queries, extents, candidates, outputs and workspace, and no gradient either."""
     import torch
     index = _index(q, "q")
+    _no_tangents("attention_fp4", q)
+    if q.requires_grad and out is None and torch.is_grad_enabled():
+        return _ending()(q, "attention_fp4", functools.partial(
+            attention_fp4, q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
+            softmax_scale=softmax_scale, candidates=candidates, ranges=ranges, lse=lse,
+            workspace=workspace, num_sms=num_sms, stream=stream))
     if index != torch.cuda.current_device():
         return _elsewhere(index, attention_fp4, q, k_pool, v_pool, k_scales, v_scales, block_tables,
                           seq_lens, softmax_scale=softmax_scale, candidates=candidates,

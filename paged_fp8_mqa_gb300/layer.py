@@ -439,6 +439,25 @@ def kv_append(k, v, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens, 
             *scales, _on(stream, index)))
 
 
+@functools.cache
+def _ending():
+    """A call as a step of autograd that has no gradient and says so when one is asked for."""
+    import torch
+
+    class NoGradient(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, name, call):
+            ctx.name = name
+            return call()
+
+        @staticmethod
+        def backward(ctx, grad):
+            raise NotImplementedError(f"{ctx.name} has no gradient: call it with q.detach(), or under "
+                                      "torch.no_grad()")
+
+    return NoGradient.apply
+
+
 def _attend(entry, index, q, pools, sizes, block_tables, seq_lens, softmax_scale, candidates, ranges,
             out, lse, workspace, num_sms, stream):
     """The attention's call by its C entry: pools, the cache's four addresses; sizes, its (blocks, Hkv,
@@ -518,9 +537,18 @@ def attention_fp8(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
     to D ** -0.5; weights are held to 2^-10 of themselves (float16 queries: 2^-14), sums in float32;
     ``lse`` (float32 [B, next_n, H]) receives the log-sums; ``workspace`` (uint8, at
     least idx_attention_workspace_bytes) is allocated if not given.  Returns out, contiguous
-    [B, next_n, H, D] in q's dtype."""
+    [B, next_n, H, D] in q's dtype.
+
+    The attention serves and has no gradient: where q requires one, a backward pass through the result is
+    an error (with ``out`` nothing is recorded), and forward-mode gradients are refused."""
     import torch
     index = _index(q, "q")
+    _no_tangents("attention_fp8", q)
+    if q.requires_grad and out is None and torch.is_grad_enabled():
+        return _ending()(q, "attention_fp8", functools.partial(
+            attention_fp8, q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
+            softmax_scale=softmax_scale, candidates=candidates, ranges=ranges, lse=lse,
+            workspace=workspace, num_sms=num_sms, stream=stream))
     if index != torch.cuda.current_device():
         return _elsewhere(index, attention_fp8, q, k_pool, v_pool, k_scales, v_scales, block_tables,
                           seq_lens, softmax_scale=softmax_scale, candidates=candidates,

@@ -670,3 +670,40 @@ def test_float32_values_next_to_a_border(D, shift, layout):
     want = np.array([codes_of_quotients(row, max(row)) for row in v[:, 0].numpy()])
     # (A zero's code has no sign.)
     assert (np.where(v[:, 0].numpy() == 0, 0, got) == want).all()
+
+
+@pytest.mark.parametrize("cache", ["fp8", "fp4"])
+def test_attention_says_that_it_has_no_gradient(cache):
+    """A query that requires a gradient (as norm_rotary leaves it in a model): the same result, and a backward
+    pass through it is an error and not silence; a tangent is refused."""
+    from torch.autograd import forward_ad
+    H, D, bs = 4, 64, 32
+    g = gen(3)
+    bt, seq = torch.tensor([[1, 0]], dtype=torch.int32, device=dev()), torch.tensor([40], dtype=torch.int32, device=dev())
+    if cache == "fp4":
+        held, call = empty_cache(2, 1, bs, D, g), idx.attention_fp4
+    else:
+        held = [torch.randint(0x40, (2, 1, bs, D), generator=g, dtype=torch.uint8).to(dev()) for _ in range(2)]
+        held += [torch.ones(2, 1, device=dev()) for _ in range(2)]
+        call = idx.attention_fp8
+    x = torch.randn(1, H, D, generator=g).bfloat16().to(dev())
+    with torch.no_grad():
+        q, _ = idx.norm_rotary(x, None)
+        want = call(q[:, None], *held, bt, seq)
+        assert not want.requires_grad
+    leaf = x.clone().requires_grad_()
+    q, _ = idx.norm_rotary(leaf, None)
+    lse = torch.zeros(1, 1, H, device=dev())
+    out = call(q[:, None], *held, bt, seq, lse=lse)
+    assert torch.equal(out, want) and out.requires_grad and (lse != 0).all()
+    with pytest.raises(NotImplementedError, match="attention_" + cache):
+        out.float().sum().backward()
+    assert leaf.grad is None
+    with torch.no_grad():
+        assert not call(q[:, None], *held, bt, seq).requires_grad
+    given = torch.empty_like(want)
+    assert call(q[:, None], *held, bt, seq, out=given) is given and not given.requires_grad
+    assert torch.equal(given, want) and not call(q[:, None].detach(), *held, bt, seq).requires_grad
+    with forward_ad.dual_level(), pytest.raises(NotImplementedError, match="attention_" + cache):
+        call(forward_ad.make_dual(want, want), *held, bt, seq)
+    clean()
