@@ -159,6 +159,9 @@ __global__ void __launch_bounds__(kThreads, BLOCKS)
       own_f[1][j] = __fmul2_rn(c, w[1][j]);
       cross[0][j] = __fmul2_rn(n, minus(w[1][j]));
       cross[1][j] = __fmul2_rn(n, w[0][j]);
+      // (Where a pair is not turned, an infinite weight times the sine of 0 must not reach its neighbour.)
+      if (!((valid >> (2 * j)) & 1u)) cross[0][j].x = cross[1][j].x = 0.0f;
+      if (!((valid >> (2 * j + 1)) & 1u)) cross[0][j].y = cross[1][j].y = 0.0f;
     }
   }
   const float inv_dim = 1.0f / static_cast<float>(a.dim);

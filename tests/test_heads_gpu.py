@@ -511,3 +511,33 @@ def test_forward_mode_gradients_are_refused():
         assert torch.equal(idx.rotary(q, pos, table, **how), turned_q)
         assert idx.norm_rotary(q, None, None, None)[1] is None
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("D,rot,offset,interleaved,name", [
+    (64, 0, 0, False, "f32"), (128, 64, 32, False, "bf16"), (128, 64, 32, True, "f16"),
+    (192, 96, 0, False, "bf16"), (96, 24, 0, True, "f32"), (80, 20, 30, False, "bf16")])
+def test_what_is_not_finite_in_a_weight_stays_with_its_element(D, rot, offset, interleaved, name):
+    """An infinite and a NaN weight of elements that are not turned, in the rotated part of a token past the
+    table too: those elements show it, all others are what they are without."""
+    clean()
+    q, k, w, pos, table, how, _ = heads_case(7, 3, 2, D, rot, offset, interleaved, 1, name, "f32", "plain")
+    odd = [d for d in range(D) if not offset <= d < offset + rot][1::5]
+    plain_w = [x.clone() for x in w]
+    for x in w:
+        x[odd[0]], x[odd[1]], x[odd[2]] = math.inf, math.nan, -math.inf
+    ok = torch.ones(D, dtype=torch.bool)
+    ok[odd[:3]] = False
+    ok = ok.to(dev())
+    got = idx.norm_rotary(q, k, *w, pos, table, **how)
+    want = idx.norm_rotary(q, k, *plain_w, pos, table, **how)
+    clean()
+    for g, e in zip(got, want):
+        assert torch.equal(g[:, :, ok], e[:, :, ok]) and not torch.isfinite(g[:, :, ~ok]).any()
+    if rot:
+        pos[:] = 500  # (past the table: nothing is turned)
+        w[0][offset + 1] = math.inf
+        ok[offset + 1] = False
+        got = idx.norm_rotary(q, None, w[0], None, pos, table, **how)[0]
+        want = idx.norm_rotary(q, None, plain_w[0], None, pos, table, **how)[0]
+        clean(idx.IDX_DEV_BAD_POSITION)
+        assert torch.equal(got[:, :, ok], want[:, :, ok]) and not torch.isfinite(got[:, :, ~ok]).any()
