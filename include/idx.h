@@ -552,8 +552,8 @@ int idx_norm_rotary(const void *q, int64_t q_token_stride, int64_t q_head_stride
  * Its gradients from q, k and the outputs' gradients (any token and head strides, 0 among them):
  * q_grad, k_grad (dtype, contiguous) and, where not NULL, q_weight_grad, k_weight_grad (weight_dtype),
  * each summed over all tokens and heads in an order that does not change from call to call.
- * workspace: device, 16-byte aligned, idx_norm_rotary_workspace_bytes(head_dim) bytes (-1: a head_dim
- * that is refused).
+ * Outputs and inputs must not overlap.  workspace: device, 16-byte aligned,
+ * idx_norm_rotary_workspace_bytes(head_dim) bytes (-1: a head_dim that is refused).
  */
 int64_t idx_norm_rotary_workspace_bytes(int32_t head_dim);
 int idx_norm_rotary_backward(

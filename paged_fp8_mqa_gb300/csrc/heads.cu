@@ -81,6 +81,16 @@ __device__ __forceinline__ float inv_sqrt(float v) {
   return v > 1e-37f && v < 1e37f ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
 }
 
+// A row whose mean square is outside of float32's range, or so small that its squares lose their bits, is
+// taken times 2^-96 or 2^96 (its elements are past some 2^59, or, with eps = 0, all below 2^-50).  Rows with
+// an infinity or a NaN are taken so too and come out as they would.
+__device__ __forceinline__ float rescale(float mean_square) {
+  return mean_square >= 7.8886090522101181e-31f && mean_square <= 3.4028234663852886e38f ? 1.0f  // (2^-100)
+         : mean_square > 1.0f ? 1.2621774483536189e-29f : 7.922816251426434e28f;
+}
+// Whether a row's 1 / sqrt(mean square) says that it need not be.
+__device__ __forceinline__ bool in_range(float r) { return r > 0.0f && r < 1.1258999068426240e15f; }
+
 // The lane's 16 weights in float32 (1 without), as the elements are unpacked.
 template <bool ADJ, typename T>
 __device__ __forceinline__ void weights_of(const HeadsArgs &a, int kind, const Pieces &p,
@@ -106,6 +116,56 @@ __device__ __forceinline__ float sum_lanes(float x) {
 #pragma unroll
   for (int o = 1; o < W; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+
+// The same by the lanes of one group alone.
+template <int W>
+__device__ __forceinline__ float sum_group(float x) {
+  const uint32_t mask = ((1u << W) - 1u) << (threadIdx.x & 31u & ~(W - 1u));
+#pragma unroll
+  for (int o = 1; o < W; o <<= 1) x += __shfl_xor_sync(mask, x, o);
+  return x;
+}
+
+// The lane's part of a row's sum of squares, and of sum a b c.
+__device__ __forceinline__ float squares(const float2 (&v)[2][4]) {
+  float2 sq = __fmul2_rn(v[0][0], v[0][0]);
+#pragma unroll
+  for (int j = 1; j < 8; ++j) sq = __ffma2_rn(v[j >> 2][j & 3], v[j >> 2][j & 3], sq);
+  return sq.x + sq.y;
+}
+__device__ __forceinline__ float products(const float2 (&a)[2][4], const float2 (&b)[2][4],
+                                          const float2 (&c)[2][4]) {
+  float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    sum = __ffma2_rn(__fmul2_rn(a[j >> 2][j & 3], b[j >> 2][j & 3]), c[j >> 2][j & 3], sum);
+  return sum.x + sum.y;
+}
+
+// The lane's elements times `by` (see rescale), and (1 / rms of such elements, by).
+template <int W>
+__device__ __forceinline__ float2 rescaled(float2 (&v)[2][4], bool idle, float inv_dim, float eps) {
+  const float by = rescale(fmaf(sum_group<W>(idle ? 0.0f : squares(v)), inv_dim, eps));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] = __fmul2_rn(v[j >> 2][j & 3], make_float2(by, by));
+  return make_float2(inv_sqrt(fmaf(sum_group<W>(idle ? 0.0f : squares(v)), inv_dim, eps * by * by)), by);
+}
+
+// The factors with which a row is turned and weighted: y0 = own[0] v0 + cross[0] v1, y1 = own[1] v1 + cross[1] v0.
+__device__ __forceinline__ void weigh(uint32_t valid, const float2 (&w)[2][4], float2 (&own)[2][4],
+                                      float2 (&cross)[2][4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 c = own[0][j], n = cross[0][j];
+    own[0][j] = __fmul2_rn(c, w[0][j]);
+    own[1][j] = __fmul2_rn(c, w[1][j]);
+    cross[0][j] = __fmul2_rn(n, minus(w[1][j]));
+    cross[1][j] = __fmul2_rn(n, w[0][j]);
+    // (Where a pair is not turned, an infinite weight times the sine of 0 must not reach its neighbour.)
+    if (!((valid >> (2 * j)) & 1u)) cross[0][j].x = cross[1][j].x = 0.0f;
+    if (!((valid >> (2 * j + 1)) & 1u)) cross[0][j].y = cross[1][j].y = 0.0f;
+  }
 }
 
 // W lanes (a power of two, 16 elements a lane; those past dim idle) walk `walk` heads of one token, of q or
@@ -145,24 +205,13 @@ __global__ void __launch_bounds__(kThreads, BLOCKS)
   if (live && h0 == 0 && kind == (a.heads[0] == 0) &&
       p.valid != ((p.on[0] ? 0x0Fu : 0u) | (p.on[1] ? 0xF0u : 0u)))
     atomicOr(&g_heads_status, IDX_DEV_BAD_POSITION);
-  // Turned and (NORM) weighted: y0 = own[0] v0 - cross[0] v1, y1 = own[1] v1 + cross[1] v0.
   float2 own_f[NORM ? 2 : 1][4], cross[NORM ? 2 : 1][4];
   angles_of(p, own_f[0], cross[0]);
   const uint32_t valid = p.valid;
   if constexpr (NORM) {
     float2 w[2][4];
     weights_of<ADJ, T>(a, kind, p, w);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 c = own_f[0][j], n = cross[0][j];
-      own_f[0][j] = __fmul2_rn(c, w[0][j]);
-      own_f[1][j] = __fmul2_rn(c, w[1][j]);
-      cross[0][j] = __fmul2_rn(n, minus(w[1][j]));
-      cross[1][j] = __fmul2_rn(n, w[0][j]);
-      // (Where a pair is not turned, an infinite weight times the sine of 0 must not reach its neighbour.)
-      if (!((valid >> (2 * j)) & 1u)) cross[0][j].x = cross[1][j].x = 0.0f;
-      if (!((valid >> (2 * j + 1)) & 1u)) cross[0][j].y = cross[1][j].y = 0.0f;
-    }
+    weigh(valid, w, own_f, cross);
   }
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
   const int at0 = p.at[0], at1 = p.at[1];
@@ -177,27 +226,33 @@ __global__ void __launch_bounds__(kThreads, BLOCKS)
         float2 v[2][4];
         unpack<ADJ, T>(own[d], v);
         if constexpr (NORM) {
-          float2 sq = __fmul2_rn(v[0][0], v[0][0]);
+          const float square = fmaf(sum_lanes<W>(idle ? 0.0f : squares(v)), inv_dim, a.eps);
+          float r = inv_sqrt(square);
+          // (A vote, so that the branch is the warp's: parted lanes, or these rows once more behind the loop,
+          // measured 55 to 62 us for 52 with 8192 tokens of 72 heads of 128.)
+          if (__any_sync(0xffffffffu, !in_range(r))) {
+            const float by = rescale(square);
 #pragma unroll
-          for (int j = 1; j < 4; ++j) sq = __ffma2_rn(v[0][j], v[0][j], sq);
+            for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] = __fmul2_rn(v[j >> 2][j & 3], make_float2(by, by));
+            r = inv_sqrt(fmaf(sum_lanes<W>(idle ? 0.0f : squares(v)), inv_dim, a.eps * by * by));
+            const float2 r2 = make_float2(r, r);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sq = __ffma2_rn(v[1][j], v[1][j], sq);
-          const float ss = sum_lanes<W>(idle ? 0.0f : sq.x + sq.y);
-          const float r = inv_sqrt(fmaf(ss, inv_dim, a.eps));
-          const float2 r2 = make_float2(r, r);
-          const bool odd = !(r > 0.0f);
+            for (int j = 0; j < 4; ++j) {
+              // (What is not turned must not meet its neighbour, which may not be finite, not even times 0.)
+              const float2 x = v[0][j], y = v[1][j];
+              float2 c0 = __fmul2_rn(y, cross[0][j]), c1 = __fmul2_rn(x, cross[1][j]);
+              if (!((valid >> (2 * j)) & 1u)) c0.x = c1.x = 0.0f;
+              if (!((valid >> (2 * j + 1)) & 1u)) c0.y = c1.y = 0.0f;
+              v[0][j] = __fmul2_rn(__ffma2_rn(x, own_f[0][j], c0), r2);
+              v[1][j] = __fmul2_rn(__ffma2_rn(y, own_f[1][j], c1), r2);
+            }
+          } else {
+            const float2 r2 = make_float2(r, r);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 x = v[0][j], y = v[1][j];
-            v[0][j] = __fmul2_rn(__ffma2_rn(x, own_f[0][j], __fmul2_rn(y, cross[0][j])), r2);
-            v[1][j] = __fmul2_rn(__ffma2_rn(y, own_f[1][j], __fmul2_rn(x, cross[1][j])), r2);
-            if (odd) {
-              // The row holds something that is not finite (or too large to be squared): what is not
-              // turned must not meet its neighbour, not even times 0.
-              const float2 a0 = __fmul2_rn(__fmul2_rn(x, r2), own_f[0][j]);
-              const float2 a1 = __fmul2_rn(__fmul2_rn(y, r2), own_f[1][j]);
-              if (!((valid >> (2 * j)) & 1u)) v[0][j].x = a0.x, v[1][j].x = a1.x;
-              if (!((valid >> (2 * j + 1)) & 1u)) v[0][j].y = a0.y, v[1][j].y = a1.y;
+            for (int j = 0; j < 4; ++j) {
+              const float2 x = v[0][j], y = v[1][j];
+              v[0][j] = __fmul2_rn(__ffma2_rn(x, own_f[0][j], __fmul2_rn(y, cross[0][j])), r2);
+              v[1][j] = __fmul2_rn(__ffma2_rn(y, own_f[1][j], __fmul2_rn(x, cross[1][j])), r2);
             }
           }
         } else {
@@ -259,8 +314,15 @@ __global__ void __launch_bounds__(32 * kAnyWarps) k_heads_any(const __grid_const
       ss = fmaf(f, f, ss);
     }
     if (a.norm) {
-      const float r = inv_sqrt(sum_lanes<32>(ss) / static_cast<float>(a.dim) + a.eps);
-      for (int d = lane; d < a.dim; d += 32) row[d] = row[d] * r * weight_at<T>(a, kind, d);
+      float square = sum_lanes<32>(ss) / static_cast<float>(a.dim) + a.eps;
+      const float by = rescale(square);  // (the same for all lanes)
+      if (by != 1.0f) {
+        ss = 0.0f;
+        for (int d = lane; d < a.dim; d += 32) ss = fmaf(row[d] * by, row[d] * by, ss);
+        square = sum_lanes<32>(ss) / static_cast<float>(a.dim) + a.eps * by * by;
+      }
+      const float r = inv_sqrt(square);
+      for (int d = lane; d < a.dim; d += 32) row[d] = row[d] * by * r * weight_at<T>(a, kind, d);
     }
     __syncwarp();
     if (a.r.table != nullptr) {
@@ -288,14 +350,71 @@ struct BackwardSplit {
   int32_t q, k, walk;
 };
 
+// The rows of the calling group whose squares leave float32's range, once more; their parts of the weight's
+// gradient are added to the group's sums.  (A function of its own behind the loop, so that it takes no
+// register from it: in the loop 55 to 59 us for 51.)
+template <typename T, int W, bool ADJ>
+__device__ __noinline__ void gradients_again(const HeadsArgs &a, const BackwardSplit &split, float *s_sum) {
+  constexpr int GROUPS = kThreads / W;
+  const int kind = static_cast<int>(blockIdx.x) >= split.q, walk = split.walk;
+  const int block = blockIdx.x - (kind ? split.q : 0), blocks = kind ? split.k : split.q;
+  const int heads = a.heads[kind], lanes = a.dim / 16, chunks = (heads + walk - 1) / walk;
+  const int group = threadIdx.x / W, lw = threadIdx.x % W, l = min(lw, lanes - 1);
+  const bool idle = lw >= lanes;
+  const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  const int64_t items = a.tokens * chunks, step = static_cast<int64_t>(blocks) * GROUPS;
+  float2 w[2][4];
+  for (int64_t i = static_cast<int64_t>(block) * GROUPS + group; i < items; i += step) {
+    const int64_t t = i / chunks;
+    const int h0 = static_cast<int>(i - t * chunks) * walk, h1 = min(h0 + walk, heads);
+    const Pieces p = pieces_of<ADJ>(a, t, l);
+    float2 c[4], m[4];
+    angles_of(p, c, m);
+    weights_of<ADJ, T>(a, kind, p, w);
+    for (int h = h0; h < h1; ++h) {
+      const T *x = static_cast<const T *>(a.x[kind]) + t * a.x_token[kind] + h * a.x_head[kind];
+      const T *dy = static_cast<const T *>(a.dy[kind]) + t * a.dy_token[kind] + h * a.dy_head[kind];
+      T *out = static_cast<T *>(a.out[kind]) + t * a.out_token[kind] + h * a.out_head[kind];
+      Piece<T, 8> row[2] = {load_piece<T, 8>(x + p.at[0]), load_piece<T, 8>(x + p.at[1])};
+      float2 v[2][4], g[2][4];
+      unpack<ADJ, T>(row, v);
+      if (in_range(inv_sqrt(fmaf(sum_group<W>(idle ? 0.0f : squares(v)), inv_dim, a.eps)))) continue;
+      const float2 r_by = rescaled<W>(v, idle, inv_dim, a.eps);
+      row[0] = load_piece<T, 8>(dy + p.at[0]);
+      row[1] = load_piece<T, 8>(dy + p.at[1]);
+      unpack<ADJ, T>(row, g);
+      turn(p.valid, c, m, g);
+      const float dot = sum_group<W>(idle ? 0.0f : products(g, w, v)), mean = -dot * r_by.x * inv_dim;
+      const float2 r2 = make_float2(r_by.x, r_by.x), k2 = make_float2(mean, mean);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 unit = __fmul2_rn(v[s][j], r2), dw = __fmul2_rn(g[s][j], unit);
+          v[s][j] = __fmul2_rn(__fmul2_rn(__ffma2_rn(g[s][j], w[s][j], __fmul2_rn(unit, k2)), r2),
+                               make_float2(r_by.y, r_by.y));
+          if (!idle && a.dweight[kind] != nullptr) {
+            s_sum[group * (16 * W) + element_at<ADJ>(p, s, j, 0)] += dw.x;
+            s_sum[group * (16 * W) + element_at<ADJ>(p, s, j, 1)] += dw.y;
+          }
+        }
+      pack<ADJ, T>(v, row);
+      if (!idle) {
+        store_piece<T, 8>(out + p.at[0], row[0]);
+        store_piece<T, 8>(out + p.at[1], row[1]);
+      }
+    }
+  }
+}
+
 // The gradients, W lanes a head.  8192 tokens of 32 + 8 heads of 128 (252 MB) take 51 us with the second
 // launch, 37 at the copy rate: 128 registers leave 16 warps an SM (three blocks of them 3 us more, five 22).
-// Walks of two heads 55 us, of eight 52; loads three heads ahead through shared memory 50.5, not worth it.  A lane's 16 elements of
-// the weight's gradient stay in its registers over all its heads; a block leaves its sums in the workspace
-// and a second launch adds the blocks', in order.
+// Walks of two heads 55 us, of eight 52; loads three heads ahead through shared memory 50.5, not worth it.  A
+// lane's 16 elements of the weight's gradient stay in its registers over all its heads; a block leaves its
+// sums in the workspace and a second launch adds the blocks', in order.
 template <typename T, int W, bool ADJ>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
-    k_heads_backward(const __grid_constant__ HeadsArgs a, const BackwardSplit split) {
+    k_heads_backward(const __grid_constant__ HeadsArgs a, const __grid_constant__ BackwardSplit split) {
   constexpr int GROUPS = kThreads / W;
   extern __shared__ float s_sum[];  // [GROUPS][16 * W]
   griddep_wait();
@@ -319,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[s][j] = make_float2(0.0f, 0.0f);
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  float least = 1.0f;  // of the rows' r (the same in all lanes of a group)
   // (All groups of a warp make the same number of rounds, so that the shuffles find all their lanes.)
   for (int64_t i0 = static_cast<int64_t>(block) * GROUPS; i0 < items; i0 += step) {
     const int64_t i = i0 + group, at = min(i, items - 1), t = at / chunks;
@@ -358,7 +478,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
         }
       const float ss = sum_lanes<W>(live_lane ? sq.x + sq.y : 0.0f);
       const float dot = sum_lanes<W>(live_lane ? sd.x + sd.y : 0.0f);
-      const float r = inv_sqrt(fmaf(ss, inv_dim, a.eps));
+      const float r_row = inv_sqrt(fmaf(ss, inv_dim, a.eps));
+      // (A row out of range counts nothing here: it is taken once more below.)
+      const float r = in_range(r_row) ? r_row : 0.0f;
+      least = fminf(least, r);
       const float mean = -dot * r * inv_dim;  // -mean(g w x r)
       if (i < items && h < n) {
         const float2 r2 = make_float2(r, r), k2 = make_float2(mean, mean);
@@ -380,8 +503,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
       out += out_head;
     }
   }
-  if (a.dweight[kind] == nullptr) return;
-  if (live_lane)
+  if (live_lane && a.dweight[kind] != nullptr)
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -389,6 +511,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
         s_sum[group * (16 * W) + element_at<ADJ>(p, s, j, 0)] = dw[s][j].x;
         s_sum[group * (16 * W) + element_at<ADJ>(p, s, j, 1)] = dw[s][j].y;
       }
+  if (least == 0.0f) gradients_again<T, W, ADJ>(a, split, s_sum);
+  if (a.dweight[kind] == nullptr) return;
   __syncthreads();
   for (int d = threadIdx.x; d < a.dim; d += kThreads) {
     float sum = 0.0f;
@@ -436,12 +560,23 @@ __global__ void __launch_bounds__(32 * kAnyWarps)
       ss = fmaf(f, f, ss);
       dot = fmaf(g[d] * weight_at<T>(a, kind, d), f, dot);
     }
-    const float r = inv_sqrt(sum_lanes<32>(ss) / dim + a.eps);
+    float square = sum_lanes<32>(ss) / dim + a.eps;
+    const float by = rescale(square);  // (the same for all lanes)
+    if (by != 1.0f) {
+      ss = dot = 0.0f;
+      for (int d = lane; d < a.dim; d += 32) {
+        const float f = to_f32(x[d]) * by;
+        ss = fmaf(f, f, ss);
+        dot = fmaf(g[d] * weight_at<T>(a, kind, d), f, dot);
+      }
+      square = sum_lanes<32>(ss) / dim + a.eps * by * by;
+    }
+    const float r = inv_sqrt(square);  // (of the elements times `by`)
     const float c = sum_lanes<32>(dot) * r / dim;
     for (int d = lane; d < a.dim; d += 32) {
-      const float unit = to_f32(x[d]) * r;
+      const float unit = to_f32(x[d]) * by * r;
       dw[d] = fmaf(g[d], unit, dw[d]);
-      out[d] = from_f32<T>(r * fmaf(g[d], weight_at<T>(a, kind, d), -unit * c));
+      out[d] = from_f32<T>(r * fmaf(g[d], weight_at<T>(a, kind, d), -unit * c) * by);
     }
     __syncwarp();
   }

@@ -225,3 +225,53 @@ def test_positions_with_a_gap_between_axes(D, name):
     one = idx.norm_rotary(*(t.detach() for t in leaves), pos[:1].expand(3, T), table, axes=axes)
     single = idx.norm_rotary(*(t.detach() for t in leaves), pos[0], table)
     assert torch.equal(one[0], single[0]) and torch.equal(one[1], single[1])
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H,Hkv,D,layout", [(1201, 64, 8, 128, "views"), (9, 5, 2, 64, "views"),
+                                              (9, 5, 2, 192, "odd"), (4, 3, 1, 72, "views")])
+def test_rows_whose_squares_leave_float32(T, H, Hkv, D, layout, name):
+    """Rows of 2^100, 2^124 and 2^-100 among ordinary ones, whose squares are infinite or 0 in float32: the
+    norm and its gradients are the formula's; a row of zeros gives zeros (with eps) or NaN (0 / 0)."""
+    clean()
+    g = torch.Generator(dev()).manual_seed(T + D)
+    table, axes = idx.rotary_table(500, 32), (0,) * 16
+    pos = torch.randint(500, (1, T), generator=g, device=dev(), dtype=torch.int32)
+    extra = 1 if layout == "odd" else 0  # (rows that are not 16-byte aligned take the general kernels)
+
+    def rows(n, powers):
+        x = torch.randn(T, n, D + extra, generator=g, device=dev())
+        at = torch.randint(len(powers), (T, n, 1), generator=g, device=dev())
+        return (x * torch.tensor([2.0 ** p for p in powers], device=dev())[at]).to(DTYPES[name])[:, :, extra:]
+
+    w = [1 + 0.3 * torch.randn(D, generator=g, device=dev()) for _ in range(2)]
+    for powers, eps in (((0, 100, 124, 0), 1e-6), ((0, 100, 124, -100, -100), 0.0)):
+        q, k = rows(H, powers), rows(Hkv, powers)
+        out = idx.norm_rotary(q, k, *w, pos[0], table, eps=eps)
+        clean()
+        for x, ww, y in zip((q, k), w, out):
+            n = x.double() * (x.double().square().mean(-1, keepdim=True) + eps).rsqrt() * ww.double()
+            close(y, rotate(n, pos, axes, table, False, 0), name, 64, n.abs().amax(-1, keepdim=True))
+    for powers, eps in (((0, 80, 100, 0), 1e-6), ((0, 100, -100, -80), 0.0)):
+        q, k = rows(H, powers), rows(Hkv, powers)
+        grads = [torch.randn(x.shape, generator=g, device=dev()).to(x.dtype) for x in (q, k)]
+        leaves = [t.detach().requires_grad_() for t in (q, k, *w)]
+        got = torch.autograd.grad(idx.norm_rotary(*leaves, pos[0], table, eps=eps), leaves, grads)
+        clean()
+        for x, ww, dy, dx, dw in zip((q, k), w, grads, got[:2], got[2:]):
+            X, W = x.double(), ww.double()
+            G = rotate(dy.double(), pos, axes, table, False, 0, back=True)
+            r = (X.square().mean(-1, keepdim=True) + eps).rsqrt()
+            gw = G * W
+            size = r * gw.abs().amax(-1, keepdim=True) + X.abs() * r ** 3 * (gw * X).abs().mean(-1, keepdim=True)
+            close(dx, r * gw - X * r ** 3 * (gw * X).mean(-1, keepdim=True), name, 96, size)
+            close(dw, (G * X * r).sum((0, 1)), "f32", 64 + 32 + T, (G * X * r).abs().sum((0, 1)))
+    q = rows(H, (0, 124))
+    q[0, 0] = 0
+    q[1, 0, 3], q[1, 1, 3] = float("inf"), float("nan")
+    y, _ = idx.norm_rotary(q, None, eps=1e-6)
+    assert (y[0, 0] == 0).all() and torch.isnan(y[1, 1]).all()
+    assert torch.isnan(y[1, 0, 3]) and (torch.cat((y[1, 0, :3], y[1, 0, 4:])) == 0).all()
+    y, _ = idx.norm_rotary(q, None, eps=0.0)
+    clean()
+    assert torch.isnan(y[0, 0]).all() and torch.isfinite(y[2:]).all()
