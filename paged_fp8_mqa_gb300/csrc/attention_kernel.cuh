@@ -57,8 +57,10 @@
 // 1K..32K, 8 rows: 218 us for 173) the shared memory's port, 312 cycles for a tile's writes, 161 for each read
 // by the tensor core, and what separates them, of 870 that a tile takes on an SM; with 32 rows (draft
 // verification, 179 us for 87) the same with three reads of K and the weights' parts, and the softmax warps'
-// latency.  Selected rows: 64-byte rows and their scales from places of their own, of which DRAM moves twice
-// what is used (serving mix, 102 us for 27).  From L2 instead of DRAM decode takes 208 us.  Not kept:
+// latency.  Float16 queries have four parts a weight and at least 16 rows: the same decode 299 us, draft
+// verification 213, head_dim 64 115 for 78.  Selected rows: 64-byte rows and their scales from places of their
+// own, of which DRAM moves twice what is used (serving mix, 102 us for 27).  From L2 instead of DRAM decode
+// takes 208 us.  Not kept:
 // prefetches into L2 by any unit (231 to 273 us), softmax warpgroups in turn on tiles (228 for 219), two or
 // more loading warps a ring (220), two tiles' positions a softmax thread as with PAIRS (261: the stages that
 // two tiles hold are missed by the loads), with 32 rows two buffers of weights and a stage of values fewer

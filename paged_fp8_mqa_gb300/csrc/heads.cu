@@ -410,8 +410,9 @@ __device__ __noinline__ void gradients_again(const HeadsArgs &a, const BackwardS
 // The gradients, W lanes a head.  8192 tokens of 32 + 8 heads of 128 (252 MB) take 51 us with the second
 // launch, 37 at the copy rate: 128 registers leave 16 warps an SM (three blocks of them 3 us more, five 22).
 // Walks of two heads 55 us, of eight 52; loads three heads ahead through shared memory 50.5, not worth it.  A
-// lane's 16 elements of the weight's gradient stay in its registers over all its heads; a block leaves its
-// sums in the workspace and a second launch adds the blocks', in order.
+// lane's 16 elements of the weight's gradient stay in its registers over all its heads (a float32 sum of as many
+// terms as there are heads for each of 4 * SMs * 128 / W groups: 34 of 8192 x 40); a block leaves its sums in the
+// workspace and a second launch adds the blocks', in order and with what the roundings left out.
 template <typename T, int W, bool ADJ>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     k_heads_backward(const __grid_constant__ HeadsArgs a, const __grid_constant__ BackwardSplit split) {
@@ -654,7 +655,11 @@ cudaError_t launch_walk(const HeadsArgs &a, int walk, cudaStream_t stream) {
   return cudaSuccess;
 }
 
-// As many heads a group as leave some thousands of warps, 16 at most; a small call takes one head a group.
+// As many heads a group as leave 8192 warps, 16 at most; a small call takes one head a group.  Norms of 72 heads
+// of 128 in bfloat16, us with 1, 2, 4, 8, 16 heads a group: 64 tokens 2.6, 2.7, 3.2, 4.3, 6.8 (1 is taken); 512
+// tokens 8.4, 6.9, 6.0, 5.1, 7.6 (1); 1024 14.9, 10.6, 8.7, 9.0, 10.2 (2); 2048 28.3, 19.6, 14.6, 14.5, 14.7 (4);
+// 8192 117, 75, 56, 51, 52 (16).  So right at both ends; between 256 and 1024 tokens more heads a group
+// would be faster.
 template <typename T, int W, bool ADJ>
 cudaError_t launch_pieces(const HeadsArgs &a, cudaStream_t stream) {
   int walk = 16;

@@ -73,15 +73,6 @@ __device__ __forceinline__ int key_exponent(float amax) {
   return max(e, -100);
 }
 
-template <typename T>
-__device__ __forceinline__ Piece<T, 8> load8(const T *p, bool whole) {
-  if (whole) return load_piece<T, 8>(p);
-  Piece<T, 8> v;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v.e[j] = p[j];
-  return v;
-}
-
 // Elements [d, d + 8) of a key, turned by the angles at `row`.  turns: the pairs lie in whole pieces,
 // eight elements and as many angles at a time.
 template <typename T>
@@ -220,7 +211,7 @@ __device__ __forceinline__ float reciprocal(float x) {
 // 34,000 tokens of 8 heads of 128 (176 MB) take 45 us, 26 at the copy rate: an instruction-bound and a
 // latency-bound half.  With eight elements a lane, whose partners another lane holds, and scalar arithmetic
 // 80 us; two rounds a warp 48; several tokens a warp, one after the other, the next one's rows asked for
-// ahead, 61 to 71 (fewer warps fit).
+// ahead, 61 to 71 (fewer warps fit).  Float32 (315 MB) 70, 7 of them for the exact side of every border.
 constexpr int kPieceThreads = 128;
 template <typename T, int D, bool ADJ, int ROUNDS>
 __global__ void __launch_bounds__(kPieceThreads, ROUNDS == 1 ? 1 : 5)
@@ -357,7 +348,9 @@ __global__ void __launch_bounds__(kPieceThreads, ROUNDS == 1 ? 1 : 5)
 }
 
 // Any other rotated part, strides or alignment: a warp takes one token and ROUNDS times 32 * 8 / D of its
-// 2 * heads rows (the keys, then the values), eight elements a lane, the partners read from memory.
+// 2 * heads rows (the keys, then the values), eight elements a lane, the partners read from memory.  32,768
+// tokens of 8 heads of 128 take 71 us with 32 elements rotated in halves, 96 with 20 (k_kv4_append_pieces 45
+// with 64 or 128).
 template <typename T, int D, int ROUNDS>
 __global__ void __launch_bounds__(kThreads) k_kv4_append(const Kv4Args a, bool pieces, bool turns) {
   constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
@@ -375,7 +368,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const Kv4Args a, bool p
   Piece<T, 8> own[ROUNDS];
 #pragma unroll
   for (int i = 0; i < ROUNDS; ++i)  // (past the last row: that one again, so that no branch parts the loads)
-    own[i] = load8<T>(row_at(min(first + i * AT_ONCE, 2 * a.heads - 1)) + d, pieces);
+    own[i] = load_whole<T>(row_at(min(first + i * AT_ONCE, 2 * a.heads - 1)) + d, pieces);
   const Spot s = spot_of(a, t, lane);
   if (s.page < 0) return;
   const float2 *angles = nullptr;
@@ -511,8 +504,10 @@ __global__ void __launch_bounds__(kThreads) k_kv4_read(const Kv4Args a, int how,
   }
 }
 
-// Rounds a warp: four while that leaves some thousands of warps, else one (a small call is one chain of
-// latencies, which more warps shorten).
+// Rounds a warp: four of more than 16384 tokens and rounds, else one (a small call is one chain of latencies,
+// which more warps shorten).  8 heads of 128, us with one and with four: 1024 tokens' append 3.6 and 3.7, read
+// 2.7 and 3.0; 4096 8.0 and 7.3, 5.6 and 5.9; 8192 15.4 and 13.0, 9.4 and 7.6; 32768 59 and 45, 35 and 31 (by the
+// general writer 5.6 and 7.1, 16.5 and 14.1, 32 and 26, 124 and 96).
 inline bool many(const Kv4Args &a, int at_once) {
   return static_cast<int64_t>(a.m.tokens) * ((2 * a.heads + at_once - 1) / at_once) > 16384;
 }
