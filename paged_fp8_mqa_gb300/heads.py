@@ -285,9 +285,9 @@ def norm_rotary(q, k, q_weight=None, k_weight=None, positions=None, table=None, 
 
     Autograd records the call where q, k or a weight requires a gradient; given outputs are refused then.
     The weights' gradients are sums in an order that does not change from call to call.  The gradients
-    cannot be differentiated again, and forward-mode gradients are refused.  A backward pass may be captured into a CUDA graph; no eager graph of the
-    same leaves (an output kept from a warm-up step) may live then, as autograd would wait for the stream
-    that it ran on."""
+    cannot be differentiated again, and forward-mode gradients are refused.  A backward pass may be captured
+    into a CUDA graph; no eager graph of the same leaves (an output kept from a warm-up step) may live then, as
+    autograd would wait for the stream that it ran on."""
     import torch
     index = _index(q, "q")
     if axes is not None and type(axes) is not tuple:
